@@ -494,6 +494,192 @@ sv_status kv_commit_draft(sv_handle* handle, const bfl_state* st, int32_t B,
 sv_status kv_rollback_contig(sv_handle* handle, int32_t B, const int32_t* accepted,
                              int32_t* write_ptr, sv_stream_t stream);
 
+/* ------------------------------------------------------------------------ *
+ * Around the verification step: the entries a pass writes, the attention that
+ * reads them, and the rules on the logits.
+ *
+ * Entries.  A verify pass processes R = N + 1 entries per request: entry 0 is
+ * the pending token at position S_b, entries 1 .. n_b are the drafted nodes
+ * (a chain's entry i sits at position S_b + i, a tree's at S_b + depth).
+ * n_nodes [B] gives n_b (NULL = R - 1; -1: the request has no entry at all).
+ * An entry's K or V of one head is `head_dim` values in one of three formats:
+ *   SV_KV_BF16, SV_KV_FP32  the values themselves;
+ *   SV_KV_E4M3              head_dim 8-bit codes (4 exponent, 3 fraction bits)
+ *                           followed by 16 bytes: the fp32 scale, then zeros.
+ *                           value = code * scale.
+ * An entry's row is therefore head_dim * 2, head_dim * 4 or head_dim + 16
+ * bytes.  The entry points that only move entries (kv_commit_copy,
+ * kv_commit_tree, bfl_reserve_cow) take the 8-bit format as a payload of
+ * elem_bytes 2 and head_dim (head_dim + 16) / 2.
+ * ------------------------------------------------------------------------ */
+typedef enum { SV_KV_BF16 = 0, SV_KV_FP32 = 1, SV_KV_E4M3 = 2 } sv_kv_format;
+
+/* Where entries live, and the layer a call works on.
+ *  paged  (block_table set): data [num_blocks][layers][2][heads][block_size][row],
+ *         the entry of position p in block block_table[b][p / block_size], slot
+ *         p % block_size; block_table [B][max_blocks].
+ *  staged (block_table NULL): data [B][rows][layers][2][heads][row], entry i of
+ *         request b at [b][i]; num_blocks, block_size, max_blocks unused.
+ * data is 16-byte aligned and a row is a multiple of 16 bytes; head_dim is a
+ * multiple of 8 (of 16 for SV_KV_E4M3) and at most 256. */
+typedef struct {
+  void* data;
+  const int32_t* block_table;
+  int32_t layers, heads, head_dim, format; /* sv_kv_format */
+  int32_t layer, rows;
+  int32_t num_blocks, block_size, max_blocks;
+  int32_t reserved0;
+} sv_kv_place;
+
+/* Ancestors of every tree node.  parent [B][N] (node i's parent parent[b][i-1]
+ * < i), n_nodes [B] (NULL = N).  mask [B][N+1][mask_ld] words: bit j % 32 of
+ * word j / 32 of row i is set iff j is i or an ancestor of i (the root, bit 0,
+ * included); depth [B][N+1] = the number of ancestors.  Rows past n_b are zero.
+ * mask_ld >= ceil((N+1)/32); words past that are zeroed too.  A parent that is
+ * not a lower node: SV_ERR_STATE in the error word, the node counts as a child
+ * of the root.  N <= SV_TREE_MAX_NODES. */
+sv_status sv_tree_mask(sv_handle* handle, int32_t B, int32_t N, const int32_t* parent,
+                       const int32_t* n_nodes, uint32_t* mask, int64_t mask_ld, int32_t* depth,
+                       sv_stream_t stream);
+
+#define SV_APPEND_PAIRS 1u /* rotary pairs (x[2i], x[2i+1]); else (x[i], x[i + rot_dim/2]) */
+
+/*
+ * Arguments of kv_append: rotate the keys (and queries) of a pass's entries and
+ * write K and V in the cache's format ([RJ] 1: what is written here is
+ * provisional until the commit).
+ *
+ * k, v    [B][R][heads][head_dim], q [B][R][Hq][head_dim] (NULL: none), of
+ *         `dtype`, with element strides {request, entry, head}; the last
+ *         dimension is contiguous, bases and strides are multiples of 16 bytes
+ *         (so slices of one projection's output serve).
+ * q_out   rotated queries, laid out by q_out_stride; may be q itself.
+ * rope    [max_pos][rot_dim / 2][2] fp32 (cos, sin) of every position and pair,
+ *         NULL: no rotation.  Any base, scaling or attention factor is in the
+ *         table.  The first rot_dim values of a head are rotated, the rest pass:
+ *         (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin), in fp32, rounded once.
+ * depth   [B][R] position of entry i past S_b; NULL = i.  Only the rotation
+ *         uses it: paged entries go to slot S_b + i.
+ * seq_len [B] S_b.
+ * dst     a paged or staged place.  SV_KV_E4M3: the scale is the smallest power
+ *         of two with max|x| <= 448 * scale (1 for an all-zero row, never below
+ *         2^-126), codes round x / scale to nearest, ties to even; NaN stays NaN.
+ * Entries past n_b: nothing is written to dst; their q_out rows are zeroed.
+ * A position outside the table's blocks, an n_b past R - 1, or (with rope) a
+ * rotary position outside [0, max_pos): SV_ERR_STATE in the error word, that
+ * entry skipped (its q_out rows are zeroed). */
+typedef struct {
+  int32_t B, R, Hq, dtype; /* dtype: sv_dtype of q, k, v, q_out */
+  uint32_t flags;
+  int32_t rot_dim, max_pos, reserved0;
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_stride[3], k_stride[3], v_stride[3], q_out_stride[3];
+  const float* rope;
+  const int32_t *depth, *seq_len, *n_nodes;
+  sv_kv_place dst;
+} sv_append_args;
+
+size_t sv_append_args_size(void);
+sv_status kv_append(sv_handle* handle, const sv_append_args* args, sv_stream_t stream);
+
+/* Read entries back, decoded: out [B][R][2][heads][head_dim] (contiguous, 16-
+ * byte aligned, bf16 or fp32 by out_dtype) receives entries 0 .. n_b of every
+ * request, from positions S_b + i of a paged place or entries i of a staged
+ * one.  Rows past n_b are zeroed, and so is an entry without a block
+ * (SV_ERR_STATE in the error word). */
+sv_status kv_read(sv_handle* handle, int32_t B, int32_t R, const int32_t* seq_len,
+                  const int32_t* n_nodes, const sv_kv_place* src, void* out, int32_t out_dtype,
+                  sv_stream_t stream);
+
+/*
+ * Arguments of sv_tree_attention: one layer's attention of a verify pass
+ * ([SD] s4: one target pass over all drafted positions; [CV] 3: trees).
+ *
+ * Query row (i, h) of request b sees the cached positions [0, S_b) and the
+ * entries j <= n_b with bit j of mask row i set; its output is
+ *   sum_x p_x V_x,  p = softmax(scale * q . K_x)
+ * over what it sees, K and V those of head h / (Hq / heads).  A row that sees
+ * nothing, and every row past n_b, is zero.  What a row does not see does not
+ * enter its result, whatever it holds (NaN and infinities included).
+ *
+ * q, out  [B][R][Hq][head_dim] with element strides {request, entry, head}
+ *         (multiples of 16 bytes, last dimension contiguous).  dtype SV_BF16
+ *         with a cache of SV_KV_BF16 or SV_KV_E4M3, SV_FP32 with SV_KV_FP32
+ *         (else SV_ERR_UNSUPPORTED).
+ * cache   the paged cache.
+ * stage   the entries' K/V, staged; data NULL: they are in the cache too, at
+ *         positions S_b + j.  Same format, heads and head_dim as the cache.
+ * mask    [B][R][mask_ld] ancestor bits as of sv_tree_mask, or any other
+ *         pattern; NULL = a chain (j <= i).
+ * seq_len [B] S_b.
+ * Scores, the softmax's sums and the output accumulate in fp32.  With a bf16
+ * output the probabilities are rounded to 8 significant bits before they meet
+ * V, as a bf16 product needs; the normaliser sums the unrounded ones.
+ * A sequence longer than its table, an n_b past R - 1: SV_ERR_STATE in the
+ * error word, the request's rows are zeroed.  A block id outside the pool:
+ * SV_ERR_STATE, the request's rows are unspecified.
+ * The workspace rules are spec_verify's: caller-owned, 256-byte aligned, zero-
+ * filled before its first use, left ready for the next call. */
+typedef struct {
+  int32_t B, R, Hq, dtype;
+  const void* q;
+  void* out;
+  int64_t q_stride[3], out_stride[3];
+  const int32_t *seq_len, *n_nodes;
+  const uint32_t* mask;
+  int64_t mask_ld;
+  float scale;
+  int32_t reserved0;
+  sv_kv_place cache, stage;
+} sv_attention_args;
+
+size_t sv_attention_args_size(void);
+sv_status sv_attention_workspace_size(sv_handle* handle, const sv_attention_args* args,
+                                      size_t* bytes);
+sv_status sv_tree_attention(sv_handle* handle, const sv_attention_args* args, void* workspace,
+                            size_t workspace_bytes, sv_stream_t stream);
+
+/*
+ * Arguments of sv_adjust_logits: rules on the target's rows before they are
+ * verified ([SD] s4, s6: penalties and grammar constraints belong to the
+ * transformed distribution).  Row i of request b, for every token x:
+ *   c = how often x occurs in history[b], plus, over the drafted nodes j >= 1
+ *       on row i's path (bits of mask row i; NULL: j <= i), in tokens[b][j-1]
+ *   l = logit; if c > 0: l = (l > 0 ? l / rep : l * rep) - frequency * c - presence
+ *   l += the sum of bias_values over the entries of bias_ids equal to x (in
+ *        list order)
+ *   l = -inf if allowed is given and bit x of the row is clear
+ * in fp32, rounded once to the row's type.  rep, presence, frequency [B] fp32
+ * (NULL: 1, 0, 0).  history [B][history_ld], tokens [B][R-1], bias_ids and
+ * bias_values [B][bias_ld]; ids outside [0, V) are ignored.  allowed
+ * [B][R][allowed_ld] words, bit x % 32 of word x / 32.  Rows past n_b are
+ * copied unchanged.  A rep that is not finite and positive: SV_ERR_STATE, the
+ * request's rows are copied unchanged.
+ * logits, out [B][R][ld] (ld and out_ld in elements, multiples of 16 bytes;
+ * out may be logits).  Elements past V are not written.
+ * history_ld, bias_ld <= 2^24. */
+typedef struct {
+  int32_t B, R, V, dtype;
+  const void* logits;
+  void* out;
+  int64_t ld, out_ld;
+  const int32_t *history, *tokens;
+  int64_t history_ld;
+  const uint32_t* mask;
+  int64_t mask_ld;
+  const int32_t* n_nodes;
+  const float *rep_penalty, *presence, *frequency;
+  const int32_t* bias_ids;
+  const float* bias_values;
+  int64_t bias_ld;
+  const uint32_t* allowed;
+  int64_t allowed_ld;
+} sv_logits_args;
+
+size_t sv_logits_args_size(void);
+sv_status sv_adjust_logits(sv_handle* handle, const sv_logits_args* args, sv_stream_t stream);
+
 /* Synchronise `stream`, then read and clear the handle's device error word
  * (host *device_code = 0 or an sv_status).  Returns SV_ERR_CUDA if the sync
  * itself failed. */

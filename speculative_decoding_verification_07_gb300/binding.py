@@ -8,7 +8,8 @@ and there is no fallback: if the library is missing the import fails loudly.
 Functions carry the C names: sv_create, sv_destroy, sv_workspace_size,
 spec_verify, bfl_init, bfl_reserve, bfl_fork_prefix, bfl_release,
 kv_commit_rollback, kv_commit_draft, bfl_reserve_cow, kv_commit_copy,
-kv_rollback_contig, sv_get_error.  ``Verifier`` and
+kv_rollback_contig, sv_get_error; around the verification step sv_tree_mask,
+kv_append, kv_read, sv_tree_attention, sv_adjust_logits.  ``Verifier`` and
 ``BlockPool`` are thin owners of a handle / workspace and of the pool arrays.
 """
 
@@ -42,8 +43,13 @@ EXPORTS = ("sv_verify_args_size", "sv_create", "sv_destroy", "sv_workspace_size"
            "spec_verify", "bfl_init", "bfl_reserve", "bfl_fork_prefix", "bfl_release",
            "kv_commit_rollback", "kv_rollback_contig", "sv_get_error", "spec_verify_static",
            "kv_commit_draft", "bfl_reserve_cow", "kv_commit_copy", "sv_tree_args_size",
-           "spec_verify_tree", "kv_commit_tree")
+           "spec_verify_tree", "kv_commit_tree", "sv_tree_mask", "sv_append_args_size",
+           "kv_append", "kv_read", "sv_attention_args_size", "sv_attention_workspace_size",
+           "sv_tree_attention", "sv_logits_args_size", "sv_adjust_logits")
 SV_TREE_MAX_NODES = 4096
+SV_KV_BF16, SV_KV_FP32, SV_KV_E4M3 = 0, 1, 2
+E4M3_TAIL = 16     # bytes after an 8-bit entry's codes: its fp32 scale, then zeros
+APPEND_PAIRS = 1   # rotary pairs (x[2i], x[2i+1]); see SV_APPEND_PAIRS
 
 
 class KvPayload(ctypes.Structure):
@@ -52,12 +58,16 @@ class KvPayload(ctypes.Structure):
 
 
 def _payload(kv: torch.Tensor) -> KvPayload:
-    """kv: [num_blocks, layers, 2, heads, block_size, head_dim], contiguous."""
+    """kv: [num_blocks, layers, 2, heads, block_size, head_dim], contiguous; an
+    8-bit cache is uint8 with head_dim + 16 bytes a row and moves as 2-byte
+    elements."""
     if kv.dim() != 6 or kv.shape[2] != 2 or not kv.is_contiguous():
         raise ValueError("kv must be a contiguous [num_blocks, layers, 2, heads, BS, head_dim] tensor")
     p = KvPayload()
     p.data, p.layers, p.heads, p.head_dim = _ptr(kv), kv.shape[1], kv.shape[3], kv.shape[5]
     p.elem_bytes = kv.element_size()
+    if kv.dtype == torch.uint8:
+        p.head_dim, p.elem_bytes = kv.shape[5] // 2, 2
     return p
 
 
@@ -90,6 +100,46 @@ class SvTreeArgs(ctypes.Structure):
                 ("num_emitted", c_void_p), ("status", c_void_p),
                 ("eos_id", c_void_p), ("max_new", c_void_p),
                 ("rep_penalty", c_void_p), ("rep_tokens", c_void_p), ("rep_ld", c_int64)]
+
+
+class SvKvPlace(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("block_table", c_void_p),
+                ("layers", c_int32), ("heads", c_int32), ("head_dim", c_int32),
+                ("format", c_int32), ("layer", c_int32), ("rows", c_int32),
+                ("num_blocks", c_int32), ("block_size", c_int32), ("max_blocks", c_int32),
+                ("reserved0", c_int32)]
+
+
+_Stride = c_int64 * 3
+
+
+class SvAppendArgs(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("R", c_int32), ("Hq", c_int32), ("dtype", c_int32),
+                ("flags", c_uint32), ("rot_dim", c_int32), ("max_pos", c_int32),
+                ("reserved0", c_int32),
+                ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("q_out", c_void_p),
+                ("q_stride", _Stride), ("k_stride", _Stride), ("v_stride", _Stride),
+                ("q_out_stride", _Stride), ("rope", c_void_p),
+                ("depth", c_void_p), ("seq_len", c_void_p), ("n_nodes", c_void_p),
+                ("dst", SvKvPlace)]
+
+
+class SvAttentionArgs(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("R", c_int32), ("Hq", c_int32), ("dtype", c_int32),
+                ("q", c_void_p), ("out", c_void_p), ("q_stride", _Stride),
+                ("out_stride", _Stride), ("seq_len", c_void_p), ("n_nodes", c_void_p),
+                ("mask", c_void_p), ("mask_ld", c_int64), ("scale", ctypes.c_float),
+                ("reserved0", c_int32), ("cache", SvKvPlace), ("stage", SvKvPlace)]
+
+
+class SvLogitsArgs(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("R", c_int32), ("V", c_int32), ("dtype", c_int32),
+                ("logits", c_void_p), ("out", c_void_p), ("ld", c_int64), ("out_ld", c_int64),
+                ("history", c_void_p), ("tokens", c_void_p), ("history_ld", c_int64),
+                ("mask", c_void_p), ("mask_ld", c_int64), ("n_nodes", c_void_p),
+                ("rep_penalty", c_void_p), ("presence", c_void_p), ("frequency", c_void_p),
+                ("bias_ids", c_void_p), ("bias_values", c_void_p), ("bias_ld", c_int64),
+                ("allowed", c_void_p), ("allowed_ld", c_int64)]
 
 
 class BflState(ctypes.Structure):
@@ -139,13 +189,27 @@ def load_library(path: str = LIB_PATH):
     lib.kv_commit_tree.argtypes = [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p,
                                    POINTER(KvPayload), c_void_p]
+    lib.sv_tree_mask.argtypes = [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                                 c_int64, c_void_p, c_void_p]
+    lib.kv_append.argtypes = [c_void_p, POINTER(SvAppendArgs), c_void_p]
+    lib.kv_read.argtypes = [c_void_p, c_int32, c_int32, c_void_p, c_void_p, POINTER(SvKvPlace),
+                            c_void_p, c_int32, c_void_p]
+    lib.sv_attention_workspace_size.argtypes = [c_void_p, POINTER(SvAttentionArgs),
+                                                POINTER(c_size_t)]
+    lib.sv_tree_attention.argtypes = [c_void_p, POINTER(SvAttentionArgs), c_void_p, c_size_t,
+                                      c_void_p]
+    lib.sv_adjust_logits.argtypes = [c_void_p, POINTER(SvLogitsArgs), c_void_p]
     for name in EXPORTS[1:]:
-        if name != "sv_tree_args_size":
-            getattr(lib, name).restype = c_int32
+        getattr(lib, name).restype = c_size_t if name.endswith("_args_size") else c_int32
     if lib.sv_verify_args_size() != ctypes.sizeof(SvVerifyArgs):
         raise ImportError("sv_verify_args layout mismatch between binding and library")
     if lib.sv_tree_args_size() != ctypes.sizeof(SvTreeArgs):
         raise ImportError("sv_tree_args layout mismatch between binding and library")
+    for fn, struct in ((lib.sv_append_args_size, SvAppendArgs),
+                       (lib.sv_attention_args_size, SvAttentionArgs),
+                       (lib.sv_logits_args_size, SvLogitsArgs)):
+        if fn() != ctypes.sizeof(struct):
+            raise ImportError(f"{struct.__name__} layout mismatch between binding and library")
     _lib = lib
     return lib
 
@@ -376,6 +440,173 @@ def kv_rollback_contig(handle, accepted, write_ptr, stream=None) -> None:
         handle, accepted.shape[0], _ptr(accepted), _ptr(write_ptr), _stream(stream)))
 
 
+# --------------------------------------------------------------------------- #
+# around the verification step
+# --------------------------------------------------------------------------- #
+_KV_FORMAT = {torch.bfloat16: SV_KV_BF16, torch.float32: SV_KV_FP32, torch.uint8: SV_KV_E4M3}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _vec(t, n, name):
+    """Pointer of an optional contiguous 4-byte vector or array of at least n values."""
+    if t is None:
+        return None
+    _need(t.element_size() == 4 and t.is_contiguous() and t.numel() >= n,
+          f"{name}: a contiguous 4-byte tensor of at least {n} values expected")
+    return _ptr(t)
+
+
+def _table(t, rows, name):
+    """(pointer, row stride) of a [rows][ld] (or [..][ld]) contiguous 4-byte tensor."""
+    if t is None:
+        return None, 0
+    _need(t.element_size() == 4 and t.is_contiguous() and t.dim() >= 2
+          and t.numel() == rows * t.shape[-1], f"{name}: a contiguous 4-byte [{rows}][..] tensor expected")
+    return _ptr(t), t.shape[-1]
+
+
+def _paged_place(kv, block_table, layer, B) -> SvKvPlace:
+    _need(kv.dim() == 6 and kv.shape[2] == 2 and kv.is_contiguous() and kv.dtype in _KV_FORMAT,
+          "kv must be a contiguous [num_blocks, layers, 2, heads, BS, row] tensor")
+    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_table.is_contiguous()
+          and block_table.dtype == torch.int32, "block_table must be a contiguous int32 [B][max_blocks]")
+    p = SvKvPlace()
+    nb, p.layers, _, p.heads, p.block_size, row = kv.shape
+    p.data, p.block_table, p.num_blocks, p.max_blocks = _ptr(kv), _ptr(block_table), nb, block_table.shape[1]
+    p.format, p.layer = _KV_FORMAT[kv.dtype], layer
+    p.head_dim = row - E4M3_TAIL if kv.dtype == torch.uint8 else row
+    return p
+
+
+def _staged_place(stage, layer, B) -> SvKvPlace:
+    _need(stage.dim() == 6 and stage.shape[3] == 2 and stage.shape[0] == B and stage.is_contiguous()
+          and stage.dtype in _KV_FORMAT, "stage must be a contiguous [B, R, layers, 2, heads, row] tensor")
+    p = SvKvPlace()
+    _, p.rows, p.layers, _, p.heads, row = stage.shape
+    p.data, p.block_table, p.format, p.layer = _ptr(stage), None, _KV_FORMAT[stage.dtype], layer
+    p.head_dim = row - E4M3_TAIL if stage.dtype == torch.uint8 else row
+    return p
+
+
+def _place(kv, block_table, stage, layer, B) -> SvKvPlace:
+    _need((kv is None) != (stage is None) and (kv is None) == (block_table is None),
+          "give either kv with block_table, or stage")
+    return _staged_place(stage, layer, B) if kv is None else _paged_place(kv, block_table, layer, B)
+
+
+def _heads(t, shape, name):
+    _need(t.dim() == 4 and tuple(t.shape) == tuple(shape) and t.stride(3) == 1,
+          f"{name}: expected {list(shape)} with a contiguous last dimension")
+    st = t.stride()
+    return _ptr(t), _Stride(st[0], st[1], st[2])
+
+
+def sv_tree_mask(handle, parent, mask, depth, n_nodes=None, stream=None) -> None:
+    """parent: [B, N] int32; mask: [B, N + 1, ld] and depth: [B, N + 1] int32 outputs."""
+    B, N = parent.shape
+    _need(parent.dtype == torch.int32 and parent.is_contiguous(), "parent must be a contiguous int32 [B][N]")
+    mp, ld = _table(mask, B * (N + 1), "mask")
+    _check("sv_tree_mask", load_library().sv_tree_mask(
+        handle, B, N, _ptr(parent) if N else None, _vec(n_nodes, B, "n_nodes"), mp, ld,
+        _vec(depth, B * (N + 1), "depth"), _stream(stream)))
+
+
+def kv_append(handle, k, v, seq_len, *, kv=None, block_table=None, stage=None, layer=0, q=None,
+              q_out=None, rope=None, interleaved=False, depth=None, n_nodes=None, stream=None) -> None:
+    """k, v: [B, R, heads, head_dim]; q, q_out: [B, R, Hq, head_dim]; rope:
+    [max_pos, rot_dim / 2, 2] fp32 (see ``rope.rope_table``)."""
+    B, R, H, D = k.shape
+    a = SvAppendArgs()
+    a.B, a.R, a.dtype, a.flags = B, R, _dtype_code(k), APPEND_PAIRS if interleaved else 0
+    a.dst = _place(kv, block_table, stage, layer, B)
+    _need(H == a.dst.heads and D == a.dst.head_dim and v.dtype == k.dtype, "k and v do not match the cache")
+    a.k, a.k_stride = _heads(k, (B, R, H, D), "k")
+    a.v, a.v_stride = _heads(v, (B, R, H, D), "v")
+    if q is not None:
+        _need(q_out is not None and q.dtype == k.dtype == q_out.dtype, "q needs q_out, of k's dtype")
+        a.Hq = q.shape[2]
+        a.q, a.q_stride = _heads(q, (B, R, a.Hq, D), "q")
+        a.q_out, a.q_out_stride = _heads(q_out, (B, R, a.Hq, D), "q_out")
+    if rope is not None:
+        _need(rope.dim() == 3 and rope.shape[2] == 2 and rope.is_contiguous() and rope.dtype == torch.float32,
+              "rope must be a contiguous fp32 [max_pos, rot_dim / 2, 2] tensor")
+        a.rope, a.max_pos, a.rot_dim = _ptr(rope), rope.shape[0], 2 * rope.shape[1]
+    a.depth, a.seq_len = _vec(depth, B * R, "depth"), _vec(seq_len, B, "seq_len")
+    a.n_nodes = _vec(n_nodes, B, "n_nodes")
+    _check("kv_append", load_library().kv_append(handle, ctypes.byref(a), _stream(stream)))
+
+
+def kv_read(handle, out, seq_len, *, kv=None, block_table=None, stage=None, layer=0, n_nodes=None,
+            stream=None) -> None:
+    """out: [B, R, 2, heads, head_dim] bf16 or fp32, contiguous."""
+    B, R = out.shape[0], out.shape[1]
+    src = _place(kv, block_table, stage, layer, B)
+    _need(tuple(out.shape[2:]) == (2, src.heads, src.head_dim) and out.is_contiguous(),
+          "out must be a contiguous [B, R, 2, heads, head_dim] tensor")
+    _check("kv_read", load_library().kv_read(
+        handle, B, R, _vec(seq_len, B, "seq_len"), _vec(n_nodes, B, "n_nodes"), ctypes.byref(src),
+        _ptr(out), _dtype_code(out), _stream(stream)))
+
+
+def make_attention_args(q, kv, block_table, seq_len, out, *, stage=None, mask=None, n_nodes=None,
+                        scale=None, layer=0) -> SvAttentionArgs:
+    """q, out: [B, R, Hq, head_dim]; mask: [B, R, ld] words of sv_tree_mask."""
+    B, R, Hq, D = q.shape
+    a = SvAttentionArgs()
+    a.B, a.R, a.Hq, a.dtype = B, R, Hq, _dtype_code(q)
+    a.cache = _paged_place(kv, block_table, layer, B)
+    _need(D == a.cache.head_dim and out.dtype == q.dtype, "q and out do not match the cache")
+    if stage is not None:
+        a.stage = _staged_place(stage, layer, B)
+    a.q, a.q_stride = _heads(q, (B, R, Hq, D), "q")
+    a.out, a.out_stride = _heads(out, (B, R, Hq, D), "out")
+    a.mask, a.mask_ld = _table(mask, B * R, "mask")
+    a.seq_len, a.n_nodes = _vec(seq_len, B, "seq_len"), _vec(n_nodes, B, "n_nodes")
+    a.scale = D ** -0.5 if scale is None else scale
+    return a
+
+
+def sv_attention_workspace_size(handle, args: SvAttentionArgs) -> int:
+    n = c_size_t()
+    _check("sv_attention_workspace_size",
+           load_library().sv_attention_workspace_size(handle, ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def sv_tree_attention(handle, args: SvAttentionArgs, workspace: torch.Tensor, stream=None) -> None:
+    _check("sv_tree_attention", load_library().sv_tree_attention(
+        handle, ctypes.byref(args), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
+def sv_adjust_logits(handle, logits, out, *, V=None, history=None, tokens=None, mask=None, n_nodes=None,
+                     rep_penalty=None, presence=None, frequency=None, bias_ids=None, bias_values=None,
+                     allowed=None, stream=None) -> None:
+    """logits, out: [B, R, ld] (out may be logits); history: [B, H]; tokens: [B, R - 1];
+    bias_ids, bias_values: [B, n]; allowed: [B, R, words]."""
+    B, R, _ = logits.shape
+    a = SvLogitsArgs()
+    a.B, a.R, a.V, a.dtype = B, R, int(V if V is not None else logits.shape[-1]), _dtype_code(logits)
+    _need(out.shape[:2] == logits.shape[:2] and out.dtype == logits.dtype, "out does not match logits")
+    a.logits, a.ld, a.out, a.out_ld = _ptr(logits), _row_ld(logits), _ptr(out), _row_ld(out)
+    _need(B <= 1 or (logits.stride(0) == R * a.ld and out.stride(0) == R * a.out_ld),
+          "logits and out must be whole [B][R][ld] rows")
+    a.history, a.history_ld = _table(history, B, "history")
+    a.tokens = _vec(tokens, B * (R - 1), "tokens")
+    a.mask, a.mask_ld = _table(mask, B * R, "mask")
+    a.n_nodes, a.rep_penalty = _vec(n_nodes, B, "n_nodes"), _vec(rep_penalty, B, "rep_penalty")
+    a.presence, a.frequency = _vec(presence, B, "presence"), _vec(frequency, B, "frequency")
+    a.bias_ids, a.bias_ld = _table(bias_ids, B, "bias_ids")
+    a.bias_values, ld = _table(bias_values, B, "bias_values")
+    _need(ld == a.bias_ld, "bias_ids and bias_values differ in shape")
+    a.allowed, a.allowed_ld = _table(allowed, B * R, "allowed")
+    _check("sv_adjust_logits", load_library().sv_adjust_logits(handle, ctypes.byref(a), _stream(stream)))
+
+
 def sv_get_error(handle, stream=None) -> int:
     code = c_int32()
     _check("sv_get_error", load_library().sv_get_error(handle, _stream(stream), ctypes.byref(code)))
@@ -422,6 +653,7 @@ class Verifier:
         self.device = torch.device("cuda", device)
         self.handle = sv_create(device)
         self.workspace = None
+        self.attention_workspace = None
         self.path_flags = 0  # kernel selection added to every verify() call
 
     def close(self):
@@ -459,6 +691,46 @@ class Verifier:
                       temperature=temperature, **out, **kw)
         ws = self.ensure_workspace(a)
         spec_verify(self.handle, a, ws, stream)
+        return out
+
+    def tree_mask(self, parent, n_nodes=None, out=None, stream=None):
+        """Ancestor bits [B, N + 1, ceil((N + 1) / 32)] and depths [B, N + 1] of trees."""
+        B, N = parent.shape
+        if out is None:
+            out = dict(mask=torch.empty(B, N + 1, (N + 32) // 32, dtype=torch.int32, device=self.device),
+                       depth=torch.empty(B, N + 1, dtype=torch.int32, device=self.device))
+        sv_tree_mask(self.handle, parent, out["mask"], out["depth"], n_nodes, stream)
+        return out
+
+    def kv_append(self, k, v, seq_len, *, q=None, q_out=None, **kw):
+        """Rotate and write the pass's entries; returns the rotated queries
+        (allocated unless given; None without q)."""
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        kv_append(self.handle, k, v, seq_len, q=q, q_out=q_out, **kw)
+        return q_out
+
+    def kv_read(self, out, seq_len, **kw):
+        """Entries 0 .. n_b decoded into out [B, R, 2, heads, head_dim]."""
+        kv_read(self.handle, out, seq_len, **kw)
+        return out
+
+    def tree_attention(self, q, kv, block_table, seq_len, *, out=None, stream=None, **kw):
+        """Attention of the pass's queries over the cache and its own entries;
+        returns out [B, R, Hq, head_dim] (allocated unless given)."""
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        a = make_attention_args(q, kv, block_table, seq_len, out, **kw)
+        need = sv_attention_workspace_size(self.handle, a)
+        if self.attention_workspace is None or self.attention_workspace.numel() < need:
+            self.attention_workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        sv_tree_attention(self.handle, a, self.attention_workspace, stream)
+        return out
+
+    def adjust_logits(self, logits, *, out=None, **kw):
+        """Penalties, biases and grammar masks on the rows; in place unless out is given."""
+        out = logits if out is None else out
+        sv_adjust_logits(self.handle, logits, out, **kw)
         return out
 
     def tree_outputs(self, B: int, N: int):
