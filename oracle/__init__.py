@@ -13,9 +13,11 @@ Modules
   kvcache   reference paged-KV cache manager (block free list, lookahead
             reserve, commit/rollback, prefix fork, release) and the contiguous
             write-pointer rollback.
+  entries   ancestor bits, rotary positions, the 8-bit entry format, the verify
+            pass's attention and the rules on the logits.
 
 Every function names the passage of the source pages it follows.  Where the
 pages are silent the docstring says which reading was taken.
 """
 
-from . import philox, sampling, kvcache  # noqa: F401
+from . import entries, philox, sampling, kvcache  # noqa: F401
