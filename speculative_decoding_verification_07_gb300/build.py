@@ -27,7 +27,7 @@ SOURCES = ["api.cu", "kv_cache.cu", "verify.cu", "verify_bf16.cu", "verify_f32.c
            "verify_static.cu", "verify_topk_bf16.cu", "verify_topk_f32.cu", "verify_topk_mixed.cu",
            "tree_verify.cu", "tree_bf16.cu", "tree_f32.cu", "tree_opts_bf16.cu", "tree_opts_f32.cu",
            "stream.cu", "stream_more.cu", "tree_mask.cu", "kv_entries.cu", "logit_rules.cu",
-           "tree_attention.cu"]
+           "tree_attention.cu", "attention_bf16.cu", "attention_e4m3.cu"]
 
 
 def nvcc() -> str:

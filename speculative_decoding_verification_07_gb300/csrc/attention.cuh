@@ -9,7 +9,7 @@ namespace sv {
 struct AttnParams {
   sv_attention_args a;
   float* part;      // partial results of split rows
-  uint32_t* ticket; // arrivals per split item, zero between calls
+  uint32_t* ticket; // arrivals per shared item, zero between calls
   int* err;
   int splits;
 };

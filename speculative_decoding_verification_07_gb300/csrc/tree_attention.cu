@@ -1,7 +1,7 @@
 // Attention of a verify pass over the paged cache and the pass's own entries:
 // the host entry, and the kernel for fp32 and for shapes outside the tensor
 // kernel's.
-#include "attention.cuh"
+#include "attention_tc.cuh"
 
 namespace sv {
 
@@ -207,12 +207,20 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
   }
 }
 
+// Tickets sit at the workspace's start whatever the shape, so that a call never
+// finds another shape's partial results in them.  Few are ever in use: only
+// items that are shared by CTAs have one, and there are fewer of them than
+// CTAs that fill the GPU twice.
+constexpr int kTickets = 1024;
+constexpr size_t kTicketBytes = kTickets * 4;
+
 // Shares of the keys: enough CTAs to fill the GPU twice, none below 64 keys.
 static int simt_splits(const sv_handle* h, const sv_attention_args* a, int64_t items) {
   const int64_t keys = (int64_t)a->cache.max_blocks * a->cache.block_size + a->R;
   int64_t s = (2 * (int64_t)h->num_sms + items - 1) / (items > 0 ? items : 1);
   const int64_t most = (keys + 63) / 64;
   if (s > most) s = most;
+  if (items > kTickets) s = 1;
   return s < 1 ? 1 : s > 64 ? 64 : (int)s;
 }
 
@@ -222,6 +230,102 @@ static int64_t simt_items(const sv_attention_args* a) {
 }
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// ---------------------------------------------------------------------------
+// The tensor kernel's host side
+// ---------------------------------------------------------------------------
+static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct TcPlan {
+  bool use;
+  int tiles, ctas;  // row tiles per CTA, grid
+  TcKernel k;
+  size_t bytes;
+};
+
+// bf16 and 8-bit caches with heads of 64 or 128 and blocks of whole 8-row
+// groups (the swizzle's unit, so that a TMA box can start at any block) run on
+// the tensor cores, from one row up: padding 4 rows to 128 costs no bytes, and
+// bytes bound them.
+static TcPlan tc_plan(const sv_handle* h, const sv_attention_args* a) {
+  TcPlan p = {};
+  const sv_kv_place& c = a->cache;
+  if (a->dtype != SV_BF16 || (c.head_dim != 64 && c.head_dim != 128) || c.block_size % 8 || c.num_blocks < 1)
+    return p;
+  const int64_t rows = (int64_t)a->R * (a->Hq / c.heads);
+  p.tiles = rows > kTile ? 2 : 1;
+  const int64_t runs = ((int64_t)c.num_blocks + 1) * c.layers * 2 * c.heads;
+  const int64_t items = (int64_t)a->B * c.heads * cdiv(rows, p.tiles * kTile);
+  const int64_t tiles = items * (cdiv((int64_t)c.max_blocks * c.block_size, kTile) + cdiv(a->R, kTile) + 1);
+  if (runs > INT32_MAX || tiles > INT32_MAX || (a->stage.data && a->B > INT32_MAX / a->stage.rows)) return p;
+  p.use = true;
+  p.k = c.format == SV_KV_E4M3 ? tc_kernel_e4m3(c.head_dim, p.tiles) : tc_kernel_bf16(c.head_dim, p.tiles);
+  p.ctas = (int)(tiles < h->num_sms ? tiles : h->num_sms);
+  if (p.ctas > kTickets) p.ctas = kTickets;
+  p.bytes = kTicketBytes + up256((size_t)p.ctas * 2 * p.k.part * 4);
+  return p;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// Rows of an 8-bit entry are mapped without their tails.
+static bool make_map(CUtensorMap* m, const sv_kv_place& pl, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     int box_rows) {
+  const bool f8 = pl.format == SV_KV_E4M3;
+  const int row = f8 ? pl.head_dim : 2 * pl.head_dim, sw = row < 128 ? row : 128;
+  const cuuint32_t box[4] = {(cuuint32_t)(f8 ? sw : sw / 2), (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
+  return encode_tiled()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, pl.data, dims,
+                        strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        sw == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPlan& plan, void* ws, cudaStream_t stream) {
+  if (!encode_tiled()) return SV_ERR_CUDA;
+  TcParams P = {};
+  P.p.a = *a;
+  P.p.ticket = static_cast<uint32_t*>(ws);
+  P.p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketBytes);
+  P.p.err = h->d_err;
+  const sv_kv_place& c = a->cache;
+  P.box = 8;
+  while (P.box < kTile && c.block_size % (2 * P.box) == 0) P.box *= 2;
+  const cuuint64_t row = (cuuint64_t)row_bytes(c), H = (cuuint64_t)c.heads;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.block_size,
+                                (cuuint64_t)c.num_blocks * c.layers * 2 * H};
+    const cuuint64_t strides[2] = {row, row * c.block_size};
+    if (!make_map(&P.pages, c, 3, dims, strides, P.box)) return SV_ERR_CUDA;
+  }
+  if (a->stage.data) {
+    const cuuint64_t per = row * a->stage.layers * 2 * H;  // bytes of an entry
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)a->stage.rows, (cuuint64_t)a->stage.layers * 2 * H,
+                                (cuuint64_t)a->B};
+    const cuuint64_t strides[3] = {per, row, per * a->stage.rows};
+    if (!make_map(&P.stage, a->stage, 4, dims, strides, kStageBox)) return SV_ERR_CUDA;
+  }
+  const sv_status rr = sv_raise_dyn_smem((const void*)plan.k.fn, (size_t)plan.k.smem);
+  if (rr != SV_OK) return rr;
+  if (sv_launch_pdl(plan.k.fn, dim3((unsigned)plan.ctas), dim3(kTcThreads), (size_t)plan.k.smem, stream, P) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  return SV_OK;
+}
 
 }  // namespace sv
 
@@ -253,9 +357,14 @@ extern "C" sv_status sv_attention_workspace_size(sv_handle* h, const sv_attentio
   if (rs != SV_OK) return rs;
   *bytes = 256;
   if (a->B == 0) return SV_OK;
+  const TcPlan plan = tc_plan(h, a);
+  if (plan.use) {
+    *bytes = plan.bytes;
+    return SV_OK;
+  }
   const int64_t items = simt_items(a);
   const int splits = simt_splits(h, a, items);
-  *bytes = up256((size_t)items * 4) + up256((size_t)items * splits * kSimtRows * (a->cache.head_dim + 4) * 4);
+  *bytes = kTicketBytes + up256((size_t)items * splits * kSimtRows * (a->cache.head_dim + 4) * 4);
   return SV_OK;
 }
 
@@ -266,11 +375,13 @@ extern "C" sv_status sv_tree_attention(sv_handle* h, const sv_attention_args* a,
   if (rs != SV_OK) return rs;
   if (a->B == 0) return SV_OK;
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < need) return SV_ERR_INVALID;
+  const TcPlan plan = tc_plan(h, a);
+  if (plan.use) return tc_launch(h, a, plan, ws, (cudaStream_t)stream);
   const int64_t items = simt_items(a);
   AttnParams P;
   P.a = *a;
   P.ticket = static_cast<uint32_t*>(ws);
-  P.part = reinterpret_cast<float*>(static_cast<char*>(ws) + up256((size_t)items * 4));
+  P.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketBytes);
   P.err = h->d_err;
   P.splits = simt_splits(h, a, items);
   const size_t smem = (size_t)(2 * kSimtKeys + kSimtRows) * (a->cache.head_dim + 4) * 4;
