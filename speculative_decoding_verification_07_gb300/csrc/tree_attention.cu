@@ -254,10 +254,9 @@ static TcPlan tc_plan(const sv_handle* h, const sv_attention_args* a) {
     return p;
   const int64_t rows = (int64_t)a->R * (a->Hq / c.heads);
   p.tiles = rows > kTile ? 2 : 1;
-  const int64_t runs = ((int64_t)c.num_blocks + 1) * c.layers * 2 * c.heads;
   const int64_t items = (int64_t)a->B * c.heads * cdiv(rows, p.tiles * kTile);
-  const int64_t tiles = items * (cdiv((int64_t)c.max_blocks * c.block_size, kTile) + cdiv(a->R, kTile) + 1);
-  if (runs > INT32_MAX || tiles > INT32_MAX || (a->stage.data && a->B > INT32_MAX / a->stage.rows)) return p;
+  const int64_t tiles = items * (cdiv((int64_t)c.max_blocks * c.block_size, kTile) + cdiv(a->R, kTile) + 1 + kLead);
+  if (tiles > INT32_MAX || (rows + 2 * kTile) * (a->Hq / c.heads) > INT32_MAX || c.num_blocks == INT32_MAX) return p;
   p.use = true;
   p.k = c.format == SV_KV_E4M3 ? tc_kernel_e4m3(c.head_dim, p.tiles) : tc_kernel_bf16(c.head_dim, p.tiles);
   p.ctas = (int)(tiles < h->num_sms ? tiles : h->num_sms);
@@ -283,12 +282,12 @@ static EncodeTiled encode_tiled() {
 }
 
 // Rows of an 8-bit entry are mapped without their tails.
-static bool make_map(CUtensorMap* m, const sv_kv_place& pl, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+static bool make_map(CUtensorMap* m, const sv_kv_place& pl, const cuuint64_t* dims, const cuuint64_t* strides,
                      int box_rows) {
   const bool f8 = pl.format == SV_KV_E4M3;
   const int row = f8 ? pl.head_dim : 2 * pl.head_dim, sw = row < 128 ? row : 128;
   const cuuint32_t box[4] = {(cuuint32_t)(f8 ? sw : sw / 2), (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
-  return encode_tiled()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, pl.data, dims,
+  return encode_tiled()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pl.data, dims,
                         strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         sw == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -304,23 +303,28 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
   const sv_kv_place& c = a->cache;
   P.box = 8;
   while (P.box < kTile && c.block_size % (2 * P.box) == 0) P.box *= 2;
+  P.block_shift = -1;
+  for (int s = 3; s < 31; ++s)
+    if (c.block_size == 1 << s) P.block_shift = s;
+  const uint32_t G = (uint32_t)(a->Hq / c.heads);
+  P.group_magic = G == 1 ? 0u : (uint32_t)((0x100000000ull + G - 1) / G);
   const cuuint64_t row = (cuuint64_t)row_bytes(c), H = (cuuint64_t)c.heads;
   {
-    const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.block_size,
-                                (cuuint64_t)c.num_blocks * c.layers * 2 * H};
-    const cuuint64_t strides[2] = {row, row * c.block_size};
-    if (!make_map(&P.pages, c, 3, dims, strides, P.box)) return SV_ERR_CUDA;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.block_size, (cuuint64_t)c.layers * 2 * H,
+                                (cuuint64_t)c.num_blocks};
+    const cuuint64_t strides[3] = {row, row * c.block_size, row * c.block_size * c.layers * 2 * H};
+    if (!make_map(&P.pages, c, dims, strides, P.box)) return SV_ERR_CUDA;
   }
   if (a->stage.data) {
     const cuuint64_t per = row * a->stage.layers * 2 * H;  // bytes of an entry
     const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)a->stage.rows, (cuuint64_t)a->stage.layers * 2 * H,
                                 (cuuint64_t)a->B};
     const cuuint64_t strides[3] = {per, row, per * a->stage.rows};
-    if (!make_map(&P.stage, a->stage, 4, dims, strides, kStageBox)) return SV_ERR_CUDA;
+    if (!make_map(&P.stage, a->stage, dims, strides, kStageBox)) return SV_ERR_CUDA;
   }
   const sv_status rr = sv_raise_dyn_smem((const void*)plan.k.fn, (size_t)plan.k.smem);
   if (rr != SV_OK) return rr;
-  if (sv_launch_pdl(plan.k.fn, dim3((unsigned)plan.ctas), dim3(kTcThreads), (size_t)plan.k.smem, stream, P) != cudaSuccess) {
+  if (sv_launch_pdl(plan.k.fn, dim3((unsigned)plan.ctas), dim3((unsigned)plan.k.threads), (size_t)plan.k.smem, stream, P) != cudaSuccess) {
     (void)cudaGetLastError();
     return SV_ERR_CUDA;
   }
