@@ -43,6 +43,8 @@ __device__ __forceinline__ int entry_of(const TcParams& P, int row) {  // row / 
 //   QM = 2: more rows; the streams are two row tiles that share every key tile.
 template <bool F8, int D, int QM>
 struct TcShape {
+  // two softmax groups of four warps; K loads; products; V loads; one for scales
+  // and dead rows
   static constexpr int kThreads = 384;
   static constexpr int kRow = F8 ? D : 2 * D;                // bytes of a row without its tail
   static constexpr int kSw = kRow < 128 ? kRow : 128;        // swizzle = bytes of a row per half
@@ -233,6 +235,62 @@ static __device__ __noinline__ float given_back(const TcParams& P, const TcSegme
   return sum;
 }
 
+// The rare steps of a tile's softmax, as calls so that they stay out of the
+// loop's instructions.
+//
+// Scores that row i does not see become -inf where they are.
+static __device__ __noinline__ void hide_unseen(const TcParams& P, int b, int i, int n, bool prefix, int valid, int u0, int ch_a,
+                                                int ch_e, uint32_t tS) {
+  for (int ch = ch_a; ch < ch_e; ++ch) {
+    const int left = valid - 32 * ch;
+    const uint32_t bits = prefix ? (left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u)
+                          : i <= n ? seen_bits(P.p.a, b, i, n, u0 + 32 * ch)
+                                   : 0u;
+    uint32_t x[32];
+    tmem_ld32(tS + 32 * ch, x);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1 ? x[e] : 0xFF800000u;
+    tmem_st32(tS + 32 * ch, x);
+  }
+  tmem_wait_st();
+}
+
+// Outputs times each row's f.
+static __device__ __noinline__ void rescale(uint32_t tO, int cols, float f) {
+  for (int col = 0; col < cols; col += 16) {
+    uint32_t o[16];
+    tmem_ld16(tO + col, o);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+    tmem_st16(tO + col, o);
+  }
+}
+
+// Rows r0 .. valid - 1 of a V tile without their non-finite values (*found is
+// set where there was one), rows valid .. r1 - 1 cleared; thread of 128.
+template <bool F8>
+static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r1, int row_vecs, int thread, volatile int* found) {
+  const int sw = row_vecs < 8 ? row_vecs : 8;  // vectors of a row per half
+  for (int x = thread; x < (r1 - r0) * row_vecs; x += 128) {
+    const int r = r0 + x / row_vecs, c = x % row_vecs;
+    uint4* d = reinterpret_cast<uint4*>(v + (c / sw * kTile + r) * sw * 16 + c % sw * 16);
+    if (r >= valid) {
+      *d = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 y = *d;
+    constexpr uint32_t kMax = F8 ? 0x7F7F7F7Fu : 0x7F807F80u;
+    auto bad = [&](uint32_t z) { return F8 ? __vcmpeq4(z & kMax, kMax) : __vcmpeq2(z & kMax, kMax); };
+    const uint32_t bx = bad(y.x), by = bad(y.y), bz = bad(y.z), bw = bad(y.w);
+    if (bx | by | bz | bw) {
+      y.x &= ~bx, y.y &= ~by, y.z &= ~bz, y.w &= ~bw;
+      *d = y;
+      *found = 1;
+    }
+  }
+  fence_async_smem();
+}
+
 template <bool F8, int D, int QM>
 __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_kernel(const __grid_constant__ TcParams P) {
   using C = TcShape<F8, D, QM>;
@@ -260,7 +318,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
                                                           // log2 of V's, 1 / V's
 
   if (tid == 0) {
-    for (int i = 0; i < C::kK; ++i) mbar_init(b_kf + 8 * i, 1), mbar_init(b_ke + 8 * i, 1);
+    for (int i = 0; i < C::kK; ++i) mbar_init(b_kf + 8 * i, 1), mbar_init(b_ke + 8 * i, QM);
     for (int i = 0; i < C::kV; ++i) mbar_init(b_vf + 8 * i, 1), mbar_init(b_ve + 8 * i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(b_s + 8 * i, 1), mbar_init(b_p + 8 * i, 4), mbar_init(b_o + 8 * i, 1);
     mbar_init(b_q, 8);
@@ -326,7 +384,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
   }
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&ints[0]);
   const TcSync sync{ints + 1, P.p.err};
-  TcSegment seg;
+  // `found` is written by a call, so it lives in memory, where asm statements
+  // make every use a load; the roles work on a copy in registers
+  TcSegment found;
 
   if (warp >= 8) {
     if (warp == 8 || warp == 10) {
@@ -336,7 +396,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       const uint32_t b_full = v ? b_vf : b_kf, b_empty = v ? b_ve : b_ke, ring = v ? sV : sK;
       constexpr int kElems = F8 ? C::kSw : C::kSw / 2;
       int slot = 0, lap = 0;
-      while (next_segment(P, walk, seg)) {
+      while (next_segment(P, walk, found)) {
+        const TcSegment seg = found;
 #pragma unroll 1
         for (int t = seg.t0; t < seg.t1; ++t) {
           const TcTile k = tile_of(a, seg, t);
@@ -369,92 +430,87 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       }
     } else if (warp == 9) {
       // ---- products --------------------------------------------------------
-      if (lane == 0) {
-        int kbase = 0, ph_p = 0, ph_q = 0;  // ph_p: a bit per stream
-        constexpr uint32_t kIdS = instr_desc(F8 ? 0 : 1, kTile, kTile, false);  // e4m3 or bf16
-        constexpr uint32_t kIdO = instr_desc(F8 ? 0 : 1, kTile, D, true) | (F8 ? 1u << 7 : 0u);  // weights of 5 exponent bits
-        while (next_segment(P, walk, seg)) {
-          const int n = seg.t1 - seg.t0, units = n * QM;
-          wait(sync, b_q, ph_q);
-          ph_q ^= 1;
-          // scores two units ahead of the outputs
+      // The whole warp runs this and one lane issues, so that descriptors stay
+      // in uniform registers; its instructions between products are kept few
+      // (the softmax gives K's slots back, tiles' places are counted and not
+      // divided for), since they add up with the products' own time.
+      const bool one = elect_one();
+      int ph_p = 0, ph_q = 0;  // ph_p: a bit per stream
+      int ks = 0, klap = 0, vs = 0, vlap = 0;
+      constexpr uint32_t kIdS = instr_desc(F8 ? 0 : 1, kTile, kTile, false);  // e4m3 or bf16
+      constexpr uint32_t kIdO = instr_desc(F8 ? 0 : 1, kTile, D, true) | (F8 ? 1u << 7 : 0u);  // weights of 5 exponent bits
+      const uint64_t q0 = smem_desc(sQ, 16, 8 * C::kSw, C::kSw), k0 = smem_desc(sK, 16, 8 * C::kSw, C::kSw);
+      const uint64_t v0 = smem_desc(sV, C::kHalfBytes, 8 * C::kSw, C::kSw);
+      while (next_segment(P, walk, found)) {
+        const TcSegment seg = found;
+        const int units = (seg.t1 - seg.t0) * QM;
+        const int whole = (a.stage.data ? seg.X.S : seg.X.S + seg.X.n + 1) / kTile;  // tiles before it are full
+        wait(sync, b_q, ph_q);
+        ph_q ^= 1;
+        // scores two units ahead of the outputs
 #pragma unroll 1
-          for (int x = 0; x < units + 2; ++x) {
-            if (x >= 2) {
-              const int u = x - 2;
-              const int st = u & 1, t = QM == 2 ? u >> 1 : u, kt = kbase + t, slot = kt % C::kV;
-              const int steps = (tile_of(a, seg, seg.t0 + t).valid + C::kStep - 1) / C::kStep;
-              wait(sync, b_vf + 8 * slot, (kt / C::kV) & 1);
-              wait(sync, b_p + 8 * st, ph_p >> st & 1);
-              ph_p ^= 1 << st;
-              if (!*sync.abort) {
-                tc_fence_after();
-                const uint64_t vd = smem_desc(sV + slot * C::kTileBytes, C::kHalfBytes, 8 * C::kSw, C::kSw);
-                const uint32_t p = tmem + st * 128, o = tmem + 256 + st * 128;
-                const bool first = u < 2;  // of this stream in this segment
-  #pragma unroll
-                for (int j = 0; j < kTile / C::kStep; ++j) {
-                  if (j >= steps) break;
-                  const uint64_t d = vd + j * (C::kStep * C::kSw >> 4);
-                  mma_ts<F8>(o, p + j * (F8 ? 24 : 8), d, kIdO, !first || j > 0);
-                  if (F8) mma_ts<F8>(o, p + j * 24 + 8, d, kIdO, true), mma_ts<F8>(o, p + j * 24 + 16, d, kIdO, true);
-                }
-                mma_commit(b_o + 8 * st);
-                if (QM == 1 || st == 1) mma_commit(b_ve + 8 * slot);
+        for (int x = 0; x < units + 2; ++x) {
+          const int st = x & 1;
+          const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
+          if (x >= 2) {
+            const int t = seg.t0 + (QM == 2 ? (x - 2) >> 1 : x - 2);
+            const int steps = t < whole ? kTile / C::kStep : (tile_of(a, seg, t).valid + C::kStep - 1) / C::kStep;
+            const uint64_t vd = v0 + vs * (C::kTileBytes >> 4);
+            const bool first = x < 4;  // of this stream in this segment
+            wait(sync, b_vf + 8 * vs, vlap & 1);
+            wait(sync, b_p + 8 * st, ph_p >> st & 1);
+            ph_p ^= 1 << st;
+            tc_fence_after();
+            if (one && !*sync.abort) {
+#pragma unroll
+              for (int j = 0; j < kTile / C::kStep; ++j) {
+                if (j >= steps) break;
+                const uint64_t d = vd + j * (C::kStep * C::kSw >> 4);
+                mma_ts<F8>(tO, tS + j * (F8 ? 24 : 8), d, kIdO, !first || j > 0);
+                if (F8) mma_ts<F8>(tO, tS + j * 24 + 8, d, kIdO, true), mma_ts<F8>(tO, tS + j * 24 + 16, d, kIdO, true);
               }
+              mma_commit(b_o + 8 * st);
+              if (QM == 1 || st == 1) mma_commit(b_ve + 8 * vs);
             }
-            if (x < units) {
-              const int u = x;
-              const int st = u & 1, kt = kbase + (QM == 2 ? u >> 1 : u), slot = kt % C::kK;
-              wait(sync, b_kf + 8 * slot, (kt / C::kK) & 1);
-              if (*sync.abort) continue;
-              tc_fence_after();
-              const uint32_t q = sQ + (QM == 2 ? st * C::kQBytes : 0), k = sK + slot * C::kTileBytes;
-              const uint64_t qd = smem_desc(q, 16, 8 * C::kSw, C::kSw), kd = smem_desc(k, 16, 8 * C::kSw, C::kSw);
-  #pragma unroll
+            __syncwarp();
+            if (QM == 1 || st == 1)
+              if (++vs == C::kV) vs = 0, ++vlap;
+          }
+          if (x < units) {
+            const uint64_t qd = q0 + (QM == 2 ? st * (C::kQBytes >> 4) : 0), kd = k0 + ks * (C::kTileBytes >> 4);
+            wait(sync, b_kf + 8 * ks, klap & 1);
+            tc_fence_after();
+            if (one && !*sync.abort) {
+#pragma unroll
               for (int j = 0; j < C::kRow / 32; ++j) {
                 const int at = j / (C::kSw / 32) * C::kHalfBytes + j % (C::kSw / 32) * 32;
-                mma_ss<F8>(tmem + st * 128, qd + (at >> 4), kd + (at >> 4), kIdS, j > 0);
-                if (F8) mma_ss<F8>(tmem + st * 128, qd + ((kTile * D + at) >> 4), kd + (at >> 4), kIdS, true);  // low parts
+                mma_ss<F8>(tS, qd + (at >> 4), kd + (at >> 4), kIdS, j > 0);
+                if (F8) mma_ss<F8>(tS, qd + ((kTile * D + at) >> 4), kd + (at >> 4), kIdS, true);  // low parts
               }
               mma_commit(b_s + 8 * st);
-              if (QM == 1 || st == 1) mma_commit(b_ke + 8 * slot);
             }
+            __syncwarp();
+            if (QM == 1 || st == 1)
+              if (++ks == C::kK) ks = 0, ++klap;
           }
-          kbase += n;
         }
       }
+      // the last arrival that the products owe this block's memory
+      if (vs + vlap > 0) wait(sync, b_ve + 8 * (vs ? vs - 1 : C::kV - 1), (vs ? vlap : vlap - 1) & 1);
     } else {  // warp 11
       if (F8) {
-        // ---- scales of 8-bit entries: four a lane, one load's latency behind
-        // the block's look-up and one ahead of their use
-        bool have_a = false, have_b = false;
-        int blk = 0, at = 0, left = 0, k = 0, t = 0;  // of the tile whose block is being looked up
-        bool staged = false;
-        float ks[4], vs[4];
-        seg.t1 = 0;
+        // ---- scales of 8-bit entries: four a lane, copied into the ring
+        // kAhead tiles before they are due, then turned into what the softmax
+        // adds and multiplies by
+        constexpr int kAhead = 5;
+        int t = 0, issued = 0, due = 0, blk = -1, at = 0, left = 0;
+        bool more = true, staged = false, have = false;  // have: a tile whose block has been looked up
+        TcSegment seg = {};
 #pragma unroll 1
-        while (true) {
-          if (have_b) {
-            const int slot = k % kScaleRing, use = k / kScaleRing;
-            if (use > 0) wait(sync, b_se + 8 * slot, (use - 1) & 1);
-            float* sc = s_sc + slot * 3 * kTile + 4 * lane;
-            float lv[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // scales are finite and positive; what is not must not reach rows that do not see the entry
-              if (!(fabsf(ks[e]) < kInf)) ks[e] = 1.0f;
-              lv[e] = lg2(fminf(fmaxf(vs[e], 1.17549435e-38f), 1.70141183e38f));
-            }
-            *reinterpret_cast<float4*>(sc) = make_float4(ks[0], ks[1], ks[2], ks[3]);
-            *reinterpret_cast<float4*>(sc + kTile) = make_float4(lv[0], lv[1], lv[2], lv[3]);
-            *reinterpret_cast<float4*>(sc + 2 * kTile) = make_float4(ex2(-lv[0]), ex2(-lv[1]), ex2(-lv[2]), ex2(-lv[3]));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_sf + 8 * slot);
-            ++k;
-          }
-          have_b = have_a;
-          if (have_a) {
+        while (more || have || due < issued) {
+          if (have) {
+            const int slot = issued % kScaleRing, lap = issued / kScaleRing;
+            if (lap > 0) wait(sync, b_se + 8 * slot, (lap - 1) & 1);
             const sv_kv_place& pl = staged ? a.stage : a.cache;
             const int64_t step = row_step(pl), rb = D + kTail, each = staged ? (int64_t)pl.layers * 2 * H * rb : rb;
             const char* row = static_cast<const char*>(pl.data) + seg.h * step + D;
@@ -462,32 +518,55 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               row += (((int64_t)seg.b * pl.rows + at) * pl.layers + pl.layer) * 2 * H * rb;
             else
               row += (((int64_t)blk * pl.layers + pl.layer) * 2 * H * pl.block_size + at) * rb;
+            if (!staged && (blk < 0 || blk >= a.cache.num_blocks)) left = 0;
+            const uint32_t dst = smem_u32(s_sc + slot * 3 * kTile + 4 * lane);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              ks[e] = vs[e] = 1.0f;
-              if (e < left) {
-                ks[e] = __ldg(reinterpret_cast<const float*>(row + e * each));
-                vs[e] = __ldg(reinterpret_cast<const float*>(row + e * each + H * step));
-              }
+              const char* src = e < left ? row + e * each : static_cast<const char*>(pl.data);
+              const uint32_t n = e < left ? 4 : 0;  // 0: zeros
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * e), "l"(src), "r"(n) : "memory");
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * kTile + 4 * e),
+                           "l"(e < left ? src + H * step : src), "r"(n)
+                           : "memory");
             }
+            ++issued;
           }
-          if (t >= seg.t1) {
-            if (!next_segment(P, walk, seg)) {
-              if (!have_b) break;
-              have_a = false;
-              seg.t1 = 0;
-              continue;
-            }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          have = false;
+          if (more && t >= seg.t1) {
+            more = next_segment(P, walk, found);
+            seg = found;
             t = seg.t0;
           }
-          const TcTile tl = tile_of(a, seg, t++);
-          staged = tl.staged, at = tl.x0 + 4 * lane, left = tl.valid - 4 * lane, have_a = true;
-          if (!staged) {  // a block holds whole groups of four
-            const int j = block_of(P, at);
-            blk = -1;
-            if (left > 0) blk = __ldg(a.cache.block_table + (int64_t)seg.b * a.cache.max_blocks + j);
-            at -= j * a.cache.block_size;
-            if (blk < 0 || blk >= a.cache.num_blocks) left = 0;
+          if (more) {
+            const TcTile tl = tile_of(a, seg, t++);
+            staged = tl.staged, at = tl.x0 + 4 * lane, left = tl.valid - 4 * lane, have = true;
+            if (!staged) {  // a block holds whole groups of four
+              const int j = block_of(P, at);
+              blk = -1;
+              if (left > 0) blk = __ldg(a.cache.block_table + (int64_t)seg.b * a.cache.max_blocks + j);
+              at -= j * a.cache.block_size;
+            }
+          }
+          if (due < issued && (issued - due > kAhead || !have)) {
+            if (have)
+              asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            else
+              asm volatile("cp.async.wait_group 0;" ::: "memory");
+            const int slot = due % kScaleRing;
+            float* sc = s_sc + slot * 3 * kTile + 4 * lane;
+            float4 ks = *reinterpret_cast<const float4*>(sc), lv = *reinterpret_cast<const float4*>(sc + kTile);
+            // scales are finite and positive; what is not must not reach rows that do not see the entry
+            auto finite = [&](float x) { return x > 0.0f && x < kInf ? x : 1.0f; };
+            auto logv = [](float x) { return lg2(fminf(fmaxf(x, 1.17549435e-38f), 1.70141183e38f)); };
+            ks = make_float4(finite(ks.x), finite(ks.y), finite(ks.z), finite(ks.w));
+            lv = make_float4(logv(lv.x), logv(lv.y), logv(lv.z), logv(lv.w));
+            *reinterpret_cast<float4*>(sc) = ks;
+            *reinterpret_cast<float4*>(sc + kTile) = lv;
+            *reinterpret_cast<float4*>(sc + 2 * kTile) = make_float4(ex2(-lv.x), ex2(-lv.y), ex2(-lv.z), ex2(-lv.w));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_sf + 8 * slot);
+            ++due;
           }
         }
       }
@@ -506,7 +585,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     const uint32_t tS = tmem + (quad << 21) + st * 128, tO = tmem + (quad << 21) + 256 + st * 128;
     int kbase = 0, ph_s = 0, done = 0;  // done: tiles this stream has handed to the products
     int index = 0;                      // of the segment
-    while (next_segment(P, walk, seg)) {
+    while (next_segment(P, walk, found)) {
+        const TcSegment seg = found;
       const int n = seg.t1 - seg.t0, units = n * QM;
       const int i0 = seg.rb * C::kRows;
       // copies of the block's rows in the tile: this thread's copy weighs the
@@ -591,26 +671,13 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         const bool full = k.prefix && k.valid == kTile;
         wait(sync, b_s + 8 * st, ph_s);
         ph_s ^= 1;
+        if (quad == 0 && lane == 0) mbar_arrive(b_ke + 8 * (kt % C::kK));  // the scores' product is done with its keys
         if (F8) wait(sync, b_sf + 8 * (kt % kScaleRing), (kt / kScaleRing) & 1);
         tc_fence_after();
         const float* sc = s_sc + (kt % kScaleRing) * 3 * kTile;
         if (warp_live) {
           const int chunks = (k.valid + 31) / 32, ch_e = min(ch_b, chunks);
-          if (!full) {  // what is not seen becomes -inf where it is
-#pragma unroll 1
-            for (int ch = ch_a; ch < ch_e; ++ch) {
-              const int left = k.valid - 32 * ch;
-              const uint32_t bits = k.prefix ? (left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u)
-                                    : live   ? seen_bits(a, seg.b, i, seg.X.n, k.u0 + 32 * ch)
-                                             : 0u;
-              uint32_t x[32];
-              tmem_ld32(tS + 32 * ch, x);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1 ? x[e] : 0xFF800000u;
-              tmem_st32(tS + 32 * ch, x);
-            }
-            tmem_wait_st();
-          }
+          if (!full) hide_unseen(P, seg.b, i, seg.X.n, k.prefix, k.valid, k.u0, ch_a, ch_e, tS);
           // Two passes over the tile's scores, 32 columns at a time, each read
           // from tensor memory: the loops stay short, which matters more than
           // the second read.
@@ -648,14 +715,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               l *= f;
               wait(sync, b_o + 8 * st, (done - 1) & 1);
               tc_fence_after();
-#pragma unroll 1
-              for (int ch = 0; ch < D / 16; ++ch) {
-                uint32_t o[16];
-                tmem_ld16(tO + 16 * ch, o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(tO + 16 * ch, o);
-              }
+              rescale(tO, D, f);
             }
             m = mn;
           }
@@ -713,29 +773,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         if (tree || k.valid % C::kStep) {
           const int slot = kt % C::kV;
           wait(sync, b_vf + 8 * slot, (kt / C::kV) & 1);
-          char* v = vslots + slot * C::kTileBytes;
-          constexpr int kVecs = C::kRow / 16, kPer = C::kSw / 16;
-          const int r0 = tree ? max(0, -k.u0) : k.valid;
-          const int r1 = (k.valid + C::kStep - 1) / C::kStep * C::kStep;
-#pragma unroll 1
-          for (int x = row; x < (r1 - r0) * kVecs; x += 128) {
-            const int r = r0 + x / kVecs, cc = x % kVecs;
-            uint4* d = reinterpret_cast<uint4*>(v + cc / kPer * C::kHalfBytes + r * C::kSw + cc % kPer * 16);
-            if (r >= k.valid) {
-              *d = make_uint4(0, 0, 0, 0);
-            } else {
-              uint4 y = *d;
-              constexpr uint32_t kMax = F8 ? 0x7F7F7F7Fu : 0x7F807F80u;
-              auto bad = [&](uint32_t z) { return F8 ? __vcmpeq4(z & kMax, kMax) : __vcmpeq2(z & kMax, kMax); };
-              const uint32_t bx = bad(y.x), by = bad(y.y), bz = bad(y.z), bw = bad(y.w);
-              if (bx | by | bz | bw) {
-                y.x &= ~bx, y.y &= ~by, y.z &= ~bz, y.w &= ~bw;
-                *d = y;
-                *reinterpret_cast<volatile int*>(&ints[2]) = 1;
-              }
-            }
-          }
-          fence_async_smem();
+          clean_rows<F8>(vslots + slot * C::kTileBytes, tree ? max(0, -k.u0) : k.valid, k.valid,
+                         (k.valid + C::kStep - 1) / C::kStep * C::kStep, C::kRow / 16, row, &ints[2]);
         }
         if (warp_live) tmem_wait_st();
         tc_fence_before();
@@ -819,14 +858,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
           reinterpret_cast<uint4*>(d)[1] = make_uint4(pack_bf16(y[8], y[9]), pack_bf16(y[10], y[11]), pack_bf16(y[12], y[13]), pack_bf16(y[14], y[15]));
           if (spoiled)
 #pragma unroll 1
-            for (int e = 0; e < 16; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back(P, seg, i, col + e));
+            for (int e = 0; e < 16; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back(P, found, i, col + e));
         } else {
           float* d = part + lrow * D + col;
 #pragma unroll
           for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
           if (spoiled)
 #pragma unroll 1
-            for (int e = 0; e < 16; ++e) d[e] += given_back(P, seg, i, col + e);
+            for (int e = 0; e < 16; ++e) d[e] += given_back(P, found, i, col + e);
         }
       }
       if (split && live && copy == 0 && (QM == 2 || st == 0))
