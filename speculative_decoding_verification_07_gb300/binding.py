@@ -17,7 +17,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from ctypes import POINTER, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 import torch
@@ -148,12 +147,12 @@ class BflState(ctypes.Structure):
                 ("free_top", c_void_p), ("refcount", c_void_p)]
 
 
-_lib = None
+_lib = _native = None
 
 
 def load_library(path: str = LIB_PATH):
     """Load libspecverify.so; raises if it was not built (no fallback exists)."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -206,11 +205,14 @@ def load_library(path: str = LIB_PATH):
         raise ImportError("sv_verify_args layout mismatch between binding and library")
     if lib.sv_tree_args_size() != ctypes.sizeof(SvTreeArgs):
         raise ImportError("sv_tree_args layout mismatch between binding and library")
-    for fn, layout, packed in ((lib.sv_append_args_size, SvAppendArgs, _APPEND),
-                               (lib.sv_attention_args_size, SvAttentionArgs, _ATTENTION),
-                               (lib.sv_logits_args_size, SvLogitsArgs, _LOGITS)):
-        if fn() != ctypes.sizeof(layout) or fn() != packed.size:
+    for fn, layout in ((lib.sv_append_args_size, SvAppendArgs),
+                       (lib.sv_attention_args_size, SvAttentionArgs),
+                       (lib.sv_logits_args_size, SvLogitsArgs)):
+        if fn() != ctypes.sizeof(layout):
             raise ImportError(f"{layout.__name__} layout mismatch between binding and library")
+    from . import _calls as native  # built beside the library; no fallback exists
+    native.open(os.path.abspath(path), SvError)
+    _native = native
     _lib = lib
     return lib
 
@@ -442,21 +444,13 @@ def kv_rollback_contig(handle, accepted, write_ptr, stream=None) -> None:
 
 
 # --------------------------------------------------------------------------- #
-# around the verification step
-#
-# These run once per layer, so their host cost counts: the argument structs are
-# packed in one go (struct formats in the C order), checks look at a tensor
-# once, and no stream object is made.
+# around the verification step: marshalled by the extension module _calls
+# (csrc/calls.cpp), since these run once per layer
 # --------------------------------------------------------------------------- #
-_KV_FORMAT = {torch.bfloat16: SV_KV_BF16, torch.float32: SV_KV_FP32, torch.uint8: SV_KV_E4M3}
-_DTYPE = {torch.bfloat16: SV_BF16, torch.float32: SV_FP32}
-_PLACE = "PP6i4i"
-_ATTENTION = struct.Struct("@4iPP6qPPPqfi" + _PLACE * 2)
-_APPEND = struct.Struct("@4iI3i4P12q4P" + _PLACE)
-_LOGITS = struct.Struct("@4iPPqqPPqPqPPPPPPqPq")
-_PLACE = struct.Struct("@" + _PLACE)
-_NO_PLACE = (0,) * 12
-_WORDS = (torch.int32, torch.float32, torch.uint32)
+def _calls():
+    if _native is None:
+        load_library()
+    return _native
 
 
 def _raw_stream(stream):
@@ -465,135 +459,35 @@ def _raw_stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _fail(what):
-    raise ValueError(what)
-
-
-def _vec(t, n, name):
-    """Pointer of an optional contiguous 4-byte vector or array of at least n values."""
-    if t is None:
-        return 0
-    if t.dtype not in _WORDS or not t.is_contiguous() or t.numel() < n:
-        _fail(f"{name}: a contiguous 4-byte tensor of at least {n} values expected")
-    return _ptr(t)
-
-
-def _table(t, rows, name):
-    """(pointer, row stride) of a [rows][ld] (or [..][ld]) contiguous 4-byte tensor."""
-    if t is None:
-        return 0, 0
-    shape = t.shape
-    if t.dtype not in _WORDS or not t.is_contiguous() or len(shape) < 2 or t.numel() != rows * shape[-1]:
-        _fail(f"{name}: a contiguous 4-byte [{rows}][..] tensor expected")
-    return _ptr(t), shape[-1]
-
-
-def _paged_place(kv, block_table, layer, B):
-    """Fields of an sv_kv_place."""
-    shape, fmt, tshape = kv.shape, _KV_FORMAT.get(kv.dtype), block_table.shape
-    if len(shape) != 6 or shape[2] != 2 or fmt is None or not kv.is_contiguous():
-        _fail("kv must be a contiguous [num_blocks, layers, 2, heads, BS, row] tensor")
-    if len(tshape) != 2 or tshape[0] != B or block_table.dtype != torch.int32 or not block_table.is_contiguous():
-        _fail("block_table must be a contiguous int32 [B][max_blocks]")
-    row = shape[5] - E4M3_TAIL if fmt == SV_KV_E4M3 else shape[5]
-    return (_ptr(kv), _ptr(block_table), shape[1], shape[3], row, fmt, layer, 0, shape[0], shape[4], tshape[1], 0)
-
-
-def _staged_place(stage, layer, B):
-    shape, fmt = stage.shape, _KV_FORMAT.get(stage.dtype)
-    if len(shape) != 6 or shape[3] != 2 or shape[0] != B or fmt is None or not stage.is_contiguous():
-        _fail("stage must be a contiguous [B, R, layers, 2, heads, row] tensor")
-    row = shape[5] - E4M3_TAIL if fmt == SV_KV_E4M3 else shape[5]
-    return (_ptr(stage), 0, shape[2], shape[4], row, fmt, layer, shape[1], 0, 0, 0, 0)
-
-
-def _place(kv, block_table, stage, layer, B):
-    if (kv is None) == (stage is None) or (kv is None) != (block_table is None):
-        _fail("give either kv with block_table, or stage")
-    return _staged_place(stage, layer, B) if kv is None else _paged_place(kv, block_table, layer, B)
-
-
-def _heads(t, B, R, H, D, name):
-    """(pointer, strides of request, entry, head)."""
-    st = t.stride()
-    if t.shape != (B, R, H, D) or st[3] != 1:
-        _fail(f"{name}: expected [{B}, {R}, {H}, {D}] with a contiguous last dimension")
-    return _ptr(t), st[:3]
+def _raw(handle):
+    return handle.value if handle is not None else None
 
 
 def sv_tree_mask(handle, parent, mask, depth, n_nodes=None, stream=None) -> None:
     """parent: [B, N] int32; mask: [B, N + 1, ld] and depth: [B, N + 1] int32 outputs."""
-    B, N = parent.shape
-    if parent.dtype != torch.int32 or not parent.is_contiguous():
-        _fail("parent must be a contiguous int32 [B][N]")
-    mp, ld = _table(mask, B * (N + 1), "mask")
-    _check("sv_tree_mask", load_library().sv_tree_mask(
-        handle, B, N, _ptr(parent), _vec(n_nodes, B, "n_nodes"), mp, ld,
-        _vec(depth, B * (N + 1), "depth"), _raw_stream(stream)))
+    _calls().tree_mask(_raw(handle), parent, n_nodes, mask, depth, _raw_stream(stream))
 
 
 def kv_append(handle, k, v, seq_len, *, kv=None, block_table=None, stage=None, layer=0, q=None,
-              q_out=None, rope=None, interleaved=False, depth=None, n_nodes=None, stream=None) -> None:
+              q_out=None, rope=None, interleaved=False, depth=None, n_nodes=None, stream=None):
     """k, v: [B, R, heads, head_dim]; q, q_out: [B, R, Hq, head_dim]; rope:
-    [max_pos, rot_dim / 2, 2] fp32 (see ``rope.rope_table``)."""
-    B, R, H, D = k.shape
-    dtype = k.dtype
-    dst = _place(kv, block_table, stage, layer, B)
-    if H != dst[3] or D != dst[4] or v.dtype != dtype or dtype not in _DTYPE:
-        _fail("k and v do not match the cache")
-    kp, ks = _heads(k, B, R, H, D, "k")
-    vp, vs = _heads(v, B, R, H, D, "v")
-    Hq = qp = op = 0
-    qs = os_ = (0, 0, 0)
-    if q is not None:
-        if q_out is None or q.dtype != dtype or q_out.dtype != dtype:
-            _fail("q needs q_out, of k's dtype")
-        Hq = q.shape[2]
-        qp, qs = _heads(q, B, R, Hq, D, "q")
-        op, os_ = _heads(q_out, B, R, Hq, D, "q_out")
-    rp = rot = max_pos = 0
-    if rope is not None:
-        shape = rope.shape
-        if len(shape) != 3 or shape[2] != 2 or rope.dtype != torch.float32 or not rope.is_contiguous():
-            _fail("rope must be a contiguous fp32 [max_pos, rot_dim / 2, 2] tensor")
-        rp, max_pos, rot = _ptr(rope), shape[0], 2 * shape[1]
-    a = SvAppendArgs()
-    _APPEND.pack_into(a, 0, B, R, Hq, _DTYPE[dtype], APPEND_PAIRS if interleaved else 0, rot, max_pos, 0,
-                      qp, kp, vp, op, *qs, *ks, *vs, *os_, rp, _vec(depth, B * R, "depth"),
-                      _vec(seq_len, B, "seq_len"), _vec(n_nodes, B, "n_nodes"), *dst)
-    _check("kv_append", load_library().kv_append(handle, a, _raw_stream(stream)))
+    [max_pos, rot_dim / 2, 2] fp32 (see ``rope.rope_table``).  Returns q_out
+    (allocated if q is given without it)."""
+    return _calls().append(_raw(handle), k, v, seq_len, kv, block_table, stage, layer, q, q_out, rope, interleaved, depth,
+                           n_nodes, _raw_stream(stream))
 
 
 def kv_read(handle, out, seq_len, *, kv=None, block_table=None, stage=None, layer=0, n_nodes=None,
             stream=None) -> None:
     """out: [B, R, 2, heads, head_dim] bf16 or fp32, contiguous."""
-    shape = out.shape
-    B, R = shape[:2]
-    src = _place(kv, block_table, stage, layer, B)
-    if shape[2:] != (2, src[3], src[4]) or out.dtype not in _DTYPE or not out.is_contiguous():
-        _fail("out must be a contiguous bf16 or fp32 [B, R, 2, heads, head_dim] tensor")
-    p = SvKvPlace()
-    _PLACE.pack_into(p, 0, *src)
-    _check("kv_read", load_library().kv_read(
-        handle, B, R, _vec(seq_len, B, "seq_len"), _vec(n_nodes, B, "n_nodes"), p, _ptr(out),
-        _DTYPE[out.dtype], _raw_stream(stream)))
+    _calls().read(_raw(handle), out, seq_len, kv, block_table, stage, layer, n_nodes, _raw_stream(stream))
 
 
 def make_attention_args(q, kv, block_table, seq_len, out, *, stage=None, mask=None, n_nodes=None,
                         scale=None, layer=0) -> SvAttentionArgs:
     """q, out: [B, R, Hq, head_dim]; mask: [B, R, ld] words of sv_tree_mask."""
-    B, R, Hq, D = q.shape
-    dtype = q.dtype
-    cache = _paged_place(kv, block_table, layer, B)
-    if D != cache[4] or out.dtype != dtype or dtype not in _DTYPE:
-        _fail("q and out do not match the cache")
-    qp, qs = _heads(q, B, R, Hq, D, "q")
-    op, os_ = _heads(out, B, R, Hq, D, "out")
-    mp, mld = _table(mask, B * R, "mask")
     a = SvAttentionArgs()
-    _ATTENTION.pack_into(a, 0, B, R, Hq, _DTYPE[dtype], qp, op, *qs, *os_, _vec(seq_len, B, "seq_len"),
-                         _vec(n_nodes, B, "n_nodes"), mp, mld, D ** -0.5 if scale is None else scale, 0, *cache,
-                         *(_NO_PLACE if stage is None else _staged_place(stage, layer, B)))
+    _calls().attention_args(ctypes.addressof(a), q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer)
     return a
 
 
@@ -614,25 +508,8 @@ def sv_adjust_logits(handle, logits, out, *, V=None, history=None, tokens=None, 
                      allowed=None, stream=None) -> None:
     """logits, out: [B, R, ld] (out may be logits); history: [B, H]; tokens: [B, R - 1];
     bias_ids, bias_values: [B, n]; allowed: [B, R, words]."""
-    B, R, width = logits.shape
-    ls, os_ = logits.stride(), out.stride()
-    if out.shape[:2] != (B, R) or out.dtype != logits.dtype or logits.dtype not in _DTYPE:
-        _fail("out does not match logits")
-    if ls[2] != 1 or os_[2] != 1 or (B > 1 and (ls[0] != R * ls[1] or os_[0] != R * os_[1])):
-        _fail("logits and out must be whole [B][R][ld] rows")
-    hp, hld = _table(history, B, "history")
-    mp, mld = _table(mask, B * R, "mask")
-    bp, bld = _table(bias_ids, B, "bias_ids")
-    vp, vld = _table(bias_values, B, "bias_values")
-    if bld != vld:
-        _fail("bias_ids and bias_values differ in shape")
-    ap, ald = _table(allowed, B * R, "allowed")
-    a = SvLogitsArgs()
-    _LOGITS.pack_into(a, 0, B, R, width if V is None else V, _DTYPE[logits.dtype], _ptr(logits), _ptr(out), ls[1], os_[1],
-                      hp, _vec(tokens, B * (R - 1), "tokens"), hld, mp, mld, _vec(n_nodes, B, "n_nodes"),
-                      _vec(rep_penalty, B, "rep_penalty"), _vec(presence, B, "presence"),
-                      _vec(frequency, B, "frequency"), bp, vp, bld, ap, ald)
-    _check("sv_adjust_logits", load_library().sv_adjust_logits(handle, a, _raw_stream(stream)))
+    _calls().logits(_raw(handle), logits, out, V, history, tokens, mask, n_nodes, rep_penalty, presence, frequency,
+                    bias_ids, bias_values, allowed, _raw_stream(stream))
 
 
 def sv_get_error(handle, stream=None) -> int:
@@ -681,13 +558,14 @@ class Verifier:
         self.device = torch.device("cuda", device)
         self.handle = sv_create(device)
         self.workspace = None
-        self.attention_workspace, self.attention_sizes = None, {}
+        self.attention_workspace = None
+        self.raw = self.handle.value
         self.path_flags = 0  # kernel selection added to every verify() call
 
     def close(self):
         if self.handle is not None:
             sv_destroy(self.handle)
-            self.handle = None
+            self.handle = self.raw = None
 
     def __del__(self):  # pragma: no cover
         try:
@@ -723,49 +601,44 @@ class Verifier:
 
     def tree_mask(self, parent, n_nodes=None, out=None, stream=None):
         """Ancestor bits [B, N + 1, ceil((N + 1) / 32)] and depths [B, N + 1] of trees."""
-        B, N = parent.shape
-        if out is None:
-            W, n = (N + 32) // 32, B * (N + 1)
-            both = parent.new_empty(n * (W + 1))  # an allocation costs more than a view
-            out = dict(mask=both.as_strided((B, N + 1, W), ((N + 1) * W, W, 1), 0),
-                       depth=both.as_strided((B, N + 1), (N + 1, 1), n * W))
-        sv_tree_mask(self.handle, parent, out["mask"], out["depth"], n_nodes, stream)
-        return out
+        out = out or {}
+        mask, depth = _calls().tree_mask(self.raw, parent, n_nodes, out.get("mask"), out.get("depth"), _raw_stream(stream))
+        return dict(mask=mask, depth=depth)
 
-    def kv_append(self, k, v, seq_len, *, q=None, q_out=None, **kw):
+    def kv_append(self, k, v, seq_len, *, kv=None, block_table=None, stage=None, layer=0, q=None, q_out=None,
+                  rope=None, interleaved=False, depth=None, n_nodes=None, stream=None):
         """Rotate and write the pass's entries; returns the rotated queries
         (allocated unless given; None without q)."""
-        if q is not None and q_out is None:
-            q_out = q.new_empty(q.shape)
-        kv_append(self.handle, k, v, seq_len, q=q, q_out=q_out, **kw)
-        return q_out
+        return _calls().append(self.raw, k, v, seq_len, kv, block_table, stage, layer, q, q_out, rope, interleaved, depth,
+                               n_nodes, _raw_stream(stream))
 
-    def kv_read(self, out, seq_len, **kw):
+    def kv_read(self, out, seq_len, *, kv=None, block_table=None, stage=None, layer=0, n_nodes=None, stream=None):
         """Entries 0 .. n_b decoded into out [B, R, 2, heads, head_dim]."""
-        kv_read(self.handle, out, seq_len, **kw)
+        _calls().read(self.raw, out, seq_len, kv, block_table, stage, layer, n_nodes, _raw_stream(stream))
         return out
 
-    def tree_attention(self, q, kv, block_table, seq_len, *, out=None, stream=None, **kw):
+    def tree_attention(self, q, kv, block_table, seq_len, *, stage=None, mask=None, n_nodes=None, scale=None, layer=0,
+                       out=None, stream=None):
         """Attention of the pass's queries over the cache and its own entries;
         returns out [B, R, Hq, head_dim] (allocated unless given)."""
-        if out is None:
-            out = q.new_empty(q.shape)
-        stage = kw.get("stage")
-        a = make_attention_args(q, kv, block_table, seq_len, out, **kw)
-        # the workspace's size follows from the shapes alone
-        shape = (q.shape, kv.shape, kv.dtype, block_table.shape[1], stage is None or stage.shape[1])
-        need = self.attention_sizes.get(shape)
-        if need is None:
-            need = self.attention_sizes[shape] = sv_attention_workspace_size(self.handle, a)
-        if self.attention_workspace is None or self.attention_workspace.numel() < need:
-            self.attention_workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        sv_tree_attention(self.handle, a, self.attention_workspace, stream)
-        return out
+        s = _raw_stream(stream)
+        got = _calls().attention(self.raw, self.attention_workspace, s, q, kv, block_table, seq_len, out, stage, mask,
+                                 n_nodes, scale, layer)
+        if type(got) is int:  # bytes of workspace: the first call, or a larger shape
+            self.attention_workspace = torch.zeros(got, dtype=torch.uint8, device=self.device)
+            if stream is not None:  # zeroed on the current stream
+                stream.wait_stream(torch.cuda.current_stream(self.device))
+            got = _calls().attention(self.raw, self.attention_workspace, s, q, kv, block_table, seq_len, out, stage, mask,
+                                     n_nodes, scale, layer)
+        return got
 
-    def adjust_logits(self, logits, *, out=None, **kw):
+    def adjust_logits(self, logits, *, out=None, V=None, history=None, tokens=None, mask=None, n_nodes=None,
+                      rep_penalty=None, presence=None, frequency=None, bias_ids=None, bias_values=None, allowed=None,
+                      stream=None):
         """Penalties, biases and grammar masks on the rows; in place unless out is given."""
         out = logits if out is None else out
-        sv_adjust_logits(self.handle, logits, out, **kw)
+        _calls().logits(self.raw, logits, out, V, history, tokens, mask, n_nodes, rep_penalty, presence, frequency,
+                        bias_ids, bias_values, allowed, _raw_stream(stream))
         return out
 
     def tree_outputs(self, B: int, N: int):

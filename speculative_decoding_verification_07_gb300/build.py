@@ -19,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -44,14 +45,36 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _build_calls() -> None:
+    """The Python side of the per-layer calls (csrc/calls.cpp): a plain
+    extension module over torch's tensor type."""
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    inc = os.path.join(root, "include")
+    cmd = [shutil.which("g++") or "g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE, "-I" + inc,
+           "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "calls.cpp"), "-o", CALLS + ".tmp", "-L" + os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-ldl", "-Wl,-rpath," + os.path.join(root, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(CALLS + ".tmp", CALLS)
+
+
 def build(verbose: bool = False, extra=(), out: str = LIB, only=None) -> str:
     """Compile the sources and link `out` (default: the package's library).
     `extra` nvcc flags apply to the translation units compiled; with `only`,
     just those sources are recompiled and the others' objects are reused."""
     os.makedirs(BUILD, exist_ok=True)
     todo = SOURCES if only is None else [s for s in SOURCES if s in only]
-    with cf.ThreadPoolExecutor(max_workers=len(todo)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(todo) + 1) as ex:
+        calls = ex.submit(_build_calls) if only is None else None
         list(ex.map(lambda s: _compile(s, list(extra)), todo))
+        if calls is not None:
+            calls.result()
     objs = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in SOURCES]
     tmp = out + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
