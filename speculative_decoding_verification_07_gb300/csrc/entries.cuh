@@ -43,11 +43,13 @@ __device__ __forceinline__ int64_t entry_offset(const sv_kv_place& p, int b, int
   const int rb = row_bytes(p);
   if (!p.block_table)
     return ((((int64_t)b * p.rows + i) * p.layers + p.layer) * 2) * p.heads * (int64_t)rb;
-  const int64_t j = pos / p.block_size;
-  if (pos < 0 || j >= p.max_blocks) return -1;
+  if (pos < 0 || pos > INT32_MAX) return -1;
+  const uint32_t at = (uint32_t)pos, bs = (uint32_t)p.block_size;
+  const uint32_t j = (bs & (bs - 1)) ? at / bs : at >> (31 - __clz(bs));
+  if (j >= (uint32_t)p.max_blocks) return -1;
   const int blk = p.block_table[(int64_t)b * p.max_blocks + j];
   if (blk < 0 || blk >= p.num_blocks) return -1;
-  return (((int64_t)blk * p.layers + p.layer) * 2 * p.heads * p.block_size + pos % p.block_size) * rb;
+  return (((int64_t)blk * p.layers + p.layer) * 2 * p.heads * p.block_size + (at - j * bs)) * rb;
 }
 
 __device__ __forceinline__ int64_t row_step(const sv_kv_place& p) {

@@ -30,99 +30,155 @@ struct AppendParams {
   int* err;
 };
 
-// One CTA per (request, entry): its queries, keys and values are rows of
-// head_dim; a thread keeps its eight columns' cos / sin in registers for all
-// heads.  Bound by memory: each value is read once and written once, the
-// table's row once per entry.
+// Eight values as they are stored.
 template <bool F32>
-__global__ void __launch_bounds__(kEntryThreads) kv_append_kernel(const __grid_constant__ AppendParams P) {
+struct Raw8 {
+  uint4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> raw8(const char* p) {
+  Raw8<F32> r;
+  r.w[0] = reinterpret_cast<const uint4*>(p)[0];
+  if (F32) r.w[F32 ? 1 : 0] = reinterpret_cast<const uint4*>(p)[1];
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void values8(const Raw8<F32>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+  if (F32) {
+    const uint4 h = r.w[F32 ? 1 : 0];
+    const uint32_t v[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]), x[4 + e] = __uint_as_float(v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[2 * e] = __uint_as_float(w[e] << 16), x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+}
+
+// How the other half of a rotary pair is reached: not at all, in the same eight
+// columns (neighbours), in another lane's (halves that are whole lanes), or in
+// memory (halves that end inside a lane's columns).
+enum Turn { kNone, kPairs, kLanes, kMemory };
+
+// x' = x cos + other * sin, with the sign of the pair's half in sin; columns
+// past the rotated ones have cos 1, sin 0.
+template <bool F32, int TURN>
+__device__ __forceinline__ void turn8(float (&x)[8], const Raw8<F32>& now, const char* row, int d0, int half, int other, uint32_t group,
+                                      const float (&co)[8], const float (&si)[8]) {
+  if (TURN == kNone) return;
+  float o[8];
+  if (TURN == kPairs) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
+  } else if (TURN == kLanes) {
+    Raw8<F32> t;
+#pragma unroll
+    for (int k = 0; k < (F32 ? 2 : 1); ++k)
+      t.w[k] = make_uint4(__shfl_sync(group, now.w[k].x, other), __shfl_sync(group, now.w[k].y, other),
+                          __shfl_sync(group, now.w[k].z, other), __shfl_sync(group, now.w[k].w, other));
+    values8<F32>(t, o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int d = d0 + e, q = d < half ? d + half : d < 2 * half ? d - half : d;
+      o[e] = F32 ? reinterpret_cast<const float*>(row)[q] : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[q]);
+    }
+    __syncwarp(group);  // queries may be rotated in place: every lane has its operands
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = x[e] * co[e] + o[e] * si[e];
+}
+
+// One CTA per (request, entry): its queries, keys and values are rows of
+// head_dim, and a thread has the same eight columns of all its rows, with their
+// cos / sin in registers.  Each value is read and written once, the table's row
+// once per entry; instructions bound it as much as bytes do, so what differs
+// between calls is settled at compile time and rows are reached by one stride.
+// A row does not depend on where its entry goes: a thread's first three are on
+// their way before the entry's length, block and position are known.
+template <bool F32, int TURN>
+__global__ void __launch_bounds__(kEntryThreads, 4) kv_append_kernel(const __grid_constant__ AppendParams P) {
   pdl_wait();
   pdl_trigger();
   const sv_append_args& a = P.a;
   const sv_kv_place& dst = a.dst;
+  constexpr int eb = F32 ? 4 : 2;
   const int b = blockIdx.x / a.R, i = blockIdx.x - b * a.R;
+  const RowLanes L(dst.head_dim);
+  const int Hq = a.q ? a.Hq : 0, H = dst.heads, d0 = 8 * L.c;
+  auto base = [&](const void* p, const int64_t* st) { return static_cast<const char*>(p) + (b * st[0] + i * st[1]) * eb; };
+  const char *q = base(a.q, a.q_stride), *k = base(a.k, a.k_stride), *v = base(a.v, a.v_stride);
+  const int64_t qs = a.q_stride[2] * eb, ks = a.k_stride[2] * eb, vs = a.v_stride[2] * eb;
+  auto kv_row = [&](int r) { return r < H ? k + r * ks : v + (r - H) * vs; };
+  Raw8<F32> q0, q1, kv0;
+  if (L.on) {
+    if (L.slot < Hq) q0 = raw8<F32>(q + L.slot * qs + d0 * eb);
+    if (L.slot + L.nslots < Hq) q1 = raw8<F32>(q + (L.slot + L.nslots) * qs + d0 * eb);
+    if (L.slot < 2 * H) kv0 = raw8<F32>(kv_row(L.slot) + d0 * eb);
+  }
   int n = a.n_nodes ? a.n_nodes[b] : a.R - 1;
   if (n >= a.R) {
     if (threadIdx.x == 0 && i == 0) report(P.err, SV_ERR_STATE);
     n = a.R - 1;
   }
-  const RowLanes L(dst.head_dim);
-  const int Hq = a.q ? a.Hq : 0, H = dst.heads, d0 = 8 * L.c;
   const int64_t S = a.seq_len[b];
   bool live = i <= n;
-  int64_t off = -1;
-  const float* cs = nullptr;
+  int64_t off = -1, pos = 0;
   if (live) {
+    if (TURN != kNone) pos = S + (a.depth ? a.depth[(int64_t)b * a.R + i] : i);
     off = entry_offset(dst, b, i, S + i);
-    live = off >= 0;
-    if (a.rope) {
-      const int64_t pos = S + (a.depth ? a.depth[(int64_t)b * a.R + i] : i);
-      live = live && pos >= 0 && pos < a.max_pos;
-      cs = a.rope + pos * a.rot_dim;
-    }
+    live = off >= 0 && (TURN == kNone || (pos >= 0 && pos < a.max_pos));
     if (!live && threadIdx.x == 0) report(P.err, SV_ERR_STATE);
   }
   if (!L.on) return;
+  char* out = static_cast<char*>(a.q_out) + (b * a.q_out_stride[0] + i * a.q_out_stride[1] + d0) * eb;
+  const int64_t os = a.q_out_stride[2] * eb;
   if (!live) {
     const float zero[8] = {};
-    for (int h = L.slot; h < Hq; h += L.nslots)
-      store8<F32>(a.q_out, b * a.q_out_stride[0] + i * a.q_out_stride[1] + h * a.q_out_stride[2] + d0, zero);
+    for (int h = L.slot; h < Hq; h += L.nslots) store8<F32>(out + h * os, 0, zero);
     return;
   }
-  // cos and (signed) sin of this thread's eight columns, and where the other
-  // half of each pair is: x' = x cos + other * sin
-  const bool pairs = a.flags & SV_APPEND_PAIRS;
   const int half = a.rot_dim >> 1;
+  const int other = TURN == kLanes && d0 < a.rot_dim ? (threadIdx.x & 31) + (d0 < half ? half >> 3 : -(half >> 3)) : threadIdx.x & 31;
   float co[8], si[8];
+  if (TURN != kNone) {
+    const float2* cs = reinterpret_cast<const float2*>(a.rope + pos * a.rot_dim);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int d = d0 + e;
-    co[e] = 1.0f, si[e] = 0.0f;
-    if (cs && d < a.rot_dim) {
-      const int p = pairs ? d >> 1 : d < half ? d : d - half;
-      const bool first = pairs ? !(d & 1) : d < half;
-      const float2 v = reinterpret_cast<const float2*>(cs)[p];
-      co[e] = v.x, si[e] = first ? -v.y : v.y;
+    for (int e = 0; e < 8; ++e) {
+      const int d = d0 + e;
+      co[e] = 1.0f, si[e] = 0.0f;
+      if (d < a.rot_dim) {
+        const float2 t = cs[TURN == kPairs ? d >> 1 : d < half ? d : d - half];
+        co[e] = t.x, si[e] = (TURN == kPairs ? !(d & 1) : d < half) ? -t.y : t.y;
+      }
+    }
+  }
+#pragma unroll 1
+  for (int h = L.slot; h < Hq; h += 2 * L.nslots) {
+    if (h != L.slot) {
+      q0 = raw8<F32>(q + h * qs + d0 * eb);
+      if (h + L.nslots < Hq) q1 = raw8<F32>(q + (h + L.nslots) * qs + d0 * eb);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int hu = h + u * L.nslots;
+      if (hu >= Hq) break;
+      float x[8];
+      const Raw8<F32>& now = u ? q1 : q0;
+      values8<F32>(now, x);
+      turn8<F32, TURN>(x, now, q + hu * qs, d0, half, other, L.group, co, si);
+      store8<F32>(out + hu * os, 0, x);
     }
   }
   const int64_t step = row_step(dst);
-  const int rows = Hq + 2 * H;
-  for (int r = L.slot; r < rows; r += L.nslots) {
-    const bool is_q = r < Hq, is_v = r >= Hq + H;
-    const int h = is_q ? r : is_v ? r - Hq - H : r - Hq;
-    const void* src = is_q ? a.q : is_v ? a.v : a.k;
-    const int64_t* st = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
-    const int64_t at = b * st[0] + i * st[1] + h * st[2];
-    float x[8], o[8];
-    load8<F32>(src, at + d0, x);
-    const bool rot = cs && !is_v && d0 < a.rot_dim;
-    if (rot) {
-      if (pairs) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
-      } else if (half % 8 == 0) {
-        load8<F32>(src, at + (d0 < half ? d0 + half : d0 - half), o);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = d0 + e;
-          const int64_t q = at + (d < half ? d + half : d < a.rot_dim ? d - half : d);
-          o[e] = F32 ? static_cast<const float*>(src)[q]
-                     : __bfloat162float(static_cast<const __nv_bfloat16*>(src)[q]);
-        }
-      }
-    }
-    __syncwarp(L.group);  // q may be rotated in place: every lane has its operands
-    if (rot) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (d0 + e < a.rot_dim) x[e] = x[e] * co[e] + o[e] * si[e];
-    }
-    if (is_q) {
-      store8<F32>(a.q_out, b * a.q_out_stride[0] + i * a.q_out_stride[1] + h * a.q_out_stride[2] + d0, x);
-      continue;
-    }
-    char* row = static_cast<char*>(dst.data) + off + (is_v ? H + h : h) * step;
+#pragma unroll 1
+  for (int r = L.slot; r < 2 * H; r += L.nslots) {
+    if (r != L.slot) kv0 = raw8<F32>(kv_row(r) + d0 * eb);
+    float x[8];
+    values8<F32>(kv0, x);
+    if (r < H) turn8<F32, TURN>(x, kv0, kv_row(r), d0, half, other, L.group, co, si);
+    char* row = static_cast<char*>(dst.data) + off + r * step;
     if (dst.format == SV_KV_FP32) {
       store8<true>(row, d0, x);
     } else if (dst.format == SV_KV_BF16) {
@@ -132,8 +188,7 @@ __global__ void __launch_bounds__(kEntryThreads) kv_append_kernel(const __grid_c
 #pragma unroll
       for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));  // NaN is left out
       const float scale = e4m3_scale(__uint_as_float(__reduce_max_sync(L.group, __float_as_uint(m))));
-      // scales are 2^-126 .. 2^120, so 1 / scale is exact
-      const float inv = 1.0f / scale;
+      const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale));  // scales are 2^-126 .. 2^120
       uint32_t w[2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -147,34 +202,50 @@ __global__ void __launch_bounds__(kEntryThreads) kv_append_kernel(const __grid_c
   }
 }
 
+constexpr int kReadEntries = 4;  // entries of a CTA, looked up together
+
 template <bool F32>
-__global__ void __launch_bounds__(kEntryThreads) kv_read_kernel(int R, const int32_t* seq_len,
+__global__ void __launch_bounds__(kEntryThreads) kv_read_kernel(int total, int R, const int32_t* seq_len,
                                                                 const int32_t* n_nodes,
                                                                 const __grid_constant__ sv_kv_place src,
                                                                 void* out, int* err) {
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x / R, i = blockIdx.x - b * R;
-  int n = n_nodes ? n_nodes[b] : R - 1;
-  if (n >= R) {
-    if (threadIdx.x == 0 && i == 0) report(err, SV_ERR_STATE);
-    n = R - 1;
-  }
-  int64_t off = -1;
-  if (i <= n) {
-    off = entry_offset(src, b, i, (int64_t)seq_len[b] + i);
-    if (off < 0 && threadIdx.x == 0) report(err, SV_ERR_STATE);
-  }
   const RowLanes L(src.head_dim);
-  if (!L.on) return;
   const int64_t step = row_step(src);
-  for (int r = L.slot; r < 2 * src.heads; r += L.nslots) {
-    float x[8] = {};
-    if (off >= 0) {
-      const char* row = static_cast<const char*>(src.data) + off + r * step;
-      load_entry8(row, src.format, 8 * L.c, entry_scale(row, src.format, src.head_dim), x);
+  int64_t off[kReadEntries];
+#pragma unroll
+  for (int u = 0; u < kReadEntries; ++u) {
+    const int e = blockIdx.x * kReadEntries + u, b = e / R, i = e - b * R;
+    off[u] = -1;
+    if (e >= total) continue;
+    int n = n_nodes ? n_nodes[b] : R - 1;
+    if (n >= R) {
+      if (threadIdx.x == 0 && i == 0) report(err, SV_ERR_STATE);
+      n = R - 1;
     }
-    store8<F32>(out, ((int64_t)blockIdx.x * 2 * src.heads + r) * src.head_dim + 8 * L.c, x);
+    if (i <= n) {
+      off[u] = entry_offset(src, b, i, (int64_t)seq_len[b] + i);
+      if (off[u] < 0 && threadIdx.x == 0) report(err, SV_ERR_STATE);
+    }
+  }
+  if (!L.on) return;
+  for (int r = L.slot; r < 2 * src.heads; r += L.nslots) {
+    float x[kReadEntries][8];
+#pragma unroll
+    for (int u = 0; u < kReadEntries; ++u) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] = 0.0f;
+      if (off[u] >= 0) {
+        const char* row = static_cast<const char*>(src.data) + off[u] + r * step;
+        load_entry8(row, src.format, 8 * L.c, entry_scale(row, src.format, src.head_dim), x[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kReadEntries; ++u) {
+      const int64_t e = (int64_t)blockIdx.x * kReadEntries + u;
+      if (e < total) store8<F32>(out, (e * 2 * src.heads + r) * src.head_dim + 8 * L.c, x[u]);
+    }
   }
 }
 
@@ -197,10 +268,13 @@ extern "C" sv_status kv_append(sv_handle* h, const sv_append_args* a, sv_stream_
                   ((uintptr_t)a->rope & 7u)))
     return SV_ERR_INVALID;
   const AppendParams P = {*a, h->d_err};
-  const dim3 grid((unsigned)(a->B * a->R)), block(kEntryThreads);
-  const cudaError_t e = a->dtype == SV_FP32
-                            ? sv_launch_pdl(kv_append_kernel<true>, grid, block, 0, (cudaStream_t)stream, P)
-                            : sv_launch_pdl(kv_append_kernel<false>, grid, block, 0, (cudaStream_t)stream, P);
+  const int turn = !a->rope ? kNone : (a->flags & SV_APPEND_PAIRS) ? kPairs : a->rot_dim % 16 == 0 ? kLanes : kMemory;
+  typedef void (*Fn)(AppendParams);
+  static const Fn fns[2][4] = {
+      {kv_append_kernel<false, kNone>, kv_append_kernel<false, kPairs>, kv_append_kernel<false, kLanes>, kv_append_kernel<false, kMemory>},
+      {kv_append_kernel<true, kNone>, kv_append_kernel<true, kPairs>, kv_append_kernel<true, kLanes>, kv_append_kernel<true, kMemory>}};
+  const cudaError_t e = sv_launch_pdl(fns[a->dtype == SV_FP32][turn], dim3((unsigned)(a->B * a->R)), dim3(kEntryThreads), 0,
+                                      (cudaStream_t)stream, P);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return SV_ERR_CUDA;
@@ -215,11 +289,12 @@ extern "C" sv_status kv_read(sv_handle* h, int32_t B, int32_t R, const int32_t* 
   if (B == 0) return SV_OK;
   if (bad_place(src) || !seq_len || !out || ((uintptr_t)out & 15u) || (int64_t)B * R > INT32_MAX) return SV_ERR_INVALID;
   if (!src->block_table && src->rows < R) return SV_ERR_INVALID;
-  const dim3 grid((unsigned)(B * R)), block(kEntryThreads);
+  const int total = B * R;
+  const dim3 grid((unsigned)((total + kReadEntries - 1) / kReadEntries)), block(kEntryThreads);
   const cudaError_t e =
       out_dtype == SV_FP32
-          ? sv_launch_pdl(kv_read_kernel<true>, grid, block, 0, (cudaStream_t)stream, (int)R, seq_len, n_nodes, *src, out, h->d_err)
-          : sv_launch_pdl(kv_read_kernel<false>, grid, block, 0, (cudaStream_t)stream, (int)R, seq_len, n_nodes, *src, out, h->d_err);
+          ? sv_launch_pdl(kv_read_kernel<true>, grid, block, 0, (cudaStream_t)stream, total, (int)R, seq_len, n_nodes, *src, out, h->d_err)
+          : sv_launch_pdl(kv_read_kernel<false>, grid, block, 0, (cudaStream_t)stream, total, (int)R, seq_len, n_nodes, *src, out, h->d_err);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return SV_ERR_CUDA;
