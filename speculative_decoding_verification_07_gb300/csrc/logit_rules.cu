@@ -5,45 +5,119 @@
 namespace sv {
 
 constexpr int kRuleThreads = 256;
-constexpr int kSlice = 4096;  // tokens of one CTA
-constexpr int kFlight = 4;    // vectors a thread has on their way
+constexpr int kSlice = 2048;  // tokens of one CTA
+constexpr int kFlight = 1;    // vectors of a batch; one batch is on its way while another is written
+constexpr int kNodes = 256;   // drafted tokens of a slice that are kept at hand
 
 struct RuleSmem {
-  int count[kSlice];       // occurrences in the history (and, while a row is patched, in its path)
+  int count[kSlice];       // occurrences in the history
   float bias[kSlice];
-  uint16_t listed[kSlice]; // tokens with a count or a bias; a row's own ones after them
+  uint16_t listed[kSlice]; // tokens with a count or a bias
   uint8_t known[kSlice];   // in the list
-  int n, n_row, n_path;    // listed, with the row's own ones, drafted tokens of this slice
+  uint16_t node[kNodes], token[kNodes];  // drafted nodes whose token is in this slice
+  int n, n_path;           // listed tokens, such nodes (more than kNodes: look through all)
 };
 
-// One CTA takes a slice of 4096 tokens of one request's rows, or of `per` of
+// One CTA takes a slice of 2048 tokens of one request's rows, or of `per` of
 // them.  The grammar mask touches every logit, the other rules a few: so the
 // rows are streamed with the mask alone (out = allowed ? logit : -inf, 16 bytes
-// a thread, four in flight, no look-up), and then the tokens that a penalty or
-// a bias concerns, listed once per slice from the history and the biases, are
-// written again from the row's logits.  Bound by memory: each logit is read and
-// written once.  Looking up counts and biases for every logit as it passed took
-// 109 us instead of 45 for 64 x 7 rows of 128256 (bf16).
+// a thread, no look-up), and then the tokens that a penalty or a bias concerns,
+// listed once per slice from the history and the biases, are written again from
+// the row's logits; a row's own path only adds to their counts, so all rows are
+// written at once.  Bound by memory: each logit is read and written once.  64 x 7
+// rows of 128256 (bf16): looking up counts and biases for every logit as it
+// passed 109 us, a list 71, rows patched together RULES_US; the copy alone 39.
 template <bool F32>
-__global__ void __launch_bounds__(kRuleThreads) logit_rules_kernel(const __grid_constant__ sv_logits_args a, int per, int* err) {
+__global__ void __launch_bounds__(kRuleThreads, 8) logit_rules_kernel(const __grid_constant__ sv_logits_args a, int per, int* err) {
   pdl_wait();
   pdl_trigger();
   __shared__ __align__(16) RuleSmem s;
   constexpr int eb = F32 ? 4 : 2;
-  const int b = blockIdx.y, t = threadIdx.x, lane = t & 31;
-  const int v0 = blockIdx.x * kSlice, len = min(kSlice, a.V - v0), groups = (len + 7) / 8;
+  // slices outermost: the first, where frequent tokens are, take longest
+  const int b = blockIdx.x, t = threadIdx.x, lane = t & 31;
+  const int v0 = blockIdx.y * kSlice, len = min(kSlice, a.V - v0), groups = (len + 7) / 8;
   const int r0 = blockIdx.z * per, r1 = min(a.R, r0 + per);
   int n = a.n_nodes ? a.n_nodes[b] : a.R - 1;
   const float rep = a.rep_penalty ? a.rep_penalty[b] : 1.0f;
   const float pres = a.presence ? a.presence[b] : 0.0f, freq = a.frequency ? a.frequency[b] : 0.0f;
   if (!(rep > 0.0f && rep < __builtin_huge_valf()) || n >= a.R) {
-    if (t == 0 && blockIdx.x == 0 && blockIdx.z == 0) report(err, SV_ERR_STATE);
+    if (t == 0 && blockIdx.y == 0 && blockIdx.z == 0) report(err, SV_ERR_STATE);
     n = -1;
   }
   const int live = min(r1, n + 1) - r0;  // rows of this CTA that the rules apply to
   const bool in_place = a.logits == a.out;
   const char* src0 = static_cast<const char*>(a.logits) + ((int64_t)b * a.R * a.ld + v0) * eb;
   char* dst0 = static_cast<char*>(a.out) + ((int64_t)b * a.R * a.out_ld + v0) * eb;
+
+  // ---- every logit: copied, or -inf ----------------------------------------
+  // A batch of vectors is always on its way: the first is asked for before the
+  // lists are made, the next before the one at hand is written.
+  const int total = !in_place ? (r1 - r0) * groups : a.allowed ? live * groups : 0;  // rows without rules are copied
+  auto row_of = [&](int k) { return groups == kSlice / 8 ? k / (kSlice / 8) : k / groups; };
+  struct Batch {
+    uint4 lo[kFlight], hi[F32 ? kFlight : 1];
+    uint32_t bits[kFlight];
+  };
+  auto fetch = [&](Batch& q, int g0) {
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int k = g0 + u * kRuleThreads, r = row_of(k), g = k - r * groups;
+      if (k >= total) continue;
+      const char* p = src0 + (int64_t)(r0 + r) * a.ld * eb + g * 8 * eb;
+      q.bits[u] = 0xFFu;
+      if (a.allowed && r < live)
+        q.bits[u] = reinterpret_cast<const uint8_t*>(a.allowed + ((int64_t)b * a.R + r0 + r) * a.allowed_ld)[v0 / 8 + g];
+      if (8 * g + 8 <= len) {
+        q.lo[u] = *reinterpret_cast<const uint4*>(p);
+        if (F32) q.hi[F32 ? u : 0] = reinterpret_cast<const uint4*>(p)[1];
+      } else {  // a row may end right after its last token
+        uint32_t w[8] = {};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (8 * g + e >= len) break;
+          if (F32)
+            w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+          else
+            w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << 16 * (e & 1);
+        }
+        q.lo[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (F32) q.hi[F32 ? u : 0] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  };
+  auto put = [&](const Batch& q, int g0) {
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int k = g0 + u * kRuleThreads, r = row_of(k), g = k - r * groups;
+      if (k >= total || (in_place && q.bits[u] == 0xFFu)) continue;
+      char* p = dst0 + (int64_t)(r0 + r) * a.out_ld * eb + g * 8 * eb;
+      const uint4 h = q.hi[F32 ? u : 0];
+      uint32_t w[8] = {q.lo[u].x, q.lo[u].y, q.lo[u].z, q.lo[u].w, h.x, h.y, h.z, h.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool ban = !(q.bits[u] >> e & 1);
+        if (F32)
+          w[e] = ban ? 0xFF800000u : w[e];
+        else if (ban)
+          w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | 0xFF800000u : (w[e >> 1] & 0xFFFF0000u) | 0xFF80u;
+      }
+      if (8 * g + 8 <= len) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (F32) reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (8 * g + e >= len) break;
+          if (F32)
+            reinterpret_cast<uint32_t*>(p)[e] = w[e];
+          else
+            reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> 16 * (e & 1));
+        }
+      }
+    }
+  };
+  Batch now;
+  fetch(now, t);
 
   // ---- the tokens the rules concern ----------------------------------------
   if (live > 0) {
@@ -55,14 +129,24 @@ __global__ void __launch_bounds__(kRuleThreads) logit_rules_kernel(const __grid_
     if (t == 0) s.n = s.n_path = 0;
     __syncthreads();
     auto list = [&](int x, int* n) { s.listed[atomicAdd(n, 1)] = (uint16_t)x; };
-    for (int i = t; i < a.history_ld; i += kRuleThreads) {
-      const int x = a.history[b * a.history_ld + i] - v0;
-      if (x >= 0 && x < len && atomicAdd(&s.count[x], 1) == 0) s.known[x] = 1, list(x, &s.n);
+    for (int i0 = t; i0 < a.history_ld; i0 += 4 * kRuleThreads) {
+      int x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kRuleThreads;
+        x[u] = i < a.history_ld ? a.history[b * a.history_ld + i] - v0 : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (x[u] >= 0 && x[u] < len && atomicAdd(&s.count[x[u]], 1) == 0) s.known[x[u]] = 1, list(x[u], &s.n);
     }
     const int np = a.mask ? n : min(n, r1 - 1);
     for (int j = t; j < np; j += kRuleThreads) {
       const int x = a.tokens[(int64_t)b * (a.R - 1) + j] - v0;
-      if (x >= 0 && x < len) s.n_path = 1;
+      if (x >= 0 && x < len) {
+        const int q = atomicAdd(&s.n_path, 1);
+        if (q < kNodes) s.node[q] = (uint16_t)(j + 1), s.token[q] = (uint16_t)x;
+      }
     }
     __syncthreads();
     // one warp adds the biases, so that a token named several times gets its
@@ -90,114 +174,72 @@ __global__ void __launch_bounds__(kRuleThreads) logit_rules_kernel(const __grid_
       }
   }
 
-  // ---- every logit: copied, or -inf ----------------------------------------
-  const int rows = in_place ? live : r1 - r0;  // rows without rules are copied
-  if (!in_place || a.allowed) {
-    const int total = rows * groups;
-    auto row_of = [&](int k) { return groups == kSlice / 8 ? k / (kSlice / 8) : k / groups; };
-    for (int g0 = t; g0 < total; g0 += kFlight * kRuleThreads) {
-      uint4 lo[kFlight], hi[kFlight];
-      uint32_t bits[kFlight];
-#pragma unroll
-      for (int u = 0; u < kFlight; ++u) {
-        const int k = g0 + u * kRuleThreads, r = row_of(k), g = k - r * groups;
-        if (k >= total) continue;
-        const char* p = src0 + (int64_t)(r0 + r) * a.ld * eb + g * 8 * eb;
-        bits[u] = 0xFFu;
-        if (a.allowed && r < live)
-          bits[u] = reinterpret_cast<const uint8_t*>(a.allowed + ((int64_t)b * a.R + r0 + r) * a.allowed_ld)[v0 / 8 + g];
-        if (8 * g + 8 <= len) {
-          lo[u] = *reinterpret_cast<const uint4*>(p);
-          if (F32) hi[u] = reinterpret_cast<const uint4*>(p)[1];
-        } else {  // a row may end right after its last token
-          uint32_t w[8] = {};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (8 * g + e >= len) break;
-            if (F32)
-              w[e] = reinterpret_cast<const uint32_t*>(p)[e];
-            else
-              w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << 16 * (e & 1);
-          }
-          lo[u] = make_uint4(w[0], w[1], w[2], w[3]), hi[u] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kFlight; ++u) {
-        const int k = g0 + u * kRuleThreads, r = row_of(k), g = k - r * groups;
-        if (k >= total || (in_place && bits[u] == 0xFFu)) continue;
-        char* p = dst0 + (int64_t)(r0 + r) * a.out_ld * eb + g * 8 * eb;
-        uint32_t w[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool ban = !(bits[u] >> e & 1);
-          if (F32)
-            w[e] = ban ? 0xFF800000u : w[e];
-          else if (ban)
-            w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | 0xFF800000u : (w[e >> 1] & 0xFFFF0000u) | 0xFF80u;
-        }
-        if (8 * g + 8 <= len) {
-          *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-          if (F32) reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (8 * g + e >= len) break;
-            if (F32)
-              reinterpret_cast<uint32_t*>(p)[e] = w[e];
-            else
-              reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> 16 * (e & 1));
-          }
-        }
-      }
-    }
+  constexpr int kStride = kFlight * kRuleThreads;
+#pragma unroll 1
+  for (int g0 = t; g0 < total; g0 += kStride) {
+    Batch next;
+    fetch(next, g0 + kStride);
+    put(now, g0);
+    now = next;
   }
   if (live <= 0) return;
   __syncthreads();
 
   // ---- the listed tokens again ---------------------------------------------
-  auto patch = [&](int r, int x) {
-    const int64_t row = (int64_t)b * a.R + r0 + r;
+  const bool kept = s.n_path <= kNodes;
+  const int nodes = kept ? s.n_path : a.mask ? n : min(n, r1 - 1);
+  auto token_of = [&](int q) { return kept ? (int)s.token[q] : a.tokens[(int64_t)b * (a.R - 1) + q] - v0; };
+  auto on_path = [&](int r, int q) {
+    const int node = kept ? s.node[q] : q + 1;
+    if (!a.mask) return node <= r0 + r;
+    return (bool)(a.mask[((int64_t)b * a.R + r0 + r) * a.mask_ld + (node >> 5)] >> (node & 31) & 1);
+  };
+  // a row's logit of a listed token; banned ones stay as they are
+  auto at = [&](int64_t ld, int r, int x) { return (int64_t)(r0 + r) * ld + x; };
+  auto banned = [&](int r, int x) {
     const int v = v0 + x;
-    if (a.allowed && !(a.allowed[row * a.allowed_ld + (v >> 5)] >> (v & 31) & 1)) return;
-    const int64_t at = (int64_t)(r0 + r) * a.ld + x, to = (int64_t)(r0 + r) * a.out_ld + x;
-    float l = F32 ? reinterpret_cast<const float*>(src0)[at]
-                  : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(src0)[at]);
-    const int c = s.count[x];
+    return a.allowed && !(a.allowed[((int64_t)b * a.R + r0 + r) * a.allowed_ld + (v >> 5)] >> (v & 31) & 1);
+  };
+  auto logit = [&](int r, int x) {
+    return F32 ? reinterpret_cast<const float*>(src0)[at(a.ld, r, x)]
+               : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(src0)[at(a.ld, r, x)]);
+  };
+  auto patch = [&](int r, int x, int c, float l) {
     if (c > 0) l = (l > 0.0f ? l / rep : l * rep) - (freq * (float)c + pres);
     if (a.bias_ld > 0) l += s.bias[x];
     if (F32)
-      reinterpret_cast<float*>(dst0)[to] = l;
+      reinterpret_cast<float*>(dst0)[at(a.out_ld, r, x)] = l;
     else
-      reinterpret_cast<__nv_bfloat16*>(dst0)[to] = __float2bfloat16_rn(l);
+      reinterpret_cast<__nv_bfloat16*>(dst0)[at(a.out_ld, r, x)] = __float2bfloat16_rn(l);
   };
   const int listed = s.n;
-  if (!s.n_path) {  // no drafted token is in this slice: every row has the same list
-    for (int k = t; k < live * listed; k += kRuleThreads) patch(k / listed, s.listed[k % listed]);
-    return;
+  for (int k0 = t; k0 < live * listed; k0 += 4 * kRuleThreads) {
+    float l[4];
+    bool off[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * kRuleThreads, r = k / listed;
+      off[u] = k >= live * listed;
+      if (off[u]) continue;
+      const int x = s.listed[k - r * listed];
+      l[u] = logit(r, x), off[u] = banned(r, x);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (off[u]) continue;
+      const int k = k0 + u * kRuleThreads, r = k / listed, x = s.listed[k - r * listed];
+      int c = s.count[x];
+      for (int q = 0; q < nodes; ++q) c += token_of(q) == x && on_path(r, q);
+      patch(r, x, c, l[u]);
+    }
   }
-  for (int r = 0; r < live; ++r) {
-    const int64_t row = (int64_t)b * a.R + r0 + r;
-    const int np = a.mask ? n : r0 + r;  // drafted nodes that may be on the path
-    auto on_path = [&](int j) -> int {   // the node's token in this slice, or -1
-      const int node = j + 1;
-      if (a.mask && !(a.mask[row * a.mask_ld + (node >> 5)] >> (node & 31) & 1)) return -1;
-      const int x = a.tokens[(int64_t)b * (a.R - 1) + j] - v0;
-      return x >= 0 && x < len ? x : -1;
-    };
-    if (t == 0) s.n_row = listed;
-    __syncthreads();
-    for (int j = t; j < np; j += kRuleThreads) {
-      const int x = on_path(j);
-      if (x >= 0 && atomicAdd(&s.count[x], 1) == 0 && !s.known[x]) s.listed[atomicAdd(&s.n_row, 1)] = (uint16_t)x;
-    }
-    __syncthreads();
-    for (int k = t; k < s.n_row; k += kRuleThreads) patch(r, s.listed[k]);
-    __syncthreads();
-    for (int j = t; j < np; j += kRuleThreads) {
-      const int x = on_path(j);
-      if (x >= 0) atomicSub(&s.count[x], 1);
-    }
+  for (int k = t; k < live * nodes; k += kRuleThreads) {  // tokens that only the path has, each once
+    const int r = k / nodes, q = k - r * nodes, x = token_of(q);
+    if (x < 0 || x >= len || s.known[x] || !on_path(r, q)) continue;
+    int c = 0, before = 0;
+    for (int p = 0; p < nodes; ++p)
+      if (token_of(p) == x && on_path(r, p)) ++c, before += p < q;
+    if (!before && !banned(r, x)) patch(r, x, c, logit(r, x));
   }
 }
 
@@ -219,14 +261,14 @@ extern "C" sv_status sv_adjust_logits(sv_handle* h, const sv_logits_args* a, sv_
   if (a->R > 1 && !a->tokens) return SV_ERR_INVALID;
   if (a->mask && a->mask_ld < (a->R + 31) / 32) return SV_ERR_INVALID;
   if (a->allowed && a->allowed_ld < ((int64_t)a->V + 31) / 32) return SV_ERR_INVALID;
-  if (a->B > 65535) return SV_ERR_UNSUPPORTED;
+  if (a->V > 65535 * (int64_t)kSlice) return SV_ERR_UNSUPPORTED;
   // Rows share a CTA's lists where there are CTAs enough without it; a small
   // call gives each row its own, so that rows do not wait for one another.
   const int64_t slices = (a->V + kSlice - 1) / kSlice, wanted = 2 * (int64_t)h->num_sms;
   int parts = (int)((wanted + slices * a->B - 1) / (slices * a->B));
   parts = parts < 1 ? 1 : parts > a->R ? a->R : parts;
   const int per = (a->R + parts - 1) / parts;
-  const dim3 grid((unsigned)slices, (unsigned)a->B, (unsigned)((a->R + per - 1) / per)), block(kRuleThreads);
+  const dim3 grid((unsigned)a->B, (unsigned)slices, (unsigned)((a->R + per - 1) / per)), block(kRuleThreads);
   const cudaError_t e =
       a->dtype == SV_FP32
           ? sv_launch_pdl(logit_rules_kernel<true>, grid, block, 0, (cudaStream_t)stream, *a, per, h->d_err)
