@@ -74,20 +74,28 @@ struct TcWalk {
   __device__ __forceinline__ int count() const { return T * items; }
 };
 
-static __device__ __noinline__ void walk_to(const TcParams& P, TcWalk& k, int b) {
+// The units of a request of extent X.
+static __device__ __noinline__ void plan(const TcParams& P, TcWalk& k, int b, Extent X) {
   const sv_attention_args& a = P.p.a;
-  k.b = b;
-  k.X = extent_of(a, b, P.p.err);
-  const Extent X = k.X;
-  if (X.n < 0) {
-    k.T = 0, k.items = 0, k.tp = 0, k.blocks = 1;
-    return;
-  }
+  k.b = b, k.X = X;
+  k.T = 0, k.items = 0, k.tp = 0, k.blocks = 1;
+  if (X.n < 0) return;
   const int G = a.Hq / a.cache.heads;
-  k.blocks = ((X.n + 1) * G + k.qrows - 1) / k.qrows;
+  k.blocks = ((X.n + 1) * G + k.qrows - 1) / k.qrows;  // qrows is 128 or 256 at compile time where it matters
   k.items = a.cache.heads * k.blocks;
   k.tp = (X.S + (a.stage.data ? 0 : X.n + 1) + kTile - 1) / kTile;
   k.T = kLead + (a.stage.data ? k.tp + (X.n + kTile) / kTile : k.tp);
+}
+static __device__ __forceinline__ void walk_to(const TcParams& P, TcWalk& k, int b) {
+  plan(P, k, b, extent_of(P.p.a, b, P.p.err));
+}
+
+// floor(x * m / d); small products without a 64-bit division, whose code alone
+// takes a cold instruction cache a microsecond.
+static __device__ __forceinline__ int mul_div(int x, int m, int d) {
+  const uint64_t p = (uint64_t)(uint32_t)x * (uint32_t)m;
+  if (p >> 32 == 0) return (int)((uint32_t)p / (uint32_t)d);
+  return (int)(p / (uint32_t)d);
 }
 
 struct TcSegment {
@@ -115,9 +123,13 @@ static __device__ __noinline__ bool next_segment(const TcParams& P, TcWalk& k, T
   return false;
 }
 
-// The CTA whose share holds unit x of the list.
+// The CTA whose share holds unit x of the list: the last whose start,
+// floor(total c / ctas), is not past x.
 static __device__ __noinline__ int share_of(int x, int total, int ctas) {
-  return (int)((((int64_t)x + 1) * ctas - 1) / total);
+  int c = min(ctas - 1, (int)__fdividef((float)x * (float)ctas, (float)total));
+  while (c + 1 < ctas && mul_div(total, c + 1, ctas) <= x) ++c;
+  while (c > 0 && mul_div(total, c, ctas) > x) --c;
+  return c;
 }
 
 // What a tile holds: `valid` keys, and u0, the entry number of its first key
@@ -358,14 +370,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     const int ctas = min((int)gridDim.x, total);
     int w0 = 0, w1 = 0;
     if ((int)blockIdx.x < ctas) {
-      w0 = (int)((int64_t)total * blockIdx.x / ctas);
-      w1 = (int)((int64_t)total * (blockIdx.x + 1) / ctas);
+      w0 = mul_div(total, blockIdx.x, ctas);
+      w1 = mul_div(total, blockIdx.x + 1, ctas);
       if (mine > 0 && first <= w0 && w0 < first + mine) {
         int at = first;
         for (int b = b0; b < b1; ++b) {
-          walk_to(P, walk, b);
+          if (per > 1) walk_to(P, walk, b);
           if (w0 < at + walk.count()) {
-            ints[4] = b, ints[5] = at;
+            ints[4] = b, ints[5] = at, ints[8] = walk.X.S, ints[9] = walk.X.n;
             break;
           }
           at += walk.count();
@@ -379,7 +391,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     walk.w = w0, walk.w1 = w1, walk.base = 0;
     if (w1 > w0) {
       walk.base = ints[5];
-      walk_to(P, walk, ints[4]);
+      plan(P, walk, ints[4], Extent{ints[8], ints[9]});
     }
   }
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&ints[0]);
@@ -592,8 +604,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       // copies of the block's rows in the tile: this thread's copy weighs the
       // 32-key groups ch_a .. ch_b - 1 of each key tile
       const int rows = min(C::kRows, (seg.X.n + 1) * G - i0);
-      const int copies = QM == 2 || rows > 64 ? 1 : rows > 32 ? 2 : 4, apart = kTile / copies;
-      const int copy = row / apart, ch_a = copy * 4 / copies, ch_b = ch_a + 4 / copies;
+      const int fold = QM == 2 || rows > 64 ? 0 : rows > 32 ? 1 : 2, copies = 1 << fold, apart = kTile >> fold;
+      const int copy = row >> (7 - fold), ch_a = copy << (2 - fold), ch_b = ch_a + (4 >> fold);
       const int lrow = QM == 2 ? st * kTile + row : row - copy * apart;  // row of the CTA's block
       const int i = entry_of(P, i0 + lrow), hq = seg.h * G + i0 + lrow - i * G;
       const bool live = i <= seg.X.n;
@@ -798,12 +810,13 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       float f0 = 1.0f, f1 = 0.0f;  // of this copy's outputs in the two streams
       if (QM == 1) {
         float M = -kInf, L = 0.0f;
-        for (int x = 0; x < copies * (both ? 2 : 1); ++x) M = fmaxf(M, s_ml[(x % copies) * apart + lrow + x / copies * kTile].x);
+        const float2* o = s_ml + lrow;
+        const int parts = both ? 2 * copies : copies;  // a copy every `apart` rows, the second stream after the first
+#pragma unroll 1
+        for (int x = 0; x < parts; ++x) M = fmaxf(M, o[x * apart].x);
         const float Mb = M == -kInf ? 0.0f : M;
-        for (int x = 0; x < copies * (both ? 2 : 1); ++x) {
-          const float2 v = s_ml[(x % copies) * apart + lrow + x / copies * kTile];
-          L += v.y * ex2(v.x - Mb);
-        }
+#pragma unroll 1
+        for (int x = 0; x < parts; ++x) L += o[x * apart].y * ex2(o[x * apart].x - Mb);
         f0 = ex2(s_ml[row].x - Mb), f1 = both ? ex2(s_ml[kTile + row].x - Mb) : 0.0f;
         m = M, l = L;
       }
@@ -884,7 +897,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         named_barrier(1, 256);
         if (*reinterpret_cast<volatile int*>(&ints[3])) {
           __threadfence();
-          const int w0 = (int)((int64_t)total * ca / ctas);
+          const int w0 = mul_div(total, ca, ctas);
           const float* first = P.p.part + (int64_t)(2 * ca + (w0 >= seg.item0 ? 0 : 1)) * C::kPart;
           auto slot = [&](int x) { return x == ca ? first : P.p.part + (int64_t)(2 * x) * C::kPart; };
           auto part_ml = [&](int x, int r) { return __ldcg(reinterpret_cast<const float2*>(slot(x) + C::kRows * D) + r); };

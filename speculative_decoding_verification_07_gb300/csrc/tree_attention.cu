@@ -5,21 +5,24 @@
 
 namespace sv {
 
-constexpr int kRowsPerWarp = 4, kSimtWarps = 4, kSimtRows = kRowsPerWarp * kSimtWarps, kSimtKeys = 32;
+constexpr int kSimtWarps = 4, kSimtKeys = 32;
 constexpr int kSimtThreads = 32 * kSimtWarps;
 
 // o = sum_x p_x V_x with the running maximum and sum of a softmax: one pass
-// over the keys, 32 at a time.  One CTA takes 16 rows (entry, head of the group)
-// of one KV head, so the keys are read once for all of them, and one of
+// over the keys, 32 at a time.  One CTA takes 4 RPW rows (entry, head of the
+// group) of one KV head, so the keys are read once for all of them, and one of
 // `splits` shares of the keys; the share that arrives last joins the others in
 // share order, which keeps results the same from call to call.  A tile's K and
 // V are decoded to fp32 in shared memory; a lane is a key for the scores and
-// four columns (per 128) for the output.  fp32 products: 16 FMA to five
-// shared-memory reads bound it.
-template <bool F32>
+// four columns (per 128) for the output.  fp32 products bound it with many
+// rows (16 FMA to five shared-memory reads), latency with few: fewer rows a warp
+// then.  One request of 6 rows over 38 keys, 4 heads of 64: 18.8 us with 4 rows a
+// warp and a tile's loads one after another, SIMT_US as it is.
+template <bool F32, int RPW>
 __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __grid_constant__ AttnParams P) {
   pdl_wait();
   pdl_trigger();
+  constexpr int kRowsPerWarp = RPW, kSimtRows = RPW * kSimtWarps;
   extern __shared__ float smem[];
   const sv_attention_args& a = P.a;
   const int D = a.cache.head_dim, DP = D + 4, H = a.cache.heads, G = a.Hq / H;
@@ -67,10 +70,15 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
   for (int t = t0; t < t1; ++t) {
     const int x0 = t * kSimtKeys;
     __syncthreads();
-    for (int c = threadIdx.x; c < kSimtKeys * (D / 8); c += kSimtThreads) {
-      const int j = c / (D / 8), d = c % (D / 8) * 8, x = x0 + j;
-      float k[8] = {}, v[8] = {};
-      if (x < keys) {
+    constexpr int kAt = 2;  // vectors of K and of V on their way
+    for (int c0 = threadIdx.x; c0 < kSimtKeys * (D / 8); c0 += kAt * kSimtThreads) {
+      float k[kAt][8], v[kAt][8];
+#pragma unroll
+      for (int u = 0; u < kAt; ++u) {
+        const int c = c0 + u * kSimtThreads, j = c / (D / 8), d = c % (D / 8) * 8, x = x0 + j;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) k[u][e] = v[u][e] = 0.0f;
+        if (j >= kSimtKeys || x >= keys) continue;
         const bool staged = a.stage.data && x >= X.S;
         const sv_kv_place& pl = staged ? a.stage : a.cache;
         const int64_t off = entry_offset(pl, b, x - X.S, x);
@@ -78,16 +86,21 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
           const int64_t step = staged ? sstep : cstep;
           const char* kr = static_cast<const char*>(pl.data) + off + h * step;
           const char* vr = kr + H * step;
-          load_entry8(kr, pl.format, d, entry_scale(kr, pl.format, D), k);
-          load_entry8(vr, pl.format, d, entry_scale(vr, pl.format, D), v);
+          load_entry8(kr, pl.format, d, entry_scale(kr, pl.format, D), k[u]);
+          load_entry8(vr, pl.format, d, entry_scale(vr, pl.format, D), v[u]);
         } else if (d == 0) {
           report(P.err, SV_ERR_STATE);
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        *reinterpret_cast<float4*>(&sK[j * DP + d + e]) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
-        *reinterpret_cast<float4*>(&sV[j * DP + d + e]) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      for (int u = 0; u < kAt; ++u) {
+        const int c = c0 + u * kSimtThreads, j = c / (D / 8), d = c % (D / 8) * 8;
+        if (j >= kSimtKeys) continue;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          *reinterpret_cast<float4*>(&sK[j * DP + d + e]) = make_float4(k[u][e], k[u][e + 1], k[u][e + 2], k[u][e + 3]);
+          *reinterpret_cast<float4*>(&sV[j * DP + d + e]) = make_float4(v[u][e], v[u][e + 1], v[u][e + 2], v[u][e + 3]);
+        }
       }
     }
     __syncthreads();
@@ -121,18 +134,22 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
       for (int e = 0; e < kMaxHeadDim / 32; ++e) o[r][e] *= alpha;
       p[r] = see ? p[r] : -1.0f;  // marks what is not seen
     }
+#pragma unroll 4
     for (int j = 0; j < kSimtKeys; ++j) {
+      float w[kRowsPerWarp];
 #pragma unroll
-      for (int r = 0; r < kRowsPerWarp; ++r) {
-        const float w = __shfl_sync(0xFFFFFFFFu, p[r], j);
-        if (w == -1.0f) continue;  // the whole warp together
+      for (int r = 0; r < kRowsPerWarp; ++r) w[r] = __shfl_sync(0xFFFFFFFFu, p[r], j);
 #pragma unroll
-        for (int c = 0; c < kMaxHeadDim / 128; ++c)
-          if (c * 128 + lane * 4 < D) {
-            const float4 v = *reinterpret_cast<const float4*>(&sV[j * DP + c * 128 + lane * 4]);
-            o[r][4 * c] += w * v.x, o[r][4 * c + 1] += w * v.y;
-            o[r][4 * c + 2] += w * v.z, o[r][4 * c + 3] += w * v.w;
+      for (int c = 0; c < kMaxHeadDim / 128; ++c) {
+        if (c * 128 + lane * 4 >= D) continue;
+        const float4 v = *reinterpret_cast<const float4*>(&sV[j * DP + c * 128 + lane * 4]);
+#pragma unroll
+        for (int r = 0; r < kRowsPerWarp; ++r) {
+          if (w[r] != -1.0f) {  // seen
+            o[r][4 * c] += w[r] * v.x, o[r][4 * c + 1] += w[r] * v.y;
+            o[r][4 * c + 2] += w[r] * v.z, o[r][4 * c + 3] += w[r] * v.w;
           }
+        }
       }
     }
   }
@@ -224,9 +241,15 @@ static int simt_splits(const sv_handle* h, const sv_attention_args* a, int64_t i
   return s < 1 ? 1 : s > 64 ? 64 : (int)s;
 }
 
+// Rows of a CTA: 4, 8 or 16.
+static int simt_rows(const sv_attention_args* a) {
+  const int64_t rows = (int64_t)a->R * (a->Hq / a->cache.heads);
+  return rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+}
+
 static int64_t simt_items(const sv_attention_args* a) {
-  const int G = a->Hq / a->cache.heads;
-  return (int64_t)a->B * a->cache.heads * (((int64_t)a->R * G + kSimtRows - 1) / kSimtRows);
+  const int64_t rows = (int64_t)a->R * (a->Hq / a->cache.heads);
+  return (int64_t)a->B * a->cache.heads * ((rows + simt_rows(a) - 1) / simt_rows(a));
 }
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -368,7 +391,7 @@ extern "C" sv_status sv_attention_workspace_size(sv_handle* h, const sv_attentio
   }
   const int64_t items = simt_items(a);
   const int splits = simt_splits(h, a, items);
-  *bytes = kTicketBytes + up256((size_t)items * splits * kSimtRows * (a->cache.head_dim + 4) * 4);
+  *bytes = kTicketBytes + up256((size_t)items * splits * simt_rows(a) * (a->cache.head_dim + 4) * 4);
   return SV_OK;
 }
 
@@ -388,8 +411,11 @@ extern "C" sv_status sv_tree_attention(sv_handle* h, const sv_attention_args* a,
   P.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketBytes);
   P.err = h->d_err;
   P.splits = simt_splits(h, a, items);
-  const size_t smem = (size_t)(2 * kSimtKeys + kSimtRows) * (a->cache.head_dim + 4) * 4;
-  void (*fn)(AttnParams) = a->dtype == SV_FP32 ? simt_attention_kernel<true> : simt_attention_kernel<false>;
+  const size_t smem = (size_t)(2 * kSimtKeys + simt_rows(a)) * (a->cache.head_dim + 4) * 4;
+  typedef void (*Fn)(AttnParams);
+  static const Fn fns[2][3] = {{simt_attention_kernel<false, 1>, simt_attention_kernel<false, 2>, simt_attention_kernel<false, 4>},
+                               {simt_attention_kernel<true, 1>, simt_attention_kernel<true, 2>, simt_attention_kernel<true, 4>}};
+  const Fn fn = fns[a->dtype == SV_FP32][simt_rows(a) / 8];
   const sv_status rr = sv_raise_dyn_smem((const void*)fn, smem);
   if (rr != SV_OK) return rr;
   if (sv_launch_pdl(fn, dim3((unsigned)items, (unsigned)P.splits), dim3(kSimtThreads), smem, (cudaStream_t)stream, P) !=
