@@ -19,6 +19,7 @@ struct TcParams {
   CUtensorMap pages, stage;  // {column, slot or entry, (layer, K or V, head), block or request}
   int box;          // cached positions per TMA box: the largest power of two up to 128 that divides block_size
   int block_shift;  // log2 of block_size, -1 if it is no power of two
+  int group;        // G: query heads of a KV head
   uint32_t group_magic;  // ceil(2^32 / G), 0 for G = 1: a row's entry without a division
 };
 
@@ -65,8 +66,14 @@ struct TcShape {
 
 // A CTA's share of the work: [w, w1) of the list of all requests' items (head,
 // row block), an item being kLead units for what it costs besides its tiles
-// (queries in, outputs out) and then one unit a key tile.
-constexpr int kLead = 2;
+// (queries in, outputs out) and then one unit a key tile.  64 requests of 128 to
+// 8192 positions, bf16, single tokens / trees of 15 nodes: 220 / 237 us with a
+// lead of 1, 211 / 230 with 2, 196 / 210 with 4, 194 / 203 with 6, 196 / 205 with 8.
+constexpr int kLead = 6;
+
+// One copy of the division's code for all of the walk (a small call waits for
+// instructions to arrive more than for anything else).
+static __device__ __noinline__ uint32_t quotient(uint32_t a, uint32_t b) { return a / b; }
 
 struct TcWalk {
   int qrows, w, w1, b, base, T, items, tp, blocks;
@@ -80,8 +87,7 @@ static __device__ __noinline__ void plan(const TcParams& P, TcWalk& k, int b, Ex
   k.b = b, k.X = X;
   k.T = 0, k.items = 0, k.tp = 0, k.blocks = 1;
   if (X.n < 0) return;
-  const int G = a.Hq / a.cache.heads;
-  k.blocks = ((X.n + 1) * G + k.qrows - 1) / k.qrows;  // qrows is 128 or 256 at compile time where it matters
+  k.blocks = ((X.n + 1) * P.group + k.qrows - 1) >> (k.qrows == kTile ? 7 : 8);
   k.items = a.cache.heads * k.blocks;
   k.tp = (X.S + (a.stage.data ? 0 : X.n + 1) + kTile - 1) / kTile;
   k.T = kLead + (a.stage.data ? k.tp + (X.n + kTile) / kTile : k.tp);
@@ -92,9 +98,9 @@ static __device__ __forceinline__ void walk_to(const TcParams& P, TcWalk& k, int
 
 // floor(x * m / d); small products without a 64-bit division, whose code alone
 // takes a cold instruction cache a microsecond.
-static __device__ __forceinline__ int mul_div(int x, int m, int d) {
+static __device__ __noinline__ int mul_div(int x, int m, int d) {
   const uint64_t p = (uint64_t)(uint32_t)x * (uint32_t)m;
-  if (p >> 32 == 0) return (int)((uint32_t)p / (uint32_t)d);
+  if (p >> 32 == 0) return (int)quotient((uint32_t)p, (uint32_t)d);
   return (int)(p / (uint32_t)d);
 }
 
@@ -110,10 +116,10 @@ static __device__ __noinline__ bool next_segment(const TcParams& P, TcWalk& k, T
       k.base += k.count();
       walk_to(P, k, k.b + 1);
     }
-    const int at = k.w - k.base, item = at / k.T, from = at % k.T, to = min(k.T, from + k.w1 - k.w);
+    const int at = k.w - k.base, item = (int)quotient(at, k.T), from = at - item * k.T, to = min(k.T, from + k.w1 - k.w);
     k.w += to - from;
     if (to <= kLead) continue;  // the share ends before the item's first tile
-    s.b = k.b, s.h = item / k.blocks, s.rb = item % k.blocks;
+    s.b = k.b, s.h = k.blocks == 1 ? item : (int)quotient(item, k.blocks), s.rb = item - s.h * k.blocks;
     s.T = k.T, s.tp = k.tp, s.X = k.X;
     s.t0 = max(0, from - kLead);
     s.t1 = to - kLead;
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
   extern __shared__ char smem_raw[];
   const sv_attention_args& a = P.p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int H = a.cache.heads, G = a.Hq / H;
+  const int H = a.cache.heads, G = P.group;
   constexpr float kInf = __builtin_huge_valf();
 
   const uint32_t raw = smem_u32(smem_raw);
@@ -360,6 +366,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       if (lane >= o) x += y;
     }
     if (lane == 31) ints[16 + warp] = x;
+    if (tid == 0 && a.B == 1) ints[10] = walk.items;
     __syncthreads();
     int before = 0, total = 0;
     for (int i = 0; i < C::kThreads / 32; ++i) {
@@ -367,7 +374,13 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       total += ints[16 + i];
     }
     const int first = before + x - mine;  // tiles of the requests before mine
-    const int ctas = min((int)gridDim.x, total);
+    int ctas = min((int)gridDim.x, total);
+    if (a.B == 1 && total > 0 && ints[10] <= ctas) {
+      // one request: whole items to a CTA while they are short (joining shares
+      // takes as long as four tiles), else equal parts of a unit or more
+      const int items = ints[10], T = (int)quotient(total, items);
+      ctas = items * (T <= kLead + 4 ? 1 : min((int)quotient(ctas, items), T));
+    }
     int w0 = 0, w1 = 0;
     if ((int)blockIdx.x < ctas) {
       w0 = mul_div(total, blockIdx.x, ctas);
@@ -823,40 +836,39 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       const int c_first = QM == 1 ? st * (D / 2) : 0;
       constexpr int kCols = QM == 1 ? D / 2 : D;
       const int total = ints[6], ctas = ints[7];
-      const int ca = share_of(seg.item0 + kLead, total, ctas), cb = share_of(seg.item0 + seg.T - 1, total, ctas);
-      const bool split = ca != cb;
+      const bool split = seg.t0 > 0 || seg.t1 + kLead < seg.T;  // other CTAs have tiles of this item
       float* part = P.p.part + (int64_t)(2 * blockIdx.x + (index == 0 ? 0 : 1)) * C::kPart;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t out0 = seg.b * a.out_stride[0], out = out0 + i * a.out_stride[1] + (int64_t)hq * a.out_stride[2];
       float4* gather = reinterpret_cast<float4*>(sm);  // the queries' place: every score is done
 #pragma unroll 1
-      for (int col = c_first; col < c_first + kCols; col += 16) {
-        float y[16];
+      for (int col = c_first; col < c_first + kCols; col += 32) {
+        float y[32];
         if (warp_live) {
-          uint32_t o[16];
+          uint32_t o[32];
           const uint32_t t0 = tmem + (quad << 21) + 256 + col;
-          tmem_ld16(QM == 1 ? t0 : t0 + st * 128, o);
+          tmem_ld32(QM == 1 ? t0 : t0 + st * 128, o);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(o[e]) * f0;
+          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * f0;
           if (both) {
-            tmem_ld16(t0 + 128, o);
+            tmem_ld32(t0 + 128, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] += __uint_as_float(o[e]) * f1;
+            for (int e = 0; e < 32; ++e) y[e] += __uint_as_float(o[e]) * f1;
           }
         }
         if (copies > 1) {  // the first copy adds the others' shares
           if (copy > 0 && warp_live) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              gather[((copy - 1) * 8 + st * 4 + e) * apart + lrow] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+            for (int e = 0; e < 8; ++e)
+              gather[((copy - 1) * 16 + st * 8 + e) * apart + lrow] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           }
           named_barrier(1, 256);
           if (copy == 0 && warp_live) {
 #pragma unroll 1
             for (int x = 0; x < copies - 1; ++x)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 v = gather[(x * 8 + st * 4 + e) * apart + lrow];
+              for (int e = 0; e < 8; ++e) {
+                const float4 v = gather[(x * 16 + st * 8 + e) * apart + lrow];
                 y[4 * e] += v.x, y[4 * e + 1] += v.y, y[4 * e + 2] += v.z, y[4 * e + 3] += v.w;
               }
           }
@@ -865,20 +877,22 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         if (!live || copy > 0) continue;
         if (!split) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = l == 0.0f ? 0.0f : y[e] * inv;
+          for (int e = 0; e < 32; ++e) y[e] = l == 0.0f ? 0.0f : y[e] * inv;
           __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.out) + out + col;
-          reinterpret_cast<uint4*>(d)[0] = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-          reinterpret_cast<uint4*>(d)[1] = make_uint4(pack_bf16(y[8], y[9]), pack_bf16(y[10], y[11]), pack_bf16(y[12], y[13]), pack_bf16(y[14], y[15]));
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            reinterpret_cast<uint4*>(d)[e / 8] = make_uint4(pack_bf16(y[e], y[e + 1]), pack_bf16(y[e + 2], y[e + 3]),
+                                                            pack_bf16(y[e + 4], y[e + 5]), pack_bf16(y[e + 6], y[e + 7]));
           if (spoiled)
 #pragma unroll 1
-            for (int e = 0; e < 16; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back(P, found, i, col + e));
+            for (int e = 0; e < 32; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back(P, found, i, col + e));
         } else {
           float* d = part + lrow * D + col;
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
           if (spoiled)
 #pragma unroll 1
-            for (int e = 0; e < 16; ++e) d[e] += given_back(P, found, i, col + e);
+            for (int e = 0; e < 32; ++e) d[e] += given_back(P, found, i, col + e);
         }
       }
       if (split && live && copy == 0 && (QM == 2 || st == 0))
@@ -889,6 +903,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         __threadfence();
         named_barrier(1, 256);
         if (tid == 0) {
+          const int ca = share_of(seg.item0 + kLead, total, ctas), cb = share_of(seg.item0 + seg.T - 1, total, ctas);
+          ints[12] = ca, ints[13] = cb;
           uint32_t* ticket = P.p.ticket + ca;  // one item at most starts in a CTA and goes on in the next
           const bool last = atomicAdd(ticket, 1u) == (uint32_t)(cb - ca);
           if (last) *ticket = 0;
@@ -897,7 +913,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         named_barrier(1, 256);
         if (*reinterpret_cast<volatile int*>(&ints[3])) {
           __threadfence();
-          const int w0 = mul_div(total, ca, ctas);
+          const int ca = ints[12], cb = ints[13], w0 = mul_div(total, ca, ctas);
           const float* first = P.p.part + (int64_t)(2 * ca + (w0 >= seg.item0 ? 0 : 1)) * C::kPart;
           auto slot = [&](int x) { return x == ca ? first : P.p.part + (int64_t)(2 * x) * C::kPart; };
           auto part_ml = [&](int x, int r) { return __ldcg(reinterpret_cast<const float2*>(slot(x) + C::kRows * D) + r); };

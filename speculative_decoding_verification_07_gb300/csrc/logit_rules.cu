@@ -26,7 +26,7 @@ struct RuleSmem {
 // the row's logits; a row's own path only adds to their counts, so all rows are
 // written at once.  Bound by memory: each logit is read and written once.  64 x 7
 // rows of 128256 (bf16): looking up counts and biases for every logit as it
-// passed 109 us, a list 71, rows patched together RULES_US; the copy alone 39.
+// passed 109 us, a list 71, rows patched together 55; the copy alone 39.
 template <bool F32>
 __global__ void __launch_bounds__(kRuleThreads, 8) logit_rules_kernel(const __grid_constant__ sv_logits_args a, int per, int* err) {
   pdl_wait();

@@ -17,7 +17,7 @@ constexpr int kSimtThreads = 32 * kSimtWarps;
 // four columns (per 128) for the output.  fp32 products bound it with many
 // rows (16 FMA to five shared-memory reads), latency with few: fewer rows a warp
 // then.  One request of 6 rows over 38 keys, 4 heads of 64: 18.8 us with 4 rows a
-// warp and a tile's loads one after another, SIMT_US as it is.
+// warp and a tile's loads one after another, 10.2 us as it is.
 template <bool F32, int RPW>
 __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __grid_constant__ AttnParams P) {
   pdl_wait();
@@ -330,6 +330,7 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
   for (int s = 3; s < 31; ++s)
     if (c.block_size == 1 << s) P.block_shift = s;
   const uint32_t G = (uint32_t)(a->Hq / c.heads);
+  P.group = (int)G;
   P.group_magic = G == 1 ? 0u : (uint32_t)((0x100000000ull + G - 1) / G);
   const cuuint64_t row = (cuuint64_t)row_bytes(c), H = (cuuint64_t)c.heads;
   {
