@@ -354,7 +354,34 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
   // number of consecutive tiles each, so no CTA waits for a longer sequence.
   TcWalk walk;
   walk.qrows = C::kRows;
-  {
+  int total = 0, ctas, w0 = 0, w1 = 0;
+  auto share = [&](int items) {
+    ctas = min((int)gridDim.x, total);
+    if (a.B == 1 && total > 0 && items <= ctas) {
+      // one request: whole items to a CTA while they are short (joining shares
+      // takes as long as four tiles), else equal parts of a unit or more
+      const int T = walk.T;
+      ctas = items * (T <= kLead + 4 ? 1 : min((int)quotient(ctas, items), T));
+    }
+    if ((int)blockIdx.x < ctas) w0 = mul_div(total, blockIdx.x, ctas), w1 = mul_div(total, blockIdx.x + 1, ctas);
+  };
+  if (a.B <= 4) {  // every thread counts for itself
+#pragma unroll 1
+    for (int b = 0; b < a.B; ++b) walk_to(P, walk, b), total += walk.count();
+    share(walk.items);
+    walk.base = 0;
+    if (w1 > w0 && a.B > 1) {
+#pragma unroll 1
+      for (int b = 0;; walk.base += walk.count(), ++b) {
+        walk_to(P, walk, b);
+        if (w0 < walk.base + walk.count()) break;
+      }
+    }
+    if (tid == 0) ints[6] = total, ints[7] = ctas;  // for the joining of partial results
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  } else {
     const int per = (a.B + C::kThreads - 1) / C::kThreads;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int mine = 0;
@@ -366,47 +393,36 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       if (lane >= o) x += y;
     }
     if (lane == 31) ints[16 + warp] = x;
-    if (tid == 0 && a.B == 1) ints[10] = walk.items;
     __syncthreads();
-    int before = 0, total = 0;
+    int before = 0;
     for (int i = 0; i < C::kThreads / 32; ++i) {
       if (i < warp) before += ints[16 + i];
       total += ints[16 + i];
     }
-    const int first = before + x - mine;  // tiles of the requests before mine
-    int ctas = min((int)gridDim.x, total);
-    if (a.B == 1 && total > 0 && ints[10] <= ctas) {
-      // one request: whole items to a CTA while they are short (joining shares
-      // takes as long as four tiles), else equal parts of a unit or more
-      const int items = ints[10], T = (int)quotient(total, items);
-      ctas = items * (T <= kLead + 4 ? 1 : min((int)quotient(ctas, items), T));
-    }
-    int w0 = 0, w1 = 0;
-    if ((int)blockIdx.x < ctas) {
-      w0 = mul_div(total, blockIdx.x, ctas);
-      w1 = mul_div(total, blockIdx.x + 1, ctas);
-      if (mine > 0 && first <= w0 && w0 < first + mine) {
-        int at = first;
-        for (int b = b0; b < b1; ++b) {
-          if (per > 1) walk_to(P, walk, b);
-          if (w0 < at + walk.count()) {
-            ints[4] = b, ints[5] = at, ints[8] = walk.X.S, ints[9] = walk.X.n;
-            break;
-          }
-          at += walk.count();
+    const int first = before + x - mine;  // units of the requests before mine
+    share(0);
+    if (w1 > w0 && mine > 0 && first <= w0 && w0 < first + mine) {
+      int at = first;
+      for (int b = b0; b < b1; ++b) {
+        if (per > 1) walk_to(P, walk, b);
+        if (w0 < at + walk.count()) {
+          ints[4] = b, ints[5] = at, ints[8] = walk.X.S, ints[9] = walk.X.n;
+          break;
         }
+        at += walk.count();
       }
     }
-    if (tid == 0) ints[6] = total, ints[7] = ctas;  // for the joining of partial results
+    if (tid == 0) ints[6] = total, ints[7] = ctas;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    walk.w = w0, walk.w1 = w1, walk.base = 0;
+    walk.base = 0;
     if (w1 > w0) {
       walk.base = ints[5];
       plan(P, walk, ints[4], Extent{ints[8], ints[9]});
     }
   }
+  walk.w = w0, walk.w1 = w1;
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&ints[0]);
   const TcSync sync{ints + 1, P.p.err};
   // `found` is written by a call, so it lives in memory, where asm statements
