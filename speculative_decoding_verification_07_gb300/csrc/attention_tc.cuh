@@ -70,6 +70,13 @@ struct TcShape {
 // 8192 positions, bf16, single tokens / trees of 15 nodes: 220 / 237 us with a
 // lead of 1, 211 / 230 with 2, 196 / 210 with 4, 194 / 203 with 6, 196 / 205 with 8.
 constexpr int kLead = 6;
+// Items of up to this many key tiles are not shared between CTAs: a tile is
+// 0.9 us for a CTA alone, joining parts 3 us and more.  A single request leaves
+// most of the GPU idle, so its items are shared earlier: one token over 777
+// positions (7 tiles, 8 heads) 13.5 us shared, 15.3 whole; six trees over 100 to
+// 1000 positions 21.1 shared, 18.4 whole; 64 over 16 to 520 51.5 and 43.5.
+constexpr int kWholeOne = 6, kWhole = 12;
+constexpr int kLeast = 2;  // units of a share: 2000 positions 28.3 us with 1, 23.1 with 2, 25.8 with 10
 
 // One copy of the division's code for all of the walk (a small call waits for
 // instructions to arrive more than for anything else).
@@ -109,21 +116,28 @@ struct TcSegment {
   Extent X;
 };
 
-// The next segment (one item's consecutive tiles); false at the end.
+// The next segment (one item's consecutive tiles); false at the end.  A share's
+// bounds inside a short item move to the item's nearer end, the same for both
+// neighbours: joining its parts would take longer than its tiles.
 static __device__ __noinline__ bool next_segment(const TcParams& P, TcWalk& k, TcSegment& s) {
   while (k.w < k.w1) {
     while (k.w >= k.base + k.count()) {
       k.base += k.count();
       walk_to(P, k, k.b + 1);
     }
-    const int at = k.w - k.base, item = (int)quotient(at, k.T), from = at - item * k.T, to = min(k.T, from + k.w1 - k.w);
-    k.w += to - from;
-    if (to <= kLead) continue;  // the share ends before the item's first tile
+    const int at = k.w - k.base, item = (int)quotient(at, k.T), item0 = k.base + item * k.T;
+    int from = k.w - item0, to = min(k.T, k.w1 - item0);
+    if (k.T <= kLead + (P.p.a.B == 1 ? kWholeOne : kWhole)) {
+      const bool mine = 2 * from < k.T;  // from > 0 only at the share's start
+      from = 0, to = mine && 2 * to >= k.T ? k.T : 0;
+    }
+    k.w = min(k.w1, item0 + k.T);
+    if (to <= kLead) continue;  // none of the item's tiles
     s.b = k.b, s.h = k.blocks == 1 ? item : (int)quotient(item, k.blocks), s.rb = item - s.h * k.blocks;
     s.T = k.T, s.tp = k.tp, s.X = k.X;
     s.t0 = max(0, from - kLead);
     s.t1 = to - kLead;
-    s.item0 = k.base + item * k.T;
+    s.item0 = item0;
     return true;
   }
   return false;
@@ -355,20 +369,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
   TcWalk walk;
   walk.qrows = C::kRows;
   int total = 0, ctas, w0 = 0, w1 = 0;
-  auto share = [&](int items) {
-    ctas = min((int)gridDim.x, total);
-    if (a.B == 1 && total > 0 && items <= ctas) {
-      // one request: whole items to a CTA while they are short (joining shares
-      // takes as long as four tiles), else equal parts of a unit or more
-      const int T = walk.T;
-      ctas = items * (T <= kLead + 4 ? 1 : min((int)quotient(ctas, items), T));
-    }
+  auto share = [&] {
+    ctas = min((int)gridDim.x, (total + kLeast - 1) / kLeast);
     if ((int)blockIdx.x < ctas) w0 = mul_div(total, blockIdx.x, ctas), w1 = mul_div(total, blockIdx.x + 1, ctas);
   };
   if (a.B <= 4) {  // every thread counts for itself
 #pragma unroll 1
     for (int b = 0; b < a.B; ++b) walk_to(P, walk, b), total += walk.count();
-    share(walk.items);
+    share();
     walk.base = 0;
     if (w1 > w0 && a.B > 1) {
 #pragma unroll 1
@@ -377,7 +385,6 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         if (w0 < walk.base + walk.count()) break;
       }
     }
-    if (tid == 0) ints[6] = total, ints[7] = ctas;  // for the joining of partial results
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       total += ints[16 + i];
     }
     const int first = before + x - mine;  // units of the requests before mine
-    share(0);
+    share();
     if (w1 > w0 && mine > 0 && first <= w0 && w0 < first + mine) {
       int at = first;
       for (int b = b0; b < b1; ++b) {
@@ -412,7 +419,6 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         at += walk.count();
       }
     }
-    if (tid == 0) ints[6] = total, ints[7] = ctas;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -625,7 +631,6 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t tS = tmem + (quad << 21) + st * 128, tO = tmem + (quad << 21) + 256 + st * 128;
     int kbase = 0, ph_s = 0, done = 0;  // done: tiles this stream has handed to the products
-    int index = 0;                      // of the segment
     while (next_segment(P, walk, found)) {
         const TcSegment seg = found;
       const int n = seg.t1 - seg.t0, units = n * QM;
@@ -851,9 +856,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       }
       const int c_first = QM == 1 ? st * (D / 2) : 0;
       constexpr int kCols = QM == 1 ? D / 2 : D;
-      const int total = ints[6], ctas = ints[7];
       const bool split = seg.t0 > 0 || seg.t1 + kLead < seg.T;  // other CTAs have tiles of this item
-      float* part = P.p.part + (int64_t)(2 * blockIdx.x + (index == 0 ? 0 : 1)) * C::kPart;
+      // a CTA has two partial results at most: of the item it starts in, and of its last
+      float* part = P.p.part + (int64_t)(2 * blockIdx.x + (w0 >= seg.item0 ? 0 : 1)) * C::kPart;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t out0 = seg.b * a.out_stride[0], out = out0 + i * a.out_stride[1] + (int64_t)hq * a.out_stride[2];
       float4* gather = reinterpret_cast<float4*>(sm);  // the queries' place: every score is done
@@ -929,8 +934,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         named_barrier(1, 256);
         if (*reinterpret_cast<volatile int*>(&ints[3])) {
           __threadfence();
-          const int ca = ints[12], cb = ints[13], w0 = mul_div(total, ca, ctas);
-          const float* first = P.p.part + (int64_t)(2 * ca + (w0 >= seg.item0 ? 0 : 1)) * C::kPart;
+          const int ca = ints[12], cb = ints[13];
+          const float* first = P.p.part + (int64_t)(2 * ca + (mul_div(total, ca, ctas) >= seg.item0 ? 0 : 1)) * C::kPart;
           auto slot = [&](int x) { return x == ca ? first : P.p.part + (int64_t)(2 * x) * C::kPart; };
           auto part_ml = [&](int x, int r) { return __ldcg(reinterpret_cast<const float2*>(slot(x) + C::kRows * D) + r); };
           for (int r = tid; r < rows; r += 256) {
@@ -970,7 +975,6 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       tc_fence_before();
       named_barrier(1, 256);
       if (tid == 0) ints[2] = 0;
-      ++index;
     }
   }
   tc_fence_before();
