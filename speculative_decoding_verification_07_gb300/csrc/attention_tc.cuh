@@ -298,6 +298,30 @@ static __device__ __noinline__ void rescale(uint32_t tO, int cols, float f) {
   }
 }
 
+// Weights times each row's f, a power of two: exact but for 8-bit parts below
+// 2^-16, 2^-26 of a row's largest weight.
+template <bool F8>
+static __device__ __noinline__ void rescale_weights(uint32_t tW, int cols, float f) {
+  tmem_wait_st();
+  for (int col = 0; col < cols; col += 8) {
+    uint32_t w[8];
+    tmem_ld8(tW + col, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (F8) {
+        const __half2 f2 = __float2half2_rn(f);
+        uint32_t even = w[e] << 8 & 0xFF00FF00u, odd = w[e] & 0xFF00FF00u;
+        const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&even), f2), b = __hmul2(*reinterpret_cast<const __half2*>(&odd), f2);
+        even = *reinterpret_cast<const uint32_t*>(&a), odd = *reinterpret_cast<const uint32_t*>(&b);
+        w[e] = (even >> 8 & 0x00FF00FFu) | (odd & 0xFF00FF00u);
+      } else {
+        w[e] = pack_bf16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
+      }
+    }
+    tmem_st8(tW + col, w);
+  }
+}
+
 // Rows r0 .. valid - 1 of a V tile without their non-finite values (*found is
 // set where there was one), rows valid .. r1 - 1 cleared; thread of 128.
 template <bool F8>
@@ -724,49 +748,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         if (warp_live) {
           const int chunks = (k.valid + 31) / 32, ch_e = min(ch_b, chunks);
           if (!full) hide_unseen(P, seg.b, i, seg.X.n, k.prefix, k.valid, k.u0, ch_a, ch_e, tS);
-          // Two passes over the tile's scores, 32 columns at a time, each read
-          // from tensor memory: the loops stay short, which matters more than
-          // the second read.
-          auto scaled = [&](int ch, float (&s)[32]) {
-            uint32_t x[32];
-            tmem_ld32(tS + 32 * ch, x);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              uint64_t v[2] = {pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                               pair(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]))};
-              if (F8) {
-                const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(sc + 32 * ch + e);
-                const ulonglong2 lv = *reinterpret_cast<const ulonglong2*>(sc + kTile + 32 * ch + e);
-                v[0] = fma2(v[0], mul2(ks.x, c2), lv.x), v[1] = fma2(v[1], mul2(ks.y, c2), lv.y);
-              }
-              const float2 v0 = unpair(v[0]), v1 = unpair(v[1]);
-              s[e] = v0.x, s[e + 1] = v0.y, s[e + 2] = v1.x, s[e + 3] = v1.y;
-            }
-          };
-          float mx = -kInf;
-#pragma unroll 1
-          for (int ch = ch_a; ch < ch_e; ++ch) {
-            float s[32];
-            scaled(ch, s);
-            float mx4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int e = 4; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], s[e]);
-            mx = fmaxf(mx, fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])));
-          }
-          if (!F8) mx *= c;
-          const float mn = fmaxf(m, mx);
-          if (__any_sync(0xFFFFFFFFu, mn > m + TcSoft<F8>::kSlack)) {
-            if (u >= 2) {
-              const float f = mn == -kInf ? 1.0f : ex2(m - mn);
-              l *= f;
-              wait(sync, b_o + 8 * st, (done - 1) & 1);
-              tc_fence_after();
-              rescale(tO, D, f);
-            }
-            m = mn;
-          }
-          const float base = (m == -kInf ? 0.0f : m) - TcSoft<F8>::kBias;
-          const uint64_t base2 = pair(-base, -base);
+          // One pass over the tile's scores, 32 columns at a time, so that the
+          // loop stays short.  A group of 32 that exceeds the reference by too
+          // much rescales what is there, the weights before it included.
           uint64_t ls[2] = {0, 0};
 #pragma unroll 1
           for (int ch = 0; ch < chunks; ++ch) {
@@ -778,32 +762,63 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               tmem_st(tS + kW * ch, w);
               continue;
             }
-            float s[32];
-            scaled(ch, s);
+            uint32_t x[32];
+            uint64_t v[16];
+            tmem_ld32(tS + 32 * ch, x);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              uint64_t v[2] = {pair(s[e], s[e + 1]), pair(s[e + 2], s[e + 3])};
+            for (int e = 0; e < 16; e += 2) {
+              v[e] = pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+              v[e + 1] = pair(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3]));
+              if (F8) {
+                const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(sc + 32 * ch + 2 * e);
+                const ulonglong2 lv = *reinterpret_cast<const ulonglong2*>(sc + kTile + 32 * ch + 2 * e);
+                v[e] = fma2(v[e], mul2(ks.x, c2), lv.x), v[e + 1] = fma2(v[e + 1], mul2(ks.y, c2), lv.y);
+              }
+            }
+            float mx4[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = unpair(v[e]);
+              mx4[e & 3] = fmaxf(mx4[e & 3], fmaxf(y.x, y.y));
+            }
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * (F8 ? 1.0f : c);
+            if (__any_sync(0xFFFFFFFFu, mx > m + TcSoft<F8>::kSlack)) {
+              const float mn = fmaxf(m, ceilf(mx)), f = mn == -kInf ? 1.0f : ex2(m - mn);
+              m = mn, l *= f;
+              const uint64_t f2 = pair(f, f);
+              ls[0] = mul2(ls[0], f2), ls[1] = mul2(ls[1], f2);
+              if (ch > ch_a) rescale_weights<F8>(tS + kW * ch_a, kW * (ch - ch_a), f);
+              if (u >= 2) {
+                wait(sync, b_o + 8 * st, (done - 1) & 1);
+                tc_fence_after();
+                rescale(tO, D, f);
+              }
+            }
+            const float base = (m == -kInf ? 0.0f : m) - TcSoft<F8>::kBias;
+            const uint64_t base2 = pair(-base, -base);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+#pragma unroll
+              for (int z = e; z < e + 2; ++z) {
                 v[z] = F8 ? add2(v[z], base2) : fma2(v[z], c2, base2);
                 const float2 y = unpair(v[z]);
                 v[z] = pair(ex2(y.x), ex2(y.y));
               }
-              const float2 y0 = unpair(v[0]), y1 = unpair(v[1]);
+              const float2 y0 = unpair(v[e]), y1 = unpair(v[e + 1]);
               if (F8) {
-                const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(sc + 2 * kTile + 32 * ch + e);
-                ls[0] = fma2(v[0], iv.x, ls[0]), ls[1] = fma2(v[1], iv.y, ls[1]);
+                const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(sc + 2 * kTile + 32 * ch + 2 * e);
+                ls[0] = fma2(v[e], iv.x, ls[0]), ls[1] = fma2(v[e + 1], iv.y, ls[1]);
                 const __half2 h0 = __floats2half2_rn(y0.x, y0.y), h1 = __floats2half2_rn(y1.x, y1.y);
                 uint32_t a0 = *reinterpret_cast<const uint32_t*>(&h0), a1 = *reinterpret_cast<const uint32_t*>(&h1);
-                w[e / 4] = __byte_perm(a0, a1, 0x7531);
+                w[e / 2] = __byte_perm(a0, a1, 0x7531);
                 a0 = less_top(a0), a1 = less_top(a1);
-                w[8 + e / 4] = __byte_perm(a0, a1, 0x7531);
+                w[8 + e / 2] = __byte_perm(a0, a1, 0x7531);
                 a0 = less_top(a0) + 0x00800080u, a1 = less_top(a1) + 0x00800080u;
-                w[16 + e / 4] = __byte_perm(a0, a1, 0x7531);
+                w[16 + e / 2] = __byte_perm(a0, a1, 0x7531);
               } else {
-                ls[0] = add2(ls[0], v[0]), ls[1] = add2(ls[1], v[1]);
-                w[e / 2] = pack_bf16(y0.x, y0.y);
-                w[e / 2 + 1] = pack_bf16(y1.x, y1.y);
+                ls[0] = add2(ls[0], v[e]), ls[1] = add2(ls[1], v[e + 1]);
+                w[e] = pack_bf16(y0.x, y0.y);
+                w[e + 1] = pack_bf16(y1.x, y1.y);
               }
             }
             tmem_st(tS + kW * ch, w);
