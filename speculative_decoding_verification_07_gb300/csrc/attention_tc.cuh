@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         // ---- scales of 8-bit entries: four a lane, copied into the ring
         // kAhead tiles before they are due, then turned into what the softmax
         // adds and multiplies by
-        constexpr int kAhead = 5;
+        constexpr int kAhead = 2;
         int t = 0, issued = 0, due = 0, blk = -1, at = 0, left = 0;
         bool more = true, staged = false, have = false;  // have: a tile whose block has been looked up
         TcSegment seg = {};
