@@ -12,11 +12,13 @@ namespace sv {
 
 constexpr int kTile = 128;        // keys of a tile, and rows of a product
 constexpr int kStageBox = 16;     // staged entries per TMA box
-constexpr int kScaleRing = 8;     // tiles whose scales are held
+constexpr int kTails = 4;         // tiles whose 8-bit entries' tails are under way
+constexpr int kScaleRing = 4;     // tiles whose scales are held
 
 struct TcParams {
   AttnParams p;
   CUtensorMap pages, stage;  // {column, slot or entry, (layer, K or V, head), block or request}
+  CUtensorMap page_tails, stage_tails;  // the same of 8-bit entries' last 16 bytes
   int box;          // cached positions per TMA box: the largest power of two up to 128 that divides block_size
   int block_shift;  // log2 of block_size, -1 if it is no power of two
   int group;        // G: query heads of a KV head
@@ -56,7 +58,7 @@ struct TcShape {
   static constexpr int kStep = F8 ? 32 : 16;                 // keys of one product of weights and V
   static constexpr int kRows = kTile * QM;
   static constexpr int kQAll = QM * kQBytes > 24576 ? QM * kQBytes : 24576;  // also holds 3 copies' 32 x 64 outputs
-  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 3 * kTile * 4 : 0);
+  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 3 * kTile * 4 + kTails * 2 * kTile * kTail : 0);
   static constexpr int kRoom = (232448 - 1024 - kMisc - kQAll) / kTileBytes;
   static constexpr int kSlots = kRoom < 12 ? kRoom : 12;     // tiles held: the first kK for K, the rest for V
   static constexpr int kK = (kSlots + 1) / 2, kV = kSlots - kK;
@@ -363,15 +365,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
   char* vslots = sm + C::kQAll + C::kK * C::kTileBytes;
   char* misc = vslots + C::kV * C::kTileBytes;
   const uint32_t bars = smem_u32(misc);
-  // K loaded / free, V loaded / free, scores, weights, outputs, queries, scales set / read
+  // K loaded / free, V loaded / free, scores, weights, outputs, queries, scales set / read, tails
   const uint32_t b_kf = bars, b_ke = b_kf + 8 * C::kK, b_vf = b_ke + 8 * C::kK, b_ve = b_vf + 8 * C::kV,
                  b_s = b_ve + 8 * C::kV, b_p = b_s + 16, b_o = b_s + 32, b_q = b_s + 48, b_sf = b_s + 56,
-                 b_se = b_sf + 8 * kScaleRing;
+                 b_se = b_sf + 8 * kScaleRing, b_t = b_se + 8 * kScaleRing;
   int* ints = reinterpret_cast<int*>(misc + 512);  // 0 tensor memory, 1 abort, 2 non-finite entries, 3 last, 4.. walk
   float2* s_ml = reinterpret_cast<float2*>(misc + 1024);  // [256] maxima and sums exchanged or joined
   float* s_qs = reinterpret_cast<float*>(misc + 3072);    // [kRows] row scales of 8-bit queries
   float* s_sc = s_qs + C::kRows;                          // [kScaleRing][3][128] of a tile's entries: K's scale,
                                                           // log2 of V's, 1 / V's
+  char* s_tails = reinterpret_cast<char*>(s_sc + kScaleRing * 3 * kTile);  // [kTails][K, V][128] of 16 bytes
 
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) mbar_init(b_kf + 8 * i, 1), mbar_init(b_ke + 8 * i, QM);
@@ -379,6 +382,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     for (int i = 0; i < 2; ++i) mbar_init(b_s + 8 * i, 1), mbar_init(b_p + 8 * i, 4), mbar_init(b_o + 8 * i, 1);
     mbar_init(b_q, 8);
     for (int i = 0; i < kScaleRing; ++i) mbar_init(b_sf + 8 * i, 1), mbar_init(b_se + 8 * i, 4 * QM);
+    for (int i = 0; i < kTails; ++i) mbar_init(b_t + 8 * i, 1);
     ints[1] = ints[2] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&P.pages);
@@ -570,71 +574,68 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       if (vs + vlap > 0) wait(sync, b_ve + 8 * (vs ? vs - 1 : C::kV - 1), (vs ? vlap : vlap - 1) & 1);
     } else {  // warp 11
       if (F8) {
-        // ---- scales of 8-bit entries: four a lane, copied into the ring
-        // kAhead tiles before they are due, then turned into what the softmax
-        // adds and multiplies by
-        constexpr int kAhead = 2;
-        int t = 0, issued = 0, due = 0, blk = -1, at = 0, left = 0;
-        bool more = true, staged = false, have = false;  // have: a tile whose block has been looked up
+        // ---- scales of 8-bit entries: tails by TMA, lanes 0 to 15 a box of K's
+        // each, 16 to 31 of V's, then turned into what the softmax adds and
+        // multiplies by.  (Four bytes of an entry by cp.async kept this warp 2000
+        // cycles a tile, and 64 single tokens at 216 us.)
+        int t = 0, issued = 0, due = 0, y = 0, w = 0;
+        bool more = true, have = false;  // have: a tile whose blocks have been looked up
         TcSegment seg = {};
+        TcTile k = {};
+        const int v = lane >> 4, bx = lane & 15;
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // what earlier kernels wrote, for TMA
 #pragma unroll 1
         while (more || have || due < issued) {
-          if (have) {
-            const int slot = issued % kScaleRing, lap = issued / kScaleRing;
-            if (lap > 0) wait(sync, b_se + 8 * slot, (lap - 1) & 1);
-            const sv_kv_place& pl = staged ? a.stage : a.cache;
-            const int64_t step = row_step(pl), rb = D + kTail, each = staged ? (int64_t)pl.layers * 2 * H * rb : rb;
-            const char* row = static_cast<const char*>(pl.data) + seg.h * step + D;
-            if (staged)
-              row += (((int64_t)seg.b * pl.rows + at) * pl.layers + pl.layer) * 2 * H * rb;
-            else
-              row += (((int64_t)blk * pl.layers + pl.layer) * 2 * H * pl.block_size + at) * rb;
-            if (!staged && (blk < 0 || blk >= a.cache.num_blocks)) left = 0;
-            const uint32_t dst = smem_u32(s_sc + slot * 3 * kTile + 4 * lane);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const char* src = e < left ? row + e * each : static_cast<const char*>(pl.data);
-              const uint32_t n = e < left ? 4 : 0;  // 0: zeros
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * e), "l"(src), "r"(n) : "memory");
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * kTile + 4 * e),
-                           "l"(e < left ? src + H * step : src), "r"(n)
-                           : "memory");
+          if (have && issued - due < kTails) {
+            const int slot = issued % kTails, box = k.staged ? kStageBox : P.box, boxes = (k.valid + box - 1) / box;
+            if (!__any_sync(0xFFFFFFFFu, *sync.abort)) {
+              if (lane == 0) mbar_expect_tx(b_t + 8 * slot, boxes * box * 2 * kTail);
+              __syncwarp();
+              if (bx < boxes)
+                tma_load_4d(smem_u32(s_tails) + ((slot * 2 + v) * kTile + bx * box) * kTail, k.staged ? &P.stage_tails : &P.page_tails,
+                            b_t + 8 * slot, 0, y, ((k.staged ? a.stage.layer : a.cache.layer) * 2 + v) * H + seg.h, w);
             }
+            have = false;
             ++issued;
           }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          have = false;
-          if (more && t >= seg.t1) {
-            more = next_segment(P, walk, found);
-            seg = found;
-            t = seg.t0;
-          }
-          if (more) {
-            const TcTile tl = tile_of(a, seg, t++);
-            staged = tl.staged, at = tl.x0 + 4 * lane, left = tl.valid - 4 * lane, have = true;
-            if (!staged) {  // a block holds whole groups of four
-              const int j = block_of(P, at);
-              blk = -1;
-              if (left > 0) blk = __ldg(a.cache.block_table + (int64_t)seg.b * a.cache.max_blocks + j);
-              at -= j * a.cache.block_size;
+          if (!have && more) {
+            if (t >= seg.t1) {
+              more = next_segment(P, walk, found);
+              seg = found;
+              t = seg.t0;
+            }
+            if (more) {
+              k = tile_of(a, seg, t++);
+              have = true;
+              const int box = k.staged ? kStageBox : P.box;
+              y = k.x0 + bx * box, w = seg.b;
+              if (!k.staged) {
+                const int j = block_of(P, y);
+                if (bx * box < k.valid) w = __ldg(a.cache.block_table + (int64_t)seg.b * a.cache.max_blocks + j);
+                if (w < 0 || w >= a.cache.num_blocks) w = a.cache.num_blocks;  // past the last: a load gives zeros
+                y -= j * a.cache.block_size;
+              }
             }
           }
-          if (due < issued && (issued - due > kAhead || !have)) {
-            if (have)
-              asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-            else
-              asm volatile("cp.async.wait_group 0;" ::: "memory");
-            const int slot = due % kScaleRing;
-            float* sc = s_sc + slot * 3 * kTile + 4 * lane;
-            float4 ks = *reinterpret_cast<const float4*>(sc), lv = *reinterpret_cast<const float4*>(sc + kTile);
-            // scales are finite and positive; what is not must not reach rows that do not see the entry
-            auto finite = [&](float x) { return x > 0.0f && x < kInf ? x : 1.0f; };
-            auto logv = [](float x) { return lg2(fminf(fmaxf(x, 1.17549435e-38f), 1.70141183e38f)); };
-            ks = make_float4(finite(ks.x), finite(ks.y), finite(ks.z), finite(ks.w));
-            lv = make_float4(logv(lv.x), logv(lv.y), logv(lv.z), logv(lv.w));
-            *reinterpret_cast<float4*>(sc) = ks;
-            *reinterpret_cast<float4*>(sc + kTile) = lv;
-            *reinterpret_cast<float4*>(sc + 2 * kTile) = make_float4(ex2(-lv.x), ex2(-lv.y), ex2(-lv.z), ex2(-lv.w));
+          if (due < issued && (!have || issued - due == kTails ||
+                               __all_sync(0xFFFFFFFFu, mbar_test_wait(b_t + 8 * (due % kTails), (due / kTails) & 1)))) {
+            const int from = due % kTails, slot = due % kScaleRing;
+            wait(sync, b_t + 8 * from, (due / kTails) & 1);
+            float ks[4], lv[4];
+            // scales are finite and positive; what is not (and what the place of a key
+            // past the valid ones held) must not reach rows that do not see the entry
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const char* tail = s_tails + (from * 2 * kTile + lane + 32 * e) * kTail;
+              const float x = *reinterpret_cast<const float*>(tail), z = *reinterpret_cast<const float*>(tail + kTile * kTail);
+              ks[e] = x > 0.0f && x < kInf ? x : 1.0f;
+              lv[e] = lg2(fminf(fmaxf(z, 1.17549435e-38f), 1.70141183e38f));
+            }
+            if (due >= kScaleRing) wait(sync, b_se + 8 * slot, (due / kScaleRing - 1) & 1);
+            float* sc = s_sc + slot * 3 * kTile + lane;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[32 * e] = ks[e], sc[kTile + 32 * e] = lv[e], sc[2 * kTile + 32 * e] = ex2(-lv[e]);
+            fence_async_smem();  // the tails have been read before their place is loaded again
             __syncwarp();
             if (lane == 0) mbar_arrive(b_sf + 8 * slot);
             ++due;
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               if (F8) {
                 const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(sc + 32 * ch + 2 * e);
                 const ulonglong2 lv = *reinterpret_cast<const ulonglong2*>(sc + kTile + 32 * ch + 2 * e);
-                v[e] = fma2(v[e], mul2(ks.x, c2), lv.x), v[e + 1] = fma2(v[e + 1], mul2(ks.y, c2), lv.y);
+                v[e] = fma2(mul2(v[e], c2), ks.x, lv.x), v[e + 1] = fma2(mul2(v[e + 1], c2), ks.y, lv.y);  // -inf stays
               }
             }
             float mx4[4] = {-kInf, -kInf, -kInf, -kInf};

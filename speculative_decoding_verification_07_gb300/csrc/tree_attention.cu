@@ -304,12 +304,21 @@ static EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Rows of an 8-bit entry are mapped without their tails.
-static bool make_map(CUtensorMap* m, const sv_kv_place& pl, const cuuint64_t* dims, const cuuint64_t* strides,
+// Rows of an 8-bit entry are mapped without their tails, which have maps of
+// their own.
+static bool make_maps(CUtensorMap* m, CUtensorMap* tails, const sv_kv_place& pl, const cuuint64_t* dims, const cuuint64_t* strides,
                      int box_rows) {
   const bool f8 = pl.format == SV_KV_E4M3;
   const int row = f8 ? pl.head_dim : 2 * pl.head_dim, sw = row < 128 ? row : 128;
   const cuuint32_t box[4] = {(cuuint32_t)(f8 ? sw : sw / 2), (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
+  if (f8) {
+    const cuuint64_t tail_dims[4] = {kTail, dims[1], dims[2], dims[3]};
+    const cuuint32_t tail_box[4] = {kTail, (cuuint32_t)box_rows, 1, 1};
+    if (encode_tiled()(tails, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, static_cast<char*>(pl.data) + row, tail_dims, strides,
+                             tail_box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
   return encode_tiled()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pl.data, dims,
                         strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         sw == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -337,14 +346,14 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
     const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.block_size, (cuuint64_t)c.layers * 2 * H,
                                 (cuuint64_t)c.num_blocks};
     const cuuint64_t strides[3] = {row, row * c.block_size, row * c.block_size * c.layers * 2 * H};
-    if (!make_map(&P.pages, c, dims, strides, P.box)) return SV_ERR_CUDA;
+    if (!make_maps(&P.pages, &P.page_tails, c, dims, strides, P.box)) return SV_ERR_CUDA;
   }
   if (a->stage.data) {
     const cuuint64_t per = row * a->stage.layers * 2 * H;  // bytes of an entry
     const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)a->stage.rows, (cuuint64_t)a->stage.layers * 2 * H,
                                 (cuuint64_t)a->B};
     const cuuint64_t strides[3] = {per, row, per * a->stage.rows};
-    if (!make_map(&P.stage, a->stage, dims, strides, kStageBox)) return SV_ERR_CUDA;
+    if (!make_maps(&P.stage, &P.stage_tails, a->stage, dims, strides, kStageBox)) return SV_ERR_CUDA;
   }
   const sv_status rr = sv_raise_dyn_smem((const void*)plan.k.fn, (size_t)plan.k.smem);
   if (rr != SV_OK) return rr;
