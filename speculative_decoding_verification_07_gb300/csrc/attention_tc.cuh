@@ -12,13 +12,12 @@ namespace sv {
 
 constexpr int kTile = 128;        // keys of a tile, and rows of a product
 constexpr int kStageBox = 16;     // staged entries per TMA box
-constexpr int kTails = 4;         // tiles whose 8-bit entries' tails are under way
 constexpr int kScaleRing = 4;     // tiles whose scales are held
 
 struct TcParams {
   AttnParams p;
   CUtensorMap pages, stage;  // {column, slot or entry, (layer, K or V, head), block or request}
-  CUtensorMap page_tails, stage_tails;  // the same of 8-bit entries' last 16 bytes
+  CUtensorMap page_tails, stage_tails;  // of 8-bit entries' last 16 bytes, K's and V's in one box
   int box;          // cached positions per TMA box: the largest power of two up to 128 that divides block_size
   int block_shift;  // log2 of block_size, -1 if it is no power of two
   int group;        // G: query heads of a KV head
@@ -58,11 +57,13 @@ struct TcShape {
   static constexpr int kStep = F8 ? 32 : 16;                 // keys of one product of weights and V
   static constexpr int kRows = kTile * QM;
   static constexpr int kQAll = QM * kQBytes > 24576 ? QM * kQBytes : 24576;  // also holds 3 copies' 32 x 64 outputs
-  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 3 * kTile * 4 + kTails * 2 * kTile * kTail : 0);
-  static constexpr int kRoom = (232448 - 1024 - kMisc - kQAll) / kTileBytes;
-  static constexpr int kSlots = kRoom < 12 ? kRoom : 12;     // tiles held: the first kK for K, the rest for V
-  static constexpr int kK = (kSlots + 1) / 2, kV = kSlots - kK;
-  static constexpr int kSmem = 1024 + kMisc + kQAll + kSlots * kTileBytes;
+  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 3 * kTile * 4 : 0);
+  // tiles held; a slot of K has its keys' tails and V's
+  static constexpr int kTails = F8 ? 2 * kTile * kTail : 0, kKBytes = kTileBytes + kTails;
+  static constexpr int kRoom = 232448 - 1024 - kMisc - kQAll, kPairs = kRoom / (kTileBytes + kKBytes);
+  static constexpr int kV = kPairs < 6 ? kPairs : 6;
+  static constexpr int kK = kPairs < 6 && kRoom - kPairs * (kTileBytes + kKBytes) >= kKBytes ? kV + 1 : kV;
+  static constexpr int kSmem = 1024 + kMisc + kQAll + kK * kKBytes + kV * kTileBytes;
   static constexpr int kPart = kRows * (D + 2);              // floats of a partial result
 };
 
@@ -361,20 +362,20 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
   char* sm = smem_raw + pad;
-  const uint32_t sQ = raw + pad, sK = sQ + C::kQAll, sV = sK + C::kK * C::kTileBytes;
-  char* vslots = sm + C::kQAll + C::kK * C::kTileBytes;
+  const uint32_t sQ = raw + pad, sK = sQ + C::kQAll, sV = sK + C::kK * C::kKBytes;
+  char* kslots = sm + C::kQAll;
+  char* vslots = kslots + C::kK * C::kKBytes;
   char* misc = vslots + C::kV * C::kTileBytes;
   const uint32_t bars = smem_u32(misc);
-  // K loaded / free, V loaded / free, scores, weights, outputs, queries, scales set / read, tails
+  // K loaded / free, V loaded / free, scores, weights, outputs, queries, scales set / read
   const uint32_t b_kf = bars, b_ke = b_kf + 8 * C::kK, b_vf = b_ke + 8 * C::kK, b_ve = b_vf + 8 * C::kV,
                  b_s = b_ve + 8 * C::kV, b_p = b_s + 16, b_o = b_s + 32, b_q = b_s + 48, b_sf = b_s + 56,
-                 b_se = b_sf + 8 * kScaleRing, b_t = b_se + 8 * kScaleRing;
+                 b_se = b_sf + 8 * kScaleRing;
   int* ints = reinterpret_cast<int*>(misc + 512);  // 0 tensor memory, 1 abort, 2 non-finite entries, 3 last, 4.. walk
   float2* s_ml = reinterpret_cast<float2*>(misc + 1024);  // [256] maxima and sums exchanged or joined
   float* s_qs = reinterpret_cast<float*>(misc + 3072);    // [kRows] row scales of 8-bit queries
   float* s_sc = s_qs + C::kRows;                          // [kScaleRing][3][128] of a tile's entries: K's scale,
                                                           // log2 of V's, 1 / V's
-  char* s_tails = reinterpret_cast<char*>(s_sc + kScaleRing * 3 * kTile);  // [kTails][K, V][128] of 16 bytes
 
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) mbar_init(b_kf + 8 * i, 1), mbar_init(b_ke + 8 * i, QM);
@@ -382,7 +383,6 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     for (int i = 0; i < 2; ++i) mbar_init(b_s + 8 * i, 1), mbar_init(b_p + 8 * i, 4), mbar_init(b_o + 8 * i, 1);
     mbar_init(b_q, 8);
     for (int i = 0; i < kScaleRing; ++i) mbar_init(b_sf + 8 * i, 1), mbar_init(b_se + 8 * i, 4 * QM);
-    for (int i = 0; i < kTails; ++i) mbar_init(b_t + 8 * i, 1);
     ints[1] = ints[2] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&P.pages);
@@ -492,12 +492,15 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
           const CUtensorMap* map = k.staged ? &P.stage : &P.pages;
           if (lap > 0) wait(sync, b_empty + 8 * slot, (lap - 1) & 1);
           if (!__any_sync(0xFFFFFFFFu, *sync.abort)) {
-            const uint32_t bar = b_full + 8 * slot, dst = ring + slot * C::kTileBytes + lane * box * C::kSw;
-            if (lane == 0) mbar_expect_tx(bar, boxes * box * C::kRow);
+            const uint32_t bar = b_full + 8 * slot, at = ring + slot * (v ? C::kTileBytes : C::kKBytes), dst = at + lane * box * C::kSw;
+            if (lane == 0) mbar_expect_tx(bar, boxes * box * (F8 && !v ? C::kRow + 2 * kTail : C::kRow));
             __syncwarp();
             if (lane < boxes) {
 #pragma unroll
               for (int hf = 0; hf < C::kHalves; ++hf) tma_load_4d(dst + hf * C::kHalfBytes, map, bar, hf * kElems, y, z, w);
+              if (F8 && !v)
+                tma_load_5d(at + C::kTileBytes + lane * box * 2 * kTail, k.staged ? &P.stage_tails : &P.page_tails, bar, 0, y, seg.h,
+                            (k.staged ? a.stage.layer : a.cache.layer) * 2, w);
             }
           }
           if (++slot == slots) slot = 0, ++lap;
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               if (++vs == C::kV) vs = 0, ++vlap;
           }
           if (x < units) {
-            const uint64_t qd = q0 + (QM == 2 ? st * (C::kQBytes >> 4) : 0), kd = k0 + ks * (C::kTileBytes >> 4);
+            const uint64_t qd = q0 + (QM == 2 ? st * (C::kQBytes >> 4) : 0), kd = k0 + ks * (C::kKBytes >> 4);
             wait(sync, b_kf + 8 * ks, klap & 1);
             tc_fence_after();
             if (one && !*sync.abort) {
@@ -574,71 +577,37 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       if (vs + vlap > 0) wait(sync, b_ve + 8 * (vs ? vs - 1 : C::kV - 1), (vs ? vlap : vlap - 1) & 1);
     } else {  // warp 11
       if (F8) {
-        // ---- scales of 8-bit entries: tails by TMA, lanes 0 to 15 a box of K's
-        // each, 16 to 31 of V's, then turned into what the softmax adds and
-        // multiplies by.  (Four bytes of an entry by cp.async kept this warp 2000
-        // cycles a tile, and 64 single tokens at 216 us.)
-        int t = 0, issued = 0, due = 0, y = 0, w = 0;
-        bool more = true, have = false;  // have: a tile whose blocks have been looked up
-        TcSegment seg = {};
-        TcTile k = {};
-        const int v = lane >> 4, bx = lane & 15;
-        asm volatile("fence.proxy.async.global;" ::: "memory");  // what earlier kernels wrote, for TMA
+        // ---- scales of 8-bit entries, from the tails that came with K into
+        // what the softmax adds and multiplies by.  (Loading four bytes of an
+        // entry by cp.async kept this warp 2000 cycles a tile: 64 single tokens
+        // 216 us; loading the tails itself 1500: 193.)
+        int slot = 0, lap = 0, due = 0;
+        while (next_segment(P, walk, found)) {
+          const TcSegment seg = found;
 #pragma unroll 1
-        while (more || have || due < issued) {
-          if (have && issued - due < kTails) {
-            const int slot = issued % kTails, box = k.staged ? kStageBox : P.box, boxes = (k.valid + box - 1) / box;
-            if (!__any_sync(0xFFFFFFFFu, *sync.abort)) {
-              if (lane == 0) mbar_expect_tx(b_t + 8 * slot, boxes * box * 2 * kTail);
-              __syncwarp();
-              if (bx < boxes)
-                tma_load_4d(smem_u32(s_tails) + ((slot * 2 + v) * kTile + bx * box) * kTail, k.staged ? &P.stage_tails : &P.page_tails,
-                            b_t + 8 * slot, 0, y, ((k.staged ? a.stage.layer : a.cache.layer) * 2 + v) * H + seg.h, w);
-            }
-            have = false;
-            ++issued;
-          }
-          if (!have && more) {
-            if (t >= seg.t1) {
-              more = next_segment(P, walk, found);
-              seg = found;
-              t = seg.t0;
-            }
-            if (more) {
-              k = tile_of(a, seg, t++);
-              have = true;
-              const int box = k.staged ? kStageBox : P.box;
-              y = k.x0 + bx * box, w = seg.b;
-              if (!k.staged) {
-                const int j = block_of(P, y);
-                if (bx * box < k.valid) w = __ldg(a.cache.block_table + (int64_t)seg.b * a.cache.max_blocks + j);
-                if (w < 0 || w >= a.cache.num_blocks) w = a.cache.num_blocks;  // past the last: a load gives zeros
-                y -= j * a.cache.block_size;
-              }
-            }
-          }
-          if (due < issued && (!have || issued - due == kTails ||
-                               __all_sync(0xFFFFFFFFu, mbar_test_wait(b_t + 8 * (due % kTails), (due / kTails) & 1)))) {
-            const int from = due % kTails, slot = due % kScaleRing;
-            wait(sync, b_t + 8 * from, (due / kTails) & 1);
+          for (int t = seg.t0; t < seg.t1; ++t, ++due) {
+            const int box = tile_of(a, seg, t).staged ? kStageBox : P.box, ring = due % kScaleRing;
+            wait(sync, b_kf + 8 * slot, lap & 1);
+            const char* tails = kslots + slot * C::kKBytes + C::kTileBytes;
             float ks[4], lv[4];
             // scales are finite and positive; what is not (and what the place of a key
             // past the valid ones held) must not reach rows that do not see the entry
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const char* tail = s_tails + (from * 2 * kTile + lane + 32 * e) * kTail;
-              const float x = *reinterpret_cast<const float*>(tail), z = *reinterpret_cast<const float*>(tail + kTile * kTail);
+              const int r = lane + 32 * e, in = r & (box - 1);
+              const char* tail = tails + ((r - in) * 2 + in) * kTail;  // a box's K, then its V
+              const float x = *reinterpret_cast<const float*>(tail), z = *reinterpret_cast<const float*>(tail + box * kTail);
               ks[e] = x > 0.0f && x < kInf ? x : 1.0f;
               lv[e] = lg2(fminf(fmaxf(z, 1.17549435e-38f), 1.70141183e38f));
             }
-            if (due >= kScaleRing) wait(sync, b_se + 8 * slot, (due / kScaleRing - 1) & 1);
-            float* sc = s_sc + slot * 3 * kTile + lane;
+            if (due >= kScaleRing) wait(sync, b_se + 8 * ring, (due / kScaleRing - 1) & 1);
+            float* sc = s_sc + ring * 3 * kTile + lane;
 #pragma unroll
             for (int e = 0; e < 4; ++e) sc[32 * e] = ks[e], sc[kTile + 32 * e] = lv[e], sc[2 * kTile + 32 * e] = ex2(-lv[e]);
             fence_async_smem();  // the tails have been read before their place is loaded again
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_sf + 8 * slot);
-            ++due;
+            if (lane == 0) mbar_arrive(b_sf + 8 * ring);
+            if (++slot == C::kK) slot = 0, ++lap;
           }
         }
       }
@@ -742,8 +711,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         const bool full = k.prefix && k.valid == kTile;
         wait(sync, b_s + 8 * st, ph_s);
         ph_s ^= 1;
-        if (quad == 0 && lane == 0) mbar_arrive(b_ke + 8 * (kt % C::kK));  // the scores' product is done with its keys
         if (F8) wait(sync, b_sf + 8 * (kt % kScaleRing), (kt / kScaleRing) & 1);
+        if (quad == 0 && lane == 0) mbar_arrive(b_ke + 8 * (kt % C::kK));  // the scores' product is done with its keys, and their tails are read
         tc_fence_after();
         const float* sc = s_sc + (kt % kScaleRing) * 3 * kTile;
         if (warp_live) {

@@ -304,21 +304,29 @@ static EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Rows of an 8-bit entry are mapped without their tails, which have maps of
-// their own.
-static bool make_maps(CUtensorMap* m, CUtensorMap* tails, const sv_kv_place& pl, const cuuint64_t* dims, const cuuint64_t* strides,
-                     int box_rows) {
+// A place's rows; rows of an 8-bit entry without their tails, which have a map
+// of their own, {byte, slot or entry, head, (layer, K or V), block or request},
+// and come for K and V at once.
+struct Rows {
+  int64_t n, step, other, outer, step_outer;  // of the second and the last dimension, and from row to row of a layer
+};
+static bool make_maps(CUtensorMap* m, CUtensorMap* tails, const sv_kv_place& pl, const Rows& r, int box_rows) {
   const bool f8 = pl.format == SV_KV_E4M3;
   const int row = f8 ? pl.head_dim : 2 * pl.head_dim, sw = row < 128 ? row : 128;
-  const cuuint32_t box[4] = {(cuuint32_t)(f8 ? sw : sw / 2), (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
+  const cuuint64_t D = (cuuint64_t)pl.head_dim, n = (cuuint64_t)r.n, H = (cuuint64_t)pl.heads, L2 = (cuuint64_t)pl.layers * 2,
+                   outer = (cuuint64_t)r.outer;
+  const cuuint64_t step = (cuuint64_t)r.step, other = (cuuint64_t)r.other, step_outer = (cuuint64_t)r.step_outer;
+  const cuuint32_t rows = (cuuint32_t)box_rows, one[5] = {1, 1, 1, 1, 1};
   if (f8) {
-    const cuuint64_t tail_dims[4] = {kTail, dims[1], dims[2], dims[3]};
-    const cuuint32_t tail_box[4] = {kTail, (cuuint32_t)box_rows, 1, 1};
-    if (encode_tiled()(tails, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, static_cast<char*>(pl.data) + row, tail_dims, strides,
-                             tail_box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    const cuuint64_t dims[5] = {kTail, n, H, L2, outer}, strides[4] = {step, other, other * H, step_outer};
+    const cuuint32_t box[5] = {kTail, rows, 1, 2, 1};
+    if (encode_tiled()(tails, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, static_cast<char*>(pl.data) + row, dims, strides, box, one,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
   }
+  const cuuint64_t dims[4] = {D, n, L2 * H, outer}, strides[3] = {step, other, step_outer};
+  const cuuint32_t box[4] = {(cuuint32_t)(f8 ? sw : sw / 2), rows, 1, 1};
   return encode_tiled()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pl.data, dims,
                         strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         sw == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -341,20 +349,13 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
   const uint32_t G = (uint32_t)(a->Hq / c.heads);
   P.group = (int)G;
   P.group_magic = G == 1 ? 0u : (uint32_t)((0x100000000ull + G - 1) / G);
-  const cuuint64_t row = (cuuint64_t)row_bytes(c), H = (cuuint64_t)c.heads;
-  {
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.block_size, (cuuint64_t)c.layers * 2 * H,
-                                (cuuint64_t)c.num_blocks};
-    const cuuint64_t strides[3] = {row, row * c.block_size, row * c.block_size * c.layers * 2 * H};
-    if (!make_maps(&P.pages, &P.page_tails, c, dims, strides, P.box)) return SV_ERR_CUDA;
-  }
-  if (a->stage.data) {
-    const cuuint64_t per = row * a->stage.layers * 2 * H;  // bytes of an entry
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)a->stage.rows, (cuuint64_t)a->stage.layers * 2 * H,
-                                (cuuint64_t)a->B};
-    const cuuint64_t strides[3] = {per, row, per * a->stage.rows};
-    if (!make_maps(&P.stage, &P.stage_tails, a->stage, dims, strides, kStageBox)) return SV_ERR_CUDA;
-  }
+  const int64_t row = row_bytes(c), per = row * 2 * c.heads;  // bytes of a row, and of an entry's layer
+  if (!make_maps(&P.pages, &P.page_tails, c,
+                 {c.block_size, row, row * c.block_size, c.num_blocks, per * c.layers * c.block_size}, P.box))
+    return SV_ERR_CUDA;
+  const sv_kv_place& g = a->stage;
+  if (g.data && !make_maps(&P.stage, &P.stage_tails, g, {g.rows, per * g.layers, row, a->B, per * g.layers * g.rows}, kStageBox))
+    return SV_ERR_CUDA;
   const sv_status rr = sv_raise_dyn_smem((const void*)plan.k.fn, (size_t)plan.k.smem);
   if (rr != SV_OK) return rr;
   if (sv_launch_pdl(plan.k.fn, dim3((unsigned)plan.ctas), dim3((unsigned)plan.k.threads), (size_t)plan.k.smem, stream, P) != cudaSuccess) {
