@@ -638,31 +638,36 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       const int i = entry_of(P, i0 + lrow), hq = seg.h * G + i0 + lrow - i * G;
       const bool live = i <= seg.X.n;
       const bool warp_live = lrow - lane < rows;
-      // queries: rows of this CTA's block, swizzled as the products read them
+      // queries: rows of this CTA's block, read once and written to each copy,
+      // swizzled as the products read them
       {
-        constexpr int kChunks = D / 8, kGroup = QM == 2 ? 128 : 256, kEach = kTile * kChunks / kGroup;
+        constexpr int kChunks = D / 8, kGroup = QM == 2 ? 128 : 256;
+        const int each = apart * kChunks / kGroup;
         const int qt = QM == 2 ? row : tid, part0 = i0 + (QM == 2 ? st * kTile : 0);
         char* q = sm + (QM == 2 ? st * C::kQBytes : 0);
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // scores are compared before they are scaled
         const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + seg.b * a.q_stride[0] + (int64_t)seg.h * G * a.q_stride[2];
         constexpr int kAt = F8 ? 2 : 4;  // loads in flight
 #pragma unroll 1
-        for (int it0 = 0; it0 < kEach; it0 += kAt) {
+        for (int it0 = 0; it0 < each; it0 += kAt) {
           uint4 x8[kAt];
 #pragma unroll
           for (int it = 0; it < kAt; ++it) {
-            const int idx = (it0 + it) * kGroup + qt, rr = part0 + (idx / kChunks & (apart - 1)), qi = entry_of(P, rr);
+            const int idx = (it0 + it) * kGroup + qt, rr = part0 + idx / kChunks, qi = entry_of(P, rr);
             x8[it] = make_uint4(0, 0, 0, 0);
-            if (qi <= seg.X.n)
+            if (it0 + it < each && qi <= seg.X.n)
               x8[it] = *reinterpret_cast<const uint4*>(q0 + qi * a.q_stride[1] + (rr - qi * G) * a.q_stride[2] + idx % kChunks * 8);
           }
 #pragma unroll
           for (int it = 0; it < kAt; ++it) {
+            if (it0 + it >= each) break;
             const int idx = (it0 + it) * kGroup + qt, r = idx / kChunks, c = idx % kChunks;  // r: row of the tile
             const uint4 v = make_uint4(x8[it].x ^ flip, x8[it].y ^ flip, x8[it].z ^ flip, x8[it].w ^ flip);
             if (!F8) {
               const int hf = c * 16 / C::kSw, in = c - hf * (C::kSw / 16);
-              *reinterpret_cast<uint4*>(q + hf * C::kHalfBytes + r * C::kSw + ((in ^ (r & 7)) << 4)) = v;
+              char* d = q + hf * C::kHalfBytes + r * C::kSw + ((in ^ (r & 7)) << 4);
+#pragma unroll 1
+              for (int x = 0; x < copies; ++x, d += apart * C::kSw) *reinterpret_cast<uint4*>(d) = v;
             } else {
               // q = scale (hi + lo): hi rounds to the 8-bit format's 4 significant
               // bits, and the rest of a bf16 value is at most 4 bits more, so the
@@ -689,9 +694,12 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               const int in = c >> 1;
               const int sw = C::kSw == 128 ? in ^ (r & 7) : in ^ ((r >> 1) & 3);
               char* d = q + r * C::kSw + sw * 16 + (c & 1) * 8;
-              *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-              *reinterpret_cast<uint2*>(d + kTile * D) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-              if (c == 0) s_qs[(QM == 2 ? st * kTile : 0) + r] = qs;
+#pragma unroll 1
+              for (int x = 0; x < copies; ++x, d += apart * C::kSw) {
+                *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                *reinterpret_cast<uint2*>(d + kTile * D) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                if (c == 0) s_qs[(QM == 2 ? st * kTile : 0) + r + x * apart] = qs;
+              }
             }
           }
         }
