@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         char* q = sm + (QM == 2 ? st * C::kQBytes : 0);
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // scores are compared before they are scaled
         const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + seg.b * a.q_stride[0] + (int64_t)seg.h * G * a.q_stride[2];
-        constexpr int kAt = F8 ? 2 : 4;  // loads in flight
+        constexpr int kAt = F8 ? 4 : 8;  // loads in flight
 #pragma unroll 1
         for (int it0 = 0; it0 < each; it0 += kAt) {
           uint4 x8[kAt];
