@@ -198,6 +198,12 @@ static __device__ __noinline__ void wait_long(volatile int* abort, int* err, uin
 __device__ __forceinline__ void wait(const TcSync& s, uint32_t bar, uint32_t parity) {
   if (!mbar_try_wait(bar, parity)) wait_long(s.abort, s.err, bar, parity);
 }
+// The same; live becomes false in a lane that finds that a wait has run out.
+__device__ __forceinline__ void wait(const TcSync& s, uint32_t bar, uint32_t parity, bool& live) {
+  if (mbar_try_wait(bar, parity)) return;
+  wait_long(s.abort, s.err, bar, parity);
+  if (*s.abort) live = false;
+}
 
 // Two fp32 values in one register pair, one instruction for both.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
@@ -514,6 +520,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       // divided for), since they add up with the products' own time.
       const bool one = elect_one();
       int ph_p = 0, ph_q = 0;  // ph_p: a bit per stream
+      bool live = true;
       int ks = 0, klap = 0, vs = 0, vlap = 0;
       constexpr uint32_t kIdS = instr_desc(F8 ? 0 : 1, kTile, kTile, false);  // e4m3 or bf16
       constexpr uint32_t kIdO = instr_desc(F8 ? 0 : 1, kTile, D, true) | (F8 ? 1u << 7 : 0u);  // weights of 5 exponent bits
@@ -530,16 +537,18 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         for (int x = 0; x < units + 2; ++x) {
           const int st = x & 1;
           const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
+          bool k_there = false;
           if (x >= 2) {
             const int t = seg.t0 + (QM == 2 ? (x - 2) >> 1 : x - 2);
             const int steps = t < whole ? kTile / C::kStep : (tile_of(a, seg, t).valid + C::kStep - 1) / C::kStep;
             const uint64_t vd = v0 + vs * (C::kTileBytes >> 4);
             const bool first = x < 4;  // of this stream in this segment
-            wait(sync, b_vf + 8 * vs, vlap & 1);
-            wait(sync, b_p + 8 * st, ph_p >> st & 1);
+            wait(sync, b_vf + 8 * vs, vlap & 1, live);
+            k_there = x < units && mbar_test_wait(b_kf + 8 * ks, klap & 1);  // while the weights are awaited
+            wait(sync, b_p + 8 * st, ph_p >> st & 1, live);
             ph_p ^= 1 << st;
             tc_fence_after();
-            if (one && !*sync.abort) {
+            if (one && live) {
 #pragma unroll
               for (int j = 0; j < kTile / C::kStep; ++j) {
                 if (j >= steps) break;
@@ -556,9 +565,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
           }
           if (x < units) {
             const uint64_t qd = q0 + (QM == 2 ? st * (C::kQBytes >> 4) : 0), kd = k0 + ks * (C::kKBytes >> 4);
-            wait(sync, b_kf + 8 * ks, klap & 1);
+            if (!k_there) wait(sync, b_kf + 8 * ks, klap & 1, live);
             tc_fence_after();
-            if (one && !*sync.abort) {
+            if (one && live) {
 #pragma unroll
               for (int j = 0; j < C::kRow / 32; ++j) {
                 const int at = j / (C::kSw / 32) * C::kHalfBytes + j % (C::kSw / 32) * 32;
