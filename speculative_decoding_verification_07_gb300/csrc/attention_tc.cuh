@@ -537,14 +537,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         for (int x = 0; x < units + 2; ++x) {
           const int st = x & 1;
           const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
-          bool k_there = false;
+          bool k_there = QM == 2 && st == 1;
           if (x >= 2) {
             const int t = seg.t0 + (QM == 2 ? (x - 2) >> 1 : x - 2);
             const int steps = t < whole ? kTile / C::kStep : (tile_of(a, seg, t).valid + C::kStep - 1) / C::kStep;
             const uint64_t vd = v0 + vs * (C::kTileBytes >> 4);
             const bool first = x < 4;  // of this stream in this segment
-            wait(sync, b_vf + 8 * vs, vlap & 1, live);
-            k_there = x < units && mbar_test_wait(b_kf + 8 * ks, klap & 1);  // while the weights are awaited
+            if (QM == 1 || st == 0) {  // the second row tile's keys are there
+              wait(sync, b_vf + 8 * vs, vlap & 1, live);
+              k_there = x < units && mbar_test_wait(b_kf + 8 * ks, klap & 1);  // while the weights are awaited
+            }
             wait(sync, b_p + 8 * st, ph_p >> st & 1, live);
             ph_p ^= 1 << st;
             tc_fence_after();
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
                 mma_ts<F8>(tO, tS + j * (F8 ? 24 : 8), d, kIdO, !first || j > 0);
                 if (F8) mma_ts<F8>(tO, tS + j * 24 + 8, d, kIdO, true), mma_ts<F8>(tO, tS + j * 24 + 16, d, kIdO, true);
               }
-              mma_commit(b_o + 8 * st);
+              if (x >= units) mma_commit(b_o + 8 * st);  // the stream's last of the segment
               if (QM == 1 || st == 1) mma_commit(b_ve + 8 * vs);
             }
             __syncwarp();
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     // ---- softmax ------------------------------------------------------------
     const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t tS = tmem + (quad << 21) + st * 128, tO = tmem + (quad << 21) + 256 + st * 128;
-    int kbase = 0, ph_s = 0, done = 0;  // done: tiles this stream has handed to the products
+    int kbase = 0, ph_s = 0, ph_o = 0;
     while (next_segment(P, walk, found)) {
         const TcSegment seg = found;
       const int n = seg.t1 - seg.t0, units = n * QM;
@@ -775,11 +777,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               const uint64_t f2 = pair(f, f);
               ls[0] = mul2(ls[0], f2), ls[1] = mul2(ls[1], f2);
               if (ch > ch_a) rescale_weights<F8>(tS + kW * ch_a, kW * (ch - ch_a), f);
-              if (u >= 2) {
-                wait(sync, b_o + 8 * st, (done - 1) & 1);
-                tc_fence_after();
-                rescale(tO, D, f);
-              }
+              if (u >= 2) rescale(tO, D, f);  // these scores were issued, and are done, after the last outputs
             }
             const float base = (m == -kInf ? 0.0f : m) - TcSoft<F8>::kBias;
             const uint64_t base2 = pair(-base, -base);
@@ -831,12 +829,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
           mbar_arrive(b_p + 8 * st);
           if (F8) mbar_arrive(b_se + 8 * (kt % kScaleRing));
         }
-        ++done;
       }
       kbase += n;
 
       // ---- the segment's outputs -------------------------------------------
-      if (st < units) wait(sync, b_o + 8 * st, (done - 1) & 1);
+      if (st < units) {
+        wait(sync, b_o + 8 * st, ph_o);
+        ph_o ^= 1;
+      }
       const bool both = QM == 1 && units > 1;  // stream 1 had a tile too
       if (QM == 1) s_ml[st * kTile + row] = make_float2(m, l);
       tc_fence_before();
