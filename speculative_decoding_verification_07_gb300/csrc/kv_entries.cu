@@ -3,7 +3,10 @@
 
 namespace sv {
 
-constexpr int kEntryThreads = 256;
+// 8164 entries of 32 + 2 x 8 heads of 128, 8-bit (186 MB): written in 52 us by
+// 256 threads, 38 by 128 (4.9 TB/s), 37 by 64; 960 entries 6.1, 5.9 and 6.2 us:
+// what a thread does before its first row is shared by more rows.
+constexpr int kAppendThreads = 128;
 
 // Lanes of a warp that share a row of head_dim values, eight values a lane;
 // rows never straddle warps, so in-place rotation and the row maximum need
@@ -98,7 +101,7 @@ __device__ __forceinline__ void turn8(float (&x)[8], const Raw8<F32>& now, const
 // A row does not depend on where its entry goes: a thread's first three are on
 // their way before the entry's length, block and position are known.
 template <bool F32, int TURN>
-__global__ void __launch_bounds__(kEntryThreads, 4) kv_append_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const __grid_constant__ AppendParams P) {
   pdl_wait();
   pdl_trigger();
   const sv_append_args& a = P.a;
@@ -202,49 +205,44 @@ __global__ void __launch_bounds__(kEntryThreads, 4) kv_append_kernel(const __gri
   }
 }
 
-constexpr int kReadEntries = 4;  // entries of a CTA, looked up together
+// One CTA per (request, entry), kReadRows rows of a thread under way at once;
+// bytes bound it.  8164 entries of 2 x 8 rows of 128, 8-bit to bf16 (52 MB),
+// with 256 threads for four entries 15.4 us, 64 for one and one row at a time
+// 9.3, two rows 9.6 (5.4 TB/s), four 10.0; 960 entries 3.3, 3.0, 2.8 and 2.7 us.
+constexpr int kReadThreads = 64, kReadRows = 2;
 
 template <bool F32>
-__global__ void __launch_bounds__(kEntryThreads) kv_read_kernel(int total, int R, const int32_t* seq_len,
-                                                                const int32_t* n_nodes,
-                                                                const __grid_constant__ sv_kv_place src,
-                                                                void* out, int* err) {
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(int R, const int32_t* seq_len, const int32_t* n_nodes,
+                                                               const __grid_constant__ sv_kv_place src, void* out, int* err) {
   pdl_wait();
   pdl_trigger();
   const RowLanes L(src.head_dim);
   const int64_t step = row_step(src);
-  int64_t off[kReadEntries];
-#pragma unroll
-  for (int u = 0; u < kReadEntries; ++u) {
-    const int e = blockIdx.x * kReadEntries + u, b = e / R, i = e - b * R;
-    off[u] = -1;
-    if (e >= total) continue;
-    int n = n_nodes ? n_nodes[b] : R - 1;
-    if (n >= R) {
-      if (threadIdx.x == 0 && i == 0) report(err, SV_ERR_STATE);
-      n = R - 1;
-    }
-    if (i <= n) {
-      off[u] = entry_offset(src, b, i, (int64_t)seq_len[b] + i);
-      if (off[u] < 0 && threadIdx.x == 0) report(err, SV_ERR_STATE);
-    }
+  const int b = blockIdx.x / R, i = blockIdx.x - b * R, rows = 2 * src.heads;
+  int n = n_nodes ? n_nodes[b] : R - 1;
+  if (n >= R) {
+    if (threadIdx.x == 0 && i == 0) report(err, SV_ERR_STATE);
+    n = R - 1;
+  }
+  int64_t off = -1;
+  if (i <= n) {
+    off = entry_offset(src, b, i, (int64_t)seq_len[b] + i);
+    if (off < 0 && threadIdx.x == 0) report(err, SV_ERR_STATE);
   }
   if (!L.on) return;
-  for (int r = L.slot; r < 2 * src.heads; r += L.nslots) {
-    float x[kReadEntries][8];
+  for (int r0 = L.slot; r0 < rows; r0 += kReadRows * L.nslots) {
+    float x[kReadRows][8] = {};
 #pragma unroll
-    for (int u = 0; u < kReadEntries; ++u) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] = 0.0f;
-      if (off[u] >= 0) {
-        const char* row = static_cast<const char*>(src.data) + off[u] + r * step;
-        load_entry8(row, src.format, 8 * L.c, entry_scale(row, src.format, src.head_dim), x[u]);
-      }
+    for (int u = 0; u < kReadRows; ++u) {
+      const int r = r0 + u * L.nslots;
+      if (off < 0 || r >= rows) continue;
+      const char* row = static_cast<const char*>(src.data) + off + r * step;
+      load_entry8(row, src.format, 8 * L.c, entry_scale(row, src.format, src.head_dim), x[u]);
     }
 #pragma unroll
-    for (int u = 0; u < kReadEntries; ++u) {
-      const int64_t e = (int64_t)blockIdx.x * kReadEntries + u;
-      if (e < total) store8<F32>(out, (e * 2 * src.heads + r) * src.head_dim + 8 * L.c, x[u]);
+    for (int u = 0; u < kReadRows; ++u) {
+      const int r = r0 + u * L.nslots;
+      if (r < rows) store8<F32>(out, ((int64_t)blockIdx.x * rows + r) * src.head_dim + 8 * L.c, x[u]);
     }
   }
 }
@@ -273,7 +271,7 @@ extern "C" sv_status kv_append(sv_handle* h, const sv_append_args* a, sv_stream_
   static const Fn fns[2][4] = {
       {kv_append_kernel<false, kNone>, kv_append_kernel<false, kPairs>, kv_append_kernel<false, kLanes>, kv_append_kernel<false, kMemory>},
       {kv_append_kernel<true, kNone>, kv_append_kernel<true, kPairs>, kv_append_kernel<true, kLanes>, kv_append_kernel<true, kMemory>}};
-  const cudaError_t e = sv_launch_pdl(fns[a->dtype == SV_FP32][turn], dim3((unsigned)(a->B * a->R)), dim3(kEntryThreads), 0,
+  const cudaError_t e = sv_launch_pdl(fns[a->dtype == SV_FP32][turn], dim3((unsigned)(a->B * a->R)), dim3(kAppendThreads), 0,
                                       (cudaStream_t)stream, P);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
@@ -289,12 +287,11 @@ extern "C" sv_status kv_read(sv_handle* h, int32_t B, int32_t R, const int32_t* 
   if (B == 0) return SV_OK;
   if (bad_place(src) || !seq_len || !out || ((uintptr_t)out & 15u) || (int64_t)B * R > INT32_MAX) return SV_ERR_INVALID;
   if (!src->block_table && src->rows < R) return SV_ERR_INVALID;
-  const int total = B * R;
-  const dim3 grid((unsigned)((total + kReadEntries - 1) / kReadEntries)), block(kEntryThreads);
+  const dim3 grid((unsigned)(B * R)), block(kReadThreads);
   const cudaError_t e =
       out_dtype == SV_FP32
-          ? sv_launch_pdl(kv_read_kernel<true>, grid, block, 0, (cudaStream_t)stream, total, (int)R, seq_len, n_nodes, *src, out, h->d_err)
-          : sv_launch_pdl(kv_read_kernel<false>, grid, block, 0, (cudaStream_t)stream, total, (int)R, seq_len, n_nodes, *src, out, h->d_err);
+          ? sv_launch_pdl(kv_read_kernel<true>, grid, block, 0, (cudaStream_t)stream, (int)R, seq_len, n_nodes, *src, out, h->d_err)
+          : sv_launch_pdl(kv_read_kernel<false>, grid, block, 0, (cudaStream_t)stream, (int)R, seq_len, n_nodes, *src, out, h->d_err);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return SV_ERR_CUDA;
