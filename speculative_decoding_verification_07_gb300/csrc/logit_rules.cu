@@ -4,8 +4,8 @@
 
 namespace sv {
 
-constexpr int kRuleThreads = 256;
-constexpr int kSlice = 2048;  // tokens of one CTA
+constexpr int kRuleThreads = 512;
+constexpr int kSlice = 4096;  // tokens of one CTA
 constexpr int kFlight = 1;    // vectors of a batch; one batch is on its way while another is written
 constexpr int kNodes = 256;   // drafted tokens of a slice that are kept at hand
 
@@ -18,7 +18,7 @@ struct RuleSmem {
   int n, n_path;           // listed tokens, such nodes (more than kNodes: look through all)
 };
 
-// One CTA takes a slice of 2048 tokens of one request's rows, or of `per` of
+// One CTA takes a slice of 4096 tokens of one request's rows, or of `per` of
 // them.  The grammar mask touches every logit, the other rules a few: so the
 // rows are streamed with the mask alone (out = allowed ? logit : -inf, 16 bytes
 // a thread, no look-up), and then the tokens that a penalty or a bias concerns,
@@ -26,9 +26,11 @@ struct RuleSmem {
 // the row's logits; a row's own path only adds to their counts, so all rows are
 // written at once.  Bound by memory: each logit is read and written once.  64 x 7
 // rows of 128256 (bf16): looking up counts and biases for every logit as it
-// passed 109 us, a list 71, rows patched together 55; the copy alone 39.
+// passed 109 us, a list 71, rows patched together 55, half as many lists (slices
+// of 4096 for 512 threads, not 2048 for 256) 50, 4.7 TB/s; the copy alone 41.
+// Larger CTAs or two vectors on their way leave fewer threads on an SM: 68 and 52.
 template <bool F32>
-__global__ void __launch_bounds__(kRuleThreads, 8) logit_rules_kernel(const __grid_constant__ sv_logits_args a, int per, int* err) {
+__global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __grid_constant__ sv_logits_args a, int per, int* err) {
   pdl_wait();
   pdl_trigger();
   __shared__ __align__(16) RuleSmem s;
