@@ -56,7 +56,7 @@ struct TcShape {
   static constexpr int kQBytes = kTile * 2 * D;              // bf16 rows, or two 8-bit parts
   static constexpr int kStep = F8 ? 32 : 16;                 // keys of one product of weights and V
   static constexpr int kRows = kTile * QM;
-  static constexpr int kQAll = QM * kQBytes > 24576 ? QM * kQBytes : 24576;  // also holds 3 copies' 32 x 64 outputs
+  static constexpr int kQAll = QM * kQBytes > 32768 ? QM * kQBytes : 32768;  // also holds 128 x 64 outputs, 32 of each half
   static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 3 * kTile * 4 : 0);
   // tiles held; a slot of K has its keys' tails and V's
   static constexpr int kTails = F8 ? 2 * kTile * kTail : 0, kKBytes = kTileBytes + kTails;
@@ -493,6 +493,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       int slot = 0, lap = 0;
       while (next_segment(P, walk, found)) {
         const TcSegment seg = found;
+        if (!v) {  // the segment's queries, on their way into L2 while the last one's tiles are worked on
+          const int rows = min(C::kRows, (seg.X.n + 1) * G - seg.rb * C::kRows);
+          const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + seg.b * a.q_stride[0] + (int64_t)seg.h * G * a.q_stride[2];
+#pragma unroll 1
+          for (int r = lane; r < rows; r += 32) {
+            const int rr = seg.rb * C::kRows + r, qi = entry_of(P, rr);
+            const __nv_bfloat16* row = q0 + qi * a.q_stride[1] + (rr - qi * G) * a.q_stride[2];
+            for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+          }
+        }
 #pragma unroll 1
         for (int t = seg.t0; t < seg.t1; ++t) {
           const TcTile k = tile_of(a, seg, t);
@@ -860,13 +870,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       float f0 = 1.0f, f1 = 0.0f;  // of this copy's outputs in the two streams
       if (QM == 1) {
         float M = -kInf, L = 0.0f;
-        const float2* o = s_ml + lrow;
         const int parts = both ? 2 * copies : copies;  // a copy every `apart` rows, the second stream after the first
-#pragma unroll 1
-        for (int x = 0; x < parts; ++x) M = fmaxf(M, o[x * apart].x);
+        float2 o[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          o[x] = x < parts ? s_ml[lrow + x * apart] : make_float2(-kInf, 0.0f);
+          M = fmaxf(M, o[x].x);
+        }
         const float Mb = M == -kInf ? 0.0f : M;
-#pragma unroll 1
-        for (int x = 0; x < parts; ++x) L += o[x * apart].y * ex2(o[x * apart].x - Mb);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) L += o[x].y * ex2(o[x].x - Mb);
         f0 = ex2(s_ml[row].x - Mb), f1 = both ? ex2(s_ml[kTile + row].x - Mb) : 0.0f;
         m = M, l = L;
       }
@@ -893,43 +906,45 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
             for (int e = 0; e < 32; ++e) y[e] += __uint_as_float(o[e]) * f1;
           }
         }
-        if (copies > 1) {  // the first copy adds the others' shares
-          if (copy > 0 && warp_live) {
+        auto put = [&](int at, const float* z) {  // eight columns of a row
+          if (!split) {
+            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.out) + out + at;
+            *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16(z[0] * inv, z[1] * inv), pack_bf16(z[2] * inv, z[3] * inv),
+                                                      pack_bf16(z[4] * inv, z[5] * inv), pack_bf16(z[6] * inv, z[7] * inv));
+            if (spoiled)
+#pragma unroll 1
+              for (int e = 0; e < 8; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back(P, found, i, at + e));
+          } else {
+            float* d = part + lrow * D + at;
+            *reinterpret_cast<float4*>(d) = make_float4(z[0], z[1], z[2], z[3]);
+            *reinterpret_cast<float4*>(d + 4) = make_float4(z[4], z[5], z[6], z[7]);
+            if (spoiled)
+#pragma unroll 1
+              for (int e = 0; e < 8; ++e) d[e] += given_back(P, found, i, at + e);
+          }
+        };
+        if (copies > 1) {  // each copy adds all shares of 32 / copies columns
+          if (warp_live)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              gather[((copy - 1) * 16 + st * 8 + e) * apart + lrow] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-          }
+              gather[(copy * 16 + st * 8 + e) * apart + lrow] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           named_barrier(1, 256);
-          if (copy == 0 && warp_live) {
+          if (live)
 #pragma unroll 1
-            for (int x = 0; x < copies - 1; ++x)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 v = gather[(x * 16 + st * 8 + e) * apart + lrow];
-                y[4 * e] += v.x, y[4 * e + 1] += v.y, y[4 * e + 2] += v.z, y[4 * e + 3] += v.w;
+            for (int g = copy; g < 4; g += copies) {
+              float z[8] = {};
+#pragma unroll 2
+              for (int x = 0; x < copies; ++x) {
+                const float4* from = gather + (x * 16 + st * 8 + 2 * g) * apart + lrow;
+                const float4 u = from[0], v = from[apart];
+                z[0] += u.x, z[1] += u.y, z[2] += u.z, z[3] += u.w, z[4] += v.x, z[5] += v.y, z[6] += v.z, z[7] += v.w;
               }
-          }
+              put(col + 8 * g, z);
+            }
           named_barrier(1, 256);
-        }
-        if (!live || copy > 0) continue;
-        if (!split) {
+        } else if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = l == 0.0f ? 0.0f : y[e] * inv;
-          __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.out) + out + col;
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            reinterpret_cast<uint4*>(d)[e / 8] = make_uint4(pack_bf16(y[e], y[e + 1]), pack_bf16(y[e + 2], y[e + 3]),
-                                                            pack_bf16(y[e + 4], y[e + 5]), pack_bf16(y[e + 6], y[e + 7]));
-          if (spoiled)
-#pragma unroll 1
-            for (int e = 0; e < 32; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back(P, found, i, col + e));
-        } else {
-          float* d = part + lrow * D + col;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-          if (spoiled)
-#pragma unroll 1
-            for (int e = 0; e < 32; ++e) d[e] += given_back(P, found, i, col + e);
+          for (int g = 0; g < 4; ++g) put(col + 8 * g, y + 8 * g);
         }
       }
       if (split && live && copy == 0 && (QM == 2 || st == 0))
