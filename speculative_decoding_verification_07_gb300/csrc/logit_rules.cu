@@ -4,7 +4,7 @@
 
 namespace sv {
 
-constexpr int kRuleThreads = 512;
+constexpr int kRuleThreads = 512, kListThreads = 64;  // of them, those that make the lists
 constexpr int kSlice = 4096;  // tokens of one CTA
 constexpr int kFlight = 1;    // vectors of a batch; one batch is on its way while another is written
 constexpr int kNodes = 256;   // drafted tokens of a slice that are kept at hand
@@ -18,6 +18,8 @@ struct RuleSmem {
   int n, n_path;           // listed tokens, such nodes (more than kNodes: look through all)
 };
 
+static __device__ __forceinline__ void list_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kListThreads) : "memory"); }
+
 // One CTA takes a slice of 4096 tokens of one request's rows, or of `per` of
 // them.  The grammar mask touches every logit, the other rules a few: so the
 // rows are streamed with the mask alone (out = allowed ? logit : -inf, 16 bytes
@@ -27,7 +29,8 @@ struct RuleSmem {
 // written at once.  Bound by memory: each logit is read and written once.  64 x 7
 // rows of 128256 (bf16): looking up counts and biases for every logit as it
 // passed 109 us, a list 71, rows patched together 55, half as many lists (slices
-// of 4096 for 512 threads, not 2048 for 256) 50, 4.7 TB/s; the copy alone 41.
+// of 4096 for 512 threads, not 2048 for 256) 50, lists made by two warps while
+// the others stream 48 (by one 53, by four 51), 4.9 TB/s; the copy alone 41.
 // Larger CTAs or two vectors on their way leave fewer threads on an SM: 68 and 52.
 template <bool F32>
 __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __grid_constant__ sv_logits_args a, int per, int* err) {
@@ -51,19 +54,16 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
   const char* src0 = static_cast<const char*>(a.logits) + ((int64_t)b * a.R * a.ld + v0) * eb;
   char* dst0 = static_cast<char*>(a.out) + ((int64_t)b * a.R * a.out_ld + v0) * eb;
 
-  // ---- every logit: copied, or -inf ----------------------------------------
-  // A batch of vectors is always on its way: the first is asked for before the
-  // lists are made, the next before the one at hand is written.
   const int total = !in_place ? (r1 - r0) * groups : a.allowed ? live * groups : 0;  // rows without rules are copied
   auto row_of = [&](int k) { return groups == kSlice / 8 ? k / (kSlice / 8) : k / groups; };
   struct Batch {
     uint4 lo[kFlight], hi[F32 ? kFlight : 1];
     uint32_t bits[kFlight];
   };
-  auto fetch = [&](Batch& q, int g0) {
+  auto fetch = [&](Batch& q, int g0, int step) {
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) {
-      const int k = g0 + u * kRuleThreads, r = row_of(k), g = k - r * groups;
+      const int k = g0 + u * step, r = row_of(k), g = k - r * groups;
       if (k >= total) continue;
       const char* p = src0 + (int64_t)(r0 + r) * a.ld * eb + g * 8 * eb;
       q.bits[u] = 0xFFu;
@@ -87,10 +87,10 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
       }
     }
   };
-  auto put = [&](const Batch& q, int g0) {
+  auto put = [&](const Batch& q, int g0, int step) {
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) {
-      const int k = g0 + u * kRuleThreads, r = row_of(k), g = k - r * groups;
+      const int k = g0 + u * step, r = row_of(k), g = k - r * groups;
       if (k >= total || (in_place && q.bits[u] == 0xFFu)) continue;
       char* p = dst0 + (int64_t)(r0 + r) * a.out_ld * eb + g * 8 * eb;
       const uint4 h = q.hi[F32 ? u : 0];
@@ -118,24 +118,22 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
       }
     }
   };
-  Batch now;
-  fetch(now, t);
 
   // ---- the tokens the rules concern ----------------------------------------
-  if (live > 0) {
-    for (int i = t; i < kSlice / 4; i += kRuleThreads) {
+  if (live > 0 && t < kListThreads) {
+    for (int i = t; i < kSlice / 4; i += kListThreads) {
       reinterpret_cast<int4*>(s.count)[i] = make_int4(0, 0, 0, 0);
       if (a.bias_ld > 0) reinterpret_cast<float4*>(s.bias)[i] = make_float4(0, 0, 0, 0);
       reinterpret_cast<uint32_t*>(s.known)[i] = 0;
     }
     if (t == 0) s.n = s.n_path = 0;
-    __syncthreads();
+    list_barrier();
     auto list = [&](int x, int* n) { s.listed[atomicAdd(n, 1)] = (uint16_t)x; };
-    for (int i0 = t; i0 < a.history_ld; i0 += 4 * kRuleThreads) {
+    for (int i0 = t; i0 < a.history_ld; i0 += 4 * kListThreads) {
       int x[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * kRuleThreads;
+        const int i = i0 + u * kListThreads;
         x[u] = i < a.history_ld ? a.history[b * a.history_ld + i] - v0 : -1;
       }
 #pragma unroll
@@ -143,14 +141,14 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
         if (x[u] >= 0 && x[u] < len && atomicAdd(&s.count[x[u]], 1) == 0) s.known[x[u]] = 1, list(x[u], &s.n);
     }
     const int np = a.mask ? n : min(n, r1 - 1);
-    for (int j = t; j < np; j += kRuleThreads) {
+    for (int j = t; j < np; j += kListThreads) {
       const int x = a.tokens[(int64_t)b * (a.R - 1) + j] - v0;
       if (x >= 0 && x < len) {
         const int q = atomicAdd(&s.n_path, 1);
         if (q < kNodes) s.node[q] = (uint16_t)(j + 1), s.token[q] = (uint16_t)x;
       }
     }
-    __syncthreads();
+    list_barrier();
     // one warp adds the biases, so that a token named several times gets its
     // values in list order
     if (t < 32)
@@ -174,15 +172,20 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
         }
         __syncwarp();
       }
-  }
-
-  constexpr int kStride = kFlight * kRuleThreads;
+  } else {
+    // ---- every logit: copied, or -inf --------------------------------------
+    // A batch of vectors is always on its way: the next is asked for before the
+    // one at hand is written.
+    const int first = live > 0 ? kListThreads : 0;
+    Batch now;
+    fetch(now, t - first, kRuleThreads - first);
 #pragma unroll 1
-  for (int g0 = t; g0 < total; g0 += kStride) {
-    Batch next;
-    fetch(next, g0 + kStride);
-    put(now, g0);
-    now = next;
+    for (int g0 = t - first; g0 < total; g0 += kFlight * (kRuleThreads - first)) {
+      Batch next;
+      fetch(next, g0 + kFlight * (kRuleThreads - first), kRuleThreads - first);
+      put(now, g0, kRuleThreads - first);
+      now = next;
+    }
   }
   if (live <= 0) return;
   __syncthreads();
