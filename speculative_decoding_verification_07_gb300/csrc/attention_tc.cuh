@@ -70,16 +70,19 @@ struct TcShape {
 // A CTA's share of the work: [w, w1) of the list of all requests' items (head,
 // row block), an item being kLead units for what it costs besides its tiles
 // (queries in, outputs out) and then one unit a key tile.  64 requests of 128 to
-// 8192 positions, bf16, single tokens / trees of 15 nodes: 220 / 237 us with a
-// lead of 1, 211 / 230 with 2, 196 / 210 with 4, 194 / 203 with 6, 196 / 205 with 8.
+// 8192 positions, bf16, single tokens / trees of 15 nodes: 193 / 215 us with a
+// lead of 3, 191 / 208 with 4, 189 / 202 with 5, 192 / 200 with 6, 193 / 204 with 8.
 constexpr int kLead = 6;
 // Items of up to this many key tiles are not shared between CTAs: a tile is
 // 0.9 us for a CTA alone, joining parts 3 us and more.  A single request leaves
 // most of the GPU idle, so its items are shared earlier: one token over 777
-// positions (7 tiles, 8 heads) 13.5 us shared, 15.3 whole; six trees over 100 to
-// 1000 positions 21.1 shared, 18.4 whole; 64 over 16 to 520 51.5 and 43.5.
+// positions (7 tiles, 8 heads) 13.1 us shared, 14.8 whole; six trees over 100 to
+// 1000 positions 20.7 shared, 18.6 whole; 64 over 16 to 520 51.2 and 42.8.
 constexpr int kWholeOne = 6, kWhole = 12;
-constexpr int kLeast = 2;  // units of a share: 2000 positions 28.3 us with 1, 23.1 with 2, 25.8 with 10
+// Units of a share: more rows take longer to join.  One token (4 rows a head)
+// over 2000 positions 16.7 us with 1, 14.6 with 2, 15.7 with 4, 22.1 with 10; a
+// tree of 15 nodes (60 rows) 27.7, 22.4, 20.6 and 26.3.
+constexpr int kLeastFew = 2, kLeastMany = 4, kFewRows = 32;
 
 // One copy of the division's code for all of the walk (a small call waits for
 // instructions to arrive more than for anything else).
@@ -363,8 +366,8 @@ static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r
 // registers, in fp32.  One persistent CTA per SM, since a CTA's products fill its
 // tensor memory and its tiles its shared memory; rows are padded to 128 because
 // bytes bound all but the widest calls.  64 requests of 128 to 8192 positions, 8 KV
-// heads of 128, bf16: single tokens 193 us, trees of 15 nodes (60 rows a head) 201
-// (5.6 and 5.5 TB/s); 8-bit 166 and 184 (3.7 and 3.4), where the chain of a
+// heads of 128, bf16: single tokens 189 us, trees of 15 nodes (60 rows a head) 199
+// (5.8 and 5.6 TB/s); 8-bit 164 and 182 (3.7 and 3.5), where the chain of a
 // stream's scores, weights and outputs bounds it: 8 + 12 products of 64 cycles and
 // 850 cycles of softmax per 32 keys.  4 requests of up to 65536 positions, 448 rows
 // a head, bf16: 184 us, 0.85 PFLOP/s; what the products' warp does between products
@@ -418,7 +421,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
   walk.qrows = C::kRows;
   int total = 0, ctas, w0 = 0, w1 = 0;
   auto share = [&] {
-    ctas = min((int)gridDim.x, (total + kLeast - 1) / kLeast);
+    const int least = a.R * G <= kFewRows ? kLeastFew : kLeastMany;
+    ctas = min((int)gridDim.x, (total + least - 1) / least);
     if ((int)blockIdx.x < ctas) w0 = mul_div(total, blockIdx.x, ctas), w1 = mul_div(total, blockIdx.x + 1, ctas);
   };
   if (a.B <= 4) {  // every thread counts for itself
