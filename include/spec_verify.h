@@ -620,8 +620,11 @@ sv_status kv_read(sv_handle* handle, int32_t B, int32_t R, const int32_t* seq_le
  * A sequence longer than its table, an n_b past R - 1: SV_ERR_STATE in the
  * error word, the request's rows are zeroed.  A block id outside the pool:
  * SV_ERR_STATE, the request's rows are unspecified.
- * The workspace rules are spec_verify's: caller-owned, 256-byte aligned, zero-
- * filled before its first use, left ready for the next call. */
+ * The workspace rules are spec_verify's: caller-owned, 256-byte aligned, left
+ * ready for the next call; its first SV_ATTENTION_CLEAR bytes are zero before
+ * its first use.  Calls that may run at once (on different streams) need one
+ * each, and it outlives the graphs that captured a call with it. */
+#define SV_ATTENTION_CLEAR 4096
 typedef struct {
   int32_t B, R, Hq, dtype;
   const void* q;

@@ -49,6 +49,7 @@ EXPORTS = ("sv_verify_args_size", "sv_create", "sv_destroy", "sv_workspace_size"
 SV_TREE_MAX_NODES = 4096
 SV_KV_BF16, SV_KV_FP32, SV_KV_E4M3 = 0, 1, 2
 E4M3_TAIL = 16     # bytes after an 8-bit entry's codes: its fp32 scale, then zeros
+ATTENTION_CLEAR = 4096  # bytes at an attention workspace's start that are zero before its first use
 APPEND_PAIRS = 1   # rotary pairs (x[2i], x[2i+1]); see SV_APPEND_PAIRS
 
 
@@ -558,7 +559,8 @@ class Verifier:
         self.device = torch.device("cuda", device)
         self.handle = sv_create(device)
         self.workspace = None
-        self.attention_workspace = None
+        self._attention_workspaces = {}  # by raw stream: calls on different streams may run at once
+        self._outgrown = []              # replaced ones, which captured graphs may still use
         self.raw = self.handle.value
         self.path_flags = 0  # kernel selection added to every verify() call
 
@@ -620,17 +622,34 @@ class Verifier:
     def tree_attention(self, q, kv, block_table, seq_len, *, stage=None, mask=None, n_nodes=None, scale=None, layer=0,
                        out=None, stream=None):
         """Attention of the pass's queries over the cache and its own entries;
-        returns out [B, R, Hq, head_dim] (allocated unless given)."""
+        returns out [B, R, Hq, head_dim] (allocated unless given).  Each stream has
+        a workspace of its own; a captured call uses its stream's, or one of the
+        graph's own, so order a graph's replays with one another and with the calls
+        on the stream it was captured on."""
         s = _raw_stream(stream)
-        got = _calls().attention(self.raw, self.attention_workspace, s, q, kv, block_table, seq_len, out, stage, mask,
-                                 n_nodes, scale, layer)
-        if type(got) is int:  # bytes of workspace: the first call, or a larger shape
-            self.attention_workspace = torch.zeros(got, dtype=torch.uint8, device=self.device)
-            if stream is not None:  # zeroed on the current stream
-                stream.wait_stream(torch.cuda.current_stream(self.device))
-            got = _calls().attention(self.raw, self.attention_workspace, s, q, kv, block_table, seq_len, out, stage, mask,
-                                     n_nodes, scale, layer)
+        ws = self._attention_workspaces.get(s)
+        got = _calls().attention(self.raw, ws, s, q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer)
+        if type(got) is int:  # bytes of workspace: the stream's first call, or a larger shape
+            ws = self._attention_workspace(s, stream, got)
+            got = _calls().attention(self.raw, ws, s, q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer)
         return got
+
+    def _attention_workspace(self, raw, stream, need):
+        """A workspace for calls on a stream, allocated and cleared on it, so that
+        it comes after what else used its memory.  The one that it replaces is
+        kept (they double, so all of them together are smaller than the last)."""
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+            old = self._attention_workspaces.get(raw)
+            captured = torch.cuda.is_current_stream_capturing()
+            if old is not None and not captured:
+                need = max(need, 2 * old.numel())
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            ws[:ATTENTION_CLEAR].zero_()
+        if not captured:  # else the graph's memory, which it clears each time that it runs
+            if old is not None:
+                self._outgrown.append(old)
+            self._attention_workspaces[raw] = ws
+        return ws
 
     def adjust_logits(self, logits, *, out=None, V=None, history=None, tokens=None, mask=None, n_nodes=None,
                       rep_penalty=None, presence=None, frequency=None, bias_ids=None, bias_values=None, allowed=None,

@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
 // CTAs that fill the GPU twice.
 constexpr int kTickets = 1024;
 constexpr size_t kTicketBytes = kTickets * 4;
+static_assert(kTicketBytes == SV_ATTENTION_CLEAR, "the tickets are all that a call reads before it wrote it");
 
 // Shares of the keys: enough CTAs to fill the GPU twice, none below 64 keys.
 static int simt_splits(const sv_handle* h, const sv_attention_args* a, int64_t items) {
