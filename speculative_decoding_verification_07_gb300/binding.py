@@ -460,6 +460,20 @@ def _raw_stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _empty_on(stream, like):
+    """An output like a given tensor for a call on an explicit stream: that
+    stream's memory, since the current one may still read what it freed, and
+    handed out again only after what the current stream was given to do with it."""
+    with torch.cuda.stream(stream):
+        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
+def _allocates(stream, given, like) -> bool:
+    return stream is not None and given is None and isinstance(like, torch.Tensor) and like.is_cuda
+
+
 def _raw(handle):
     return handle.value if handle is not None else None
 
@@ -474,6 +488,8 @@ def kv_append(handle, k, v, seq_len, *, kv=None, block_table=None, stage=None, l
     """k, v: [B, R, heads, head_dim]; q, q_out: [B, R, Hq, head_dim]; rope:
     [max_pos, rot_dim / 2, 2] fp32 (see ``rope.rope_table``).  Returns q_out
     (allocated if q is given without it)."""
+    if _allocates(stream, q_out, q):
+        q_out = _empty_on(stream, q)
     return _calls().append(_raw(handle), k, v, seq_len, kv, block_table, stage, layer, q, q_out, rope, interleaved, depth,
                            n_nodes, _raw_stream(stream))
 
@@ -604,13 +620,21 @@ class Verifier:
     def tree_mask(self, parent, n_nodes=None, out=None, stream=None):
         """Ancestor bits [B, N + 1, ceil((N + 1) / 32)] and depths [B, N + 1] of trees."""
         out = out or {}
-        mask, depth = _calls().tree_mask(self.raw, parent, n_nodes, out.get("mask"), out.get("depth"), _raw_stream(stream))
+        args = self.raw, parent, n_nodes, out.get("mask"), out.get("depth"), _raw_stream(stream)
+        if stream is None or out:
+            mask, depth = _calls().tree_mask(*args)
+        else:  # as _empty_on
+            with torch.cuda.stream(stream):
+                mask, depth = _calls().tree_mask(*args)
+            mask.record_stream(torch.cuda.current_stream(self.device))  # depth is of the same allocation
         return dict(mask=mask, depth=depth)
 
     def kv_append(self, k, v, seq_len, *, kv=None, block_table=None, stage=None, layer=0, q=None, q_out=None,
                   rope=None, interleaved=False, depth=None, n_nodes=None, stream=None):
         """Rotate and write the pass's entries; returns the rotated queries
         (allocated unless given; None without q)."""
+        if _allocates(stream, q_out, q):
+            q_out = _empty_on(stream, q)
         return _calls().append(self.raw, k, v, seq_len, kv, block_table, stage, layer, q, q_out, rope, interleaved, depth,
                                n_nodes, _raw_stream(stream))
 
@@ -626,6 +650,8 @@ class Verifier:
         a workspace of its own; a captured call uses its stream's, or one of the
         graph's own, so order a graph's replays with one another and with the calls
         on the stream it was captured on."""
+        if _allocates(stream, out, q):
+            out = _empty_on(stream, q)
         s = _raw_stream(stream)
         ws = self._attention_workspaces.get(s)
         got = _calls().attention(self.raw, ws, s, q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer)

@@ -117,3 +117,43 @@ def test_a_captured_call_keeps_its_workspace(ver, warm):
         assert torch.equal(out, want)
     assert all(k.eq(255).all() for k in keep)
     assert ver.error() == 0
+
+
+@pytest.mark.parametrize("call", ["attention", "append", "mask"])
+def test_outputs_allocated_for_another_stream(ver, call):
+    """An output does not take memory that the current stream still reads."""
+    side = torch.cuda.Stream()
+    q, kv, t, S = job(2, 700, 8, 5)
+    k = torch.randn(2, 8, 2, 128, device=DEV).bfloat16()
+    stage = torch.zeros(2, 8, 1, 2, 2, 128, dtype=torch.bfloat16, device=DEV)
+    parent = torch.zeros(2, 4095, dtype=torch.int32, device=DEV)
+    run = {"attention": lambda **s: ver.tree_attention(q, kv, t, S, **s),
+           "append": lambda **s: ver.kv_append(k, k, S, q=q, stage=stage, **s),
+           "mask": lambda **s: ver.tree_mask(parent, **s)["mask"]}[call]
+    torch.cuda.synchronize()
+    want = run(stream=side)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        held = torch.full((want.untyped_storage().nbytes(),), 7, dtype=torch.uint8, device=DEV)
+        copy = torch.zeros_like(held)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)   # about 10 ms: the read below is still to come
+        copy.copy_(held)
+        del held                        # the current stream's to hand out again
+        got = run(stream=side)
+        torch.cuda.synchronize()
+        assert copy.eq(7).all()
+        assert torch.equal(got, want)
+    # and, used on the current stream, it is not handed out on its own before that use
+    got = run(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    copy = torch.empty_like(got)
+    torch.cuda._sleep(20_000_000)
+    copy.copy_(got)
+    del got
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            torch.full((want.untyped_storage().nbytes(),), 9, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
+    assert ver.error() == 0
