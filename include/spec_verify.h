@@ -506,7 +506,8 @@ sv_status kv_rollback_contig(sv_handle* handle, int32_t B, const int32_t* accept
  *   SV_KV_BF16, SV_KV_FP32  the values themselves;
  *   SV_KV_E4M3              head_dim 8-bit codes (4 exponent, 3 fraction bits)
  *                           followed by 16 bytes: the fp32 scale, then zeros.
- *                           value = code * scale.
+ *                           value = code * scale; scales are 0 .. 2^120 (what
+ *                           reads entries may take any other as it likes).
  * An entry's row is therefore head_dim * 2, head_dim * 4 or head_dim + 16
  * bytes.  The entry points that only move entries (kv_commit_copy,
  * kv_commit_tree, bfl_reserve_cow) take the 8-bit format as a payload of
@@ -562,8 +563,10 @@ sv_status sv_tree_mask(sv_handle* handle, int32_t B, int32_t N, const int32_t* p
  *         uses it: paged entries go to slot S_b + i.
  * seq_len [B] S_b.
  * dst     a paged or staged place.  SV_KV_E4M3: the scale is the smallest power
- *         of two with max|x| <= 448 * scale (1 for an all-zero row, never below
- *         2^-126), codes round x / scale to nearest, ties to even; NaN stays NaN.
+ *         of two with max|x| <= 448 * scale, never below 2^-126 (an all-zero row:
+ *         1 for K, 2^-126 for V, so that its key does not bind the range of the
+ *         attention's weights); codes round x / scale to nearest, ties to even;
+ *         NaN stays NaN.
  * Entries past n_b: nothing is written to dst; their q_out rows are zeroed.
  * A position outside the table's blocks, an n_b past R - 1, or (with rope) a
  * rotary position outside [0, max_pos): SV_ERR_STATE in the error word, that
@@ -615,8 +618,10 @@ sv_status kv_read(sv_handle* handle, int32_t B, int32_t R, const int32_t* seq_le
  * seq_len [B] S_b.
  * Scores, the softmax's sums and the output accumulate in fp32.  With a bf16
  * output the probabilities are rounded to 8 significant bits before they meet
- * V, as a bf16 product needs (9 over 8-bit caches, by three products); the
- * normaliser sums the unrounded ones.
+ * V, as a bf16 product needs; the normaliser sums the unrounded ones.  Over 8-bit
+ * caches it is the products p * (scale of V) that are rounded, to 9 significant
+ * bits within 2^-18 of a row's largest such product; smaller ones are off by
+ * 2^-24 of it (of 2^-115 at least) at most.
  * A sequence longer than its table, an n_b past R - 1: SV_ERR_STATE in the
  * error word, the request's rows are zeroed.  A block id outside the pool:
  * SV_ERR_STATE, the request's rows are unspecified.

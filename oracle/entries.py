@@ -59,7 +59,8 @@ def e4m3_value(code):
 
 
 def e4m3_scale(x):
-    """Smallest power of two s with max|x| <= 448 s over the last axis (1 for zeros)."""
+    """Smallest power of two s with max|x| <= 448 s over the last axis (1 for zeros, as
+    keys are stored; values that are all zeros have 2^-126)."""
     big = np.nanmax(np.abs(np.asarray(x, np.float64)), axis=-1)
     out = np.ones_like(big)
     for at in np.ndindex(big.shape):

@@ -57,7 +57,7 @@ struct TcShape {
   static constexpr int kStep = F8 ? 32 : 16;                 // keys of one product of weights and V
   static constexpr int kRows = kTile * QM;
   static constexpr int kQAll = QM * kQBytes > 32768 ? QM * kQBytes : 32768;  // also holds 128 x 64 outputs, 32 of each half
-  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 3 * kTile * 4 : 0);
+  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 2 * kTile * 4 + 2 * kTile * 4 : 0);
   // tiles held; a slot of K has its keys' tails and V's
   static constexpr int kTails = F8 ? 2 * kTile * kTail : 0, kKBytes = kTileBytes + kTails;
   static constexpr int kRoom = 232448 - 1024 - kMisc - kQAll, kPairs = kRoom / (kTileBytes + kKBytes);
@@ -242,20 +242,37 @@ __device__ __forceinline__ uint32_t less_top(uint32_t v) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Each row's softmax keeps a reference maximum m (log2 units, a whole number, so
-// that rescaling is exact); it moves only when a group of 32 scores exceeds it
-// by more than kSlack, so that outputs in tensor memory are rescaled rarely.  Weights are 2^(kBias + kSlack) at most.  bf16 weights
-// have fp32's range.  Over 8-bit caches a weight starts as fp16, 2^15 at most,
-// and is split in three: the upper byte of an fp16 value is an 8-bit value of 5
-// exponent and 2 fraction bits, and so are the upper bytes of what is left
-// after the first and the second.  Three products of 8 bits then weigh V with
-// 9 bits down to 2^-22 of a row's largest weight and lose nothing above 2^-30.
-// (The format of V's codes, split in two, flushes weights 2^-18 below the
-// largest, and most of a long sequence's mass may lie there.)
-template <bool F8>
-struct TcSoft {
-  static constexpr float kSlack = F8 ? 4.0f : 8.0f, kBias = F8 ? 11.0f : 0.0f;
-};
+// Each row's softmax keeps a reference m of its scores (log2 units, a whole number,
+// so that rescaling is exact), which moves rarely.  Over bf16 caches it moves when
+// a score exceeds it by more than kSlack, and the outputs in tensor memory with it;
+// weights are 2^kSlack at most and have fp32's range.  Their 8 bits are what a bf16
+// product takes: V is bf16, and both operands of a product have one type.
+constexpr float kSlack = 8.0f;
+
+// Over 8-bit caches a weight is p times its key's V scale, so that V's codes are
+// multiplied as they are, and weights have a reference of their own, the largest
+// such product so far: V's scales may differ by any factor, and the sum of p must
+// not depend on them.  (One reference for both lost every other key where a row
+// that weighs much has a scale far above theirs, and the sum overflowed where the
+// first scales were below 2^-112.)  m then moves when 32 p add up to more than
+// kMostSum, so that one maximum is taken per score, the products'.
+//
+// A weight starts as fp16, in 2^(kBias - 1) .. 2^kBias for the largest when its
+// reference is set and kMost at most, and is split in three: the upper byte of an
+// fp16 value is an 8-bit value of 5 exponent and 2 fraction bits, and so are the
+// upper bytes of what is left after the first and the second.  Their smallest step
+// is 2^-16: three products of 8 bits weigh V with 9 bits down to 2^-18 of a row's
+// largest weight, 5 bits at 2^-22, and are off by 2^-27 of it at most (2^-24 after
+// weights were rescaled, below).  (The format of V's codes, split in two, flushes
+// weights 2^-18 below the largest, and most of a long sequence's mass may lie there.)
+constexpr float kBias = 11.0f, kMost = 0x1p15f;
+constexpr float kMostSum = 0x1p7f;   // with scales of 2^120 at most, products stay finite
+// log2 of what a product is multiplied by at most to become a weight: where a row's
+// largest is below 2^-115, weights lose bits rather than the factor its range.
+constexpr float kMaxRaise = 126.0f;
+
+// The whole number above log2(x), -126 for zero and subnormal numbers.
+__device__ __forceinline__ float above_log2(float x) { return (float)((int)(__float_as_uint(x) >> 23) - 126); }
 
 // What non-finite values of V, cleared from a segment's tiles, add to column
 // `col` of entry i's row: 0, or an infinity or NaN.
@@ -299,6 +316,36 @@ static __device__ __noinline__ void hide_unseen(const TcParams& P, int b, int i,
   tmem_wait_st();
 }
 
+// The references (m, weights') of the rows that need others for 32 scores: a whole
+// number at or above the largest score, and above the largest product of p and V's
+// scale, or what kMaxRaise leaves.  Both stay -inf for a row that sees nothing.
+static __device__ __noinline__ float2 references(uint32_t tS, float c, const float* sc, float m, float wr, bool need) {
+  uint32_t x[32];
+  tmem_ld32(tS, x);
+  if (!need) return make_float2(m, wr);
+  float mx = m, top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 ks = *reinterpret_cast<const float4*>(sc + e);
+    const float s[4] = {__uint_as_float(x[e]) * c * ks.x, __uint_as_float(x[e + 1]) * c * ks.y, __uint_as_float(x[e + 2]) * c * ks.z,
+                        __uint_as_float(x[e + 3]) * c * ks.w};
+#pragma unroll
+    for (int z = 0; z < 4; ++z) x[e + z] = __float_as_uint(s[z]);
+    mx = fmaxf(fmaxf(mx, fmaxf(s[0], s[1])), fmaxf(s[2], s[3]));
+  }
+  mx = ceilf(mx);
+  if (mx == -__builtin_huge_valf()) return make_float2(m, wr);
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 vs = *reinterpret_cast<const float4*>(sc + kTile + e);
+    const float v[4] = {vs.x, vs.y, vs.z, vs.w};
+#pragma unroll
+    for (int z = 0; z < 4; ++z) top[z] = fmaxf(top[z], ex2(__uint_as_float(x[e + z]) - mx) * v[z]);
+  }
+  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  return make_float2(mx, fmaxf(fmaxf(wr, mx + above_log2(most)), mx + kBias - kMaxRaise));
+}
+
 // Outputs times each row's f.
 static __device__ __noinline__ void rescale(uint32_t tO, int cols, float f) {
   for (int col = 0; col < cols; col += 16) {
@@ -310,8 +357,8 @@ static __device__ __noinline__ void rescale(uint32_t tO, int cols, float f) {
   }
 }
 
-// Weights times each row's f, a power of two: exact but for 8-bit parts below
-// 2^-16, 2^-26 of a row's largest weight.
+// Weights times each row's f, a power of two: exact but for what the three 8-bit
+// parts lose below 2^-16 each, 3 x 2^-26 of a row's largest weight.
 template <bool F8>
 static __device__ __noinline__ void rescale_weights(uint32_t tW, int cols, float f) {
   tmem_wait_st();
@@ -397,8 +444,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
   int* ints = reinterpret_cast<int*>(misc + 512);  // 0 tensor memory, 1 abort, 2 non-finite entries, 3 last, 4.. walk
   float2* s_ml = reinterpret_cast<float2*>(misc + 1024);  // [256] maxima and sums exchanged or joined
   float* s_qs = reinterpret_cast<float*>(misc + 3072);    // [kRows] row scales of 8-bit queries
-  float* s_sc = s_qs + C::kRows;                          // [kScaleRing][3][128] of a tile's entries: K's scale,
-                                                          // log2 of V's, 1 / V's
+  float* s_sc = s_qs + C::kRows;                          // [kScaleRing][2][128] scales of a tile's entries, K's and V's
+  float* s_wr = s_sc + kScaleRing * 2 * kTile;            // [256] references of 8-bit weights, exchanged
 
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) mbar_init(b_kf + 8 * i, 1), mbar_init(b_ke + 8 * i, QM);
@@ -628,21 +675,21 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
             const int box = tile_of(a, seg, t).staged ? kStageBox : P.box, ring = due % kScaleRing;
             wait(sync, b_kf + 8 * slot, lap & 1);
             const char* tails = kslots + slot * C::kKBytes + C::kTileBytes;
-            float ks[4], lv[4];
-            // scales are finite and positive; what is not (and what the place of a key
-            // past the valid ones held) must not reach rows that do not see the entry
+            float ks[4], vs[4];
+            // scales are 0 .. 2^120; what is not (and what the place of a key past the
+            // valid ones held) must not reach rows that do not see the entry
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int r = lane + 32 * e, in = r & (box - 1);
               const char* tail = tails + ((r - in) * 2 + in) * kTail;  // a box's K, then its V
               const float x = *reinterpret_cast<const float*>(tail), z = *reinterpret_cast<const float*>(tail + box * kTail);
               ks[e] = x > 0.0f && x < kInf ? x : 1.0f;
-              lv[e] = lg2(fminf(fmaxf(z, 1.17549435e-38f), 1.70141183e38f));
+              vs[e] = fminf(fmaxf(z, 0.0f), 0x1p120f);
             }
             if (due >= kScaleRing) wait(sync, b_se + 8 * ring, (due / kScaleRing - 1) & 1);
-            float* sc = s_sc + ring * 3 * kTile + lane;
+            float* sc = s_sc + ring * 2 * kTile + lane;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[32 * e] = ks[e], sc[kTile + 32 * e] = lv[e], sc[2 * kTile + 32 * e] = ex2(-lv[e]);
+            for (int e = 0; e < 4; ++e) sc[32 * e] = ks[e], sc[kTile + 32 * e] = vs[e];
             fence_async_smem();  // the tails have been read before their place is loaded again
             __syncwarp();
             if (lane == 0) mbar_arrive(b_sf + 8 * ring);
@@ -721,7 +768,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               }
 #pragma unroll
               for (int o = 1; o < kChunks; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-              const float qs = e4m3_scale(m), inv = ex2(-lg2(qs));
+              const float qs = e4m3_scale(m, 1.0f), inv = ex2(-lg2(qs));
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -750,7 +797,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       // positive, so that what is not seen stays -inf when it is scaled
       const float c = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? s_qs[(QM == 2 ? st * kTile : 0) + row] : 1.0f), 1e-37f);
       const uint64_t c2 = pair(c, c);
-      float m = -kInf, l = 0.0f;
+      // wr: reference of 8-bit weights, log2 units; raise = 2^(kBias + m - wr)
+      float m = -kInf, l = 0.0f, wr = -kInf, raise = 0.0f;
       for (int u = st; u < units; u += 2) {
         const int tt = QM == 2 ? u >> 1 : u;
         const TcTile k = tile_of(a, seg, seg.t0 + tt);
@@ -761,7 +809,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         if (F8) wait(sync, b_sf + 8 * (kt % kScaleRing), (kt / kScaleRing) & 1);
         if (quad == 0 && lane == 0) mbar_arrive(b_ke + 8 * (kt % C::kK));  // the scores' product is done with its keys, and their tails are read
         tc_fence_after();
-        const float* sc = s_sc + (kt % kScaleRing) * 3 * kTile;
+        const float* sc = s_sc + (kt % kScaleRing) * 2 * kTile;
         if (warp_live) {
           const int chunks = (k.valid + 31) / 32, ch_e = min(ch_b, chunks);
           if (!full) hide_unseen(P, seg.b, i, seg.X.n, k.prefix, k.valid, k.u0, ch_a, ch_e, tS);
@@ -779,56 +827,89 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               tmem_st(tS + kW * ch, w);
               continue;
             }
-            uint32_t x[32];
-            uint64_t v[16];
-            tmem_ld32(tS + 32 * ch, x);
+            if (F8) {
+              // Weights by the references so far; where their sum or the largest shows
+              // that one is too low, once more after they have moved.
+              bool bad = m == -kInf, moved = false;
+              uint64_t gs[2];
+#pragma unroll 1
+              while (true) {
+                if (__any_sync(0xFFFFFFFFu, bad)) {
+                  const float2 n = references(tS + 32 * ch, c, sc + 32 * ch, m, wr, bad);
+                  const float f = n.x > m ? ex2(m - n.x) : 1.0f, fw = n.y > wr ? ex2(wr - n.y) : 1.0f;
+                  l *= f, ls[0] = mul2(ls[0], pair(f, f)), ls[1] = mul2(ls[1], pair(f, f));
+                  m = n.x, wr = n.y;
+                  raise = m == -kInf ? 0.0f : ex2(kBias + m - wr);
+                  if (__any_sync(0xFFFFFFFFu, fw != 1.0f)) {
+                    if (ch > ch_a) rescale_weights<F8>(tS + kW * ch_a, kW * (ch - ch_a), fw);
+                    if (u >= 2) rescale(tO, D, fw);  // these scores were issued, and are done, after the last outputs
+                  }
+                  moved = true;
+                }
+                uint32_t x[32];
+                tmem_ld32(tS + 32 * ch, x);
+                const float base = m == -kInf ? -kInf : -m;  // nothing seen: p is 0
+                const uint64_t base2 = pair(base, base), raise2 = pair(raise, raise);
+                float t4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                gs[0] = gs[1] = 0;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              v[e] = pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-              v[e + 1] = pair(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3]));
-              if (F8) {
-                const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(sc + 32 * ch + 2 * e);
-                const ulonglong2 lv = *reinterpret_cast<const ulonglong2*>(sc + kTile + 32 * ch + 2 * e);
-                v[e] = fma2(mul2(v[e], c2), ks.x, lv.x), v[e + 1] = fma2(mul2(v[e + 1], c2), ks.y, lv.y);  // -inf stays
+                for (int e = 0; e < 16; e += 2) {
+                  const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(sc + 32 * ch + 2 * e);
+                  const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(sc + kTile + 32 * ch + 2 * e);
+                  float2 y[2];
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    const uint64_t s2 = mul2(pair(__uint_as_float(x[2 * (e + z)]), __uint_as_float(x[2 * (e + z) + 1])), c2);
+                    const float2 d = unpair(fma2(s2, z ? ks.y : ks.x, base2));  // -inf stays
+                    const uint64_t p2 = pair(ex2(d.x), ex2(d.y));
+                    gs[z] = add2(gs[z], p2);
+                    y[z] = unpair(mul2(mul2(p2, z ? vs.y : vs.x), raise2));
+                    float& top = t4[(e & 2) + z];
+                    top = fmaxf(top, fmaxf(y[z].x, y[z].y));
+                  }
+                  const __half2 h0 = __floats2half2_rn(y[0].x, y[0].y), h1 = __floats2half2_rn(y[1].x, y[1].y);
+                  uint32_t a0 = *reinterpret_cast<const uint32_t*>(&h0), a1 = *reinterpret_cast<const uint32_t*>(&h1);
+                  w[e / 2] = __byte_perm(a0, a1, 0x7531);
+                  a0 = less_top(a0), a1 = less_top(a1);
+                  w[8 + e / 2] = __byte_perm(a0, a1, 0x7531);
+                  a0 = less_top(a0) + 0x00800080u, a1 = less_top(a1) + 0x00800080u;
+                  w[16 + e / 2] = __byte_perm(a0, a1, 0x7531);
+                }
+                const float2 g2 = unpair(add2(gs[0], gs[1]));
+                bad = !(g2.x + g2.y <= kMostSum) || fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) > kMost;
+                if (moved || !__any_sync(0xFFFFFFFFu, bad)) break;
               }
-            }
-            float mx4[4] = {-kInf, -kInf, -kInf, -kInf};
+              ls[0] = add2(ls[0], gs[0]), ls[1] = add2(ls[1], gs[1]);
+            } else {
+              uint32_t x[32];
+              uint64_t v[16];
+              tmem_ld32(tS + 32 * ch, x);
+              float mx4[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 y = unpair(v[e]);
-              mx4[e & 3] = fmaxf(mx4[e & 3], fmaxf(y.x, y.y));
-            }
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * (F8 ? 1.0f : c);
-            if (__any_sync(0xFFFFFFFFu, mx > m + TcSoft<F8>::kSlack)) {
-              const float mn = fmaxf(m, ceilf(mx)), f = mn == -kInf ? 1.0f : ex2(m - mn);
-              m = mn, l *= f;
-              const uint64_t f2 = pair(f, f);
-              ls[0] = mul2(ls[0], f2), ls[1] = mul2(ls[1], f2);
-              if (ch > ch_a) rescale_weights<F8>(tS + kW * ch_a, kW * (ch - ch_a), f);
-              if (u >= 2) rescale(tO, D, f);  // these scores were issued, and are done, after the last outputs
-            }
-            const float base = (m == -kInf ? 0.0f : m) - TcSoft<F8>::kBias;
-            const uint64_t base2 = pair(-base, -base);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-#pragma unroll
-              for (int z = e; z < e + 2; ++z) {
-                v[z] = F8 ? add2(v[z], base2) : fma2(v[z], c2, base2);
-                const float2 y = unpair(v[z]);
-                v[z] = pair(ex2(y.x), ex2(y.y));
+              for (int e = 0; e < 16; ++e) {
+                v[e] = pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                mx4[e & 3] = fmaxf(mx4[e & 3], fmaxf(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])));
               }
-              const float2 y0 = unpair(v[e]), y1 = unpair(v[e + 1]);
-              if (F8) {
-                const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(sc + 2 * kTile + 32 * ch + 2 * e);
-                ls[0] = fma2(v[e], iv.x, ls[0]), ls[1] = fma2(v[e + 1], iv.y, ls[1]);
-                const __half2 h0 = __floats2half2_rn(y0.x, y0.y), h1 = __floats2half2_rn(y1.x, y1.y);
-                uint32_t a0 = *reinterpret_cast<const uint32_t*>(&h0), a1 = *reinterpret_cast<const uint32_t*>(&h1);
-                w[e / 2] = __byte_perm(a0, a1, 0x7531);
-                a0 = less_top(a0), a1 = less_top(a1);
-                w[8 + e / 2] = __byte_perm(a0, a1, 0x7531);
-                a0 = less_top(a0) + 0x00800080u, a1 = less_top(a1) + 0x00800080u;
-                w[16 + e / 2] = __byte_perm(a0, a1, 0x7531);
-              } else {
+              const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+              if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
+                const float mn = fmaxf(m, ceilf(mx)), f = mn == -kInf ? 1.0f : ex2(m - mn);
+                m = mn, l *= f;
+                const uint64_t f2 = pair(f, f);
+                ls[0] = mul2(ls[0], f2), ls[1] = mul2(ls[1], f2);
+                if (ch > ch_a) rescale_weights<F8>(tS + kW * ch_a, kW * (ch - ch_a), f);
+                if (u >= 2) rescale(tO, D, f);  // these scores were issued, and are done, after the last outputs
+              }
+              const float base = m == -kInf ? 0.0f : m;
+              const uint64_t base2 = pair(-base, -base);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+#pragma unroll
+                for (int z = e; z < e + 2; ++z) {
+                  v[z] = fma2(v[z], c2, base2);
+                  const float2 y = unpair(v[z]);
+                  v[z] = pair(ex2(y.x), ex2(y.y));
+                }
+                const float2 y0 = unpair(v[e]), y1 = unpair(v[e + 1]);
                 ls[0] = add2(ls[0], v[e]), ls[1] = add2(ls[1], v[e + 1]);
                 w[e] = pack_bf16(y0.x, y0.y);
                 w[e + 1] = pack_bf16(y1.x, y1.y);
@@ -867,11 +948,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       }
       const bool both = QM == 1 && units > 1;  // stream 1 had a tile too
       if (QM == 1) s_ml[st * kTile + row] = make_float2(m, l);
+      const float unit = F8 ? wr - kBias : m;  // of the outputs, log2
+      if (F8 && QM == 1) s_wr[st * kTile + row] = unit;
       tc_fence_before();
       named_barrier(1, 256);
       tc_fence_after();
       const bool spoiled = *reinterpret_cast<volatile int*>(&ints[2]) != 0;
       float f0 = 1.0f, f1 = 0.0f;  // of this copy's outputs in the two streams
+      if (F8 && QM == 2) f0 = ex2(unit - (m == -kInf ? 0.0f : m));
       if (QM == 1) {
         float M = -kInf, L = 0.0f;
         const int parts = both ? 2 * copies : copies;  // a copy every `apart` rows, the second stream after the first
@@ -884,7 +968,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         const float Mb = M == -kInf ? 0.0f : M;
 #pragma unroll
         for (int x = 0; x < 8; ++x) L += o[x].y * ex2(o[x].x - Mb);
-        f0 = ex2(s_ml[row].x - Mb), f1 = both ? ex2(s_ml[kTile + row].x - Mb) : 0.0f;
+        f0 = ex2((F8 ? s_wr[row] : s_ml[row].x) - Mb);
+        f1 = both ? ex2((F8 ? s_wr[kTile + row] : s_ml[kTile + row].x) - Mb) : 0.0f;
         m = M, l = L;
       }
       const int c_first = QM == 1 ? st * (D / 2) : 0;

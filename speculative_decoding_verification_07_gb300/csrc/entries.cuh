@@ -123,10 +123,13 @@ __device__ __forceinline__ float entry_scale(const char* row, int format, int he
 // [1, 2) and 448 = 1.75 * 2^8, so 2^(x - 8), or 2^(x - 7) where f > 1.75.  A
 // power of two makes x / scale exact (but for underflow), so codes do not
 // depend on how the division rounds, and the format's relative precision is
-// the same at every scale.  Clamped to normal numbers; infinity gives 2^120.
-__device__ __forceinline__ float e4m3_scale(float amax) {
+// the same at every scale.  Clamped to normal numbers; infinity gives 2^120, zero
+// what the caller says.
+constexpr float kLeastScale = 0x1p-126f;
+
+__device__ __forceinline__ float e4m3_scale(float amax, float of_zeros) {
   const uint32_t u = __float_as_uint(amax);
-  if (u == 0) return 1.0f;
+  if (u == 0) return of_zeros;
   const int e = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u && u < 0x7F800000u ? 1 : 0);
   return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
 }

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const __gr
       float m = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));  // NaN is left out
-      const float scale = e4m3_scale(__uint_as_float(__reduce_max_sync(L.group, __float_as_uint(m))));
+      const float scale = e4m3_scale(__uint_as_float(__reduce_max_sync(L.group, __float_as_uint(m))), r < H ? 1.0f : kLeastScale);
       const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale));  // scales are 2^-126 .. 2^120
       uint32_t w[2];
 #pragma unroll
