@@ -828,9 +828,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               continue;
             }
             if (F8) {
-              // Weights by the references so far; where their sum or the largest shows
-              // that one is too low, once more after they have moved.
-              bool bad = m == -kInf, moved = false;
+              // Weights by the references so far; where a row's sum or largest shows that
+              // one is too low, once more after they have moved.
+              bool bad = m == -kInf, again = false;
               uint64_t gs[2];
 #pragma unroll 1
               while (true) {
@@ -844,7 +844,6 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
                     if (ch > ch_a) rescale_weights<F8>(tS + kW * ch_a, kW * (ch - ch_a), fw);
                     if (u >= 2) rescale(tO, D, fw);  // these scores were issued, and are done, after the last outputs
                   }
-                  moved = true;
                 }
                 uint32_t x[32];
                 tmem_ld32(tS + 32 * ch, x);
@@ -877,7 +876,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
                 }
                 const float2 g2 = unpair(add2(gs[0], gs[1]));
                 bad = !(g2.x + g2.y <= kMostSum) || fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) > kMost;
-                if (moved || !__any_sync(0xFFFFFFFFu, bad)) break;
+                if (again || !__any_sync(0xFFFFFFFFu, bad)) break;
+                again = true;
               }
               ls[0] = add2(ls[0], gs[0]), ls[1] = add2(ls[1], gs[1]);
             } else {

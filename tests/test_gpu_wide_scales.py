@@ -108,6 +108,15 @@ def test_scales_of_all_sizes(ver, G, D, course):
     check(ver, np.repeat(u[None], G, 0) * rng.choice([1.0, -0.5], (G, 1)), k, v)
 
 
+@pytest.mark.parametrize("G", [1, 4, 31, 40, 100, 150, 250])
+@pytest.mark.parametrize("n", [50, 90, 700])
+def test_steep_scores_beside_rows_that_see_nothing(ver, G, n):
+    """Heads that fill no whole warp: the others' references move all the same."""
+    rng = np.random.default_rng(G + n)
+    q, k = 3 * rng.standard_normal((G, 128)), rng.standard_normal((n, 128))
+    check(ver, q, k * np.where(np.arange(n) % 40 > 35, 1.5, 0.5)[:, None], rng.standard_normal((n, 128)))
+
+
 @pytest.mark.parametrize("G", [4, 40, 150])
 @pytest.mark.parametrize("n", [20, 500])
 def test_zero_filled_entries(ver, G, n):
