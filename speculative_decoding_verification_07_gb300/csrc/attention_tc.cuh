@@ -676,14 +676,15 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
             wait(sync, b_kf + 8 * slot, lap & 1);
             const char* tails = kslots + slot * C::kKBytes + C::kTileBytes;
             float ks[4], vs[4];
-            // scales are 0 .. 2^120; what is not (and what the place of a key past the
-            // valid ones held) must not reach rows that do not see the entry
+            // Scales are 0 .. 2^120; what is not (and what the place of a key past the
+            // valid ones held) must not reach rows that do not see the entry.  K's is
+            // 2^-126 at least (0 counts as that), so that an unseen score's -inf stays.
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int r = lane + 32 * e, in = r & (box - 1);
               const char* tail = tails + ((r - in) * 2 + in) * kTail;  // a box's K, then its V
               const float x = *reinterpret_cast<const float*>(tail), z = *reinterpret_cast<const float*>(tail + box * kTail);
-              ks[e] = x > 0.0f && x < kInf ? x : 1.0f;
+              ks[e] = fminf(fmaxf(x, kLeastScale), 0x1p120f);
               vs[e] = fminf(fmaxf(z, 0.0f), 0x1p120f);
             }
             if (due >= kScaleRing) wait(sync, b_se + 8 * ring, (due / kScaleRing - 1) & 1);

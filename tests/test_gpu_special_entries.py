@@ -1,0 +1,50 @@
+"""Infinities, NaN and zeros where entries are rotated, decoded and attended."""
+
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import entries as E
+from speculative_decoding_verification_07_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def ver():
+    if not os.path.exists(binding.LIB_PATH):
+        from speculative_decoding_verification_07_gb300 import build
+        build.build()
+    v = binding.Verifier(0)
+    yield v
+    v.close()
+
+
+def ints(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("G", [4, 40, 150])
+def test_a_scale_of_zero_is_zero(ver, G):
+    """value = code * scale: keys of scale 0 score 0 whatever their codes, values
+    of scale 0 are 0.  Held to the bound of the attention's own tests."""
+    D, n = 128, 50
+    rng = np.random.default_rng(G)
+    g = torch.Generator(DEV).manual_seed(G)
+    k, v = torch.randn(2, 1, n, 1, D, generator=g, device=DEV).bfloat16()
+    kv = torch.zeros(4, 1, 2, 1, 16, D + E.TAIL, dtype=torch.uint8, device=DEV)
+    t = ints([[3, 0, 1, 2]])
+    ver.kv_append(k, v, ints([0]), kv=kv, block_table=t)
+    for which, i in ((0, 3), (0, 40), (1, 7), (1, 33)):
+        kv[t[0, i // 16], 0, which, 0, i % 16, D:] = 0
+    held = ver.kv_read(torch.empty(1, n, 2, 1, D, device=DEV), ints([0]), kv=kv, block_table=t)[0, :, :, 0].double().cpu().numpy()
+    assert not held[[3, 40], 0].any() and not held[[7, 33], 1].any()
+    q = torch.tensor(rng.standard_normal((G, D)) * 3, dtype=torch.bfloat16, device=DEV)
+    got = ver.tree_attention(q[None, None], kv, t, ints([n - 1]))[0, 0].double().cpu().numpy()
+    assert ver.error() == 0
+    for h in range(G):
+        o, size, _ = E.attend(q[h].double().cpu().numpy(), held[:, 0], held[:, 1], np.ones(n, bool), D ** -0.5)
+        assert (np.abs(got[h] - o) <= (2.0 ** -8 + 2.0 ** -10) * size + 2.0 ** -8 * np.abs(o)).all()
