@@ -769,7 +769,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               }
 #pragma unroll
               for (int o = 1; o < kChunks; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-              const float qs = e4m3_scale(m, 1.0f), inv = ex2(-lg2(qs));
+              const float qs = e4m3_scale(m, 1.0f);
+              // 1 / qs by its exponent; an infinite query's codes are NaN, as its scores
+              const float inv = m < kInf ? __uint_as_float(0x7F000000u - __float_as_uint(qs)) : __uint_as_float(0x7FC00000u);
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {

@@ -48,3 +48,26 @@ def test_a_scale_of_zero_is_zero(ver, G):
     for h in range(G):
         o, size, _ = E.attend(q[h].double().cpu().numpy(), held[:, 0], held[:, 1], np.ones(n, bool), D ** -0.5)
         assert (np.abs(got[h] - o) <= (2.0 ** -8 + 2.0 ** -10) * size + 2.0 ** -8 * np.abs(o)).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G", [4, 40, 150])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_query_that_is_not_finite_gives_nan(ver, fmt, G, bad):
+    """Its scores are infinite or NaN, with one infinity of each sign among them."""
+    D, n, H = 128, 40, 1
+    g = torch.Generator(DEV).manual_seed(G)
+    k = torch.randn(1, n, H, D, generator=g, device=DEV).bfloat16()
+    k[..., 5] *= 2.0 ** -12  # codes of 2^-3 and less: half of the largest number times them is finite
+    row = D + E.TAIL if fmt == "e4m3" else D
+    kv = torch.zeros(3, 1, 2, H, 16, row, dtype=torch.uint8 if fmt == "e4m3" else torch.bfloat16, device=DEV)
+    t = ints([[2, 0, 1]])
+    ver.kv_append(k, k, ints([0]), kv=kv, block_table=t)
+    q = torch.randn(1, 1, G, D, generator=g, device=DEV).bfloat16()
+    want = ver.tree_attention(q, kv, t, ints([n - 1]))
+    q[0, 0, 2, 5] = bad
+    got = ver.tree_attention(q, kv, t, ints([n - 1]))
+    assert ver.error() == 0
+    assert torch.isnan(got[0, 0, 2]).all()
+    others = [h for h in range(G) if h != 2]
+    assert torch.equal(got[0, 0, others], want[0, 0, others])
