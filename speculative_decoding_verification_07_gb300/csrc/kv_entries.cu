@@ -64,10 +64,11 @@ __device__ __forceinline__ void values8(const Raw8<F32>& r, float (&x)[8]) {
 // memory (halves that end inside a lane's columns).
 enum Turn { kNone, kPairs, kLanes, kMemory };
 
-// x' = x cos + other * sin, with the sign of the pair's half in sin; columns
-// past the rotated ones have cos 1, sin 0.
+// x' = x cos + other * sin in the first `turned` of the eight columns, with the
+// sign of the pair's half in sin; the others stay as they are, whatever they and
+// their neighbours hold.
 template <bool F32, int TURN>
-__device__ __forceinline__ void turn8(float (&x)[8], const Raw8<F32>& now, const char* row, int d0, int half, int other, uint32_t group,
+__device__ __forceinline__ void turn8(float (&x)[8], const Raw8<F32>& now, const char* row, int d0, int half, int turned, int other, uint32_t group,
                                       const float (&co)[8], const float (&si)[8]) {
   if (TURN == kNone) return;
   float o[8];
@@ -90,7 +91,7 @@ __device__ __forceinline__ void turn8(float (&x)[8], const Raw8<F32>& now, const
     __syncwarp(group);  // queries may be rotated in place: every lane has its operands
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = x[e] * co[e] + o[e] * si[e];
+  for (int e = 0; e < 8; ++e) x[e] = (TURN == kLanes ? 0 : e) < turned ? x[e] * co[e] + o[e] * si[e] : x[e];
 }
 
 // One CTA per (request, entry): its queries, keys and values are rows of
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const __gr
     for (int h = L.slot; h < Hq; h += L.nslots) store8<F32>(out + h * os, 0, zero);
     return;
   }
-  const int half = a.rot_dim >> 1;
+  const int half = a.rot_dim >> 1, turned = a.rot_dim - d0;
   const int other = TURN == kLanes && d0 < a.rot_dim ? (threadIdx.x & 31) + (d0 < half ? half >> 3 : -(half >> 3)) : threadIdx.x & 31;
   float co[8], si[8];
   if (TURN != kNone) {
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const __gr
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int d = d0 + e;
-      co[e] = 1.0f, si[e] = 0.0f;
+      co[e] = si[e] = 0.0f;
       if (d < a.rot_dim) {
         const float2 t = cs[TURN == kPairs ? d >> 1 : d < half ? d : d - half];
         co[e] = t.x, si[e] = (TURN == kPairs ? !(d & 1) : d < half) ? -t.y : t.y;
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const __gr
       float x[8];
       const Raw8<F32>& now = u ? q1 : q0;
       values8<F32>(now, x);
-      turn8<F32, TURN>(x, now, q + hu * qs, d0, half, other, L.group, co, si);
+      turn8<F32, TURN>(x, now, q + hu * qs, d0, half, turned, other, L.group, co, si);
       store8<F32>(out + hu * os, 0, x);
     }
   }
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const __gr
     if (r != L.slot) kv0 = raw8<F32>(kv_row(r) + d0 * eb);
     float x[8];
     values8<F32>(kv0, x);
-    if (r < H) turn8<F32, TURN>(x, kv0, kv_row(r), d0, half, other, L.group, co, si);
+    if (r < H) turn8<F32, TURN>(x, kv0, kv_row(r), d0, half, turned, other, L.group, co, si);
     char* row = static_cast<char*>(dst.data) + off + r * step;
     if (dst.format == SV_KV_FP32) {
       store8<true>(row, d0, x);

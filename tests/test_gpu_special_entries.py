@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import entries as E
-from speculative_decoding_verification_07_gb300 import binding
+from speculative_decoding_verification_07_gb300 import binding, rope
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -71,3 +71,25 @@ def test_a_query_that_is_not_finite_gives_nan(ver, fmt, G, bad):
     assert torch.isnan(got[0, 0, 2]).all()
     others = [h for h in range(G) if h != 2]
     assert torch.equal(got[0, 0, others], want[0, 0, others])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rot,pairs", [(16, False), (16, True), (6, False), (6, True), (12, True)])
+def test_columns_past_the_rotation_pass_unchanged(ver, dtype, rot, pairs):
+    """Bit for bit, whatever they and their neighbours hold (a NaN: any NaN)."""
+    D, R, H = 64, 5, 2
+    g = torch.Generator(DEV).manual_seed(rot)
+    x = torch.randn(1, R, H, D, generator=g, device=DEV).to(dtype)
+    special = torch.tensor([float("inf"), -float("inf"), float("nan"), -0.0, 0.0, 3.0, 1e-39, float("inf")], dtype=dtype, device=DEV)
+    x[:, 1:, :, rot:] = special.repeat(D)[:D - rot]
+    x[:, 2:, :, rot:] = special.repeat(D)[1:D - rot + 1]
+    stage = torch.zeros(1, R, 1, 2, H, D, dtype=dtype, device=DEV)
+    q = ver.kv_append(x, x, ints([3]), q=x, stage=stage, interleaved=pairs, rope=rope.rope_table(16, rope.rope_frequencies(rot)))
+    assert ver.error() == 0
+    word = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    for y in (q, stage[:, :, 0, 0]):
+        got, want = y[..., rot:].contiguous(), x[..., rot:].contiguous()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got.view(word)[~torch.isnan(got)], want.view(word)[~torch.isnan(want)])
+        assert torch.isfinite(y[..., :rot]).all()
+        assert not torch.equal(y[..., :rot], x[..., :rot])
