@@ -11,6 +11,7 @@
 #include <cmath>
 #include <stdexcept>
 #include <string>
+#include <type_traits>
 
 #include "spec_verify.h"
 
@@ -68,28 +69,35 @@ T* ptr(const at::Tensor& t) {
   return static_cast<T*>(t.data_ptr());
 }
 
-bool word(const at::Tensor& t) {
-  return t.scalar_type() == at::kInt || t.scalar_type() == at::kFloat || t.scalar_type() == at::kUInt32;
+// Whether a tensor holds what a call reads: fp32, int32, or words of bits.
+template <class T>
+bool holds(const at::Tensor& t) {
+  if (std::is_same_v<std::remove_const_t<T>, float>) return t.scalar_type() == at::kFloat;
+  return t.scalar_type() == at::kInt || (std::is_same_v<std::remove_const_t<T>, uint32_t> && t.scalar_type() == at::kUInt32);
+}
+template <class T>
+std::string type_name() {
+  return std::is_same_v<std::remove_const_t<T>, float> ? "fp32" : std::is_same_v<std::remove_const_t<T>, uint32_t> ? "int32 or uint32" : "int32";
 }
 
-// An optional contiguous 4-byte array of at least n values.
+// An optional contiguous array of at least n values.
 template <class T>
 T* vec(PyObject* o, int64_t n, const char* name) {
   Arg t(o, name);
   if (!t) return nullptr;
-  if (!word(*t.t) || !t->is_contiguous() || t->numel() < n)
-    refuse(std::string(name) + ": a contiguous 4-byte tensor of at least " + std::to_string(n) + " values expected");
+  if (!holds<T>(*t.t) || !t->is_contiguous() || t->numel() < n)
+    refuse(std::string(name) + ": a contiguous " + type_name<T>() + " tensor of at least " + std::to_string(n) + " values expected");
   return ptr<T>(*t.t);
 }
 
-// An optional contiguous 4-byte [rows][ld] (or [..][ld]) table.
+// An optional contiguous [rows][ld] (or [..][ld]) table.
 template <class T>
 T* table(PyObject* o, int64_t rows, int64_t* ld, const char* name) {
   Arg t(o, name);
   *ld = 0;
   if (!t) return nullptr;
-  if (!word(*t.t) || !t->is_contiguous() || t->dim() < 2 || t->numel() != rows * t->size(-1))
-    refuse(std::string(name) + ": a contiguous 4-byte [" + std::to_string(rows) + "][..] tensor expected");
+  if (!holds<T>(*t.t) || !t->is_contiguous() || t->dim() < 2 || t->numel() != rows * t->size(-1))
+    refuse(std::string(name) + ": a contiguous " + type_name<T>() + " [" + std::to_string(rows) + "][..] tensor expected");
   *ld = t->size(-1);
   return ptr<T>(*t.t);
 }
