@@ -90,6 +90,17 @@ T* vec(PyObject* o, int64_t n, const char* name) {
   return ptr<T>(*t.t);
 }
 
+// An optional contiguous [rows][cols] array: one row of another width would shift
+// all that follow.
+template <class T>
+T* grid(PyObject* o, int64_t rows, int64_t cols, const char* name) {
+  Arg t(o, name);
+  if (!t) return nullptr;
+  if (!holds<T>(*t.t) || !t->is_contiguous() || t->numel() != rows * cols || (t->dim() > 1 && t->size(-1) != cols))
+    refuse(std::string(name) + ": a contiguous " + type_name<T>() + " [" + std::to_string(rows) + "][" + std::to_string(cols) + "] tensor expected");
+  return ptr<T>(*t.t);
+}
+
 // An optional contiguous [rows][ld] (or [..][ld]) table.
 template <class T>
 T* table(PyObject* o, int64_t rows, int64_t* ld, const char* name) {
@@ -189,7 +200,7 @@ PyObject* tree_mask(PyObject* const* a) {
     depth = both.as_strided({B, N + 1}, {N + 1, 1}, n * W);
   } else {
     table<uint32_t>(a[3], n, &ld, "mask");
-    if (!vec<int32_t>(a[4], n, "depth")) refuse("depth: tensor expected");
+    if (!grid<int32_t>(a[4], B, N + 1, "depth")) refuse("depth: tensor expected");
     mask = THPVariable_Unpack(a[3]), depth = THPVariable_Unpack(a[4]);
   }
   done("sv_tree_mask", api.tree_mask(handle_of(a[0]), (int)B, (int)N, ptr<int32_t>(*parent.t), vec<int32_t>(a[2], B, "n_nodes"),
@@ -233,7 +244,7 @@ PyObject* append(PyObject* const* a) {
       p.rope = ptr<float>(*rope.t), p.max_pos = (int)rope->size(0), p.rot_dim = 2 * (int)rope->size(1);
     }
     if (PyObject_IsTrue(a[11])) p.flags = SV_APPEND_PAIRS;
-    p.depth = vec<int32_t>(a[12], B * R, "depth");
+    p.depth = grid<int32_t>(a[12], B, R, "depth");
     p.seq_len = vec<int32_t>(a[3], B, "seq_len");
     p.n_nodes = vec<int32_t>(a[13], B, "n_nodes");
     done("kv_append", api.append(handle_of(a[0]), &p, stream_of(a[14])));
@@ -328,7 +339,7 @@ PyObject* logits(PyObject* const* a) {
   p.logits = ptr(*x.t), p.out = ptr(*y.t), p.ld = x->stride(1), p.out_ld = y->stride(1);
   int64_t values;
   p.history = table<int32_t>(a[4], B, &p.history_ld, "history");
-  p.tokens = vec<int32_t>(a[5], B * (R - 1), "tokens");
+  p.tokens = grid<int32_t>(a[5], B, R - 1, "tokens");
   p.mask = table<uint32_t>(a[6], B * R, &p.mask_ld, "mask");
   p.n_nodes = vec<int32_t>(a[7], B, "n_nodes");
   p.rep_penalty = vec<float>(a[8], B, "rep_penalty");

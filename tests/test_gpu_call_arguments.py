@@ -75,3 +75,27 @@ def test_factors_are_fp32(ver, name, shape):
     for dtype in (I32, torch.uint32, torch.float64, torch.bfloat16):
         with pytest.raises(ValueError):
             calls(ver, {name: other(shape, dtype)})
+
+
+def test_tables_of_another_width_are_refused(ver):
+    """Padded draft buffers would be read as rows of R - 1 (or R) values."""
+    B, R, D = 2, 4, 64
+    x = torch.zeros(B, R, 64, device=DEV)
+    k = torch.zeros(B, R, 1, D, device=DEV)
+    stage = torch.zeros(B, R, 1, 2, 1, D, device=DEV)
+    zero = torch.zeros(B, dtype=torch.int32, device=DEV)
+    for w in (R - 2, R, R + 5):
+        with pytest.raises(ValueError):
+            ver.adjust_logits(x, tokens=torch.zeros(B, w, dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError):
+        ver.adjust_logits(x, tokens=torch.zeros(R - 1, B, dtype=torch.int32, device=DEV))
+    ver.adjust_logits(x, tokens=torch.zeros(B, R - 1, dtype=torch.int32, device=DEV))
+    for w in (R - 1, R + 1):
+        with pytest.raises(ValueError):
+            ver.kv_append(k, k, zero, stage=stage, depth=torch.zeros(B, w, dtype=torch.int32, device=DEV))
+    ver.kv_append(k, k, zero, stage=stage, depth=torch.zeros(B, R, dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError):  # depths of a mask call, where they are given
+        ver.tree_mask(torch.zeros(2, B, dtype=torch.int32, device=DEV), out=dict(mask=torch.zeros(2, B + 1, 1, dtype=torch.int32, device=DEV),
+                                                               depth=torch.zeros(2, B + 4, dtype=torch.int32, device=DEV)))
+    torch.cuda.synchronize()
+    assert ver.error() == 0
