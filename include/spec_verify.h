@@ -667,7 +667,7 @@ sv_status sv_tree_attention(sv_handle* handle, const sv_attention_args* args, vo
  * request's rows are copied unchanged.
  * logits, out [B][R][ld] (ld and out_ld in elements, multiples of 16 bytes;
  * out may be logits).  Elements past V are not written.
- * history_ld, bias_ld <= 2^24. */
+ * history_ld, bias_ld <= 2^24, R <= 2^22. */
 typedef struct {
   int32_t B, R, V, dtype;
   const void* logits;

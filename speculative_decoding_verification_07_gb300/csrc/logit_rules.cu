@@ -14,7 +14,8 @@ struct RuleSmem {
   float bias[kSlice];
   uint16_t listed[kSlice]; // tokens with a count or a bias
   uint8_t known[kSlice];   // in the list
-  uint16_t node[kNodes], token[kNodes];  // drafted nodes whose token is in this slice
+  int node[kNodes];  // drafted nodes whose token is in this slice, and the token
+  uint16_t token[kNodes];
   int n, n_path;           // listed tokens, such nodes (more than kNodes: look through all)
 };
 
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
       const int x = a.tokens[(int64_t)b * (a.R - 1) + j] - v0;
       if (x >= 0 && x < len) {
         const int q = atomicAdd(&s.n_path, 1);
-        if (q < kNodes) s.node[q] = (uint16_t)(j + 1), s.token[q] = (uint16_t)x;
+        if (q < kNodes) s.node[q] = j + 1, s.token[q] = (uint16_t)x;
       }
     }
     list_barrier();
@@ -266,13 +267,16 @@ extern "C" sv_status sv_adjust_logits(sv_handle* h, const sv_logits_args* a, sv_
   if (a->R > 1 && !a->tokens) return SV_ERR_INVALID;
   if (a->mask && a->mask_ld < (a->R + 31) / 32) return SV_ERR_INVALID;
   if (a->allowed && a->allowed_ld < ((int64_t)a->V + 31) / 32) return SV_ERR_INVALID;
-  if (a->V > 65535 * (int64_t)kSlice) return SV_ERR_UNSUPPORTED;
+  if (a->V > 65535 * (int64_t)kSlice || a->R > 1 << 22) return SV_ERR_UNSUPPORTED;
   // Rows share a CTA's lists where there are CTAs enough without it; a small
   // call gives each row its own, so that rows do not wait for one another.
   const int64_t slices = (a->V + kSlice - 1) / kSlice, wanted = 2 * (int64_t)h->num_sms;
   int parts = (int)((wanted + slices * a->B - 1) / (slices * a->B));
   parts = parts < 1 ? 1 : parts > a->R ? a->R : parts;
-  const int per = (a->R + parts - 1) / parts;
+  // a CTA counts rows x listed tokens and rows x drafted tokens in 32 bits
+  const int most = (1 << 30) / (a->R > kSlice ? a->R : kSlice);
+  int per = (a->R + parts - 1) / parts;
+  per = per > most ? most : per;
   const dim3 grid((unsigned)a->B, (unsigned)slices, (unsigned)((a->R + per - 1) / per)), block(kRuleThreads);
   const cudaError_t e =
       a->dtype == SV_FP32

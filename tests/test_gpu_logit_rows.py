@@ -1,0 +1,56 @@
+"""Rows of the logit rules at the edges of their layouts."""
+
+import os
+
+import pytest
+import torch
+
+from speculative_decoding_verification_07_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def ver():
+    if not os.path.exists(binding.LIB_PATH):
+        from speculative_decoding_verification_07_gb300 import build
+        build.build()
+    v = binding.Verifier(0)
+    yield v
+    v.close()
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_more_than_65536_drafted_tokens(ver, masked):
+    """A node counts from its own row on, whatever its number."""
+    V, R, node = 8, 66000, 65536 + 40
+    x = torch.ones(1, R, V, device=DEV)
+    tokens = torch.full((1, R - 1), -1, dtype=torch.int32, device=DEV)  # ids outside [0, V) are ignored
+    tokens[0, node - 1] = 3
+    tokens[0, 100 - 1] = 3
+    tokens[0, node + 50 - 1] = 5
+    kw = {}
+    if masked:  # every node sees itself alone but for one row, which sees the late node
+        mask = torch.zeros(1, R, (R + 31) // 32, dtype=torch.int32, device=DEV)
+        mask[0, 7, node // 32] = 1 << node % 32
+        mask[0, 9, (node - 65536) // 32] = 1 << node % 32
+        kw["mask"] = mask
+    y = ver.adjust_logits(x, out=torch.empty_like(x), tokens=tokens, frequency=torch.full((1,), 0.25, device=DEV), **kw)
+    assert ver.error() == 0
+    want = x.clone()
+    if masked:
+        want[0, 7, 3] -= 0.25
+    else:
+        want[0, 100:, 3] -= 0.25
+        want[0, node:, 3] -= 0.25
+        want[0, node + 50:, 5] -= 0.25
+    assert torch.equal(y, want)
+
+
+def test_more_rows_than_are_counted_are_refused(ver):
+    R = (1 << 22) + 1
+    with pytest.raises(binding.SvError) as e:
+        ver.adjust_logits(torch.zeros(1, R, 4, device=DEV), tokens=torch.zeros(1, R - 1, dtype=torch.int32, device=DEV))
+    assert e.value.code == binding.SV_ERR_UNSUPPORTED
+    assert ver.error() == 0
