@@ -336,6 +336,7 @@ PyObject* logits(PyObject* const* a) {
     refuse("logits and out must be whole [B][R][ld] rows");
   sv_logits_args p = {};
   p.B = (int)B, p.R = (int)R, p.V = a[3] == Py_None ? (int)x->size(2) : integer(a[3]), p.dtype = dtype_of(*x.t, "logits");
+  if (p.V > x->size(2) || p.V > y->size(2)) done("sv_adjust_logits", SV_ERR_INVALID);  // ld alone may reach past a view's end
   p.logits = ptr(*x.t), p.out = ptr(*y.t), p.ld = x->stride(1), p.out_ld = y->stride(1);
   int64_t values;
   p.history = table<int32_t>(a[4], B, &p.history_ld, "history");

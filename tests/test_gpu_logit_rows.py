@@ -54,3 +54,17 @@ def test_more_rows_than_are_counted_are_refused(ver):
         ver.adjust_logits(torch.zeros(1, R, 4, device=DEV), tokens=torch.zeros(1, R - 1, dtype=torch.int32, device=DEV))
     assert e.value.code == binding.SV_ERR_UNSUPPORTED
     assert ver.error() == 0
+
+
+def test_columns_past_a_view_are_refused(ver):
+    """A view's rows may be followed by no more of their buffer."""
+    whole = torch.zeros(1, 2, 128, device=DEV)
+    tokens = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    view = whole[:, :, 64:]
+    for x, out in ((view, whole), (whole, view)):
+        with pytest.raises(binding.SvError) as e:
+            ver.adjust_logits(x, out=out, V=65, tokens=tokens)
+        assert e.value.code == binding.SV_ERR_INVALID
+    ver.adjust_logits(view, V=64, tokens=tokens)
+    torch.cuda.synchronize()
+    assert ver.error() == 0
