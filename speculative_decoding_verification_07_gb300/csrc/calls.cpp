@@ -332,12 +332,14 @@ PyObject* logits(PyObject* const* a) {
     refuse("out does not match logits");
   const int64_t B = x->size(0), R = x->size(1);
   if (x->stride(2) != 1 || y->stride(2) != 1 ||
-      (B > 1 && (x->stride(0) != R * x->stride(1) || y->stride(0) != R * y->stride(1))))
+      (B > 1 && R > 1 && (x->stride(0) != R * x->stride(1) || y->stride(0) != R * y->stride(1))))
     refuse("logits and out must be whole [B][R][ld] rows");
   sv_logits_args p = {};
   p.B = (int)B, p.R = (int)R, p.V = a[3] == Py_None ? (int)x->size(2) : integer(a[3]), p.dtype = dtype_of(*x.t, "logits");
   if (p.V > x->size(2) || p.V > y->size(2)) done("sv_adjust_logits", SV_ERR_INVALID);  // ld alone may reach past a view's end
-  p.logits = ptr(*x.t), p.out = ptr(*y.t), p.ld = x->stride(1), p.out_ld = y->stride(1);
+  // one row a request: the requests' distance; one row in all: anything that holds it
+  const auto ld = [&](const Arg& t) { return R > 1 ? t->stride(1) : B > 1 ? t->stride(0) : (t->size(2) + 7) / 8 * 8; };
+  p.logits = ptr(*x.t), p.out = ptr(*y.t), p.ld = ld(x), p.out_ld = ld(y);
   int64_t values;
   p.history = table<int32_t>(a[4], B, &p.history_ld, "history");
   p.tokens = grid<int32_t>(a[5], B, R - 1, "tokens");

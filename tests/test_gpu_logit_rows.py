@@ -68,3 +68,23 @@ def test_columns_past_a_view_are_refused(ver):
     ver.adjust_logits(view, V=64, tokens=tokens)
     torch.cuda.synchronize()
     assert ver.error() == 0
+
+
+@pytest.mark.parametrize("B", [1, 3])
+def test_one_row_a_request_out_of_longer_ones(ver, B):
+    """One row of each request: the requests' distance is the row's stride."""
+    V, T = 61, 4
+    g = torch.Generator(DEV).manual_seed(B)
+    rows = torch.randn(B, T, 64, generator=g, device=DEV)
+    bias = dict(bias_ids=torch.full((B, 1), 60, dtype=torch.int32, device=DEV), bias_values=torch.ones(B, 1, device=DEV))
+    for x in (rows[:, 2:3], rows[:, 3:, :V], rows[:, 1, :V].unsqueeze(1)):
+        want = x[..., :V].clone()
+        want[..., 60] += 1
+        out = torch.empty(B, 1, 64, device=DEV)
+        ver.adjust_logits(x, out=out, V=V, **bias)
+        assert torch.equal(out[..., :V], want)
+    keep = rows.clone()
+    ver.adjust_logits(rows[:, 1, :V].unsqueeze(1), **bias)
+    keep[:, 1, 60] += 1
+    assert torch.equal(rows, keep)
+    assert ver.error() == 0
