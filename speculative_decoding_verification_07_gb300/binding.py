@@ -148,12 +148,12 @@ class BflState(ctypes.Structure):
                 ("free_top", c_void_p), ("refcount", c_void_p)]
 
 
-_lib = _native = None
+_lib = _native = _path = None
 
 
 def load_library(path: str = LIB_PATH):
     """Load libspecverify.so; raises if it was not built (no fallback exists)."""
-    global _lib, _native
+    global _lib, _path
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -211,10 +211,7 @@ def load_library(path: str = LIB_PATH):
                        (lib.sv_logits_args_size, SvLogitsArgs)):
         if fn() != ctypes.sizeof(layout):
             raise ImportError(f"{layout.__name__} layout mismatch between binding and library")
-    from . import _calls as native  # built beside the library; no fallback exists
-    native.open(os.path.abspath(path), SvError)
-    _native = native
-    _lib = lib
+    _lib, _path = lib, os.path.abspath(path)
     return lib
 
 
@@ -449,8 +446,12 @@ def kv_rollback_contig(handle, accepted, write_ptr, stream=None) -> None:
 # (csrc/calls.cpp), since these run once per layer
 # --------------------------------------------------------------------------- #
 def _calls():
+    global _native
     if _native is None:
         load_library()
+        from . import _calls as native  # built beside the library; no fallback exists
+        native.open(_path, SvError)
+        _native = native
     return _native
 
 

@@ -73,8 +73,6 @@ def build(verbose: bool = False, extra=(), out: str = LIB, only=None) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(todo) + 1) as ex:
         calls = ex.submit(_build_calls) if only is None else None
         list(ex.map(lambda s: _compile(s, list(extra)), todo))
-        if calls is not None:
-            calls.result()
     objs = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in SOURCES]
     tmp = out + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
@@ -82,6 +80,8 @@ def build(verbose: bool = False, extra=(), out: str = LIB, only=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, out)
+    if calls is not None:
+        calls.result()  # the library stands without it
     if verbose:
         print("built", out, file=sys.stderr)
     return out

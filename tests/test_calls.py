@@ -1,0 +1,39 @@
+"""The extension module that marshals the per-layer calls, as far as no GPU is
+needed."""
+
+import os
+import subprocess
+import sys
+
+import pytest
+
+from speculative_decoding_verification_07_gb300 import binding
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not os.path.exists(binding.LIB_PATH):
+        from speculative_decoding_verification_07_gb300 import build
+        build.build()
+
+
+def test_the_library_loads_without_the_extension_module():
+    """The verification and the cache calls need the C library alone; the
+    per-layer calls fail loudly."""
+    code = """
+import sys
+from speculative_decoding_verification_07_gb300 import binding
+sys.modules["speculative_decoding_verification_07_gb300._calls"] = None
+lib = binding.load_library()
+a = binding.SvVerifyArgs()
+a.B, a.kmax = 64, 4
+assert binding.sv_workspace_size(a) > 0
+try:
+    binding._calls()
+except ImportError:
+    print("loud")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.split() == ["loud"], r.stderr
