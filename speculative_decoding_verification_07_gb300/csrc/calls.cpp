@@ -6,6 +6,7 @@
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/ops/empty.h>
 #include <dlfcn.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -185,6 +186,29 @@ int integer(PyObject* o) {
 
 PyObject* none() { Py_RETURN_NONE; }
 
+// A reference that the call owns: what the caller gave, or a new output.
+class Owned {
+ public:
+  explicit Owned(PyObject* given) : o_(given) { Py_INCREF(o_); }
+  ~Owned() { Py_XDECREF(o_); }
+  Owned(const Owned&) = delete;
+  Owned& operator=(const Owned&) = delete;
+  void allocate(const at::Tensor& like) {
+    PyObject* made = THPVariable_Wrap(at::empty(like.sizes(), like.options()));
+    Py_DECREF(o_);
+    o_ = made;
+  }
+  PyObject* get() const { return o_; }
+  PyObject* release() {
+    PyObject* o = o_;
+    o_ = nullptr;
+    return o;
+  }
+
+ private:
+  PyObject* o_;
+};
+
 // (handle, parent, n_nodes, mask, depth, stream) -> (mask, depth)
 PyObject* tree_mask(PyObject* const* a) {
   Arg parent = need(a[1], "parent");
@@ -223,36 +247,27 @@ PyObject* append(PyObject* const* a) {
     refuse("k and v do not match the cache");
   p.k = heads<const void>(*k.t, B, R, H, D, p.k_stride, "k");
   p.v = heads<const void>(*v.t, B, R, H, D, p.v_stride, "v");
-  PyObject* out = a[9];
-  Py_INCREF(out);
-  try {
-    if (q) {
-      if (out == Py_None) {
-        Py_DECREF(out);
-        out = THPVariable_Wrap(at::empty(q->sizes(), q->options()));
-      }
-      Arg o = need(out, "q_out");
-      if (q->scalar_type() != k->scalar_type() || o->scalar_type() != k->scalar_type() || q->dim() != 4)
-        refuse("q and q_out need k's dtype");
-      p.Hq = (int)q->size(2);
-      p.q = heads<const void>(*q.t, B, R, p.Hq, D, p.q_stride, "q");
-      p.q_out = heads<void>(*o.t, B, R, p.Hq, D, p.q_out_stride, "q_out");
-    }
-    if (rope) {
-      if (rope->dim() != 3 || rope->size(2) != 2 || rope->scalar_type() != at::kFloat || !rope->is_contiguous())
-        refuse("rope must be a contiguous fp32 [max_pos, rot_dim / 2, 2] tensor");
-      p.rope = ptr<float>(*rope.t), p.max_pos = (int)rope->size(0), p.rot_dim = 2 * (int)rope->size(1);
-    }
-    if (PyObject_IsTrue(a[11])) p.flags = SV_APPEND_PAIRS;
-    p.depth = grid<int32_t>(a[12], B, R, "depth");
-    p.seq_len = vec<int32_t>(a[3], B, "seq_len");
-    p.n_nodes = vec<int32_t>(a[13], B, "n_nodes");
-    done("kv_append", api.append(handle_of(a[0]), &p, stream_of(a[14])));
-  } catch (...) {
-    Py_DECREF(out);
-    throw;
+  Owned out(a[9]);
+  if (q) {
+    if (out.get() == Py_None) out.allocate(*q.t);
+    Arg o = need(out.get(), "q_out");
+    if (q->scalar_type() != k->scalar_type() || o->scalar_type() != k->scalar_type() || q->dim() != 4)
+      refuse("q and q_out need k's dtype");
+    p.Hq = (int)q->size(2);
+    p.q = heads<const void>(*q.t, B, R, p.Hq, D, p.q_stride, "q");
+    p.q_out = heads<void>(*o.t, B, R, p.Hq, D, p.q_out_stride, "q_out");
   }
-  return out;
+  if (rope) {
+    if (rope->dim() != 3 || rope->size(2) != 2 || rope->scalar_type() != at::kFloat || !rope->is_contiguous())
+      refuse("rope must be a contiguous fp32 [max_pos, rot_dim / 2, 2] tensor");
+    p.rope = ptr<float>(*rope.t), p.max_pos = (int)rope->size(0), p.rot_dim = 2 * (int)rope->size(1);
+  }
+  if (PyObject_IsTrue(a[11])) p.flags = SV_APPEND_PAIRS;
+  p.depth = grid<int32_t>(a[12], B, R, "depth");
+  p.seq_len = vec<int32_t>(a[3], B, "seq_len");
+  p.n_nodes = vec<int32_t>(a[13], B, "n_nodes");
+  done("kv_append", api.append(handle_of(a[0]), &p, stream_of(a[14])));
+  return out.release();
 }
 
 // (handle, out, seq_len, kv, block_table, stage, layer, n_nodes, stream)
@@ -301,27 +316,15 @@ PyObject* attention_args(PyObject* const* a) {
 // -> out, or the bytes of workspace that the call needs and was not given
 PyObject* attention(PyObject* const* a) {
   Arg ws(a[1], "workspace"), q = need(a[3], "q");
-  PyObject* out = a[7];
-  Py_INCREF(out);
-  try {
-    if (out == Py_None) {
-      Py_DECREF(out);
-      out = THPVariable_Wrap(at::empty(q->sizes(), q->options()));
-    }
-    sv_attention_args p = {};
-    fill(&p, a + 3, *need(out, "out").t);
-    size_t bytes = 0;
-    done("sv_attention_workspace_size", api.attention_size(handle_of(a[0]), &p, &bytes));
-    if (!ws || (size_t)ws->nbytes() < bytes) {
-      Py_DECREF(out);
-      return PyLong_FromSize_t(bytes);
-    }
-    done("sv_tree_attention", api.attention(handle_of(a[0]), &p, ptr(*ws.t), ws->nbytes(), stream_of(a[2])));
-  } catch (...) {
-    Py_DECREF(out);
-    throw;
-  }
-  return out;
+  Owned out(a[7]);
+  if (out.get() == Py_None) out.allocate(*q.t);
+  sv_attention_args p = {};
+  fill(&p, a + 3, *need(out.get(), "out").t);
+  size_t bytes = 0;
+  done("sv_attention_workspace_size", api.attention_size(handle_of(a[0]), &p, &bytes));
+  if (!ws || (size_t)ws->nbytes() < bytes) return PyLong_FromSize_t(bytes);
+  done("sv_tree_attention", api.attention(handle_of(a[0]), &p, ptr(*ws.t), ws->nbytes(), stream_of(a[2])));
+  return out.release();
 }
 
 // (handle, logits, out, V, history, tokens, mask, n_nodes, rep, presence, frequency, bias_ids, bias_values, allowed, stream)
@@ -356,7 +359,7 @@ PyObject* logits(PyObject* const* a) {
   return none();
 }
 
-// No C++ exception leaves a call.
+// No C++ exception leaves a call; torch's keep their Python types.
 template <PyObject* (*fn)(PyObject* const*), int kArgs>
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != kArgs) {
@@ -366,8 +369,8 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
   try {
     return fn(a);
   } catch (const Refused&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -6,6 +6,8 @@ import subprocess
 import sys
 
 import pytest
+import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from speculative_decoding_verification_07_gb300 import binding
 
@@ -37,3 +39,17 @@ except ImportError:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.split() == ["loud"], r.stderr
+
+
+class Refusing(TorchDispatchMode):
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        raise torch.OutOfMemoryError("no room")
+
+
+def test_an_exception_of_an_allocation_keeps_its_type():
+    q = torch.zeros(1, 1, 2, 64)
+    call = binding._calls().attention
+    args = (None, None, 0, q, None, None, None, None, None, None, None, None, 0)
+    for _ in range(3):
+        with Refusing(), pytest.raises(torch.OutOfMemoryError, match="no room"):
+            call(*args)
