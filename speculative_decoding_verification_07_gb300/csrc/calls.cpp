@@ -215,6 +215,7 @@ PyObject* tree_mask(PyObject* const* a) {
   if (parent->dim() != 2 || parent->scalar_type() != at::kInt || !parent->is_contiguous())
     refuse("parent must be a contiguous int32 [B][N]");
   const int64_t B = parent->size(0), N = parent->size(1), W = (N + 32) / 32, n = B * (N + 1);
+  if ((a[3] == Py_None) != (a[4] == Py_None)) refuse("mask and depth: give both or neither");
   at::Tensor mask, depth;
   int64_t ld = W;
   if (a[3] == Py_None) {
@@ -224,7 +225,7 @@ PyObject* tree_mask(PyObject* const* a) {
     depth = both.as_strided({B, N + 1}, {N + 1, 1}, n * W);
   } else {
     table<uint32_t>(a[3], n, &ld, "mask");
-    if (!grid<int32_t>(a[4], B, N + 1, "depth")) refuse("depth: tensor expected");
+    grid<int32_t>(a[4], B, N + 1, "depth");
     mask = THPVariable_Unpack(a[3]), depth = THPVariable_Unpack(a[4]);
   }
   done("sv_tree_mask", api.tree_mask(handle_of(a[0]), (int)B, (int)N, ptr<int32_t>(*parent.t), vec<int32_t>(a[2], B, "n_nodes"),

@@ -53,3 +53,15 @@ def test_an_exception_of_an_allocation_keeps_its_type():
     for _ in range(3):
         with Refusing(), pytest.raises(torch.OutOfMemoryError, match="no room"):
             call(*args)
+
+
+def test_refusals_without_a_gpu():
+    c = binding._calls()
+    x = torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="parent"):
+        c.tree_mask(None, x.long(), None, None, None, 0)
+    with pytest.raises(TypeError):
+        c.tree_mask(None, x)
+    for mask, depth in ((x, None), (None, x)):  # one of the two would be ignored or missed
+        with pytest.raises(ValueError, match="mask and depth"):
+            c.tree_mask(None, x, None, mask, depth, 0)
