@@ -114,33 +114,12 @@ class SvKvPlace(ctypes.Structure):
 _Stride = c_int64 * 3
 
 
-class SvAppendArgs(ctypes.Structure):
-    _fields_ = [("B", c_int32), ("R", c_int32), ("Hq", c_int32), ("dtype", c_int32),
-                ("flags", c_uint32), ("rot_dim", c_int32), ("max_pos", c_int32),
-                ("reserved0", c_int32),
-                ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("q_out", c_void_p),
-                ("q_stride", _Stride), ("k_stride", _Stride), ("v_stride", _Stride),
-                ("q_out_stride", _Stride), ("rope", c_void_p),
-                ("depth", c_void_p), ("seq_len", c_void_p), ("n_nodes", c_void_p),
-                ("dst", SvKvPlace)]
-
-
 class SvAttentionArgs(ctypes.Structure):
     _fields_ = [("B", c_int32), ("R", c_int32), ("Hq", c_int32), ("dtype", c_int32),
                 ("q", c_void_p), ("out", c_void_p), ("q_stride", _Stride),
                 ("out_stride", _Stride), ("seq_len", c_void_p), ("n_nodes", c_void_p),
                 ("mask", c_void_p), ("mask_ld", c_int64), ("scale", ctypes.c_float),
                 ("reserved0", c_int32), ("cache", SvKvPlace), ("stage", SvKvPlace)]
-
-
-class SvLogitsArgs(ctypes.Structure):
-    _fields_ = [("B", c_int32), ("R", c_int32), ("V", c_int32), ("dtype", c_int32),
-                ("logits", c_void_p), ("out", c_void_p), ("ld", c_int64), ("out_ld", c_int64),
-                ("history", c_void_p), ("tokens", c_void_p), ("history_ld", c_int64),
-                ("mask", c_void_p), ("mask_ld", c_int64), ("n_nodes", c_void_p),
-                ("rep_penalty", c_void_p), ("presence", c_void_p), ("frequency", c_void_p),
-                ("bias_ids", c_void_p), ("bias_values", c_void_p), ("bias_ld", c_int64),
-                ("allowed", c_void_p), ("allowed_ld", c_int64)]
 
 
 class BflState(ctypes.Structure):
@@ -190,27 +169,18 @@ def load_library(path: str = LIB_PATH):
     lib.kv_commit_tree.argtypes = [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p,
                                    POINTER(KvPayload), c_void_p]
-    lib.sv_tree_mask.argtypes = [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
-                                 c_int64, c_void_p, c_void_p]
-    lib.kv_append.argtypes = [c_void_p, POINTER(SvAppendArgs), c_void_p]
-    lib.kv_read.argtypes = [c_void_p, c_int32, c_int32, c_void_p, c_void_p, POINTER(SvKvPlace),
-                            c_void_p, c_int32, c_void_p]
     lib.sv_attention_workspace_size.argtypes = [c_void_p, POINTER(SvAttentionArgs),
                                                 POINTER(c_size_t)]
     lib.sv_tree_attention.argtypes = [c_void_p, POINTER(SvAttentionArgs), c_void_p, c_size_t,
                                       c_void_p]
-    lib.sv_adjust_logits.argtypes = [c_void_p, POINTER(SvLogitsArgs), c_void_p]
     for name in EXPORTS[1:]:
         getattr(lib, name).restype = c_size_t if name.endswith("_args_size") else c_int32
     if lib.sv_verify_args_size() != ctypes.sizeof(SvVerifyArgs):
         raise ImportError("sv_verify_args layout mismatch between binding and library")
     if lib.sv_tree_args_size() != ctypes.sizeof(SvTreeArgs):
         raise ImportError("sv_tree_args layout mismatch between binding and library")
-    for fn, layout in ((lib.sv_append_args_size, SvAppendArgs),
-                       (lib.sv_attention_args_size, SvAttentionArgs),
-                       (lib.sv_logits_args_size, SvLogitsArgs)):
-        if fn() != ctypes.sizeof(layout):
-            raise ImportError(f"{layout.__name__} layout mismatch between binding and library")
+    if lib.sv_attention_args_size() != ctypes.sizeof(SvAttentionArgs):
+        raise ImportError("sv_attention_args layout mismatch between binding and library")
     _lib, _path = lib, os.path.abspath(path)
     return lib
 

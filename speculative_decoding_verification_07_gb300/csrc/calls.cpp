@@ -391,10 +391,17 @@ PyObject* open_library(PyObject*, PyObject* args) {
     if (!f) PyErr_Format(PyExc_ImportError, "%s has no %s", path, name);
     return f != nullptr;
   };
+  decltype(&sv_append_args_size) append_size, attention_size, logits_size;
   if (!sym("sv_tree_mask", api.tree_mask) || !sym("kv_append", api.append) || !sym("kv_read", api.read) ||
       !sym("sv_attention_workspace_size", api.attention_size) || !sym("sv_tree_attention", api.attention) ||
-      !sym("sv_adjust_logits", api.logits))
+      !sym("sv_adjust_logits", api.logits) || !sym("sv_append_args_size", append_size) ||
+      !sym("sv_attention_args_size", attention_size) || !sym("sv_logits_args_size", logits_size))
     return nullptr;
+  if (append_size() != sizeof(sv_append_args) || attention_size() != sizeof(sv_attention_args) ||
+      logits_size() != sizeof(sv_logits_args)) {
+    PyErr_Format(PyExc_ImportError, "%s was built from another header", path);
+    return nullptr;
+  }
   Py_INCREF(cls);
   g_error = cls;
   return none();

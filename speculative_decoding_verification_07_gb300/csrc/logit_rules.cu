@@ -6,7 +6,6 @@ namespace sv {
 
 constexpr int kRuleThreads = 512, kListThreads = 64;  // of them, those that make the lists
 constexpr int kSlice = 4096;  // tokens of one CTA
-constexpr int kFlight = 1;    // vectors of a batch; one batch is on its way while another is written
 constexpr int kNodes = 256;   // drafted tokens of a slice that are kept at hand
 
 struct RuleSmem {
@@ -57,65 +56,59 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
 
   const int total = !in_place ? (r1 - r0) * groups : a.allowed ? live * groups : 0;  // rows without rules are copied
   auto row_of = [&](int k) { return groups == kSlice / 8 ? k / (kSlice / 8) : k / groups; };
-  struct Batch {
-    uint4 lo[kFlight], hi[F32 ? kFlight : 1];
-    uint32_t bits[kFlight];
+  struct Vector {
+    uint4 lo, hi;  // eight logits; hi of fp32 alone
+    uint32_t bits;
   };
-  auto fetch = [&](Batch& q, int g0, int step) {
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int k = g0 + u * step, r = row_of(k), g = k - r * groups;
-      if (k >= total) continue;
-      const char* p = src0 + (int64_t)(r0 + r) * a.ld * eb + g * 8 * eb;
-      q.bits[u] = 0xFFu;
-      if (a.allowed && r < live)
-        q.bits[u] = reinterpret_cast<const uint8_t*>(a.allowed + ((int64_t)b * a.R + r0 + r) * a.allowed_ld)[v0 / 8 + g];
-      if (8 * g + 8 <= len) {
-        q.lo[u] = *reinterpret_cast<const uint4*>(p);
-        if (F32) q.hi[F32 ? u : 0] = reinterpret_cast<const uint4*>(p)[1];
-      } else {  // a row may end right after its last token
-        uint32_t w[8] = {};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (8 * g + e >= len) break;
-          if (F32)
-            w[e] = reinterpret_cast<const uint32_t*>(p)[e];
-          else
-            w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << 16 * (e & 1);
-        }
-        q.lo[u] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (F32) q.hi[F32 ? u : 0] = make_uint4(w[4], w[5], w[6], w[7]);
-      }
-    }
-  };
-  auto put = [&](const Batch& q, int g0, int step) {
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int k = g0 + u * step, r = row_of(k), g = k - r * groups;
-      if (k >= total || (in_place && q.bits[u] == 0xFFu)) continue;
-      char* p = dst0 + (int64_t)(r0 + r) * a.out_ld * eb + g * 8 * eb;
-      const uint4 h = q.hi[F32 ? u : 0];
-      uint32_t w[8] = {q.lo[u].x, q.lo[u].y, q.lo[u].z, q.lo[u].w, h.x, h.y, h.z, h.w};
+  auto fetch = [&](Vector& q, int k) {
+    if (k >= total) return;
+    const int r = row_of(k), g = k - r * groups;
+    const char* p = src0 + (int64_t)(r0 + r) * a.ld * eb + g * 8 * eb;
+    q.bits = 0xFFu;
+    if (a.allowed && r < live)
+      q.bits = reinterpret_cast<const uint8_t*>(a.allowed + ((int64_t)b * a.R + r0 + r) * a.allowed_ld)[v0 / 8 + g];
+    if (8 * g + 8 <= len) {
+      q.lo = *reinterpret_cast<const uint4*>(p);
+      if (F32) q.hi = reinterpret_cast<const uint4*>(p)[1];
+    } else {  // a row may end right after its last token
+      uint32_t w[8] = {};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool ban = !(q.bits[u] >> e & 1);
+        if (8 * g + e >= len) break;
         if (F32)
-          w[e] = ban ? 0xFF800000u : w[e];
-        else if (ban)
-          w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | 0xFF800000u : (w[e >> 1] & 0xFFFF0000u) | 0xFF80u;
+          w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+        else
+          w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << 16 * (e & 1);
       }
-      if (8 * g + 8 <= len) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (F32) reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      } else {
+      q.lo = make_uint4(w[0], w[1], w[2], w[3]);
+      if (F32) q.hi = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  };
+  auto put = [&](const Vector& q, int k) {
+    if (in_place && q.bits == 0xFFu) return;
+    const int r = row_of(k), g = k - r * groups;
+    char* p = dst0 + (int64_t)(r0 + r) * a.out_ld * eb + g * 8 * eb;
+    uint32_t w[8] = {q.lo.x, q.lo.y, q.lo.z, q.lo.w};
+    if (F32) w[4] = q.hi.x, w[5] = q.hi.y, w[6] = q.hi.z, w[7] = q.hi.w;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (8 * g + e >= len) break;
-          if (F32)
-            reinterpret_cast<uint32_t*>(p)[e] = w[e];
-          else
-            reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> 16 * (e & 1));
-        }
+    for (int e = 0; e < 8; ++e) {
+      const bool ban = !(q.bits >> e & 1);
+      if (F32)
+        w[e] = ban ? 0xFF800000u : w[e];
+      else if (ban)
+        w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | 0xFF800000u : (w[e >> 1] & 0xFFFF0000u) | 0xFF80u;
+    }
+    if (8 * g + 8 <= len) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (F32) reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (8 * g + e >= len) break;
+        if (F32)
+          reinterpret_cast<uint32_t*>(p)[e] = w[e];
+        else
+          reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> 16 * (e & 1));
       }
     }
   };
@@ -175,16 +168,16 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
       }
   } else {
     // ---- every logit: copied, or -inf --------------------------------------
-    // A batch of vectors is always on its way: the next is asked for before the
-    // one at hand is written.
-    const int first = live > 0 ? kListThreads : 0;
-    Batch now;
-    fetch(now, t - first, kRuleThreads - first);
+    // A vector is always on its way: the next is asked for before the one at hand
+    // is written.
+    const int first = live > 0 ? kListThreads : 0, step = kRuleThreads - first;
+    Vector now;
+    fetch(now, t - first);
 #pragma unroll 1
-    for (int g0 = t - first; g0 < total; g0 += kFlight * (kRuleThreads - first)) {
-      Batch next;
-      fetch(next, g0 + kFlight * (kRuleThreads - first), kRuleThreads - first);
-      put(now, g0, kRuleThreads - first);
+    for (int k = t - first; k < total; k += step) {
+      Vector next;
+      fetch(next, k + step);
+      put(now, k);
       now = next;
     }
   }
