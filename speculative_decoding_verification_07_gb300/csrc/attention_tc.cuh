@@ -797,8 +797,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         if (lane == 0) mbar_arrive(b_q);
         if (F8) named_barrier(QM == 2 ? 2 + st : 1, kGroup);  // the rows' scales
       }
-      // positive, so that what is not seen stays -inf when it is scaled
-      const float c = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? s_qs[(QM == 2 ? st * kTile : 0) + row] : 1.0f), 1e-37f);
+      // positive (a subnormal at least), so that what is not seen stays -inf when it is scaled
+      const float c = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? s_qs[(QM == 2 ? st * kTile : 0) + row] : 1.0f), 0x1p-149f);
       const uint64_t c2 = pair(c, c);
       // wr: reference of 8-bit weights, log2 units; raise = 2^(kBias + m - wr)
       float m = -kInf, l = 0.0f, wr = -kInf, raise = 0.0f;

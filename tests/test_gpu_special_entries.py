@@ -93,3 +93,27 @@ def test_columns_past_the_rotation_pass_unchanged(ver, dtype, rot, pairs):
         assert torch.equal(got.view(word)[~torch.isnan(got)], want.view(word)[~torch.isnan(want)])
         assert torch.isfinite(y[..., :rot]).all()
         assert not torch.equal(y[..., :rot], x[..., :rot])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G", [4, 40, 150])
+def test_tiny_queries_and_huge_keys(ver, fmt, G):
+    """Ordinary scores of factors near both ends of fp32 (a factor of the scores may be
+    subnormal, with 20 bits: 2^-20 of a score's size more), held to the bound of
+    the attention's own tests."""
+    D, n = 128, 50
+    rng = np.random.default_rng(G)
+    bf = lambda x: torch.tensor(x, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    k, v = bf(2.0 ** 117 * rng.standard_normal((n, D))), bf(rng.standard_normal((n, D)))
+    row = D + E.TAIL if fmt == "e4m3" else D
+    kv = torch.zeros(4, 1, 2, 1, 16, row, dtype=torch.uint8 if fmt == "e4m3" else torch.bfloat16, device=DEV)
+    t = ints([[3, 0, 1, 2]])
+    ver.kv_append(k[None, :, None], v[None, :, None], ints([0]), kv=kv, block_table=t)
+    held = ver.kv_read(torch.empty(1, n, 2, 1, D, device=DEV), ints([0]), kv=kv, block_table=t)[0, :, :, 0].double().cpu().numpy()
+    q = bf(2.0 ** -117 * rng.choice([-0.25, 0.25], (G, D)))
+    got = ver.tree_attention(q[None, None], kv, t, ints([n - 1]))[0, 0].double().cpu().numpy()
+    assert ver.error() == 0
+    for h in range(G):
+        o, size, scores = E.attend(q[h].double().cpu().numpy(), held[:, 0], held[:, 1], np.ones(n, bool), D ** -0.5)
+        assert 1 < scores < 40
+        assert (np.abs(got[h] - o) <= (2.0 ** -8 + 2.0 ** -10) * size + 2.0 ** -8 * np.abs(o)).all()
