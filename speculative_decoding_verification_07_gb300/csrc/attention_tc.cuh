@@ -265,7 +265,10 @@ constexpr float kSlack = 8.0f;
 // largest weight, 5 bits at 2^-22, and are off by 2^-27 of it at most (2^-24 after
 // weights were rescaled, below).  (The format of V's codes, split in two, flushes
 // weights 2^-18 below the largest, and most of a long sequence's mass may lie there.)
-constexpr float kBias = 11.0f, kMost = 0x1p15f;
+// kMost is the largest fp16 value: a limit of 2^15 moved a reference once or twice
+// more per warp and item, and a group weighed twice holds a stream up by 1500 cycles
+// (64 trees of 15 nodes, scales of 2^-8 to 2^-6: 203 us; 191 as it is).
+constexpr float kBias = 11.0f, kMost = 65504.0f;
 constexpr float kMostSum = 0x1p7f;   // with scales of 2^120 at most, products stay finite
 // log2 of what a product is multiplied by at most to become a weight: where a row's
 // largest is below 2^-115, weights lose bits rather than the factor its range.
