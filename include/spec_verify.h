@@ -604,7 +604,9 @@ sv_status kv_read(sv_handle* handle, int32_t B, int32_t R, const int32_t* seq_le
  *   sum_x p_x V_x,  p = softmax(scale * q . K_x)
  * over what it sees, K and V those of head h / (Hq / heads).  A row that sees
  * nothing, and every row past n_b, is zero.  What a row does not see does not
- * enter its result, whatever it holds (NaN and infinities included).
+ * enter its result, whatever it holds (NaN and infinities included).  A NaN that
+ * it sees makes it NaN; an infinite V that it sees makes its column that infinity
+ * or NaN.
  *
  * q, out  [B][R][Hq][head_dim] with element strides {request, entry, head}
  *         (multiples of 16 bytes, last dimension contiguous).  dtype SV_BF16

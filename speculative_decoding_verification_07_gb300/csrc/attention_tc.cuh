@@ -417,11 +417,12 @@ static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r
 // tensor memory and its tiles its shared memory; rows are padded to 128 because
 // bytes bound all but the widest calls.  64 requests of 128 to 8192 positions, 8 KV
 // heads of 128, bf16: single tokens 189 us, trees of 15 nodes (60 rows a head) 199
-// (5.8 and 5.6 TB/s); 8-bit 164 and 182 (3.7 and 3.5), where the chain of a
-// stream's scores, weights and outputs bounds it: 8 + 12 products of 64 cycles and
-// 850 cycles of softmax per 32 keys.  4 requests of up to 65536 positions, 448 rows
-// a head, bf16: 184 us, 0.85 PFLOP/s; what the products' warp does between products
-// (waits, commits: a third of its time) bounds that.  Handing scores over in halves
+// (5.8 and 5.6 TB/s); 8-bit 166 and 189 (3.7 and 3.3), where a stream's chain
+// bounds it: with trees, a tile's softmax takes 2100 cycles (at 1.94 GHz; 750 per 32
+// keys a warp) and waits 1800 for its scores, in which the products' warp issues
+// both streams' 8 + 12 products and their commits (1500 a tile).  4 requests of up
+// to 65536 positions, 448 rows a head, bf16: 184 us, 0.85 PFLOP/s; what the products'
+// warp does between products (waits, commits: a third of its time) bounds that.  Handing scores over in halves
 // of 64 keys, to have the next half's under way, doubled those steps: 249 us.
 template <bool F8, int D, int QM>
 __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_kernel(const __grid_constant__ TcParams P) {

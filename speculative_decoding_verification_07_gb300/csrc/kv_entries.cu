@@ -4,8 +4,10 @@
 namespace sv {
 
 // 8164 entries of 32 + 2 x 8 heads of 128, 8-bit (186 MB): written in 52 us by
-// 256 threads, 38 by 128 (4.9 TB/s), 37 by 64; 960 entries 6.1, 5.9 and 6.2 us:
-// what a thread does before its first row is shared by more rows.
+// 256 threads, 38 by 128, 37 by 64; 960 entries 6.1, 5.9 and 6.2 us: what a
+// thread does before its first row is shared by more rows.  (39.6, 4.7 TB/s, and
+// 5.8 since columns past the rotated ones are left alone; bf16 38.8, 5.2 TB/s,
+// fp32 65.4, 6.1.)
 constexpr int kAppendThreads = 128;
 
 // Lanes of a warp that share a row of head_dim values, eight values a lane;
