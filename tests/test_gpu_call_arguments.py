@@ -1,5 +1,5 @@
-"""What the calls around the verification step refuse, and shapes that they read
-as they are: each used to be read as something else."""
+"""Types and shapes that the calls around the verification step refuse, since they
+would be read as others."""
 
 import os
 
