@@ -630,7 +630,28 @@ sv_status kv_read(sv_handle* handle, int32_t B, int32_t R, const int32_t* seq_le
  * The workspace rules are spec_verify's: caller-owned, 256-byte aligned, left
  * ready for the next call; its first SV_ATTENTION_CLEAR bytes are zero before
  * its first use.  Calls that may run at once (on different streams) need one
- * each, and it outlives the graphs that captured a call with it. */
+ * each, and it outlives the graphs that captured a call with it.
+ *
+ * Forms of the scores (all fields zero: none).  With s = scale * q . K_x, and the
+ * distance d = |pos(row) - pos(x)| (a cached position is its own, entry j sits at
+ * S_b + depth[b][j]):
+ *   softcap > 0   s = softcap * tanh(s / softcap); 2^-60 .. 2^60
+ *   slopes        s = s - slopes[h] * d, [Hq] fp32, finite
+ *   window > 0    the row sees x only where d < window
+ * in this order.  depth [B][R] (NULL = i) is read for slopes and window alone;
+ * what is not in 0 .. R - 1 counts as the nearest of them.
+ *
+ * Prefixes that requests share: shared_len and shared_members [B], as of
+ * sv_prefix_groups (give both or neither).  members_b consecutive requests from b
+ * on hold the same K and V (the same blocks, or equal ones) at their first
+ * shared_len positions, which are then read once for all of their rows; members_b
+ * is 0 for requests that start no group and shared_len_b 0 for those in none.
+ * The results are those of the call without them but for the order of sums (the
+ * weights' reference is each part's own).  A shared_len that is negative or past S_b
+ * counts as none.  Groups that reach past the batch, overlap, or disagree on their
+ * shared_len: SV_ERR_STATE in the error word, the rows of the requests they name are
+ * unspecified.  Calls with a window, over fp32 caches or with heads other than 64 and
+ * 128 read every request's own blocks. */
 #define SV_ATTENTION_CLEAR 4096
 typedef struct {
   int32_t B, R, Hq, dtype;
@@ -643,6 +664,10 @@ typedef struct {
   float scale;
   int32_t reserved0;
   sv_kv_place cache, stage;
+  float softcap;
+  int32_t window;
+  const float* slopes;
+  const int32_t *depth, *shared_len, *shared_members;
 } sv_attention_args;
 
 size_t sv_attention_args_size(void);
@@ -650,6 +675,22 @@ sv_status sv_attention_workspace_size(sv_handle* handle, const sv_attention_args
                                       size_t* bytes);
 sv_status sv_tree_attention(sv_handle* handle, const sv_attention_args* args, void* workspace,
                             size_t workspace_bytes, sv_stream_t stream);
+
+/* Which neighbouring requests hold the same leading blocks ([CV] 4: shared
+ * prefixes), from the block tables and lengths alone: made once a step, for every
+ * layer's attention.  With n_b the leading entries in which rows b - 1 and b of
+ * block_table [B][max_blocks] agree (ids of 0 and up, among the blocks that both
+ * requests have filled: floor(min(S_{b-1}, S_b) / block_size)), request b belongs to
+ * its left neighbour's group iff n_b > 0 and n_b * block_size >= least.  A group of
+ * two requests and more shares block_size * (the smallest n_b of its later members)
+ * positions: shared_len [B] gets that for each of them and members [B] the group's
+ * size at its first request; all else is 0.
+ * A seq_len that is negative or longer than its table: SV_ERR_STATE in the error
+ * word, the request is alone.  B, max_blocks >= 0, block_size >= 1. */
+sv_status sv_prefix_groups(sv_handle* handle, int32_t B, const int32_t* seq_len,
+                           const int32_t* block_table, int32_t max_blocks, int32_t block_size,
+                           int32_t least, int32_t* shared_len, int32_t* shared_members,
+                           sv_stream_t stream);
 
 /*
  * Arguments of sv_adjust_logits: rules on the target's rows before they are

@@ -118,3 +118,49 @@ def adjust(l, V, counts, rep, pres, freq, bias, allowed):
     if allowed is not None:
         l[~allowed] = -np.inf
     return l, size
+
+
+def shaped(s, far, softcap=None, slope=None):
+    """Scores with a form: capped by a tanh, then less by a slope times the distance."""
+    s = np.asarray(s, np.float64)
+    if softcap is not None:
+        s = softcap * np.tanh(s / softcap)
+    return s if slope is None else s - slope * far
+
+
+def attend_shaped(q, K, V, seen, scale, far, softcap=None, slope=None, window=None):
+    """``attend`` with a form of the scores; far [n]: the keys' distances from the row.
+    Returns (o, sum p |v|, the largest sum of score parts, the largest distance term)."""
+    seen = seen if window is None else seen & (far < window)
+    idx = np.flatnonzero(seen)
+    D = q.shape[0]
+    if idx.size == 0:
+        return np.zeros(D), np.zeros(D), 0.0, 0.0
+    K, V, far = K[idx], V[idx], far[idx].astype(np.float64)
+    s = shaped((K @ q) * scale, far, softcap, slope)
+    size = (np.abs(K) @ np.abs(q)).max() * abs(scale)
+    p = np.exp(s - s.max())
+    p /= p.sum()
+    return p @ V, p @ np.abs(V), size, 0.0 if slope is None else abs(slope) * far.max()
+
+
+def prefix_groups(table, lens, BS, least):
+    """(shared positions [B], group sizes at first members [B]) from tables and lengths."""
+    B = len(lens)
+    length, members = np.zeros(B, np.int32), np.zeros(B, np.int32)
+
+    def common(b):
+        n = 0
+        while n < min(lens[b - 1], lens[b]) // BS and table[b - 1][n] == table[b][n] and table[b][n] >= 0:
+            n += 1
+        return n
+
+    start = 0
+    for b in range(1, B + 1):
+        if b < B and common(b) > 0 and common(b) * BS >= least:
+            continue
+        if b - start > 1:
+            members[start] = b - start
+            length[start:b] = BS * min(common(x) for x in range(start + 1, b))
+        start = b
+    return length, members

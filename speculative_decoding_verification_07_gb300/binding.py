@@ -9,8 +9,8 @@ Functions carry the C names: sv_create, sv_destroy, sv_workspace_size,
 spec_verify, bfl_init, bfl_reserve, bfl_fork_prefix, bfl_release,
 kv_commit_rollback, kv_commit_draft, bfl_reserve_cow, kv_commit_copy,
 kv_rollback_contig, sv_get_error; around the verification step sv_tree_mask,
-kv_append, kv_read, sv_tree_attention, sv_adjust_logits.  ``Verifier`` and
-``BlockPool`` are thin owners of a handle / workspace and of the pool arrays.
+kv_append, kv_read, sv_tree_attention, sv_prefix_groups, sv_adjust_logits.
+``Verifier`` and ``BlockPool`` are thin owners of a handle / workspace and of the pool arrays.
 """
 
 from __future__ import annotations
@@ -45,7 +45,7 @@ EXPORTS = ("sv_verify_args_size", "sv_create", "sv_destroy", "sv_workspace_size"
            "kv_commit_draft", "bfl_reserve_cow", "kv_commit_copy", "sv_tree_args_size",
            "spec_verify_tree", "kv_commit_tree", "sv_tree_mask", "sv_append_args_size",
            "kv_append", "kv_read", "sv_attention_args_size", "sv_attention_workspace_size",
-           "sv_tree_attention", "sv_logits_args_size", "sv_adjust_logits")
+           "sv_tree_attention", "sv_logits_args_size", "sv_adjust_logits", "sv_prefix_groups")
 SV_TREE_MAX_NODES = 4096
 SV_KV_BF16, SV_KV_FP32, SV_KV_E4M3 = 0, 1, 2
 E4M3_TAIL = 16     # bytes after an 8-bit entry's codes: its fp32 scale, then zeros
@@ -119,7 +119,9 @@ class SvAttentionArgs(ctypes.Structure):
                 ("q", c_void_p), ("out", c_void_p), ("q_stride", _Stride),
                 ("out_stride", _Stride), ("seq_len", c_void_p), ("n_nodes", c_void_p),
                 ("mask", c_void_p), ("mask_ld", c_int64), ("scale", ctypes.c_float),
-                ("reserved0", c_int32), ("cache", SvKvPlace), ("stage", SvKvPlace)]
+                ("reserved0", c_int32), ("cache", SvKvPlace), ("stage", SvKvPlace),
+                ("softcap", ctypes.c_float), ("window", c_int32), ("slopes", c_void_p),
+                ("depth", c_void_p), ("shared_len", c_void_p), ("shared_members", c_void_p)]
 
 
 class BflState(ctypes.Structure):
@@ -471,11 +473,23 @@ def kv_read(handle, out, seq_len, *, kv=None, block_table=None, stage=None, laye
     _calls().read(_raw(handle), out, seq_len, kv, block_table, stage, layer, n_nodes, _raw_stream(stream))
 
 
+def _forms(softcap, slopes, window, depth, groups):
+    """The last arguments of an attention call, or () if none is given."""
+    if softcap is None and slopes is None and window is None and depth is None and groups is None:
+        return ()
+    length, members = (None, None) if groups is None else (groups["length"], groups["members"])
+    return softcap, slopes, window, depth, length, members
+
+
 def make_attention_args(q, kv, block_table, seq_len, out, *, stage=None, mask=None, n_nodes=None,
-                        scale=None, layer=0) -> SvAttentionArgs:
-    """q, out: [B, R, Hq, head_dim]; mask: [B, R, ld] words of sv_tree_mask."""
+                        scale=None, layer=0, softcap=None, slopes=None, window=None, depth=None,
+                        groups=None) -> SvAttentionArgs:
+    """q, out: [B, R, Hq, head_dim]; mask: [B, R, ld] words of sv_tree_mask; slopes: [Hq] fp32;
+    depth: [B, R]; groups: dict(length, members) of [B] each."""
     a = SvAttentionArgs()
-    _calls().attention_args(ctypes.addressof(a), q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer)
+    forms = _forms(softcap, slopes, window, depth, groups)
+    fill = _calls().attention_args_forms if forms else _calls().attention_args
+    fill(ctypes.addressof(a), q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer, *forms)
     return a
 
 
@@ -489,6 +503,11 @@ def sv_attention_workspace_size(handle, args: SvAttentionArgs) -> int:
 def sv_tree_attention(handle, args: SvAttentionArgs, workspace: torch.Tensor, stream=None) -> None:
     _check("sv_tree_attention", load_library().sv_tree_attention(
         handle, args, _ptr(workspace), workspace.nbytes, _raw_stream(stream)))
+
+
+def sv_prefix_groups(handle, block_table, seq_len, block_size, length, members, *, least=128, stream=None) -> None:
+    """block_table: [B, max_blocks]; length, members: [B] int32 outputs."""
+    _calls().prefix_groups(_raw(handle), block_table, seq_len, block_size, least, length, members, _raw_stream(stream))
 
 
 def sv_adjust_logits(handle, logits, out, *, V=None, history=None, tokens=None, mask=None, n_nodes=None,
@@ -614,21 +633,43 @@ class Verifier:
         _calls().read(self.raw, out, seq_len, kv, block_table, stage, layer, n_nodes, _raw_stream(stream))
         return out
 
+    def prefix_groups(self, block_table, seq_len, block_size, *, least=128, out=None, stream=None):
+        """Which neighbouring requests hold the same leading blocks, for tree_attention's
+        `groups`: dict(length=[B] positions, members=[B] group sizes at their first requests).
+        Neighbours with fewer than `least` positions in common stay apart."""
+        out = out or {}
+        args = (self.raw, block_table, seq_len, block_size, least, out.get("length"), out.get("members"), _raw_stream(stream))
+        if stream is None or out:
+            length, members = _calls().prefix_groups(*args)
+        else:  # as _empty_on
+            with torch.cuda.stream(stream):
+                length, members = _calls().prefix_groups(*args)
+            length.record_stream(torch.cuda.current_stream(self.device))  # members is of the same allocation
+        return dict(length=length, members=members)
+
     def tree_attention(self, q, kv, block_table, seq_len, *, stage=None, mask=None, n_nodes=None, scale=None, layer=0,
-                       out=None, stream=None):
+                       out=None, stream=None, softcap=None, slopes=None, window=None, depth=None, groups=None):
         """Attention of the pass's queries over the cache and its own entries;
         returns out [B, R, Hq, head_dim] (allocated unless given).  Each stream has
         a workspace of its own; a captured call uses its stream's, or one of the
         graph's own, so order a graph's replays with one another and with the calls
-        on the stream it was captured on."""
+        on the stream it was captured on.
+
+        softcap: scores s become softcap * tanh(s / softcap).  slopes [Hq]: scores
+        are less by a head's slope times the distance.  window: rows see the keys
+        at smaller distances alone.  depth [B, R]: the entries' positions past S
+        (tree_mask's), for slopes and windows; None: a chain.  groups: what
+        prefix_groups gave for these tables, so that a group's prefix is read once."""
         if _allocates(stream, out, q):
             out = _empty_on(stream, q)
         s = _raw_stream(stream)
         ws = self._attention_workspaces.get(s)
-        got = _calls().attention(self.raw, ws, s, q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer)
+        forms = _forms(softcap, slopes, window, depth, groups)
+        call = _calls().attention_forms if forms else _calls().attention
+        got = call(self.raw, ws, s, q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer, *forms)
         if type(got) is int:  # bytes of workspace: the stream's first call, or a larger shape
             ws = self._attention_workspace(s, stream, got)
-            got = _calls().attention(self.raw, ws, s, q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer)
+            got = call(self.raw, ws, s, q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer, *forms)
         return got
 
     def _attention_workspace(self, raw, stream, need):

@@ -50,4 +50,12 @@ __device__ __forceinline__ uint32_t seen_bits(const sv_attention_args& a, int b,
   return u < 0 ? w << -u | ((1u << -u) - 1u) : w;
 }
 
+// Position of entry i past S_b, for distances.
+__device__ __forceinline__ int depth_of(const sv_attention_args& a, int b, int i) {
+  return a.depth ? min(max(__ldg(a.depth + (int64_t)b * a.R + i), 0), a.R - 1) : i;
+}
+
+// The first cached position that any row of request b may see: no row sits before S.
+__device__ __forceinline__ int first_seen(const sv_attention_args& a, int S) { return a.window > 0 ? max(0, S - a.window + 1) : 0; }
+
 }  // namespace sv

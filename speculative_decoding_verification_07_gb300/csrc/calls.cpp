@@ -25,6 +25,7 @@ struct Api {
   decltype(&sv_attention_workspace_size) attention_size;
   decltype(&sv_tree_attention) attention;
   decltype(&sv_adjust_logits) logits;
+  decltype(&sv_prefix_groups) prefix_groups;
 } api;
 PyObject* g_error = nullptr;  // SvError(function, code)
 
@@ -305,6 +306,28 @@ void fill(sv_attention_args* p, PyObject* const* a, const at::Tensor& out) {
   p->scale = (float)scale;
 }
 
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused();
+  return v;
+}
+
+// softcap, slopes, window, depth, shared_len, shared_members at a[0..5], after fill
+void fill_forms(sv_attention_args* p, PyObject* const* a) {
+  if (a[0] != Py_None) {
+    const double cap = number(a[0]);
+    if (!(cap >= 0x1p-60 && cap <= 0x1p60)) refuse("softcap: 2^-60 .. 2^60 expected");
+    p->softcap = (float)cap;
+  }
+  if (Arg slopes(a[1], "slopes"); slopes && slopes->numel() != p->Hq) refuse("slopes: one value per query head expected");
+  p->slopes = vec<float>(a[1], p->Hq, "slopes");
+  if (a[2] != Py_None && (p->window = integer(a[2])) < 1) refuse("window: at least one position expected");
+  p->depth = grid<int32_t>(a[3], p->B, p->R, "depth");
+  if ((a[4] == Py_None) != (a[5] == Py_None)) refuse("groups: length and members: give both or neither");
+  p->shared_len = vec<int32_t>(a[4], p->B, "length");
+  p->shared_members = vec<int32_t>(a[5], p->B, "members");
+}
+
 // (address of an sv_attention_args, q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer)
 PyObject* attention_args(PyObject* const* a) {
   sv_attention_args p = {};
@@ -313,19 +336,59 @@ PyObject* attention_args(PyObject* const* a) {
   return none();
 }
 
+// The same and softcap, slopes, window, depth, shared_len, shared_members.
+PyObject* attention_args_forms(PyObject* const* a) {
+  sv_attention_args p = {};
+  fill(&p, a + 1, *need(a[5], "out").t);
+  fill_forms(&p, a + 11);
+  *static_cast<sv_attention_args*>(PyLong_AsVoidPtr(a[0])) = p;
+  return none();
+}
+
 // (handle, workspace, stream, q, kv, block_table, seq_len, out, stage, mask, n_nodes, scale, layer)
 // -> out, or the bytes of workspace that the call needs and was not given
-PyObject* attention(PyObject* const* a) {
+template <bool kForms>
+PyObject* attend(PyObject* const* a) {
   Arg ws(a[1], "workspace"), q = need(a[3], "q");
   Owned out(a[7]);
   if (out.get() == Py_None) out.allocate(*q.t);
   sv_attention_args p = {};
   fill(&p, a + 3, *need(out.get(), "out").t);
+  if (kForms) fill_forms(&p, a + 13);
   size_t bytes = 0;
   done("sv_attention_workspace_size", api.attention_size(handle_of(a[0]), &p, &bytes));
   if (!ws || (size_t)ws->nbytes() < bytes) return PyLong_FromSize_t(bytes);
   done("sv_tree_attention", api.attention(handle_of(a[0]), &p, ptr(*ws.t), ws->nbytes(), stream_of(a[2])));
   return out.release();
+}
+PyObject* attention(PyObject* const* a) { return attend<false>(a); }
+// The same and softcap, slopes, window, depth, shared_len, shared_members.
+PyObject* attention_forms(PyObject* const* a) { return attend<true>(a); }
+
+// (handle, block_table, seq_len, block_size, least, shared_len, shared_members, stream) -> (shared_len, shared_members)
+PyObject* prefix_groups(PyObject* const* a) {
+  Arg t = need(a[1], "block_table"), len = need(a[2], "seq_len");
+  if (t->dim() != 2 || t->scalar_type() != at::kInt || !t->is_contiguous())
+    refuse("block_table must be a contiguous int32 [B][max_blocks]");
+  const int64_t B = t->size(0);
+  if (B > INT32_MAX || t->size(1) > INT32_MAX) refuse("block_table: too large");
+  if ((a[5] == Py_None) != (a[6] == Py_None)) refuse("length and members: give both or neither");
+  at::Tensor length, members;
+  if (a[5] == Py_None) {
+    at::AutoDispatchBelowADInplaceOrView plain;  // no gradients are kept here
+    const at::Tensor both = at::empty({2 * B}, t->options());  // one allocation
+    length = both.as_strided({B}, {1}, 0), members = both.as_strided({B}, {1}, B);
+  } else {
+    grid<int32_t>(a[5], 1, B, "length"), grid<int32_t>(a[6], 1, B, "members");
+    length = THPVariable_Unpack(a[5]), members = THPVariable_Unpack(a[6]);
+  }
+  done("sv_prefix_groups", api.prefix_groups(handle_of(a[0]), (int)B, vec<int32_t>(a[2], B, "seq_len"), ptr<int32_t>(*t.t),
+                                             (int)t->size(1), integer(a[3]), integer(a[4]), ptr<int32_t>(length),
+                                             ptr<int32_t>(members), stream_of(a[7])));
+  if (a[5] != Py_None) return PyTuple_Pack(2, a[5], a[6]);
+  PyObject *l = THPVariable_Wrap(length), *m = THPVariable_Wrap(members), *r = PyTuple_Pack(2, l, m);
+  Py_DECREF(l), Py_DECREF(m);
+  return r;
 }
 
 // (handle, logits, out, V, history, tokens, mask, n_nodes, rep, presence, frequency, bias_ids, bias_values, allowed, stream)
@@ -394,7 +457,7 @@ PyObject* open_library(PyObject*, PyObject* args) {
   decltype(&sv_append_args_size) append_size, attention_size, logits_size;
   if (!sym("sv_tree_mask", api.tree_mask) || !sym("kv_append", api.append) || !sym("kv_read", api.read) ||
       !sym("sv_attention_workspace_size", api.attention_size) || !sym("sv_tree_attention", api.attention) ||
-      !sym("sv_adjust_logits", api.logits) || !sym("sv_append_args_size", append_size) ||
+      !sym("sv_adjust_logits", api.logits) || !sym("sv_prefix_groups", api.prefix_groups) || !sym("sv_append_args_size", append_size) ||
       !sym("sv_attention_args_size", attention_size) || !sym("sv_logits_args_size", logits_size))
     return nullptr;
   if (append_size() != sizeof(sv_append_args) || attention_size() != sizeof(sv_attention_args) ||
@@ -414,6 +477,9 @@ PyMethodDef kMethods[] = {{"open", open_library, METH_VARARGS, nullptr},
                           SV_CALL("read", read, 9),
                           SV_CALL("attention_args", attention_args, 11),
                           SV_CALL("attention", attention, 13),
+                          SV_CALL("attention_args_forms", attention_args_forms, 17),
+                          SV_CALL("attention_forms", attention_forms, 19),
+                          SV_CALL("prefix_groups", prefix_groups, 8),
                           SV_CALL("logits", logits, 15),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -18,7 +18,8 @@ constexpr int kSimtThreads = 32 * kSimtWarps;
 // rows (16 FMA to five shared-memory reads), latency with few: fewer rows a warp
 // then.  One request of 6 rows over 38 keys, 4 heads of 64: 18.8 us with 4 rows a
 // warp and a tile's loads one after another, 10.2 us as it is.
-template <bool F32, int RPW>
+// X: the scores may have a form (capped, less with the distance, a window).
+template <bool F32, int RPW, bool X>
 __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __grid_constant__ AttnParams P) {
   pdl_wait();
   pdl_trigger();
@@ -34,7 +35,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
   const int blocks = (a.R * G + kSimtRows - 1) / kSimtRows;
   const int item = blockIdx.x, rb = item % blocks, h = item / blocks % H, b = item / blocks / H;
   const int split = blockIdx.y;
-  const Extent X = extent_of(a, b, P.err);
+  const Extent E = extent_of(a, b, P.err);
   const int row0 = rb * kSimtRows;
   const int64_t q0 = b * a.q_stride[0], o0 = b * a.out_stride[0];
   // rows of this block that are past the request's entries are zero
@@ -42,11 +43,12 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
     for (int c = threadIdx.x; c < kSimtRows * (D / 8); c += kSimtThreads) {
       const int r = row0 + c / (D / 8), i = r / G;
       const float zero[8] = {};
-      if (i < a.R && i > X.n)
+      if (i < a.R && i > E.n)
         store8<F32>(a.out, o0 + i * a.out_stride[1] + (h * G + r % G) * a.out_stride[2] + c % (D / 8) * 8, zero);
     }
-  if (row0 / G > X.n) return;
-  const int keys = X.S + X.n + 1, tiles = (keys + kSimtKeys - 1) / kSimtKeys;
+  if (row0 / G > E.n) return;
+  const int begin = X ? first_seen(a, E.S) : 0;
+  const int keys = E.S + E.n + 1, tiles = (keys - begin + kSimtKeys - 1) / kSimtKeys;
   const int per = (tiles + P.splits - 1) / P.splits;
   const int t0 = split * per, t1 = min(tiles, t0 + per);
   const int used = (tiles + per - 1) / per;  // shares with work
@@ -55,7 +57,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
   for (int c = threadIdx.x; c < kSimtRows * (D / 8); c += kSimtThreads) {
     const int r = row0 + c / (D / 8), i = r / G, d = c % (D / 8) * 8;
     float x[8] = {};
-    if (i <= X.n) load8<F32>(a.q, q0 + i * a.q_stride[1] + (h * G + r % G) * a.q_stride[2] + d, x);
+    if (i <= E.n) load8<F32>(a.q, q0 + i * a.q_stride[1] + (h * G + r % G) * a.q_stride[2] + d, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sQ[c / (D / 8) * DP + d + e] = x[e] * (a.scale * kLog2e);
   }
@@ -68,7 +70,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
   }
   const float* q = sQ + warp * kRowsPerWarp * DP;
   for (int t = t0; t < t1; ++t) {
-    const int x0 = t * kSimtKeys;
+    const int x0 = begin + t * kSimtKeys;
     __syncthreads();
     constexpr int kAt = 2;  // vectors of K and of V on their way
     for (int c0 = threadIdx.x; c0 < kSimtKeys * (D / 8); c0 += kAt * kSimtThreads) {
@@ -79,9 +81,9 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
 #pragma unroll
         for (int e = 0; e < 8; ++e) k[u][e] = v[u][e] = 0.0f;
         if (j >= kSimtKeys || x >= keys) continue;
-        const bool staged = a.stage.data && x >= X.S;
+        const bool staged = a.stage.data && x >= E.S;
         const sv_kv_place& pl = staged ? a.stage : a.cache;
-        const int64_t off = entry_offset(pl, b, x - X.S, x);
+        const int64_t off = entry_offset(pl, b, x - E.S, x);
         if (off >= 0) {
           const int64_t step = staged ? sstep : cstep;
           const char* kr = static_cast<const char*>(pl.data) + off + h * step;
@@ -114,11 +116,19 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
       }
     }
     float p[kRowsPerWarp];
+    // where this lane's key is, past S
+    const int at = !X || x0 + lane < E.S || x0 + lane >= keys ? x0 + lane - E.S : depth_of(a, b, x0 + lane - E.S);
 #pragma unroll
     for (int r = 0; r < kRowsPerWarp; ++r) {
       const int i = (row0 + warp * kRowsPerWarp + r) / G;
-      const uint32_t bits = i > X.n ? 0u : seen_bits(a, b, i, X.n, x0 - X.S);
-      const bool see = bits >> lane & 1;
+      const uint32_t bits = i > E.n ? 0u : seen_bits(a, b, i, E.n, x0 - E.S);
+      bool see = bits >> lane & 1;
+      if (X) {
+        const int hq = h * G + (row0 + warp * kRowsPerWarp + r) % G, far = i > E.n ? 0 : abs(depth_of(a, b, i) - at);
+        if (a.softcap > 0.0f) s[r] = (a.softcap * kLog2e) * tanhf(s[r] / (a.softcap * kLog2e));
+        if (a.slopes) s[r] -= a.slopes[hq] * kLog2e * (float)far;
+        if (a.window > 0 && far >= a.window) see = false;
+      }
       // a key that is not seen takes no part, whatever its score is; a NaN
       // score that is seen stays NaN through the sums
       float mx = see ? s[r] : -__int_as_float(0x7F800000);
@@ -207,7 +217,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
 #pragma unroll
   for (int r = 0; r < kRowsPerWarp; ++r) {
     const int row = row0 + warp * kRowsPerWarp + r, i = row / G;
-    if (i > X.n) continue;
+    if (i > E.n) continue;
     const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
     const int64_t at = o0 + i * a.out_stride[1] + (h * G + row % G) * a.out_stride[2];
 #pragma unroll
@@ -372,6 +382,8 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
 
 using namespace sv;
 
+static bool has_form(const sv_attention_args* a) { return a->softcap > 0.0f || a->slopes || a->window > 0; }
+
 static sv_status check(const sv_handle* h, const sv_attention_args* a) {
   if (!h || !a || a->B < 0 || a->R < 1 || a->Hq < 1 || (a->dtype != SV_BF16 && a->dtype != SV_FP32)) return SV_ERR_INVALID;
   if (a->B == 0) return SV_OK;
@@ -385,6 +397,8 @@ static sv_status check(const sv_handle* h, const sv_attention_args* a) {
     return SV_ERR_INVALID;
   if (a->mask && a->mask_ld < (a->R + 31) / 32) return SV_ERR_INVALID;
   if (!(a->scale == a->scale)) return SV_ERR_INVALID;
+  if (!(a->softcap == 0.0f || (a->softcap >= 0x1p-60f && a->softcap <= 0x1p60f)) || a->window < 0) return SV_ERR_INVALID;
+  if (!a->shared_len != !a->shared_members) return SV_ERR_INVALID;
   if ((a->dtype == SV_FP32) != (a->cache.format == SV_KV_FP32)) return SV_ERR_UNSUPPORTED;
   if (simt_items(a) > INT32_MAX) return SV_ERR_UNSUPPORTED;
   return SV_OK;
@@ -399,7 +413,7 @@ extern "C" sv_status sv_attention_workspace_size(sv_handle* h, const sv_attentio
   *bytes = 256;
   if (a->B == 0) return SV_OK;
   const TcPlan plan = tc_plan(h, a);
-  if (plan.use) {
+  if (plan.use && !has_form(a)) {
     *bytes = plan.bytes;
     return SV_OK;
   }
@@ -417,7 +431,7 @@ extern "C" sv_status sv_tree_attention(sv_handle* h, const sv_attention_args* a,
   if (a->B == 0) return SV_OK;
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < need) return SV_ERR_INVALID;
   const TcPlan plan = tc_plan(h, a);
-  if (plan.use) return tc_launch(h, a, plan, ws, (cudaStream_t)stream);
+  if (plan.use && !has_form(a)) return tc_launch(h, a, plan, ws, (cudaStream_t)stream);
   const int64_t items = simt_items(a);
   AttnParams P;
   P.a = *a;
@@ -427,9 +441,11 @@ extern "C" sv_status sv_tree_attention(sv_handle* h, const sv_attention_args* a,
   P.splits = simt_splits(h, a, items);
   const size_t smem = (size_t)(2 * kSimtKeys + simt_rows(a)) * (a->cache.head_dim + 4) * 4;
   typedef void (*Fn)(AttnParams);
-  static const Fn fns[2][3] = {{simt_attention_kernel<false, 1>, simt_attention_kernel<false, 2>, simt_attention_kernel<false, 4>},
-                               {simt_attention_kernel<true, 1>, simt_attention_kernel<true, 2>, simt_attention_kernel<true, 4>}};
-  const Fn fn = fns[a->dtype == SV_FP32][simt_rows(a) / 8];
+#define SV_SIMT(x) {{simt_attention_kernel<false, 1, x>, simt_attention_kernel<false, 2, x>, simt_attention_kernel<false, 4, x>}, \
+                    {simt_attention_kernel<true, 1, x>, simt_attention_kernel<true, 2, x>, simt_attention_kernel<true, 4, x>}}
+  static const Fn fns[2][2][3] = {SV_SIMT(false), SV_SIMT(true)};
+#undef SV_SIMT
+  const Fn fn = fns[has_form(a)][a->dtype == SV_FP32][simt_rows(a) / 8];
   const sv_status rr = sv_raise_dyn_smem((const void*)fn, smem);
   if (rr != SV_OK) return rr;
   if (sv_launch_pdl(fn, dim3((unsigned)items, (unsigned)P.splits), dim3(kSimtThreads), smem, (cudaStream_t)stream, P) !=
