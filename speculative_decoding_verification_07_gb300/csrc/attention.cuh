@@ -12,6 +12,7 @@ struct AttnParams {
   uint32_t* ticket; // arrivals per shared item, zero between calls
   int* err;
   int splits;
+  float* carry;  // set: rows of requests that share a prefix go on from its part (see Carry)
 };
 
 // A request's extent: S cached positions, then n + 1 entries (n = -1: none).
@@ -57,5 +58,11 @@ __device__ __forceinline__ int depth_of(const sv_attention_args& a, int b, int i
 
 // The first cached position that any row of request b may see: no row sits before S.
 __device__ __forceinline__ int first_seen(const sv_attention_args& a, int S) { return a.window > 0 ? max(0, S - a.window + 1) : 0; }
+
+// The positions that request b shares with its group, whole blocks.
+__device__ __forceinline__ int shared_of(const sv_attention_args& a, int b) {
+  const int n = a.shared_len[b], S = a.seq_len[b];
+  return n <= 0 || n > S || S > (int64_t)a.cache.max_blocks * a.cache.block_size ? 0 : n / a.cache.block_size * a.cache.block_size;
+}
 
 }  // namespace sv

@@ -22,7 +22,30 @@ struct TcParams {
   int block_shift;  // log2 of block_size, -1 if it is no power of two
   int group;        // G: query heads of a KV head
   uint32_t group_magic;  // ceil(2^32 / G), 0 for G = 1: a row's entry without a division
+  // of calls with forms or shared prefixes
+  int forms, sharing;  // whether scores have a form; 1 where requests share prefixes
+  float* carry;        // outputs of parts: the prefix's, and the request's own (see Carry)
 };
+
+// Parts of rows that are joined by a later kernel: a prefix's, computed for a group's
+// rows together, and a request's own where that is long.  Each is [request][KV head][row
+// of the head] rows of D outputs relative to a reference in log2 units, then the rows'
+// (reference, sum).
+struct Carry {
+  float* o;
+  float2* ml;
+};
+__host__ __device__ __forceinline__ int64_t carry_rows(const sv_attention_args& a) {
+  return ((int64_t)a.B * a.R * a.Hq + 1) / 2 * 2;  // parts start at multiples of 16 bytes
+}
+__device__ __forceinline__ Carry carry_of(const sv_attention_args& a, float* carry, int own) {
+  const int64_t rows = carry_rows(a);
+  float* at = carry + own * rows * (a.cache.head_dim + 2);
+  return {at, reinterpret_cast<float2*>(at + rows * a.cache.head_dim)};
+}
+// Keys of its own up to which a request's part is not worth an item of the tensor
+// kernel, whose start and end cost six tiles' time.
+constexpr int kOwnShort = 128;
 
 // The instruction cache is shared by roles that run different code at the same
 // time: with every wait, walk and division inlined the kernel was 138 KB and
@@ -43,7 +66,8 @@ __device__ __forceinline__ int entry_of(const TcParams& P, int row) {  // row / 
 //           weighs a half (a quarter) of a tile's keys: all warps share the
 //           exponentials of a few rows, and a product of 128 rows costs the same.
 //   QM = 2: more rows; the streams are two row tiles that share every key tile.
-template <bool F8, int D, int QM>
+//   X: scores may have a form, requests may share prefixes.
+template <bool F8, int D, int QM, bool X>
 struct TcShape {
   // two softmax groups of four warps; K loads; products; V loads; one for scales
   // and dead rows
@@ -57,7 +81,7 @@ struct TcShape {
   static constexpr int kStep = F8 ? 32 : 16;                 // keys of one product of weights and V
   static constexpr int kRows = kTile * QM;
   static constexpr int kQAll = QM * kQBytes > 32768 ? QM * kQBytes : 32768;  // also holds 128 x 64 outputs, 32 of each half
-  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 2 * kTile * 4 + 2 * kTile * 4 : 0);
+  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 2 * kTile * 4 + 2 * kTile * 4 + (X ? 128 : 0) : 0);
   // tiles held; a slot of K has its keys' tails and V's
   static constexpr int kTails = F8 ? 2 * kTile * kTail : 0, kKBytes = kTileBytes + kTails;
   static constexpr int kRoom = 232448 - 1024 - kMisc - kQAll, kPairs = kRoom / (kTileBytes + kKBytes);
@@ -88,25 +112,59 @@ constexpr int kLeastFew = 2, kLeastMany = 4, kFewRows = 32;
 // instructions to arrive more than for anything else).
 static __device__ __noinline__ uint32_t quotient(uint32_t a, uint32_t b) { return a / b; }
 
+// An item's place in the list.  X: `pre` items are a group's prefix for all its
+// rows, the others a request's own positions from `begin` on; carry says where an
+// item's outputs go: 0 out, 1 the prefix's parts, 2 the own ones'.
 struct TcWalk {
   int qrows, w, w1, b, base, T, items, tp, blocks;
   Extent X;
+  int begin, carry;
   __device__ __forceinline__ int count() const { return T * items; }
 };
 
 // The units of a request of extent X.
-static __device__ __noinline__ void plan(const TcParams& P, TcWalk& k, int b, Extent X) {
+template <bool X>
+static __device__ __noinline__ void plan(const TcParams& P, TcWalk& k, int b, Extent E) {
   const sv_attention_args& a = P.p.a;
-  k.b = b, k.X = X;
+  k.b = b, k.X = E;
   k.T = 0, k.items = 0, k.tp = 0, k.blocks = 1;
-  if (X.n < 0) return;
-  k.blocks = ((X.n + 1) * P.group + k.qrows - 1) >> (k.qrows == kTile ? 7 : 8);
+  if (E.n < 0) return;
+  k.blocks = ((E.n + 1) * P.group + k.qrows - 1) >> (k.qrows == kTile ? 7 : 8);
   k.items = a.cache.heads * k.blocks;
-  k.tp = (X.S + (a.stage.data ? 0 : X.n + 1) + kTile - 1) / kTile;
-  k.T = kLead + (a.stage.data ? k.tp + (X.n + kTile) / kTile : k.tp);
+  const bool staged = a.stage.data && !(X && k.carry == 1);
+  const int cached = E.S - (X ? k.begin : 0) + (a.stage.data || (X && k.carry == 1) ? 0 : E.n + 1);
+  k.tp = (cached + kTile - 1) / kTile;
+  k.T = kLead + (staged ? k.tp + (E.n + kTile) / kTile : k.tp);
 }
-static __device__ __forceinline__ void walk_to(const TcParams& P, TcWalk& k, int b) {
-  plan(P, k, b, extent_of(P.p.a, b, P.p.err));
+// Request b's item kinds; X with shared prefixes: 2 b is the prefix of the group that b
+// starts, 2 b + 1 the request's own part.
+template <bool X>
+static __device__ __forceinline__ void walk_to(const TcParams& P, TcWalk& k, int v) {
+  const sv_attention_args& a = P.p.a;
+  if (!X) {
+    plan<X>(P, k, v, extent_of(a, v, P.p.err));
+    return;
+  }
+  const int b = v >> P.sharing;
+  k.begin = k.carry = 0;
+  Extent E;
+  if (P.sharing && !(v & 1)) {
+    const int m = a.shared_members[b];
+    k.carry = 1;
+    E.S = shared_of(a, b);
+    E.n = E.S > 0 && m > 0 && m <= a.B - b ? m * a.R - 1 : -1;
+  } else {
+    E = extent_of(a, b, P.p.err);
+    if (P.sharing) {
+      if ((k.begin = shared_of(a, b)) > 0) {
+        k.carry = 2;
+        if (E.S - k.begin + E.n + 1 <= kOwnShort) E.n = -1;  // the joining kernel's
+      }
+    } else {
+      k.begin = first_seen(a, E.S) & -P.box;  // a TMA box starts at a multiple of its rows
+    }
+  }
+  plan<X>(P, k, v, E);
 }
 
 // floor(x * m / d); small products without a 64-bit division, whose code alone
@@ -120,16 +178,18 @@ static __device__ __noinline__ int mul_div(int x, int m, int d) {
 struct TcSegment {
   int b, h, rb, t0, t1, T, tp, item0;  // T: units of the item, item0: where it starts in the list
   Extent X;
+  int begin, carry;
 };
 
 // The next segment (one item's consecutive tiles); false at the end.  A share's
 // bounds inside a short item move to the item's nearer end, the same for both
 // neighbours: joining its parts would take longer than its tiles.
+template <bool X>
 static __device__ __noinline__ bool next_segment(const TcParams& P, TcWalk& k, TcSegment& s) {
   while (k.w < k.w1) {
     while (k.w >= k.base + k.count()) {
       k.base += k.count();
-      walk_to(P, k, k.b + 1);
+      walk_to<X>(P, k, k.b + 1);
     }
     const int at = k.w - k.base, item = (int)quotient(at, k.T), item0 = k.base + item * k.T;
     int from = k.w - item0, to = min(k.T, k.w1 - item0);
@@ -139,11 +199,12 @@ static __device__ __noinline__ bool next_segment(const TcParams& P, TcWalk& k, T
     }
     k.w = min(k.w1, item0 + k.T);
     if (to <= kLead) continue;  // none of the item's tiles
-    s.b = k.b, s.h = k.blocks == 1 ? item : (int)quotient(item, k.blocks), s.rb = item - s.h * k.blocks;
+    s.b = X ? k.b >> P.sharing : k.b, s.h = k.blocks == 1 ? item : (int)quotient(item, k.blocks), s.rb = item - s.h * k.blocks;
     s.T = k.T, s.tp = k.tp, s.X = k.X;
     s.t0 = max(0, from - kLead);
     s.t1 = to - kLead;
     s.item0 = item0;
+    if (X) s.begin = k.begin, s.carry = k.carry;
     return true;
   }
   return false;
@@ -166,15 +227,48 @@ struct TcTile {
   int x0, valid, u0;
 };
 
+template <bool X>
 __device__ __forceinline__ TcTile tile_of(const sv_attention_args& a, const TcSegment& s, int t) {
   TcTile k;
-  k.staged = a.stage.data && t >= s.tp;
-  k.x0 = k.staged ? (t - s.tp) * kTile : t * kTile;
-  const int limit = k.staged ? s.X.n + 1 : a.stage.data ? s.X.S : s.X.S + s.X.n + 1;
+  const bool apart = a.stage.data || (X && s.carry == 1);  // no entries among the cached positions
+  k.staged = a.stage.data && !(X && s.carry == 1) && t >= s.tp;
+  k.x0 = k.staged ? (t - s.tp) * kTile : (X ? s.begin : 0) + t * kTile;
+  const int limit = k.staged ? s.X.n + 1 : apart ? s.X.S : s.X.S + s.X.n + 1;
   k.valid = min(kTile, limit - k.x0);
   k.u0 = k.staged ? k.x0 : k.x0 - s.X.S;
-  k.prefix = !k.staged && (a.stage.data || k.x0 + k.valid <= s.X.S);
+  k.prefix = !k.staged && (apart || k.x0 + k.valid <= s.X.S);
   return k;
+}
+
+// Whose row a row of an item is: the request, the entry and the query head.  The
+// prefix's items have the rows of all members, R entries each.
+struct TcRow {
+  int b, i, hq;
+};
+template <bool X>
+__device__ __forceinline__ TcRow row_of(const TcParams& P, const TcSegment& s, int row) {
+  const int e = entry_of(P, row), hq = s.h * P.group + row - e * P.group;
+  if (!X || s.carry != 1) return {s.b, e, hq};
+  const int m = e / P.p.a.R;
+  return {s.b + m, e - m * P.p.a.R, hq};
+}
+// Where the outputs of a row of an item go in a part.
+__device__ __forceinline__ int64_t carry_row(const sv_attention_args& a, int group, const TcRow& r) {
+  return (((int64_t)r.b * a.cache.heads + r.hq / group) * a.R + r.i) * group + r.hq % group;
+}
+
+// Rows of V in a tile, [r0, r1), that some row of the item may not see though another
+// does, or that are next to such: entries, and with a window the positions that the
+// deepest row no longer sees.
+template <bool X>
+__device__ __forceinline__ void half_seen(const sv_attention_args& a, const TcTile& k, const TcSegment& s, int* r0, int* r1) {
+  const bool tree = X ? !k.prefix : k.valid > -k.u0 && !(a.stage.data && !k.staged);
+  *r0 = tree ? max(0, -k.u0) : k.valid;
+  *r1 = k.valid;
+  if (X && a.window > 0 && !k.staged) {
+    const int last = (int)min((int64_t)k.valid, (int64_t)s.X.S + a.R - a.window - k.x0);
+    if (last > 0) *r0 = 0, *r1 = tree ? k.valid : last;
+  }
 }
 
 // Waits are bounded (1 s): one that runs out reports SV_ERR_TIMEOUT and turns
@@ -279,15 +373,20 @@ __device__ __forceinline__ float above_log2(float x) { return (float)((int)(__fl
 
 // What non-finite values of V, cleared from a segment's tiles, add to column
 // `col` of entry i's row: 0, or an infinity or NaN.
+template <bool X>
 static __device__ __noinline__ float given_back(const TcParams& P, const TcSegment& seg, int i, int col) {
   const sv_attention_args& a = P.p.a;
   float sum = 0.0f;
   for (int t = seg.t0; t < seg.t1; ++t) {
-    const TcTile k = tile_of(a, seg, t);
-    if (a.stage.data && !k.staged) continue;
+    const TcTile k = tile_of<X>(a, seg, t);
+    if (!X && a.stage.data && !k.staged) continue;
     const sv_kv_place& pl = k.staged ? a.stage : a.cache;
-    for (int r = max(0, -k.u0); r < k.valid; ++r) {
-      if (!(seen_bits(a, seg.b, i, seg.X.n, k.u0 + r) & 1)) continue;
+    int r0 = max(0, -k.u0), r1 = k.valid;
+    if (X) half_seen<X>(a, k, seg, &r0, &r1);
+    for (int r = r0; r < r1; ++r) {
+      const int u = k.u0 + r;
+      if (u >= 0 && !(seen_bits(a, seg.b, i, seg.X.n, u) & 1)) continue;
+      if (X && a.window > 0 && abs(depth_of(a, seg.b, i) - (u < 0 ? u : depth_of(a, seg.b, u))) >= a.window) continue;
       const int64_t off = entry_offset(pl, seg.b, k.x0 + r, k.x0 + r);
       if (off < 0) continue;
       const char* vr = static_cast<const char*>(pl.data) + off + (a.cache.heads + seg.h) * row_step(pl);
@@ -319,17 +418,121 @@ static __device__ __noinline__ void hide_unseen(const TcParams& P, int b, int i,
   tmem_wait_st();
 }
 
+// What a row's scores get from their form.
+struct TcForm {
+  int at;       // the row's position
+  float slope;  // of its head, log2 units
+};
+
+// Scores of a tile become what the softmax takes: times c (and K's scales ks), capped,
+// less the distance's share, -inf where row i does not see the key; log2 units.  In a
+// pass of its own over tensor memory: inside the softmax's loop it would be there
+// twice (once more where a reference moves).
+//   cap tanh(s / cap) = cap - 2 cap / (1 + 2^(2 s log2(e) / cap)); where all of a group's
+// scores are below 0.3 cap, as nearly all are, the series of tanh to the ninth power
+// (the next term is 5e-8 of it) saves two of the three special functions an element.
+template <bool F8>
+static __device__ __noinline__ void shape_scores(const TcParams& P, const TcSegment& seg, const TcTile& k, const TcForm& f, int i,
+                                                 float c, const float* ks, int ch_a, int ch_e, uint32_t tS) {
+  const sv_attention_args& a = P.p.a;
+  const float cap = a.softcap * kLog2e, per = a.softcap > 0.0f ? 1.0f / cap : 0.0f;
+  const uint64_t c2 = pair(c, c), slope2 = pair(f.slope, f.slope), one2 = pair(1.0f, 1.0f);
+#pragma unroll 1
+  for (int ch = ch_a; ch < ch_e; ++ch) {
+    uint32_t x[32];
+    uint64_t v[16];
+    tmem_ld32(tS + 32 * ch, x);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      v[e] = mul2(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2);
+      v[e + 1] = mul2(pair(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3])), c2);
+      if (F8) {
+        const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(ks + 32 * ch + 2 * e);
+        v[e] = mul2(v[e], s2.x), v[e + 1] = mul2(v[e + 1], s2.y);
+      }
+    }
+    if (a.softcap > 0.0f) {
+      const uint64_t per2 = pair(per, per);
+      float most[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float2 y = unpair(v[e]);
+        most[e & 3] = fmaxf(most[e & 3], fmaxf(fabsf(y.x), fabsf(y.y)));
+      }
+      if (!__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * per > 0.3f)) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint64_t w = mul2(v[e], per2), w2 = mul2(w, w);
+          uint64_t t = fma2(w2, pair(62.0f / 2835.0f, 62.0f / 2835.0f), pair(-17.0f / 315.0f, -17.0f / 315.0f));
+          t = fma2(w2, t, pair(2.0f / 15.0f, 2.0f / 15.0f));
+          t = fma2(w2, t, pair(-1.0f / 3.0f, -1.0f / 3.0f));
+          v[e] = mul2(v[e], fma2(w2, t, one2));
+        }
+      } else {
+        const float up = 2.0f * kLog2e * per;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 y = unpair(v[e]);
+          float z[2] = {y.x, y.y};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float w = z[h] * per, w2 = w * w;
+            const float small = z[h] * (1.0f + w2 * (-1.0f / 3.0f + w2 * (2.0f / 15.0f + w2 * (-17.0f / 315.0f + w2 * (62.0f / 2835.0f)))));
+            const float large = cap - 2.0f * cap * rcp(1.0f + ex2(z[h] * up));
+            z[h] = fabsf(w) < 0.3f ? small : large;
+          }
+          v[e] = pair(z[0], z[1]);
+        }
+      }
+    }
+    // keys between the nearest and the window's edge; among the entries both depend
+    // on the keys' depths
+    const int left = k.valid - 32 * ch;
+    uint32_t bits = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u;
+    if (k.prefix) {
+      const int far = f.at - (k.x0 + 32 * ch);  // of the first key
+      if (a.window > 0 && far >= a.window) bits &= far - a.window >= 31 ? 0u : 0xFFFFFFFEu << (far - a.window);
+      if (a.slopes) {
+        const float b = (float)far;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = fma2(slope2, pair((float)(2 * e) - b, (float)(2 * e + 1) - b), v[e]);
+      }
+    } else {
+      bits &= i <= seg.X.n ? seen_bits(a, seg.b, i, seg.X.n, k.u0 + 32 * ch) : 0u;
+      if (a.slopes || a.window > 0) {
+        const int d = f.at - seg.X.S;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int u = k.u0 + 32 * ch + 2 * e;
+          const int far0 = abs(d - (u < 0 || u > seg.X.n ? u : depth_of(a, seg.b, u)));
+          const int far1 = abs(d - (u + 1 < 0 || u + 1 > seg.X.n ? u + 1 : depth_of(a, seg.b, u + 1)));
+          if (a.window > 0) bits &= ~((far0 >= a.window ? 1u : 0u) << (2 * e) | (far1 >= a.window ? 1u : 0u) << (2 * e + 1));
+          if (a.slopes) v[e] = fma2(slope2, pair(-(float)far0, -(float)far1), v[e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 y = unpair(v[e]);
+      x[2 * e] = bits >> (2 * e) & 1 ? __float_as_uint(y.x) : 0xFF800000u;
+      x[2 * e + 1] = bits >> (2 * e + 1) & 1 ? __float_as_uint(y.y) : 0xFF800000u;
+    }
+    tmem_st32(tS + 32 * ch, x);
+  }
+  tmem_wait_st();
+}
+
 // The references (m, weights') of the rows that need others for 32 scores: a whole
 // number at or above the largest score, and above the largest product of p and V's
 // scale, or what kMaxRaise leaves.  Both stay -inf for a row that sees nothing.
-static __device__ __noinline__ float2 references(uint32_t tS, float c, const float* sc, float m, float wr, bool need) {
+static __device__ __noinline__ float2 references(uint32_t tS, float c, const float* kp, const float* sc, float m, float wr, bool need) {
   uint32_t x[32];
   tmem_ld32(tS, x);
   if (!need) return make_float2(m, wr);
   float mx = m, top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
-    const float4 ks = *reinterpret_cast<const float4*>(sc + e);
+    const float4 ks = *reinterpret_cast<const float4*>(kp + e);
     const float s[4] = {__uint_as_float(x[e]) * c * ks.x, __uint_as_float(x[e + 1]) * c * ks.y, __uint_as_float(x[e + 2]) * c * ks.z,
                         __uint_as_float(x[e + 3]) * c * ks.w};
 #pragma unroll
@@ -409,6 +612,28 @@ static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r
   fence_async_smem();
 }
 
+// Whether every request is in the group that its shared_len says, by a warp a request:
+// members that agree with their first, no group inside another, none past the batch.
+static __device__ __noinline__ void check_groups(const sv_attention_args& a, int* err) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const int own = shared_of(a, b), m = a.shared_members[b];
+    bool bad = m < 0 || m > a.B - b;
+    if (!bad)
+      for (int j = 1 + lane; j < m; j += 32) bad |= shared_of(a, b + j) != own || a.shared_members[b + j] != 0;
+    if (own > 0 && m == 0) {  // the nearest request before it that starts a group
+      int first = -1;
+      for (int j0 = b - 1; j0 >= 0 && first < 0; j0 -= 32) {
+        const uint32_t starts = __ballot_sync(0xFFFFFFFFu, j0 - lane >= 0 && a.shared_members[max(0, j0 - lane)] != 0);
+        if (starts) first = j0 - (__ffs(starts) - 1);
+      }
+      bad |= first < 0 || a.shared_members[max(0, first)] <= b - first;
+    }
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) report(err, SV_ERR_STATE);
+  }
+}
+
 // o = sum_x p_x V_x, p = softmax(scale q K^T), in one pass over the keys: scores
 // of 128 rows and 128 keys as a product with its result in tensor memory, their
 // weights against the running reference maximum back into the same columns, and
@@ -424,9 +649,9 @@ static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r
 // to 65536 positions, 448 rows a head, bf16: 184 us, 0.85 PFLOP/s; what the products'
 // warp does between products (waits, commits: a third of its time) bounds that.  Handing scores over in halves
 // of 64 keys, to have the next half's under way, doubled those steps: 249 us.
-template <bool F8, int D, int QM>
-__global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_kernel(const __grid_constant__ TcParams P) {
-  using C = TcShape<F8, D, QM>;
+template <bool F8, int D, int QM, bool X>
+__global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attention_kernel(const __grid_constant__ TcParams P) {
+  using C = TcShape<F8, D, QM, X>;
   extern __shared__ char smem_raw[];
   const sv_attention_args& a = P.p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -450,6 +675,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
   float* s_qs = reinterpret_cast<float*>(misc + 3072);    // [kRows] row scales of 8-bit queries
   float* s_sc = s_qs + C::kRows;                          // [kScaleRing][2][128] scales of a tile's entries, K's and V's
   float* s_wr = s_sc + kScaleRing * 2 * kTile;            // [256] references of 8-bit weights, exchanged
+  float* s_ones = s_wr + 2 * kTile;                       // [32] K's scales of scores that have them already
 
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) mbar_init(b_kf + 8 * i, 1), mbar_init(b_ke + 8 * i, QM);
@@ -463,6 +689,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     if (a.stage.data) tma_prefetch_map(&P.stage);
   }
   if (warp == 9) tmem_alloc(smem_u32(&ints[0]), 512);
+  if (X && F8 && warp == 11) s_ones[lane] = 1.0f;
   pdl_wait();
   pdl_trigger();
 
@@ -476,15 +703,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     ctas = min((int)gridDim.x, (total + least - 1) / least);
     if ((int)blockIdx.x < ctas) w0 = mul_div(total, blockIdx.x, ctas), w1 = mul_div(total, blockIdx.x + 1, ctas);
   };
-  if (a.B <= 4) {  // every thread counts for itself
+  const int B = X ? a.B << P.sharing : a.B;
+  if (B <= 4) {  // every thread counts for itself
 #pragma unroll 1
-    for (int b = 0; b < a.B; ++b) walk_to(P, walk, b), total += walk.count();
+    for (int b = 0; b < B; ++b) walk_to<X>(P, walk, b), total += walk.count();
     share();
     walk.base = 0;
-    if (w1 > w0 && a.B > 1) {
+    if (w1 > w0 && B > 1) {
 #pragma unroll 1
       for (int b = 0;; walk.base += walk.count(), ++b) {
-        walk_to(P, walk, b);
+        walk_to<X>(P, walk, b);
         if (w0 < walk.base + walk.count()) break;
       }
     }
@@ -492,10 +720,10 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     __syncthreads();
     tc_fence_after();
   } else {
-    const int per = (a.B + C::kThreads - 1) / C::kThreads;
-    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    const int per = (B + C::kThreads - 1) / C::kThreads;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     int mine = 0;
-    for (int b = b0; b < b1; ++b) walk_to(P, walk, b), mine += walk.count();
+    for (int b = b0; b < b1; ++b) walk_to<X>(P, walk, b), mine += walk.count();
     int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -514,7 +742,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     if (w1 > w0 && mine > 0 && first <= w0 && w0 < first + mine) {
       int at = first;
       for (int b = b0; b < b1; ++b) {
-        if (per > 1) walk_to(P, walk, b);
+        if (per > 1) walk_to<X>(P, walk, b);
         if (w0 < at + walk.count()) {
           ints[4] = b, ints[5] = at, ints[8] = walk.X.S, ints[9] = walk.X.n;
           break;
@@ -528,7 +756,10 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     walk.base = 0;
     if (w1 > w0) {
       walk.base = ints[5];
-      plan(P, walk, ints[4], Extent{ints[8], ints[9]});
+      if (X)
+        walk_to<X>(P, walk, ints[4]);
+      else
+        plan<X>(P, walk, ints[4], Extent{ints[8], ints[9]});
     }
   }
   walk.w = w0, walk.w1 = w1;
@@ -546,7 +777,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       const uint32_t b_full = v ? b_vf : b_kf, b_empty = v ? b_ve : b_ke, ring = v ? sV : sK;
       constexpr int kElems = F8 ? C::kSw : C::kSw / 2;
       int slot = 0, lap = 0;
-      while (next_segment(P, walk, found)) {
+      while (next_segment<X>(P, walk, found)) {
         const TcSegment seg = found;
         if (!v) {  // the segment's queries, on their way into L2 while the last one's tiles are worked on
           const int rows = min(C::kRows, (seg.X.n + 1) * G - seg.rb * C::kRows);
@@ -555,12 +786,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
           for (int r = lane; r < rows; r += 32) {
             const int rr = seg.rb * C::kRows + r, qi = entry_of(P, rr);
             const __nv_bfloat16* row = q0 + qi * a.q_stride[1] + (rr - qi * G) * a.q_stride[2];
+            if (X && seg.carry == 1) {
+              const TcRow at = row_of<X>(P, seg, rr);
+              row = static_cast<const __nv_bfloat16*>(a.q) + at.b * a.q_stride[0] + at.i * a.q_stride[1] + at.hq * a.q_stride[2];
+            }
             for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
           }
         }
 #pragma unroll 1
         for (int t = seg.t0; t < seg.t1; ++t) {
-          const TcTile k = tile_of(a, seg, t);
+          const TcTile k = tile_of<X>(a, seg, t);
           const int box = k.staged ? kStageBox : P.box, boxes = (k.valid + box - 1) / box;
           // each lane looks up its box's block before the slot is free
           int y = k.x0 + lane * box, w = seg.b;
@@ -605,10 +840,10 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       constexpr uint32_t kIdO = instr_desc(F8 ? 0 : 1, kTile, D, true) | (F8 ? 1u << 7 : 0u);  // weights of 5 exponent bits
       const uint64_t q0 = smem_desc(sQ, 16, 8 * C::kSw, C::kSw), k0 = smem_desc(sK, 16, 8 * C::kSw, C::kSw);
       const uint64_t v0 = smem_desc(sV, C::kHalfBytes, 8 * C::kSw, C::kSw);
-      while (next_segment(P, walk, found)) {
+      while (next_segment<X>(P, walk, found)) {
         const TcSegment seg = found;
         const int units = (seg.t1 - seg.t0) * QM;
-        const int whole = (a.stage.data ? seg.X.S : seg.X.S + seg.X.n + 1) / kTile;  // tiles before it are full
+        const int whole = ((a.stage.data || (X && seg.carry == 1) ? seg.X.S : seg.X.S + seg.X.n + 1) - (X ? seg.begin : 0)) / kTile;  // tiles before it are full
         wait(sync, b_q, ph_q);
         ph_q ^= 1;
         // scores two units ahead of the outputs
@@ -619,7 +854,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
           bool k_there = QM == 2 && st == 1;
           if (x >= 2) {
             const int t = seg.t0 + (QM == 2 ? (x - 2) >> 1 : x - 2);
-            const int steps = t < whole ? kTile / C::kStep : (tile_of(a, seg, t).valid + C::kStep - 1) / C::kStep;
+            const int steps = t < whole ? kTile / C::kStep : (tile_of<X>(a, seg, t).valid + C::kStep - 1) / C::kStep;
             const uint64_t vd = v0 + vs * (C::kTileBytes >> 4);
             const bool first = x < 4;  // of this stream in this segment
             if (QM == 1 || st == 0) {  // the second row tile's keys are there
@@ -672,11 +907,11 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         // entry by cp.async kept this warp 2000 cycles a tile: 64 single tokens
         // 216 us; loading the tails itself 1500: 193.)
         int slot = 0, lap = 0, due = 0;
-        while (next_segment(P, walk, found)) {
+        while (next_segment<X>(P, walk, found)) {
           const TcSegment seg = found;
 #pragma unroll 1
           for (int t = seg.t0; t < seg.t1; ++t, ++due) {
-            const int box = tile_of(a, seg, t).staged ? kStageBox : P.box, ring = due % kScaleRing;
+            const int box = tile_of<X>(a, seg, t).staged ? kStageBox : P.box, ring = due % kScaleRing;
             wait(sync, b_kf + 8 * slot, lap & 1);
             const char* tails = kslots + slot * C::kKBytes + C::kTileBytes;
             float ks[4], vs[4];
@@ -702,6 +937,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
           }
         }
       }
+      if (X && P.sharing) check_groups(a, P.p.err);
       // ---- rows past each request's entries --------------------------------
       for (int r = blockIdx.x; r < a.B * a.R; r += gridDim.x) {
         const int b = r / a.R, i = r - b * a.R;
@@ -716,7 +952,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
     const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t tS = tmem + (quad << 21) + st * 128, tO = tmem + (quad << 21) + 256 + st * 128;
     int kbase = 0, ph_s = 0, ph_o = 0;
-    while (next_segment(P, walk, found)) {
+    while (next_segment<X>(P, walk, found)) {
         const TcSegment seg = found;
       const int n = seg.t1 - seg.t0, units = n * QM;
       const int i0 = seg.rb * C::kRows;
@@ -728,6 +964,12 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       const int lrow = QM == 2 ? st * kTile + row : row - copy * apart;  // row of the CTA's block
       const int i = entry_of(P, i0 + lrow), hq = seg.h * G + i0 + lrow - i * G;
       const bool live = i <= seg.X.n;
+      TcForm form = {};
+      if (X && P.forms && live) {
+        const TcRow at = row_of<X>(P, seg, i0 + lrow);
+        form.at = (seg.carry == 1 ? a.seq_len[at.b] : seg.X.S) + depth_of(a, at.b, at.i);
+        form.slope = a.slopes ? a.slopes[at.hq] * kLog2e : 0.0f;
+      }
       const bool warp_live = lrow - lane < rows;
       // queries: rows of this CTA's block, read once and written to each copy,
       // swizzled as the products read them
@@ -746,7 +988,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
           for (int it = 0; it < kAt; ++it) {
             const int idx = (it0 + it) * kGroup + qt, rr = part0 + idx / kChunks, qi = entry_of(P, rr);
             x8[it] = make_uint4(0, 0, 0, 0);
-            if (it0 + it < each && qi <= seg.X.n)
+            if (X && seg.carry == 1) {
+              if (it0 + it < each && qi <= seg.X.n) {
+                const TcRow at = row_of<X>(P, seg, rr);
+                if (!a.n_nodes || at.i <= a.n_nodes[at.b])
+                  x8[it] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at.b * a.q_stride[0] +
+                                                           at.i * a.q_stride[1] + at.hq * a.q_stride[2] + idx % kChunks * 8);
+              }
+            } else if (it0 + it < each && qi <= seg.X.n)
               x8[it] = *reinterpret_cast<const uint4*>(q0 + qi * a.q_stride[1] + (rr - qi * G) * a.q_stride[2] + idx % kChunks * 8);
           }
 #pragma unroll
@@ -802,13 +1051,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         if (F8) named_barrier(QM == 2 ? 2 + st : 1, kGroup);  // the rows' scales
       }
       // positive (a subnormal at least), so that what is not seen stays -inf when it is scaled
-      const float c = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? s_qs[(QM == 2 ? st * kTile : 0) + row] : 1.0f), 0x1p-149f);
+      const float c_raw = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? s_qs[(QM == 2 ? st * kTile : 0) + row] : 1.0f), 0x1p-149f);
+      const float c = X && P.forms ? 1.0f : c_raw;  // shaped scores have it already
       const uint64_t c2 = pair(c, c);
       // wr: reference of 8-bit weights, log2 units; raise = 2^(kBias + m - wr)
       float m = -kInf, l = 0.0f, wr = -kInf, raise = 0.0f;
       for (int u = st; u < units; u += 2) {
         const int tt = QM == 2 ? u >> 1 : u;
-        const TcTile k = tile_of(a, seg, seg.t0 + tt);
+        const TcTile k = tile_of<X>(a, seg, seg.t0 + tt);
         const int kt = kbase + tt;
         const bool full = k.prefix && k.valid == kTile;
         wait(sync, b_s + 8 * st, ph_s);
@@ -819,7 +1069,10 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         const float* sc = s_sc + (kt % kScaleRing) * 2 * kTile;
         if (warp_live) {
           const int chunks = (k.valid + 31) / 32, ch_e = min(ch_b, chunks);
-          if (!full) hide_unseen(P, seg.b, i, seg.X.n, k.prefix, k.valid, k.u0, ch_a, ch_e, tS);
+          if (X && P.forms)
+            shape_scores<F8>(P, found, k, form, i, c_raw, sc, ch_a, ch_e, tS);
+          else if (!full)
+            hide_unseen(P, seg.b, i, seg.X.n, k.prefix, k.valid, k.u0, ch_a, ch_e, tS);
           // One pass over the tile's scores, 32 columns at a time, so that the
           // loop stays short.  A group of 32 that exceeds the reference by too
           // much rescales what is there, the weights before it included.
@@ -837,12 +1090,13 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
             if (F8) {
               // Weights by the references so far; where a row's sum or largest shows that
               // one is too low, once more after they have moved.
+              const float* kp = X && P.forms ? s_ones : sc + 32 * ch;
               bool bad = m == -kInf, again = false;
               uint64_t gs[2];
 #pragma unroll 1
               while (true) {
                 if (__any_sync(0xFFFFFFFFu, bad)) {
-                  const float2 n = references(tS + 32 * ch, c, sc + 32 * ch, m, wr, bad);
+                  const float2 n = references(tS + 32 * ch, c, kp, sc + 32 * ch, m, wr, bad);
                   const float f = n.x > m ? ex2(m - n.x) : 1.0f, fw = n.y > wr ? ex2(wr - n.y) : 1.0f;
                   l *= f, ls[0] = mul2(ls[0], pair(f, f)), ls[1] = mul2(ls[1], pair(f, f));
                   m = n.x, wr = n.y;
@@ -860,7 +1114,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
                 gs[0] = gs[1] = 0;
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                  const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(sc + 32 * ch + 2 * e);
+                  const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(kp + 2 * e);
                   const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(sc + kTile + 32 * ch + 2 * e);
                   float2 y[2];
 #pragma unroll
@@ -931,12 +1185,17 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
         // past the valid ones are cleared.  Entries some rows do not see must
         // not ruin them through 0 * NaN: non-finite values of V are cleared and
         // given back to the rows that see them at the end.
-        const bool tree = k.valid > -k.u0 && !(a.stage.data && !k.staged);
-        if (tree || k.valid % C::kStep) {
-          const int slot = kt % C::kV;
+        int r0, r1;
+        half_seen<X>(a, k, seg, &r0, &r1);
+        if (r0 < r1 || k.valid % C::kStep) {
+          const int slot = kt % C::kV, end = (k.valid + C::kStep - 1) / C::kStep * C::kStep;
+          char* v = vslots + slot * C::kTileBytes;
           wait(sync, b_vf + 8 * slot, (kt / C::kV) & 1);
-          clean_rows<F8>(vslots + slot * C::kTileBytes, tree ? max(0, -k.u0) : k.valid, k.valid,
-                         (k.valid + C::kStep - 1) / C::kStep * C::kStep, C::kRow / 16, row, &ints[2]);
+          if (X && r1 < k.valid) {
+            clean_rows<F8>(v, r0, r1, r1, C::kRow / 16, row, &ints[2]);
+            r0 = k.valid;
+          }
+          clean_rows<F8>(v, r0, k.valid, end, C::kRow / 16, row, &ints[2]);
         }
         if (warp_live) tmem_wait_st();
         tc_fence_before();
@@ -986,6 +1245,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       float* part = P.p.part + (int64_t)(2 * blockIdx.x + (w0 >= seg.item0 ? 0 : 1)) * C::kPart;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t out0 = seg.b * a.out_stride[0], out = out0 + i * a.out_stride[1] + (int64_t)hq * a.out_stride[2];
+      const Carry carry = X && seg.carry ? carry_of(a, P.carry, seg.carry == 2) : Carry{};
+      const int64_t crow = X && seg.carry && live ? carry_row(a, G, row_of<X>(P, seg, i0 + lrow)) : 0;
       float4* gather = reinterpret_cast<float4*>(sm);  // the queries' place: every score is done
 #pragma unroll 1
       for (int col = c_first; col < c_first + kCols; col += 32) {
@@ -1003,20 +1264,27 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
           }
         }
         auto put = [&](int at, const float* z) {  // eight columns of a row
-          if (!split) {
+          if (X && !split && seg.carry) {
+            float* d = carry.o + crow * D + at;
+            *reinterpret_cast<float4*>(d) = make_float4(z[0], z[1], z[2], z[3]);
+            *reinterpret_cast<float4*>(d + 4) = make_float4(z[4], z[5], z[6], z[7]);
+            if (spoiled)
+#pragma unroll 1
+              for (int e = 0; e < 8; ++e) d[e] += given_back<X>(P, found, i, at + e);
+          } else if (!split) {
             __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.out) + out + at;
             *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16(z[0] * inv, z[1] * inv), pack_bf16(z[2] * inv, z[3] * inv),
                                                       pack_bf16(z[4] * inv, z[5] * inv), pack_bf16(z[6] * inv, z[7] * inv));
             if (spoiled)
 #pragma unroll 1
-              for (int e = 0; e < 8; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back(P, found, i, at + e));
+              for (int e = 0; e < 8; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back<X>(P, found, i, at + e));
           } else {
             float* d = part + lrow * D + at;
             *reinterpret_cast<float4*>(d) = make_float4(z[0], z[1], z[2], z[3]);
             *reinterpret_cast<float4*>(d + 4) = make_float4(z[4], z[5], z[6], z[7]);
             if (spoiled)
 #pragma unroll 1
-              for (int e = 0; e < 8; ++e) d[e] += given_back(P, found, i, at + e);
+              for (int e = 0; e < 8; ++e) d[e] += given_back<X>(P, found, i, at + e);
           }
         };
         if (copies > 1) {  // each copy adds all shares of 32 / copies columns
@@ -1045,6 +1313,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
       }
       if (split && live && copy == 0 && (QM == 2 || st == 0))
         reinterpret_cast<float2*>(part + C::kRows * D)[lrow] = make_float2(m, l);
+      if (X && !split && seg.carry && live && copy == 0 && (QM == 2 || st == 0)) carry.ml[crow] = make_float2(m, l);
       if (split) {
         // the last of the item's CTAs joins the partial results, in the order
         // of the CTAs, so that results do not depend on who was last
@@ -1090,6 +1359,12 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM>::kThreads, 1) tc_attention_
               y[0] += v0.x * f, y[1] += v0.y * f, y[2] += v0.z * f, y[3] += v0.w * f;
               y[4] += v1.x * f, y[5] += v1.y * f, y[6] += v1.z * f, y[7] += v1.w * f;
             }
+            if (X && seg.carry) {
+              const int64_t cr = carry_row(a, G, row_of<X>(P, seg, i0 + r));
+              store8<true>(carry.o, cr * D + col, y);
+              if (col == 0) carry.ml[cr] = make_float2(ML.y == 0.0f ? -kInf : ML.x, ML.y);  // a row that saw nothing binds no reference
+              continue;
+            }
             const float iv = 1.0f / ML.y;
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = ML.y == 0.0f ? 0.0f : y[e] * iv;
@@ -1120,13 +1395,16 @@ struct TcKernel {
   int threads, smem, part;  // block, dynamic shared memory, floats of a partial result
 };
 
-// head_dim 64 or 128; tiles: row tiles per CTA, 1 or 2.
+// head_dim 64 or 128; tiles: row tiles per CTA, 1 or 2; with forms or shared prefixes.
 TcKernel tc_kernel_bf16(int head_dim, int tiles);
 TcKernel tc_kernel_e4m3(int head_dim, int tiles);
+TcKernel tc_kernel_bf16_more(int head_dim, int tiles);
+TcKernel tc_kernel_e4m3_more(int head_dim, int tiles);
 
-template <bool F8, int D, int QM>
+template <bool F8, int D, int QM, bool X>
 TcKernel tc_kernel() {
-  return {tc_attention_kernel<F8, D, QM>, TcShape<F8, D, QM>::kThreads, TcShape<F8, D, QM>::kSmem, TcShape<F8, D, QM>::kPart};
+  using C = TcShape<F8, D, QM, X>;
+  return {tc_attention_kernel<F8, D, QM, X>, C::kThreads, C::kSmem, C::kPart};
 }
 
 }  // namespace sv

@@ -110,6 +110,12 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float rcp(float x) {  // 1 ulp
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Programmatic dependent launch (sm_90+).  A kernel launched with the
 // programmatic-stream-serialization attribute may start while the kernel
 // before it in the stream is still running: pdl_wait() blocks until that

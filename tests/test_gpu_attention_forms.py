@@ -301,6 +301,18 @@ def test_lengths_inside_a_block_and_no_groups(ver):
         x.check(out, depth=False)
 
 
+def test_groups_that_cannot_be_are_reported(ver):
+    x = shared_batch("bf16", 128, 8, 2, 16, "chain:3", True, 20, [1, 2, 3, 4], [4])
+    for length, members in (([320] * 4, [5, 0, 0, 0]), ([320] * 4, [0, 4, 0, 0]), ([320, 320, 160, 320], [4, 0, 0, 0]),
+                            ([320] * 4, [0, 0, 0, 0]), ([320] * 4, [3, 0, 0, 0]), ([320] * 4, [4, 0, 2, 0]),
+                            ([320] * 4, [-1, 0, 0, 0]), ([320] * 4, [2 ** 31 - 1, 0, 0, 0])):
+        x.run(ver, groups=dict(length=ints(length), members=ints(members)))
+        assert ver.error() == binding.SV_ERR_STATE, (length, members)
+    out = x.run(ver, groups=dict(length=ints([10 ** 6, -5, 400, 0]), members=ints([0, 0, 0, 0])))  # none
+    assert ver.error() == 0
+    x.check(out, depth=False)
+
+
 def test_special_values_in_a_prefix_reach_its_rows_alone(ver):
     x = shared_batch("bf16", 128, 8, 2, 16, "chain:3", True, 20, [1, 2, 3, 4], [2, 2])
     g = grouped(ver, x)
