@@ -29,7 +29,9 @@ SOURCES = ["api.cu", "kv_cache.cu", "verify.cu", "verify_bf16.cu", "verify_f32.c
            "tree_verify.cu", "tree_bf16.cu", "tree_f32.cu", "tree_opts_bf16.cu", "tree_opts_f32.cu",
            "stream.cu", "stream_more.cu", "tree_mask.cu", "kv_entries.cu", "logit_rules.cu",
            "tree_attention.cu", "prefix_groups.cu", "attention_bf16.cu", "attention_e4m3.cu",
-           "attention_bf16_more.cu", "attention_e4m3_more.cu"]
+           "attention_plan.cu",
+           "attention_bf16_forms.cu", "attention_bf16_shared.cu", "attention_bf16_both.cu",
+           "attention_e4m3_forms.cu", "attention_e4m3_shared.cu", "attention_e4m3_both.cu"]
 
 
 def nvcc() -> str:

@@ -12,7 +12,6 @@ struct AttnParams {
   uint32_t* ticket; // arrivals per shared item, zero between calls
   int* err;
   int splits;
-  float* carry;  // set: rows of requests that share a prefix go on from its part (see Carry)
 };
 
 // A request's extent: S cached positions, then n + 1 entries (n = -1: none).

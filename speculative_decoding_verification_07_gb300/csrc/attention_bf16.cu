@@ -3,9 +3,6 @@
 
 namespace sv {
 
-TcKernel tc_kernel_bf16(int head_dim, int tiles) {
-  if (head_dim == 64) return tiles == 1 ? tc_kernel<false, 64, 1, false>() : tc_kernel<false, 64, 2, false>();
-  return tiles == 1 ? tc_kernel<false, 128, 1, false>() : tc_kernel<false, 128, 2, false>();
-}
+TcKernel tc_kernel_bf16(int head_dim, int tiles) { return tc_kernel<false, 0>(head_dim, tiles); }
 
 }  // namespace sv

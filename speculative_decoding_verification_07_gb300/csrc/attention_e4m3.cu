@@ -3,9 +3,6 @@
 
 namespace sv {
 
-TcKernel tc_kernel_e4m3(int head_dim, int tiles) {
-  if (head_dim == 64) return tiles == 1 ? tc_kernel<true, 64, 1, false>() : tc_kernel<true, 64, 2, false>();
-  return tiles == 1 ? tc_kernel<true, 128, 1, false>() : tc_kernel<true, 128, 2, false>();
-}
+TcKernel tc_kernel_e4m3(int head_dim, int tiles) { return tc_kernel<true, 0>(head_dim, tiles); }
 
 }  // namespace sv

@@ -6,46 +6,31 @@
 #include <cuda_fp16.h>
 
 #include "attention.cuh"
+#include "attention_plan.cuh"
 #include "tcgen05.cuh"
 
 namespace sv {
 
-constexpr int kTile = 128;        // keys of a tile, and rows of a product
-constexpr int kStageBox = 16;     // staged entries per TMA box
 constexpr int kScaleRing = 4;     // tiles whose scales are held
+constexpr int kSegments = 4;      // items whose places are held (calls with forms or shared prefixes)
 
 struct TcParams {
   AttnParams p;
   CUtensorMap pages, stage;  // {column, slot or entry, (layer, K or V, head), block or request}
   CUtensorMap page_tails, stage_tails;  // of 8-bit entries' last 16 bytes, K's and V's in one box
-  int box;          // cached positions per TMA box: the largest power of two up to 128 that divides block_size
+  int box;          // cached positions per TMA box: the largest power of two up to 128 (16 where
+                    // requests share prefixes) that divides block_size
+  int stage_box;    // staged entries per TMA box: kStageBox, or box where requests share prefixes
   int block_shift;  // log2 of block_size, -1 if it is no power of two
   int group;        // G: query heads of a KV head
   uint32_t group_magic;  // ceil(2^32 / G), 0 for G = 1: a row's entry without a division
   // of calls with forms or shared prefixes
-  int forms, sharing;  // whether scores have a form; 1 where requests share prefixes
-  float* carry;        // outputs of parts: the prefix's, and the request's own (see Carry)
+  uint32_t entries_magic;  // the same for R
+  int box_shift;           // log2 of box
+  bool down;               // items' tiles from the last to the first
+  bool dead;               // this launch writes the rows past each request's entries
+  TcList list;             // what plan_kernel made
 };
-
-// Parts of rows that are joined by a later kernel: a prefix's, computed for a group's
-// rows together, and a request's own where that is long.  Each is [request][KV head][row
-// of the head] rows of D outputs relative to a reference in log2 units, then the rows'
-// (reference, sum).
-struct Carry {
-  float* o;
-  float2* ml;
-};
-__host__ __device__ __forceinline__ int64_t carry_rows(const sv_attention_args& a) {
-  return ((int64_t)a.B * a.R * a.Hq + 1) / 2 * 2;  // parts start at multiples of 16 bytes
-}
-__device__ __forceinline__ Carry carry_of(const sv_attention_args& a, float* carry, int own) {
-  const int64_t rows = carry_rows(a);
-  float* at = carry + own * rows * (a.cache.head_dim + 2);
-  return {at, reinterpret_cast<float2*>(at + rows * a.cache.head_dim)};
-}
-// Keys of its own up to which a request's part is not worth an item of the tensor
-// kernel, whose start and end cost six tiles' time.
-constexpr int kOwnShort = 128;
 
 // The instruction cache is shared by roles that run different code at the same
 // time: with every wait, walk and division inlined the kernel was 138 KB and
@@ -58,6 +43,28 @@ __device__ __forceinline__ int entry_of(const TcParams& P, int row) {  // row / 
   return P.group_magic ? (int)__umulhi((uint32_t)row, P.group_magic) : row;
 }
 
+// lo: the item's first tile; rev: t0 + t1 - 1 where tiles go down, else -1.  m > 0: the
+// rows of m requests from b on share their first X.S positions, X.n + 1 = m R entries, and
+// have nb boxes of their own.
+struct TcSegment {
+  int b, h, rb, t0, t1, T, tp, item0;  // T: units of the item, item0: where it starts in the list
+  Extent X;
+  int begin, m, nb, lo, rev;
+};
+
+// Requests that share a prefix have their rows in one item, whose tiles are the
+// prefix's and then their own keys': boxes of `box` rows, the cached positions past the
+// prefix and the staged entries of one request after the other, packed so that a few
+// own keys of each do not cost a tile of each.  A row sees the boxes of its own request.
+struct TcMembers {
+  int start[kMembers + 1];  // the request's first box
+  int S[kMembers], n[kMembers];
+};
+struct TcPlace {
+  TcSegment seg;  // T = 0: the end
+  TcMembers mem;
+};
+
 // F8: an 8-bit cache.  D: head_dim.  QM: row tiles of 128 per CTA.
 //   QM = 1: up to 128 rows; the two streams (score, weight and output regions
 //           of tensor memory, each with its softmax group of four warps) take
@@ -66,8 +73,9 @@ __device__ __forceinline__ int entry_of(const TcParams& P, int row) {  // row / 
 //           weighs a half (a quarter) of a tile's keys: all warps share the
 //           exponentials of a few rows, and a product of 128 rows costs the same.
 //   QM = 2: more rows; the streams are two row tiles that share every key tile.
-//   X: scores may have a form, requests may share prefixes.
-template <bool F8, int D, int QM, bool X>
+//   kMode: 0, or kForms and kShare: scores have a form, requests share prefixes; items then
+//           come from a list made by a kernel before (see attention_plan.cuh).
+template <bool F8, int D, int QM, int kMode>
 struct TcShape {
   // two softmax groups of four warps; K loads; products; V loads; one for scales
   // and dead rows
@@ -81,7 +89,8 @@ struct TcShape {
   static constexpr int kStep = F8 ? 32 : 16;                 // keys of one product of weights and V
   static constexpr int kRows = kTile * QM;
   static constexpr int kQAll = QM * kQBytes > 32768 ? QM * kQBytes : 32768;  // also holds 128 x 64 outputs, 32 of each half
-  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 2 * kTile * 4 + 2 * kTile * 4 + (X ? 128 : 0) : 0);
+  static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 2 * kTile * 4 + 2 * kTile * 4 + (kMode ? 128 : 0) : 0) +
+                               (kMode ? kSegments * (int)sizeof(TcPlace) : 0);
   // tiles held; a slot of K has its keys' tails and V's
   static constexpr int kTails = F8 ? 2 * kTile * kTail : 0, kKBytes = kTileBytes + kTails;
   static constexpr int kRoom = 232448 - 1024 - kMisc - kQAll, kPairs = kRoom / (kTileBytes + kKBytes);
@@ -91,12 +100,6 @@ struct TcShape {
   static constexpr int kPart = kRows * (D + 2);              // floats of a partial result
 };
 
-// A CTA's share of the work: [w, w1) of the list of all requests' items (head,
-// row block), an item being kLead units for what it costs besides its tiles
-// (queries in, outputs out) and then one unit a key tile.  64 requests of 128 to
-// 8192 positions, bf16, single tokens / trees of 15 nodes: 193 / 215 us with a
-// lead of 3, 191 / 208 with 4, 189 / 202 with 5, 192 / 200 with 6, 193 / 204 with 8.
-constexpr int kLead = 6;
 // Items of up to this many key tiles are not shared between CTAs: a tile is
 // 0.9 us for a CTA alone, joining parts 3 us and more.  A single request leaves
 // most of the GPU idle, so its items are shared earlier: one token over 777
@@ -112,59 +115,25 @@ constexpr int kLeastFew = 2, kLeastMany = 4, kFewRows = 32;
 // instructions to arrive more than for anything else).
 static __device__ __noinline__ uint32_t quotient(uint32_t a, uint32_t b) { return a / b; }
 
-// An item's place in the list.  X: `pre` items are a group's prefix for all its
-// rows, the others a request's own positions from `begin` on; carry says where an
-// item's outputs go: 0 out, 1 the prefix's parts, 2 the own ones'.
 struct TcWalk {
   int qrows, w, w1, b, base, T, items, tp, blocks;
   Extent X;
-  int begin, carry;
   __device__ __forceinline__ int count() const { return T * items; }
 };
 
 // The units of a request of extent X.
-template <bool X>
-static __device__ __noinline__ void plan(const TcParams& P, TcWalk& k, int b, Extent E) {
+static __device__ __noinline__ void plan(const TcParams& P, TcWalk& k, int b, Extent X) {
   const sv_attention_args& a = P.p.a;
-  k.b = b, k.X = E;
+  k.b = b, k.X = X;
   k.T = 0, k.items = 0, k.tp = 0, k.blocks = 1;
-  if (E.n < 0) return;
-  k.blocks = ((E.n + 1) * P.group + k.qrows - 1) >> (k.qrows == kTile ? 7 : 8);
+  if (X.n < 0) return;
+  k.blocks = ((X.n + 1) * P.group + k.qrows - 1) >> (k.qrows == kTile ? 7 : 8);
   k.items = a.cache.heads * k.blocks;
-  const bool staged = a.stage.data && !(X && k.carry == 1);
-  const int cached = E.S - (X ? k.begin : 0) + (a.stage.data || (X && k.carry == 1) ? 0 : E.n + 1);
-  k.tp = (cached + kTile - 1) / kTile;
-  k.T = kLead + (staged ? k.tp + (E.n + kTile) / kTile : k.tp);
+  k.tp = (X.S + (a.stage.data ? 0 : X.n + 1) + kTile - 1) / kTile;
+  k.T = kLead + (a.stage.data ? k.tp + (X.n + kTile) / kTile : k.tp);
 }
-// Request b's item kinds; X with shared prefixes: 2 b is the prefix of the group that b
-// starts, 2 b + 1 the request's own part.
-template <bool X>
-static __device__ __forceinline__ void walk_to(const TcParams& P, TcWalk& k, int v) {
-  const sv_attention_args& a = P.p.a;
-  if (!X) {
-    plan<X>(P, k, v, extent_of(a, v, P.p.err));
-    return;
-  }
-  const int b = v >> P.sharing;
-  k.begin = k.carry = 0;
-  Extent E;
-  if (P.sharing && !(v & 1)) {
-    const int m = a.shared_members[b];
-    k.carry = 1;
-    E.S = shared_of(a, b);
-    E.n = E.S > 0 && m > 0 && m <= a.B - b ? m * a.R - 1 : -1;
-  } else {
-    E = extent_of(a, b, P.p.err);
-    if (P.sharing) {
-      if ((k.begin = shared_of(a, b)) > 0) {
-        k.carry = 2;
-        if (E.S - k.begin + E.n + 1 <= kOwnShort) E.n = -1;  // the joining kernel's
-      }
-    } else {
-      k.begin = first_seen(a, E.S) & -P.box;  // a TMA box starts at a multiple of its rows
-    }
-  }
-  plan<X>(P, k, v, E);
+static __device__ __forceinline__ void walk_to(const TcParams& P, TcWalk& k, int b) {
+  plan(P, k, b, extent_of(P.p.a, b, P.p.err));
 }
 
 // floor(x * m / d); small products without a 64-bit division, whose code alone
@@ -175,21 +144,14 @@ static __device__ __noinline__ int mul_div(int x, int m, int d) {
   return (int)(p / (uint32_t)d);
 }
 
-struct TcSegment {
-  int b, h, rb, t0, t1, T, tp, item0;  // T: units of the item, item0: where it starts in the list
-  Extent X;
-  int begin, carry;
-};
-
 // The next segment (one item's consecutive tiles); false at the end.  A share's
 // bounds inside a short item move to the item's nearer end, the same for both
 // neighbours: joining its parts would take longer than its tiles.
-template <bool X>
 static __device__ __noinline__ bool next_segment(const TcParams& P, TcWalk& k, TcSegment& s) {
   while (k.w < k.w1) {
     while (k.w >= k.base + k.count()) {
       k.base += k.count();
-      walk_to<X>(P, k, k.b + 1);
+      walk_to(P, k, k.b + 1);
     }
     const int at = k.w - k.base, item = (int)quotient(at, k.T), item0 = k.base + item * k.T;
     int from = k.w - item0, to = min(k.T, k.w1 - item0);
@@ -199,12 +161,11 @@ static __device__ __noinline__ bool next_segment(const TcParams& P, TcWalk& k, T
     }
     k.w = min(k.w1, item0 + k.T);
     if (to <= kLead) continue;  // none of the item's tiles
-    s.b = X ? k.b >> P.sharing : k.b, s.h = k.blocks == 1 ? item : (int)quotient(item, k.blocks), s.rb = item - s.h * k.blocks;
+    s.b = k.b, s.h = k.blocks == 1 ? item : (int)quotient(item, k.blocks), s.rb = item - s.h * k.blocks;
     s.T = k.T, s.tp = k.tp, s.X = k.X;
     s.t0 = max(0, from - kLead);
     s.t1 = to - kLead;
     s.item0 = item0;
-    if (X) s.begin = k.begin, s.carry = k.carry;
     return true;
   }
   return false;
@@ -219,53 +180,180 @@ static __device__ __noinline__ int share_of(int x, int total, int ctas) {
   return c;
 }
 
+// A CTA's place in the list of lots.
+struct TcWalker {
+  int w, w1, at, count;
+  TcLot lot;
+};
+
+static __device__ __noinline__ void load_lot(const TcList& l, TcWalker& k, int at) {
+  const int4* p = reinterpret_cast<const int4*>(l.lots + at);
+  const int4 x = __ldcg(p), y = __ldcg(p + 1), z = __ldcg(p + 2);
+  k.at = at;
+  k.lot = TcLot{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+}
+
+// The lot that holds unit w0, by a whole warp: 32 probes at a time.
+static __device__ __noinline__ void find_lot(const TcList& l, TcWalker& k) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = k.count;  // lots[lo].cum <= w < lots[hi].cum
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, i < hi && __ldcg(&l.lots[i].cum) <= k.w)) - 1;
+    lo += max(0, n) * step, hi = min(hi, lo + step);
+  }
+  load_lot(l, k, lo);
+}
+
+// next_segment over the list, by a whole warp, into shared memory.
+template <int kMode>
+static __device__ __noinline__ bool next_place(const TcParams& P, TcWalker& k, TcPlace* to) {
+  const int lane = threadIdx.x & 31;
+  TcSegment s = {};
+  while (k.w < k.w1) {
+    while (k.w >= k.lot.cum + k.lot.units) {
+      if (k.at + 1 >= k.count) {
+        k.w = k.w1;
+        break;
+      }
+      load_lot(P.list, k, k.at + 1);
+    }
+    if (k.w >= k.w1) break;
+    const int at = k.w - k.lot.cum;
+    int item = (int)quotient(at, k.lot.T), item0 = k.lot.cum + item * k.lot.T, T = k.lot.T, lo = 0;
+    if ((kMode & kForms) && P.list.ranges && k.lot.blocks > 1) {  // the row block within the head
+      const int* cum = P.list.ranges + (int64_t)k.lot.b * P.list.words;
+      const int in = at - item * T;
+      int rb = 0;
+      for (int r0 = 0; r0 < k.lot.blocks; r0 += 32)
+        rb += __popc(__ballot_sync(0xFFFFFFFFu, r0 + lane < k.lot.blocks && __ldcg(cum + min(r0 + lane, k.lot.blocks)) <= in));
+      --rb;
+      item0 += cum[rb], T = cum[rb + 1] - cum[rb], item = item * k.lot.blocks + rb;
+      lo = cum[(P.list.words + 1) / 2 + rb];
+    }
+    int from = k.w - item0, upto = min(T, k.w1 - item0);
+    if (T <= kLead + (P.p.a.B == 1 ? kWholeOne : kWhole)) {
+      const bool mine = 2 * from < T;  // from > 0 only at the share's start
+      from = 0, upto = mine && 2 * upto >= T ? T : 0;
+    }
+    k.w = min(k.w1, item0 + T);
+    if (upto <= kLead) continue;  // none of the item's tiles
+    s.b = k.lot.b, s.h = k.lot.blocks == 1 ? item : (int)quotient(item, k.lot.blocks), s.rb = item - s.h * k.lot.blocks;
+    s.T = T, s.tp = k.lot.tp, s.X = {k.lot.S, k.lot.n};
+    s.t0 = max(0, from - kLead), s.t1 = upto - kLead, s.item0 = item0;
+    s.begin = k.lot.begin, s.m = k.lot.m, s.nb = k.lot.nb, s.lo = lo, s.rev = P.down ? s.t0 + s.t1 - 1 : -1;
+    break;
+  }
+  if (lane == 0) to->seg = s;
+  if ((kMode & kShare) && s.m > 0) {
+    Extent E = {0, -1};
+    if (lane < s.m) E = extent_of(P.p.a, s.b + lane, nullptr);
+    const int mine = own_boxes(P.p.a, P.box, P.box_shift, s.X.S, E);
+    int x = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    to->mem.start[lane] = x - mine, to->mem.S[lane] = E.S, to->mem.n[lane] = E.n;
+    if (lane == 31) to->mem.start[kMembers] = x;
+  }
+  return s.T > 0;
+}
+
 // What a tile holds: `valid` keys, and u0, the entry number of its first key
 // (negative: cached positions before entry 0).  prefix: cached positions only,
-// all of them seen.
+// all of them seen (but for a window).  own: boxes of the requests of a group, x0
+// the first of them.
 struct TcTile {
-  bool staged, prefix;
+  bool staged, prefix, own;
   int x0, valid, u0;
 };
 
-template <bool X>
-__device__ __forceinline__ TcTile tile_of(const sv_attention_args& a, const TcSegment& s, int t) {
+// The tile that a segment's t-th one is.
+template <int kMode>
+__device__ __forceinline__ int place_of(const TcSegment& s, int t) {
+  return kMode & kForms ? (s.rev >= 0 ? s.rev - t : t) + s.lo : t;
+}
+template <int kMode>
+__device__ __forceinline__ TcTile tile_of(const TcParams& P, const TcSegment& s, int t) {
+  const sv_attention_args& a = P.p.a;
   TcTile k;
-  const bool apart = a.stage.data || (X && s.carry == 1);  // no entries among the cached positions
-  k.staged = a.stage.data && !(X && s.carry == 1) && t >= s.tp;
-  k.x0 = k.staged ? (t - s.tp) * kTile : (X ? s.begin : 0) + t * kTile;
-  const int limit = k.staged ? s.X.n + 1 : apart ? s.X.S : s.X.S + s.X.n + 1;
+  t = place_of<kMode>(s, t);
+  k.own = (kMode & kShare) && s.m > 0 && t >= s.tp;
+  if ((kMode & kShare) && s.m > 0) {
+    k.staged = false, k.prefix = !k.own;
+    k.x0 = k.own ? (t - s.tp) << (7 - P.box_shift) : t * kTile;
+    k.valid = min(kTile, k.own ? (s.nb - k.x0) << P.box_shift : s.X.S - k.x0);
+    k.u0 = 0;
+    return k;
+  }
+  k.staged = a.stage.data && t >= s.tp;
+  k.x0 = k.staged ? (t - s.tp) * kTile : (kMode & kForms ? s.begin : 0) + t * kTile;
+  const int limit = k.staged ? s.X.n + 1 : a.stage.data ? s.X.S : s.X.S + s.X.n + 1;
   k.valid = min(kTile, limit - k.x0);
   k.u0 = k.staged ? k.x0 : k.x0 - s.X.S;
-  k.prefix = !k.staged && (apart || k.x0 + k.valid <= s.X.S);
+  k.prefix = !k.staged && (a.stage.data || k.x0 + k.valid <= s.X.S);
   return k;
 }
 
-// Whose row a row of an item is: the request, the entry and the query head.  The
-// prefix's items have the rows of all members, R entries each.
+// Whose row a row of an item is: the request (the j-th of its lot), the entry and the
+// query head.
 struct TcRow {
-  int b, i, hq;
+  int j, b, i, hq;
 };
-template <bool X>
+template <int kMode>
 __device__ __forceinline__ TcRow row_of(const TcParams& P, const TcSegment& s, int row) {
   const int e = entry_of(P, row), hq = s.h * P.group + row - e * P.group;
-  if (!X || s.carry != 1) return {s.b, e, hq};
-  const int m = e / P.p.a.R;
-  return {s.b + m, e - m * P.p.a.R, hq};
+  if (!(kMode & kShare) || s.m <= 1) return {0, s.b, e, hq};
+  const int j = min(P.entries_magic ? (int)__umulhi((uint32_t)e, P.entries_magic) : e, s.m - 1);  // e < 256
+  return {j, s.b + j, e - j * P.p.a.R, hq};
 }
-// Where the outputs of a row of an item go in a part.
-__device__ __forceinline__ int64_t carry_row(const sv_attention_args& a, int group, const TcRow& r) {
-  return (((int64_t)r.b * a.cache.heads + r.hq / group) * a.R + r.i) * group + r.hq % group;
+
+// What row (member j, entry i) sees of 32 keys of a tile that holds entries or own
+// boxes: their bits, and in u the entry number of the first of each 8 keys (negative:
+// cached positions before the request's entry 0).
+template <int kMode>
+static __device__ __noinline__ uint32_t seen_of(const TcParams& P, const TcPlace& s, const TcTile& k, int j, int i, int ch, int (&u)[4]) {
+  const sv_attention_args& a = P.p.a;
+  if (!(kMode & kShare) || !k.own) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) u[g] = k.u0 + 32 * ch + 8 * g;
+    const int left = k.valid - 32 * ch;
+    const uint32_t all = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u;
+    return i <= s.seg.X.n ? seen_bits(a, s.seg.b, i, s.seg.X.n, u[0]) & all : 0u;
+  }
+  const int S = s.mem.S[j], n = s.mem.n[j], first = s.mem.start[j], end = s.mem.start[j + 1];
+  uint32_t bits = 0;
+  const int x0 = k.x0 + (32 * ch >> P.box_shift);
+  if (x0 >= end || x0 + (32 >> P.box_shift) <= first || i > n) return 0u;
+  const int cached = cached_boxes(a, P.box, P.box_shift, s.seg.X.S, {S, n});
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    const int in = 8 * g & (P.box - 1), x = x0 + (8 * g >> P.box_shift);
+    u[g] = 0;
+    if (x < first || x >= end) continue;
+    const bool staged = x - first >= cached;
+    u[g] = (staged ? (x - first - cached) << P.box_shift : s.seg.X.S + ((x - first) << P.box_shift) - S) + in;
+    uint32_t w;
+    if (a.stage.data && !staged)
+      w = u[g] >= 0 ? 0u : u[g] <= -8 ? 0xFFu : (1u << -u[g]) - 1u;
+    else
+      w = seen_bits(a, s.seg.b + j, i, n, u[g]) & 0xFFu;
+    bits |= w << (8 * g);
+  }
+  return bits;
 }
 
 // Rows of V in a tile, [r0, r1), that some row of the item may not see though another
-// does, or that are next to such: entries, and with a window the positions that the
-// deepest row no longer sees.
-template <bool X>
+// does, or that are next to such: entries, other requests' own keys, and with a window
+// the positions that the deepest row no longer sees.
+template <int kMode>
 __device__ __forceinline__ void half_seen(const sv_attention_args& a, const TcTile& k, const TcSegment& s, int* r0, int* r1) {
-  const bool tree = X ? !k.prefix : k.valid > -k.u0 && !(a.stage.data && !k.staged);
+  const bool tree = kMode ? !k.prefix : k.valid > -k.u0 && !(a.stage.data && !k.staged);
   *r0 = tree ? max(0, -k.u0) : k.valid;
   *r1 = k.valid;
-  if (X && a.window > 0 && !k.staged) {
+  if ((kMode & kForms) && a.window > 0 && !k.staged) {
     const int last = (int)min((int64_t)k.valid, (int64_t)s.X.S + a.R - a.window - k.x0);
     if (last > 0) *r0 = 0, *r1 = tree ? k.valid : last;
   }
@@ -372,22 +460,35 @@ constexpr float kMaxRaise = 126.0f;
 __device__ __forceinline__ float above_log2(float x) { return (float)((int)(__float_as_uint(x) >> 23) - 126); }
 
 // What non-finite values of V, cleared from a segment's tiles, add to column
-// `col` of entry i's row: 0, or an infinity or NaN.
-template <bool X>
-static __device__ __noinline__ float given_back(const TcParams& P, const TcSegment& seg, int i, int col) {
+// `col` of a row: 0, or an infinity or NaN.
+template <int kMode>
+static __device__ __noinline__ float given_back(const TcParams& P, const TcPlace& at, const TcRow& row, int col) {
   const sv_attention_args& a = P.p.a;
+  const TcSegment& seg = at.seg;
   float sum = 0.0f;
   for (int t = seg.t0; t < seg.t1; ++t) {
-    const TcTile k = tile_of<X>(a, seg, t);
-    if (!X && a.stage.data && !k.staged) continue;
-    const sv_kv_place& pl = k.staged ? a.stage : a.cache;
-    int r0 = max(0, -k.u0), r1 = k.valid;
-    if (X) half_seen<X>(a, k, seg, &r0, &r1);
+    const TcTile k = tile_of<kMode>(P, seg, t);
+    int r0, r1;
+    half_seen<kMode>(a, k, seg, &r0, &r1);
     for (int r = r0; r < r1; ++r) {
-      const int u = k.u0 + r;
-      if (u >= 0 && !(seen_bits(a, seg.b, i, seg.X.n, u) & 1)) continue;
-      if (X && a.window > 0 && abs(depth_of(a, seg.b, i) - (u < 0 ? u : depth_of(a, seg.b, u))) >= a.window) continue;
-      const int64_t off = entry_offset(pl, seg.b, k.x0 + r, k.x0 + r);
+      bool staged = k.staged;
+      int u = k.u0 + r, x = k.x0 + r;  // entry number, and entry or position
+      if (kMode) {
+        int first[4];
+        const uint32_t bits = seen_of<kMode>(P, at, k, row.j, row.i, r >> 5, first);
+        if (!(bits >> (r & 31) & 1)) continue;
+        if ((kMode & kShare) && k.own) {
+          const Extent E = {at.mem.S[row.j], at.mem.n[row.j]};
+          u = first[r >> 3 & 3] + (r & 7);
+          staged = k.x0 + (r >> P.box_shift) - at.mem.start[row.j] >= cached_boxes(a, P.box, P.box_shift, seg.X.S, E);
+          x = staged ? u : E.S + u;
+        }
+        if (a.window > 0 && abs(depth_of(a, row.b, row.i) - (u < 0 ? u : depth_of(a, row.b, u))) >= a.window) continue;
+      } else if (!(seen_bits(a, row.b, row.i, seg.X.n, u) & 1)) {
+        continue;
+      }
+      const sv_kv_place& pl = staged ? a.stage : a.cache;
+      const int64_t off = entry_offset(pl, row.b, x, x);
       if (off < 0) continue;
       const char* vr = static_cast<const char*>(pl.data) + off + (a.cache.heads + seg.h) * row_step(pl);
       const float v = pl.format == SV_KV_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(vr)[col])
@@ -420,106 +521,123 @@ static __device__ __noinline__ void hide_unseen(const TcParams& P, int b, int i,
 
 // What a row's scores get from their form.
 struct TcForm {
-  int at;       // the row's position
-  float slope;  // of its head, log2 units
+  int S, depth;  // the row's request's length, and its depth below that
+  float slope;   // of its head, log2 units
 };
 
-// Scores of a tile become what the softmax takes: times c (and K's scales ks), capped,
-// less the distance's share, -inf where row i does not see the key; log2 units.  In a
-// pass of its own over tensor memory: inside the softmax's loop it would be there
-// twice (once more where a reference moves).
+// Scores of a tile become what the softmax takes: -inf where a row does not see the
+// key; with a form times c (and K's scales ks) before, capped, and less the distance's
+// share, in log2 units.  The groups of 32 keys that any row of the warp sees are
+// returned; the others are left as they are.  In a pass of its own over tensor memory,
+// 16 columns at a time: the softmax's loop would have it twice (once more where a
+// reference moves), and 32 unrolled columns were 3100 cycles a group, mostly waits for
+// instructions (64 single tokens under a window of 1024, capped: 104 us).
 //   cap tanh(s / cap) = cap - 2 cap / (1 + 2^(2 s log2(e) / cap)); where all of a group's
 // scores are below 0.3 cap, as nearly all are, the series of tanh to the ninth power
 // (the next term is 5e-8 of it) saves two of the three special functions an element.
-template <bool F8>
-static __device__ __noinline__ void shape_scores(const TcParams& P, const TcSegment& seg, const TcTile& k, const TcForm& f, int i,
-                                                 float c, const float* ks, int ch_a, int ch_e, uint32_t tS) {
+template <bool F8, int kMode>
+static __device__ __noinline__ uint32_t shape_scores(const TcParams& P, const TcPlace& at, const TcTile& k, const TcForm& f, int j, int i,
+                                                     float c, const float* ks, int ch_a, int ch_e, uint32_t tS) {
   const sv_attention_args& a = P.p.a;
-  const float cap = a.softcap * kLog2e, per = a.softcap > 0.0f ? 1.0f / cap : 0.0f;
-  const uint64_t c2 = pair(c, c), slope2 = pair(f.slope, f.slope), one2 = pair(1.0f, 1.0f);
+  constexpr bool kShape = kMode & kForms;
+  const float cap = kShape ? a.softcap * kLog2e : 0.0f, per = cap > 0.0f ? 1.0f / cap : 0.0f;
+  const uint64_t c2 = pair(c, c), slope2 = pair(f.slope, f.slope);
+  uint32_t some = 0;
 #pragma unroll 1
   for (int ch = ch_a; ch < ch_e; ++ch) {
-    uint32_t x[32];
-    uint64_t v[16];
-    tmem_ld32(tS + 32 * ch, x);
-#pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      v[e] = mul2(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2);
-      v[e + 1] = mul2(pair(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3])), c2);
-      if (F8) {
-        const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(ks + 32 * ch + 2 * e);
-        v[e] = mul2(v[e], s2.x), v[e + 1] = mul2(v[e + 1], s2.y);
-      }
-    }
-    if (a.softcap > 0.0f) {
-      const uint64_t per2 = pair(per, per);
-      float most[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float2 y = unpair(v[e]);
-        most[e & 3] = fmaxf(most[e & 3], fmaxf(fabsf(y.x), fabsf(y.y)));
-      }
-      if (!__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * per > 0.3f)) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint64_t w = mul2(v[e], per2), w2 = mul2(w, w);
-          uint64_t t = fma2(w2, pair(62.0f / 2835.0f, 62.0f / 2835.0f), pair(-17.0f / 315.0f, -17.0f / 315.0f));
-          t = fma2(w2, t, pair(2.0f / 15.0f, 2.0f / 15.0f));
-          t = fma2(w2, t, pair(-1.0f / 3.0f, -1.0f / 3.0f));
-          v[e] = mul2(v[e], fma2(w2, t, one2));
-        }
-      } else {
-        const float up = 2.0f * kLog2e * per;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 y = unpair(v[e]);
-          float z[2] = {y.x, y.y};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float w = z[h] * per, w2 = w * w;
-            const float small = z[h] * (1.0f + w2 * (-1.0f / 3.0f + w2 * (2.0f / 15.0f + w2 * (-17.0f / 315.0f + w2 * (62.0f / 2835.0f)))));
-            const float large = cap - 2.0f * cap * rcp(1.0f + ex2(z[h] * up));
-            z[h] = fabsf(w) < 0.3f ? small : large;
-          }
-          v[e] = pair(z[0], z[1]);
-        }
-      }
-    }
-    // keys between the nearest and the window's edge; among the entries both depend
-    // on the keys' depths
-    const int left = k.valid - 32 * ch;
-    uint32_t bits = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u;
+    // what is seen by the mask, and by the window
+    const int left = k.valid - 32 * ch, far = f.S + f.depth - (k.x0 + 32 * ch);  // of a prefix's first key
+    int u[4];
+    uint32_t bits;
     if (k.prefix) {
-      const int far = f.at - (k.x0 + 32 * ch);  // of the first key
-      if (a.window > 0 && far >= a.window) bits &= far - a.window >= 31 ? 0u : 0xFFFFFFFEu << (far - a.window);
-      if (a.slopes) {
-        const float b = (float)far;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = fma2(slope2, pair((float)(2 * e) - b, (float)(2 * e + 1) - b), v[e]);
-      }
+      bits = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u;
+      if (kShape && a.window > 0 && far >= a.window) bits &= far - a.window >= 31 ? 0u : 0xFFFFFFFEu << (far - a.window);
     } else {
-      bits &= i <= seg.X.n ? seen_bits(a, seg.b, i, seg.X.n, k.u0 + 32 * ch) : 0u;
-      if (a.slopes || a.window > 0) {
-        const int d = f.at - seg.X.S;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int u = k.u0 + 32 * ch + 2 * e;
-          const int far0 = abs(d - (u < 0 || u > seg.X.n ? u : depth_of(a, seg.b, u)));
-          const int far1 = abs(d - (u + 1 < 0 || u + 1 > seg.X.n ? u + 1 : depth_of(a, seg.b, u + 1)));
-          if (a.window > 0) bits &= ~((far0 >= a.window ? 1u : 0u) << (2 * e) | (far1 >= a.window ? 1u : 0u) << (2 * e + 1));
-          if (a.slopes) v[e] = fma2(slope2, pair(-(float)far0, -(float)far1), v[e]);
+      bits = seen_of<kMode>(P, at, k, j, i, ch, u);
+      if (kShape && a.window > 0) {
+#pragma unroll 1
+        for (int e = 0; e < 32; ++e) {
+          const int x = u[e >> 3] + (e & 7);
+          if (bits >> e & 1 && abs(f.depth - (x < 0 ? x : depth_of(a, at.seg.b, x))) >= a.window) bits &= ~(1u << e);
         }
       }
     }
+    if (!__any_sync(0xFFFFFFFFu, bits != 0)) continue;
+    some |= 1u << ch;
+    if (!kShape && __all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) continue;
+#pragma unroll 1
+    for (int g = 0; g < 32; g += 16) {
+      uint32_t x[16];
+      uint64_t v[8];
+      tmem_ld16(tS + 32 * ch + g, x);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float2 y = unpair(v[e]);
-      x[2 * e] = bits >> (2 * e) & 1 ? __float_as_uint(y.x) : 0xFF800000u;
-      x[2 * e + 1] = bits >> (2 * e + 1) & 1 ? __float_as_uint(y.y) : 0xFF800000u;
+      for (int e = 0; e < 8; ++e) v[e] = pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+      if (kShape) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] = mul2(v[e], c2);
+          if (F8) v[e] = mul2(v[e], *reinterpret_cast<const uint64_t*>(ks + 32 * ch + g + 2 * e));
+        }
+        if (cap > 0.0f) {
+          const uint64_t per2 = pair(per, per);
+          float most = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 y = unpair(v[e]);
+            most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
+          }
+          if (!__any_sync(0xFFFFFFFFu, most * per > 0.3f)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint64_t w = mul2(v[e], per2), w2 = mul2(w, w);
+              uint64_t t = fma2(w2, pair(62.0f / 2835.0f, 62.0f / 2835.0f), pair(-17.0f / 315.0f, -17.0f / 315.0f));
+              t = fma2(w2, t, pair(2.0f / 15.0f, 2.0f / 15.0f));
+              t = fma2(w2, t, pair(-1.0f / 3.0f, -1.0f / 3.0f));
+              v[e] = mul2(v[e], fma2(w2, t, pair(1.0f, 1.0f)));
+            }
+          } else {
+            const float up = 2.0f * kLog2e * per;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 y = unpair(v[e]);
+              float z[2] = {y.x, y.y};
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float w = z[h] * per, w2 = w * w;
+                const float small = z[h] * (1.0f + w2 * (-1.0f / 3.0f + w2 * (2.0f / 15.0f + w2 * (-17.0f / 315.0f + w2 * (62.0f / 2835.0f)))));
+                const float large = cap - 2.0f * cap * rcp(1.0f + ex2(z[h] * up));
+                z[h] = fabsf(w) < 0.3f ? small : large;
+              }
+              v[e] = pair(z[0], z[1]);
+            }
+          }
+        }
+        if (a.slopes && k.prefix) {
+          const float b = (float)(far - g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = fma2(slope2, pair((float)(2 * e) - b, (float)(2 * e + 1) - b), v[e]);
+        } else if (a.slopes) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int z = u[(g + e) >> 3] + (e & 7);
+            const int d = z < 0 || !(bits >> (g + e) & 1) ? z : depth_of(a, at.seg.b + j, z);
+            x[e] = __float_as_uint(-(float)abs(f.depth - d));
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = fma2(slope2, pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), v[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 y = unpair(v[e]);
+        x[2 * e] = bits >> (g + 2 * e) & 1 ? __float_as_uint(y.x) : 0xFF800000u;
+        x[2 * e + 1] = bits >> (g + 2 * e + 1) & 1 ? __float_as_uint(y.y) : 0xFF800000u;
+      }
+      tmem_st16(tS + 32 * ch + g, x);
     }
-    tmem_st32(tS + 32 * ch, x);
   }
   tmem_wait_st();
+  return some;
 }
 
 // The references (m, weights') of the rows that need others for 32 scores: a whole
@@ -612,28 +730,6 @@ static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r
   fence_async_smem();
 }
 
-// Whether every request is in the group that its shared_len says, by a warp a request:
-// members that agree with their first, no group inside another, none past the batch.
-static __device__ __noinline__ void check_groups(const sv_attention_args& a, int* err) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int own = shared_of(a, b), m = a.shared_members[b];
-    bool bad = m < 0 || m > a.B - b;
-    if (!bad)
-      for (int j = 1 + lane; j < m; j += 32) bad |= shared_of(a, b + j) != own || a.shared_members[b + j] != 0;
-    if (own > 0 && m == 0) {  // the nearest request before it that starts a group
-      int first = -1;
-      for (int j0 = b - 1; j0 >= 0 && first < 0; j0 -= 32) {
-        const uint32_t starts = __ballot_sync(0xFFFFFFFFu, j0 - lane >= 0 && a.shared_members[max(0, j0 - lane)] != 0);
-        if (starts) first = j0 - (__ffs(starts) - 1);
-      }
-      bad |= first < 0 || a.shared_members[max(0, first)] <= b - first;
-    }
-    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) report(err, SV_ERR_STATE);
-  }
-}
-
 // o = sum_x p_x V_x, p = softmax(scale q K^T), in one pass over the keys: scores
 // of 128 rows and 128 keys as a product with its result in tensor memory, their
 // weights against the running reference maximum back into the same columns, and
@@ -649,9 +745,9 @@ static __device__ __noinline__ void check_groups(const sv_attention_args& a, int
 // to 65536 positions, 448 rows a head, bf16: 184 us, 0.85 PFLOP/s; what the products'
 // warp does between products (waits, commits: a third of its time) bounds that.  Handing scores over in halves
 // of 64 keys, to have the next half's under way, doubled those steps: 249 us.
-template <bool F8, int D, int QM, bool X>
-__global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attention_kernel(const __grid_constant__ TcParams P) {
-  using C = TcShape<F8, D, QM, X>;
+template <bool F8, int D, int QM, int kMode>
+__global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_attention_kernel(const __grid_constant__ TcParams P) {
+  using C = TcShape<F8, D, QM, kMode>;
   extern __shared__ char smem_raw[];
   const sv_attention_args& a = P.p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -669,13 +765,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
   // K loaded / free, V loaded / free, scores, weights, outputs, queries, scales set / read
   const uint32_t b_kf = bars, b_ke = b_kf + 8 * C::kK, b_vf = b_ke + 8 * C::kK, b_ve = b_vf + 8 * C::kV,
                  b_s = b_ve + 8 * C::kV, b_p = b_s + 16, b_o = b_s + 32, b_q = b_s + 48, b_sf = b_s + 56,
-                 b_se = b_sf + 8 * kScaleRing;
+                 b_se = b_sf + 8 * kScaleRing, b_gf = b_se + 8 * kScaleRing, b_ge = b_gf + 8 * kSegments;  // places set / read
   int* ints = reinterpret_cast<int*>(misc + 512);  // 0 tensor memory, 1 abort, 2 non-finite entries, 3 last, 4.. walk
   float2* s_ml = reinterpret_cast<float2*>(misc + 1024);  // [256] maxima and sums exchanged or joined
   float* s_qs = reinterpret_cast<float*>(misc + 3072);    // [kRows] row scales of 8-bit queries
   float* s_sc = s_qs + C::kRows;                          // [kScaleRing][2][128] scales of a tile's entries, K's and V's
   float* s_wr = s_sc + kScaleRing * 2 * kTile;            // [256] references of 8-bit weights, exchanged
   float* s_ones = s_wr + 2 * kTile;                       // [32] K's scales of scores that have them already
+  TcPlace* places = reinterpret_cast<TcPlace*>(misc + C::kMisc) - kSegments;  // [kSegments]
 
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) mbar_init(b_kf + 8 * i, 1), mbar_init(b_ke + 8 * i, QM);
@@ -683,13 +780,15 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
     for (int i = 0; i < 2; ++i) mbar_init(b_s + 8 * i, 1), mbar_init(b_p + 8 * i, 4), mbar_init(b_o + 8 * i, 1);
     mbar_init(b_q, 8);
     for (int i = 0; i < kScaleRing; ++i) mbar_init(b_sf + 8 * i, 1), mbar_init(b_se + 8 * i, 4 * QM);
+    if (kMode)
+      for (int i = 0; i < kSegments; ++i) mbar_init(b_gf + 8 * i, 1), mbar_init(b_ge + 8 * i, 11);
     ints[1] = ints[2] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&P.pages);
     if (a.stage.data) tma_prefetch_map(&P.stage);
   }
   if (warp == 9) tmem_alloc(smem_u32(&ints[0]), 512);
-  if (X && F8 && warp == 11) s_ones[lane] = 1.0f;
+  if (kMode && F8 && warp == 11) s_ones[lane] = 1.0f;
   pdl_wait();
   pdl_trigger();
 
@@ -703,16 +802,21 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
     ctas = min((int)gridDim.x, (total + least - 1) / least);
     if ((int)blockIdx.x < ctas) w0 = mul_div(total, blockIdx.x, ctas), w1 = mul_div(total, blockIdx.x + 1, ctas);
   };
-  const int B = X ? a.B << P.sharing : a.B;
-  if (B <= 4) {  // every thread counts for itself
+  if (kMode) {  // a kernel before has counted
+    total = __ldcg(P.list.head);
+    share();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  } else if (a.B <= 4) {  // every thread counts for itself
 #pragma unroll 1
-    for (int b = 0; b < B; ++b) walk_to<X>(P, walk, b), total += walk.count();
+    for (int b = 0; b < a.B; ++b) walk_to(P, walk, b), total += walk.count();
     share();
     walk.base = 0;
-    if (w1 > w0 && B > 1) {
+    if (w1 > w0 && a.B > 1) {
 #pragma unroll 1
       for (int b = 0;; walk.base += walk.count(), ++b) {
-        walk_to<X>(P, walk, b);
+        walk_to(P, walk, b);
         if (w0 < walk.base + walk.count()) break;
       }
     }
@@ -720,10 +824,10 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
     __syncthreads();
     tc_fence_after();
   } else {
-    const int per = (B + C::kThreads - 1) / C::kThreads;
-    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    const int per = (a.B + C::kThreads - 1) / C::kThreads;
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int mine = 0;
-    for (int b = b0; b < b1; ++b) walk_to<X>(P, walk, b), mine += walk.count();
+    for (int b = b0; b < b1; ++b) walk_to(P, walk, b), mine += walk.count();
     int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -742,7 +846,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
     if (w1 > w0 && mine > 0 && first <= w0 && w0 < first + mine) {
       int at = first;
       for (int b = b0; b < b1; ++b) {
-        if (per > 1) walk_to<X>(P, walk, b);
+        if (per > 1) walk_to(P, walk, b);
         if (w0 < at + walk.count()) {
           ints[4] = b, ints[5] = at, ints[8] = walk.X.S, ints[9] = walk.X.n;
           break;
@@ -756,10 +860,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
     walk.base = 0;
     if (w1 > w0) {
       walk.base = ints[5];
-      if (X)
-        walk_to<X>(P, walk, ints[4]);
-      else
-        plan<X>(P, walk, ints[4], Extent{ints[8], ints[9]});
+      plan(P, walk, ints[4], Extent{ints[8], ints[9]});
     }
   }
   walk.w = w0, walk.w1 = w1;
@@ -767,7 +868,29 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
   const TcSync sync{ints + 1, P.p.err};
   // `found` is written by a call, so it lives in memory, where asm statements
   // make every use a load; the roles work on a copy in registers
-  TcSegment found;
+  TcPlace plain;
+  TcSegment& found = plain.seg;
+  // With a list, one warp finds the items' places for all: a role takes the next one
+  // and gives it back after its last tile.  (A role that finds that a wait has run out
+  // ends; the softmax's warps, which meet at barriers, agree on that.)
+  int taken = 0;
+  auto next = [&](TcSegment& seg) {
+    if (!kMode) {
+      const bool any = next_segment(P, walk, found);
+      seg = found;
+      return any;
+    }
+    wait(sync, b_gf + 8 * (taken % kSegments), taken / kSegments & 1);
+    if (__any_sync(0xFFFFFFFFu, *sync.abort)) return false;
+    seg = places[taken % kSegments].seg;
+    return seg.T > 0;
+  };
+  auto give_back_place = [&] {
+    if (!kMode) return;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_ge + 8 * (taken % kSegments));
+    ++taken;
+  };
 
   if (warp >= 8) {
     if (warp == 8 || warp == 10) {
@@ -777,8 +900,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
       const uint32_t b_full = v ? b_vf : b_kf, b_empty = v ? b_ve : b_ke, ring = v ? sV : sK;
       constexpr int kElems = F8 ? C::kSw : C::kSw / 2;
       int slot = 0, lap = 0;
-      while (next_segment<X>(P, walk, found)) {
-        const TcSegment seg = found;
+      TcSegment seg;
+      for (; next(seg); give_back_place()) {
+        const TcMembers& mem = places[taken % kSegments].mem;
         if (!v) {  // the segment's queries, on their way into L2 while the last one's tiles are worked on
           const int rows = min(C::kRows, (seg.X.n + 1) * G - seg.rb * C::kRows);
           const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + seg.b * a.q_stride[0] + (int64_t)seg.h * G * a.q_stride[2];
@@ -786,30 +910,43 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
           for (int r = lane; r < rows; r += 32) {
             const int rr = seg.rb * C::kRows + r, qi = entry_of(P, rr);
             const __nv_bfloat16* row = q0 + qi * a.q_stride[1] + (rr - qi * G) * a.q_stride[2];
-            if (X && seg.carry == 1) {
-              const TcRow at = row_of<X>(P, seg, rr);
-              row = static_cast<const __nv_bfloat16*>(a.q) + at.b * a.q_stride[0] + at.i * a.q_stride[1] + at.hq * a.q_stride[2];
+            if ((kMode & kShare) && seg.m > 1) {
+              const TcRow to = row_of<kMode>(P, seg, rr);
+              row = static_cast<const __nv_bfloat16*>(a.q) + to.b * a.q_stride[0] + to.i * a.q_stride[1] + to.hq * a.q_stride[2];
             }
             for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
           }
         }
 #pragma unroll 1
         for (int t = seg.t0; t < seg.t1; ++t) {
-          const TcTile k = tile_of<X>(a, seg, t);
-          const int box = k.staged ? kStageBox : P.box, boxes = (k.valid + box - 1) / box;
+          const TcTile k = tile_of<kMode>(P, seg, t);
+          const int box = k.staged ? (kMode ? P.stage_box : kStageBox) : P.box, boxes = (k.valid + box - 1) / box;
           // each lane looks up its box's block before the slot is free
           int y = k.x0 + lane * box, w = seg.b;
-          if (!k.staged && lane < boxes) {
+          bool staged = k.staged;
+          if ((kMode & kShare) && k.own && lane < boxes) {  // whose box it is
+            const int x = k.x0 + lane;
+            int lo = 0, hi = kMembers;  // start[lo] <= x < start[hi]
+#pragma unroll 1
+            while (hi - lo > 1) {
+              const int mid = (lo + hi) / 2;
+              if (mem.start[mid] <= x) lo = mid; else hi = mid;
+            }
+            const int in = x - mem.start[lo], cached = cached_boxes(a, P.box, P.box_shift, seg.X.S, {mem.S[lo], mem.n[lo]});
+            staged = in >= cached;
+            w = seg.b + lo, y = staged ? (in - cached) * box : seg.X.S + in * box;
+          }
+          if (!staged && lane < boxes) {
             const int j = block_of(P, y);
-            w = __ldg(a.cache.block_table + (int64_t)seg.b * a.cache.max_blocks + j);
+            w = __ldg(a.cache.block_table + (int64_t)w * a.cache.max_blocks + j);
             if (w < 0 || w >= a.cache.num_blocks) {
               report(P.p.err, SV_ERR_STATE);
               w = a.cache.num_blocks;  // past the last: a load gives zeros
             }
             y -= j * a.cache.block_size;
           }
-          const int z = ((k.staged ? a.stage.layer : a.cache.layer) * 2 + v) * H + seg.h;
-          const CUtensorMap* map = k.staged ? &P.stage : &P.pages;
+          const int z = ((staged ? a.stage.layer : a.cache.layer) * 2 + v) * H + seg.h;
+          const CUtensorMap* map = staged ? &P.stage : &P.pages;
           if (lap > 0) wait(sync, b_empty + 8 * slot, (lap - 1) & 1);
           if (!__any_sync(0xFFFFFFFFu, *sync.abort)) {
             const uint32_t bar = b_full + 8 * slot, at = ring + slot * (v ? C::kTileBytes : C::kKBytes), dst = at + lane * box * C::kSw;
@@ -819,8 +956,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
 #pragma unroll
               for (int hf = 0; hf < C::kHalves; ++hf) tma_load_4d(dst + hf * C::kHalfBytes, map, bar, hf * kElems, y, z, w);
               if (F8 && !v)
-                tma_load_5d(at + C::kTileBytes + lane * box * 2 * kTail, k.staged ? &P.stage_tails : &P.page_tails, bar, 0, y, seg.h,
-                            (k.staged ? a.stage.layer : a.cache.layer) * 2, w);
+                tma_load_5d(at + C::kTileBytes + lane * box * 2 * kTail, staged ? &P.stage_tails : &P.page_tails, bar, 0, y, seg.h,
+                            (staged ? a.stage.layer : a.cache.layer) * 2, w);
             }
           }
           if (++slot == slots) slot = 0, ++lap;
@@ -840,10 +977,11 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
       constexpr uint32_t kIdO = instr_desc(F8 ? 0 : 1, kTile, D, true) | (F8 ? 1u << 7 : 0u);  // weights of 5 exponent bits
       const uint64_t q0 = smem_desc(sQ, 16, 8 * C::kSw, C::kSw), k0 = smem_desc(sK, 16, 8 * C::kSw, C::kSw);
       const uint64_t v0 = smem_desc(sV, C::kHalfBytes, 8 * C::kSw, C::kSw);
-      while (next_segment<X>(P, walk, found)) {
-        const TcSegment seg = found;
+      TcSegment seg;
+      for (; next(seg); give_back_place()) {
         const int units = (seg.t1 - seg.t0) * QM;
-        const int whole = ((a.stage.data || (X && seg.carry == 1) ? seg.X.S : seg.X.S + seg.X.n + 1) - (X ? seg.begin : 0)) / kTile;  // tiles before it are full
+        const bool apart = a.stage.data || ((kMode & kShare) && seg.m > 0);  // no entries among the cached positions
+        const int whole = ((apart ? seg.X.S : seg.X.S + seg.X.n + 1) - (kMode & kForms ? seg.begin : 0)) / kTile;  // tiles before it are full
         wait(sync, b_q, ph_q);
         ph_q ^= 1;
         // scores two units ahead of the outputs
@@ -854,7 +992,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
           bool k_there = QM == 2 && st == 1;
           if (x >= 2) {
             const int t = seg.t0 + (QM == 2 ? (x - 2) >> 1 : x - 2);
-            const int steps = t < whole ? kTile / C::kStep : (tile_of<X>(a, seg, t).valid + C::kStep - 1) / C::kStep;
+            const int steps = place_of<kMode>(seg, t) < whole ? kTile / C::kStep : (tile_of<kMode>(P, seg, t).valid + C::kStep - 1) / C::kStep;
             const uint64_t vd = v0 + vs * (C::kTileBytes >> 4);
             const bool first = x < 4;  // of this stream in this segment
             if (QM == 1 || st == 0) {  // the second row tile's keys are there
@@ -901,17 +1039,47 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
       // the last arrival that the products owe this block's memory
       if (vs + vlap > 0) wait(sync, b_ve + 8 * (vs ? vs - 1 : C::kV - 1), (vs ? vlap : vlap - 1) & 1);
     } else {  // warp 11
+      // ---- the items' places, one ahead of the others -----------------------
+      TcWalker list;
+      bool more = true;
+      int set = 0;
+      auto publish = [&] {
+        if (set >= kSegments) wait(sync, b_ge + 8 * (set % kSegments), (set / kSegments - 1) & 1);
+        if (__any_sync(0xFFFFFFFFu, *sync.abort)) {
+          more = false;
+          return;
+        }
+        more = next_place<kMode>(P, list, &places[set % kSegments]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_gf + 8 * (set % kSegments));
+        ++set;
+      };
+      if (kMode) {
+        list.w = w0, list.w1 = w1, list.count = __ldcg(P.list.head + 1);
+        if (w0 < w1) find_lot(P.list, list);
+        publish();
+        if (!F8)
+          while (more) publish();
+      }
       if (F8) {
         // ---- scales of 8-bit entries, from the tails that came with K into
         // what the softmax adds and multiplies by.  (Loading four bytes of an
         // entry by cp.async kept this warp 2000 cycles a tile: 64 single tokens
         // 216 us; loading the tails itself 1500: 193.)
         int slot = 0, lap = 0, due = 0;
-        while (next_segment<X>(P, walk, found)) {
-          const TcSegment seg = found;
+        TcSegment seg;
+        for (;; ++taken) {
+          if (kMode) {
+            if (taken >= set) break;
+            seg = places[taken % kSegments].seg;
+            if (seg.T == 0) break;
+            if (more) publish();
+          } else if (!next(seg)) {
+            break;
+          }
 #pragma unroll 1
           for (int t = seg.t0; t < seg.t1; ++t, ++due) {
-            const int box = tile_of<X>(a, seg, t).staged ? kStageBox : P.box, ring = due % kScaleRing;
+            const int box = tile_of<kMode>(P, seg, t).staged ? (kMode ? P.stage_box : kStageBox) : P.box, ring = due % kScaleRing;
             wait(sync, b_kf + 8 * slot, lap & 1);
             const char* tails = kslots + slot * C::kKBytes + C::kTileBytes;
             float ks[4], vs[4];
@@ -937,9 +1105,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
           }
         }
       }
-      if (X && P.sharing) check_groups(a, P.p.err);
       // ---- rows past each request's entries --------------------------------
-      for (int r = blockIdx.x; r < a.B * a.R; r += gridDim.x) {
+      for (int r = kMode && !P.dead ? a.B * a.R : blockIdx.x; r < a.B * a.R; r += gridDim.x) {
         const int b = r / a.R, i = r - b * a.R;
         if (i <= extent_of(a, b, P.p.err).n) continue;
         const float zero[8] = {};
@@ -952,8 +1119,20 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
     const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t tS = tmem + (quad << 21) + st * 128, tO = tmem + (quad << 21) + 256 + st * 128;
     int kbase = 0, ph_s = 0, ph_o = 0;
-    while (next_segment<X>(P, walk, found)) {
-        const TcSegment seg = found;
+    TcSegment seg;
+    for (;; give_back_place()) {
+      if (kMode) {
+        if (warp == 0) {
+          const bool any = next(seg);
+          if (lane == 0) ints[14] = any;
+        }
+        named_barrier(1, 256);
+        if (!*reinterpret_cast<volatile int*>(&ints[14])) break;
+        seg = places[taken % kSegments].seg;
+      } else if (!next(seg)) {
+        break;
+      }
+      const TcPlace& place = kMode ? places[taken % kSegments] : plain;
       const int n = seg.t1 - seg.t0, units = n * QM;
       const int i0 = seg.rb * C::kRows;
       // copies of the block's rows in the tile: this thread's copy weighs the
@@ -962,13 +1141,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
       const int fold = QM == 2 || rows > 64 ? 0 : rows > 32 ? 1 : 2, copies = 1 << fold, apart = kTile >> fold;
       const int copy = row >> (7 - fold), ch_a = copy << (2 - fold), ch_b = ch_a + (4 >> fold);
       const int lrow = QM == 2 ? st * kTile + row : row - copy * apart;  // row of the CTA's block
-      const int i = entry_of(P, i0 + lrow), hq = seg.h * G + i0 + lrow - i * G;
-      const bool live = i <= seg.X.n;
+      const TcRow me = row_of<kMode>(P, seg, i0 + lrow);
+      const int i = me.i, hq = me.hq;
+      const bool live = (kMode & kShare) && seg.m > 0 ? lrow < rows && i <= place.mem.n[me.j] : i <= seg.X.n;
       TcForm form = {};
-      if (X && P.forms && live) {
-        const TcRow at = row_of<X>(P, seg, i0 + lrow);
-        form.at = (seg.carry == 1 ? a.seq_len[at.b] : seg.X.S) + depth_of(a, at.b, at.i);
-        form.slope = a.slopes ? a.slopes[at.hq] * kLog2e : 0.0f;
+      if ((kMode & kForms) && live) {
+        form.S = (kMode & kShare) && seg.m > 0 ? place.mem.S[me.j] : seg.X.S;
+        form.depth = depth_of(a, me.b, i);
+        form.slope = a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
       }
       const bool warp_live = lrow - lane < rows;
       // queries: rows of this CTA's block, read once and written to each copy,
@@ -988,13 +1168,11 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
           for (int it = 0; it < kAt; ++it) {
             const int idx = (it0 + it) * kGroup + qt, rr = part0 + idx / kChunks, qi = entry_of(P, rr);
             x8[it] = make_uint4(0, 0, 0, 0);
-            if (X && seg.carry == 1) {
-              if (it0 + it < each && qi <= seg.X.n) {
-                const TcRow at = row_of<X>(P, seg, rr);
-                if (!a.n_nodes || at.i <= a.n_nodes[at.b])
-                  x8[it] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at.b * a.q_stride[0] +
-                                                           at.i * a.q_stride[1] + at.hq * a.q_stride[2] + idx % kChunks * 8);
-              }
+            if ((kMode & kShare) && seg.m > 1) {
+              const TcRow to = row_of<kMode>(P, seg, rr);
+              if (it0 + it < each && qi <= seg.X.n && to.i <= place.mem.n[to.j])
+                x8[it] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + to.b * a.q_stride[0] + to.i * a.q_stride[1] +
+                                                         to.hq * a.q_stride[2] + idx % kChunks * 8);
             } else if (it0 + it < each && qi <= seg.X.n)
               x8[it] = *reinterpret_cast<const uint4*>(q0 + qi * a.q_stride[1] + (rr - qi * G) * a.q_stride[2] + idx % kChunks * 8);
           }
@@ -1052,13 +1230,13 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
       }
       // positive (a subnormal at least), so that what is not seen stays -inf when it is scaled
       const float c_raw = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? s_qs[(QM == 2 ? st * kTile : 0) + row] : 1.0f), 0x1p-149f);
-      const float c = X && P.forms ? 1.0f : c_raw;  // shaped scores have it already
+      const float c = kMode & kForms ? 1.0f : c_raw;  // shaped scores have it already
       const uint64_t c2 = pair(c, c);
       // wr: reference of 8-bit weights, log2 units; raise = 2^(kBias + m - wr)
       float m = -kInf, l = 0.0f, wr = -kInf, raise = 0.0f;
       for (int u = st; u < units; u += 2) {
         const int tt = QM == 2 ? u >> 1 : u;
-        const TcTile k = tile_of<X>(a, seg, seg.t0 + tt);
+        const TcTile k = tile_of<kMode>(P, seg, seg.t0 + tt);
         const int kt = kbase + tt;
         const bool full = k.prefix && k.valid == kTile;
         wait(sync, b_s + 8 * st, ph_s);
@@ -1069,8 +1247,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
         const float* sc = s_sc + (kt % kScaleRing) * 2 * kTile;
         if (warp_live) {
           const int chunks = (k.valid + 31) / 32, ch_e = min(ch_b, chunks);
-          if (X && P.forms)
-            shape_scores<F8>(P, found, k, form, i, c_raw, sc, ch_a, ch_e, tS);
+          uint32_t some = 15;  // groups of 32 keys that a row of the warp sees
+          if (kMode & kForms || ((kMode & kShare) && !full))
+            some = shape_scores<F8, kMode>(P, place, k, form, me.j, live ? i : INT32_MAX, c_raw, sc, ch_a, ch_e, tS);
           else if (!full)
             hide_unseen(P, seg.b, i, seg.X.n, k.prefix, k.valid, k.u0, ch_a, ch_e, tS);
           // One pass over the tile's scores, 32 columns at a time, so that the
@@ -1081,7 +1260,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
           for (int ch = 0; ch < chunks; ++ch) {
             constexpr int kW = F8 ? 24 : 16;  // columns of 32 weights
             uint32_t w[kW];
-            if (ch < ch_a || ch >= ch_b) {  // another copy's keys
+            if (ch < ch_a || ch >= ch_b || (kMode && !(some >> ch & 1))) {  // another copy's keys, or no one's
 #pragma unroll
               for (int e = 0; e < kW; ++e) w[e] = 0u;
               tmem_st(tS + kW * ch, w);
@@ -1090,7 +1269,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
             if (F8) {
               // Weights by the references so far; where a row's sum or largest shows that
               // one is too low, once more after they have moved.
-              const float* kp = X && P.forms ? s_ones : sc + 32 * ch;
+              const float* kp = kMode & kForms ? s_ones : sc + 32 * ch;
               bool bad = m == -kInf, again = false;
               uint64_t gs[2];
 #pragma unroll 1
@@ -1186,12 +1365,12 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
         // not ruin them through 0 * NaN: non-finite values of V are cleared and
         // given back to the rows that see them at the end.
         int r0, r1;
-        half_seen<X>(a, k, seg, &r0, &r1);
+        half_seen<kMode>(a, k, seg, &r0, &r1);
         if (r0 < r1 || k.valid % C::kStep) {
           const int slot = kt % C::kV, end = (k.valid + C::kStep - 1) / C::kStep * C::kStep;
           char* v = vslots + slot * C::kTileBytes;
           wait(sync, b_vf + 8 * slot, (kt / C::kV) & 1);
-          if (X && r1 < k.valid) {
+          if ((kMode & kForms) && r1 < k.valid) {
             clean_rows<F8>(v, r0, r1, r1, C::kRow / 16, row, &ints[2]);
             r0 = k.valid;
           }
@@ -1244,9 +1423,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
       // a CTA has two partial results at most: of the item it starts in, and of its last
       float* part = P.p.part + (int64_t)(2 * blockIdx.x + (w0 >= seg.item0 ? 0 : 1)) * C::kPart;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const int64_t out0 = seg.b * a.out_stride[0], out = out0 + i * a.out_stride[1] + (int64_t)hq * a.out_stride[2];
-      const Carry carry = X && seg.carry ? carry_of(a, P.carry, seg.carry == 2) : Carry{};
-      const int64_t crow = X && seg.carry && live ? carry_row(a, G, row_of<X>(P, seg, i0 + lrow)) : 0;
+      const int64_t out = me.b * a.out_stride[0] + i * a.out_stride[1] + (int64_t)hq * a.out_stride[2];
       float4* gather = reinterpret_cast<float4*>(sm);  // the queries' place: every score is done
 #pragma unroll 1
       for (int col = c_first; col < c_first + kCols; col += 32) {
@@ -1264,27 +1441,20 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
           }
         }
         auto put = [&](int at, const float* z) {  // eight columns of a row
-          if (X && !split && seg.carry) {
-            float* d = carry.o + crow * D + at;
-            *reinterpret_cast<float4*>(d) = make_float4(z[0], z[1], z[2], z[3]);
-            *reinterpret_cast<float4*>(d + 4) = make_float4(z[4], z[5], z[6], z[7]);
-            if (spoiled)
-#pragma unroll 1
-              for (int e = 0; e < 8; ++e) d[e] += given_back<X>(P, found, i, at + e);
-          } else if (!split) {
+          if (!split) {
             __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.out) + out + at;
             *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16(z[0] * inv, z[1] * inv), pack_bf16(z[2] * inv, z[3] * inv),
                                                       pack_bf16(z[4] * inv, z[5] * inv), pack_bf16(z[6] * inv, z[7] * inv));
             if (spoiled)
 #pragma unroll 1
-              for (int e = 0; e < 8; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back<X>(P, found, i, at + e));
+              for (int e = 0; e < 8; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back<kMode>(P, place, me, at + e));
           } else {
             float* d = part + lrow * D + at;
             *reinterpret_cast<float4*>(d) = make_float4(z[0], z[1], z[2], z[3]);
             *reinterpret_cast<float4*>(d + 4) = make_float4(z[4], z[5], z[6], z[7]);
             if (spoiled)
 #pragma unroll 1
-              for (int e = 0; e < 8; ++e) d[e] += given_back<X>(P, found, i, at + e);
+              for (int e = 0; e < 8; ++e) d[e] += given_back<kMode>(P, place, me, at + e);
           }
         };
         if (copies > 1) {  // each copy adds all shares of 32 / copies columns
@@ -1313,7 +1483,6 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
       }
       if (split && live && copy == 0 && (QM == 2 || st == 0))
         reinterpret_cast<float2*>(part + C::kRows * D)[lrow] = make_float2(m, l);
-      if (X && !split && seg.carry && live && copy == 0 && (QM == 2 || st == 0)) carry.ml[crow] = make_float2(m, l);
       if (split) {
         // the last of the item's CTAs joins the partial results, in the order
         // of the CTAs, so that results do not depend on who was last
@@ -1359,17 +1528,12 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, X>::kThreads, 1) tc_attenti
               y[0] += v0.x * f, y[1] += v0.y * f, y[2] += v0.z * f, y[3] += v0.w * f;
               y[4] += v1.x * f, y[5] += v1.y * f, y[6] += v1.z * f, y[7] += v1.w * f;
             }
-            if (X && seg.carry) {
-              const int64_t cr = carry_row(a, G, row_of<X>(P, seg, i0 + r));
-              store8<true>(carry.o, cr * D + col, y);
-              if (col == 0) carry.ml[cr] = make_float2(ML.y == 0.0f ? -kInf : ML.x, ML.y);  // a row that saw nothing binds no reference
-              continue;
-            }
+            const TcRow to = row_of<kMode>(P, seg, i0 + r);
+            if ((kMode & kShare) && seg.m > 0 && to.i > place.mem.n[to.j]) continue;
             const float iv = 1.0f / ML.y;
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = ML.y == 0.0f ? 0.0f : y[e] * iv;
-            const int qi = entry_of(P, i0 + r);
-            store8<false>(a.out, out0 + qi * a.out_stride[1] + (seg.h * G + i0 + r - qi * G) * a.out_stride[2] + col, y);
+            store8<false>(a.out, to.b * a.out_stride[0] + to.i * a.out_stride[1] + to.hq * a.out_stride[2] + col, y);
           }
         }
       }
@@ -1395,16 +1559,24 @@ struct TcKernel {
   int threads, smem, part;  // block, dynamic shared memory, floats of a partial result
 };
 
-// head_dim 64 or 128; tiles: row tiles per CTA, 1 or 2; with forms or shared prefixes.
+// head_dim 64 or 128; tiles: row tiles per CTA, 1 or 2.
 TcKernel tc_kernel_bf16(int head_dim, int tiles);
 TcKernel tc_kernel_e4m3(int head_dim, int tiles);
-TcKernel tc_kernel_bf16_more(int head_dim, int tiles);
-TcKernel tc_kernel_e4m3_more(int head_dim, int tiles);
+TcKernel tc_kernel_bf16_forms(int head_dim, int tiles);
+TcKernel tc_kernel_e4m3_forms(int head_dim, int tiles);
+TcKernel tc_kernel_bf16_shared(int head_dim, int tiles);
+TcKernel tc_kernel_e4m3_shared(int head_dim, int tiles);
+TcKernel tc_kernel_bf16_both(int head_dim, int tiles);
+TcKernel tc_kernel_e4m3_both(int head_dim, int tiles);
 
-template <bool F8, int D, int QM, bool X>
-TcKernel tc_kernel() {
-  using C = TcShape<F8, D, QM, X>;
-  return {tc_attention_kernel<F8, D, QM, X>, C::kThreads, C::kSmem, C::kPart};
+template <bool F8, int kMode>
+TcKernel tc_kernel(int head_dim, int tiles) {
+  auto k = [](auto shape, void (*fn)(TcParams)) { return TcKernel{fn, shape.kThreads, shape.kSmem, shape.kPart}; };
+  if (head_dim == 64)
+    return tiles == 1 ? k(TcShape<F8, 64, 1, kMode>(), tc_attention_kernel<F8, 64, 1, kMode>)
+                      : k(TcShape<F8, 64, 2, kMode>(), tc_attention_kernel<F8, 64, 2, kMode>);
+  return tiles == 1 ? k(TcShape<F8, 128, 1, kMode>(), tc_attention_kernel<F8, 128, 1, kMode>)
+                    : k(TcShape<F8, 128, 2, kMode>(), tc_attention_kernel<F8, 128, 2, kMode>);
 }
 
 }  // namespace sv

@@ -18,9 +18,7 @@ constexpr int kSimtThreads = 32 * kSimtWarps;
 // rows (16 FMA to five shared-memory reads), latency with few: fewer rows a warp
 // then.  One request of 6 rows over 38 keys, 4 heads of 64: 18.8 us with 4 rows a
 // warp and a tile's loads one after another, 10.2 us as it is.
-// X: the scores may have a form (capped, less with the distance, a window); with
-// P.carry rows of requests that share a prefix go on from its part, and from the
-// request's own where the tensor kernel has made that; the others are done.
+// X: the scores may have a form (capped, less with the distance, a window).
 template <bool F32, int RPW, bool X>
 __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __grid_constant__ AttnParams P) {
   pdl_wait();
@@ -39,11 +37,9 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
   const int split = blockIdx.y;
   const Extent E = extent_of(a, b, P.err);
   const int row0 = rb * kSimtRows;
-  const int shared = X && P.carry ? shared_of(a, b) : 0;
-  if (X && P.carry && shared == 0) return;
   const int64_t q0 = b * a.q_stride[0], o0 = b * a.out_stride[0];
   // rows of this block that are past the request's entries are zero
-  if (split == 0 && !(X && P.carry))
+  if (split == 0)
     for (int c = threadIdx.x; c < kSimtRows * (D / 8); c += kSimtThreads) {
       const int r = row0 + c / (D / 8), i = r / G;
       const float zero[8] = {};
@@ -51,13 +47,11 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
         store8<F32>(a.out, o0 + i * a.out_stride[1] + (h * G + r % G) * a.out_stride[2] + c % (D / 8) * 8, zero);
     }
   if (row0 / G > E.n) return;
-  const int begin = X ? P.carry ? shared : first_seen(a, E.S) : 0;
-  const int keys = E.S + E.n + 1;
-  const bool parts = X && P.carry && keys - begin > kOwnShort;  // the request's own keys are done too
-  const int tiles = parts ? 0 : (keys - begin + kSimtKeys - 1) / kSimtKeys;
-  const int per = max(1, (tiles + P.splits - 1) / P.splits);
+  const int begin = X ? first_seen(a, E.S) : 0;
+  const int keys = E.S + E.n + 1, tiles = (keys - begin + kSimtKeys - 1) / kSimtKeys;
+  const int per = (tiles + P.splits - 1) / P.splits;
   const int t0 = split * per, t1 = min(tiles, t0 + per);
-  const int used = max(1, (tiles + per - 1) / per);  // shares with work
+  const int used = (tiles + per - 1) / per;  // shares with work
   if (split >= used) return;
   const int64_t cstep = row_step(a.cache), sstep = a.stage.data ? row_step(a.stage) : 0;
   for (int c = threadIdx.x; c < kSimtRows * (D / 8); c += kSimtThreads) {
@@ -73,29 +67,6 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
     m[r] = -__int_as_float(0x7F800000), l[r] = 0.0f;
 #pragma unroll
     for (int e = 0; e < kMaxHeadDim / 32; ++e) o[r][e] = 0.0f;
-  }
-  if (X && P.carry) {
-    for (int own = 0; own <= (parts ? 1 : 0); ++own) {
-      const Carry c = carry_of(a, P.carry, own);
-#pragma unroll
-      for (int r = 0; r < kRowsPerWarp; ++r) {
-        const int row = row0 + warp * kRowsPerWarp + r;
-        if (row / G > E.n) continue;
-        const int64_t at = ((int64_t)b * H + h) * a.R * G + row;
-        const float2 ml = c.ml[at];
-        const float mn = fmaxf(m[r], ml.x), base = mn == -__int_as_float(0x7F800000) ? 0.0f : mn;
-        const float f = exp2f(m[r] - base), g = exp2f(ml.x - base);
-        m[r] = mn;
-        l[r] = l[r] * f + (lane == 0 ? ml.y * g : 0.0f);
-#pragma unroll
-        for (int d = 0; d < kMaxHeadDim / 128; ++d)
-          if (d * 128 + lane * 4 < D) {
-            const float4 v = *reinterpret_cast<const float4*>(c.o + at * D + d * 128 + lane * 4);
-            o[r][4 * d] = o[r][4 * d] * f + v.x * g, o[r][4 * d + 1] = o[r][4 * d + 1] * f + v.y * g;
-            o[r][4 * d + 2] = o[r][4 * d + 2] * f + v.z * g, o[r][4 * d + 3] = o[r][4 * d + 3] * f + v.w * g;
-          }
-      }
-    }
   }
   const float* q = sQ + warp * kRowsPerWarp * DP;
   for (int t = t0; t < t1; ++t) {
@@ -301,10 +272,11 @@ static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct TcPlan {
   bool use;
-  bool sharing;     // groups' prefixes are read once
-  int tiles, ctas;  // row tiles per CTA, grid
-  TcKernel k;
-  size_t bytes, carry;  // of workspace, and where the parts start in it
+  bool sharing;  // groups' prefixes are read once
+  int which;     // row tiles per CTA: 1, 2, or 3 for a launch of each
+  int ctas;      // grid
+  TcKernel k[2];
+  size_t list, ranges, bytes;  // where the list and the ranges start in the workspace, and its bytes
 };
 
 static bool has_form(const sv_attention_args* a) { return a->softcap > 0.0f || a->slopes || a->window > 0; }
@@ -319,25 +291,30 @@ static TcPlan tc_plan(const sv_handle* h, const sv_attention_args* a) {
   if (a->dtype != SV_BF16 || (c.head_dim != 64 && c.head_dim != 128) || c.block_size % 8 || c.num_blocks < 1)
     return p;
   const int64_t rows = (int64_t)a->R * (a->Hq / c.heads);
-  p.tiles = rows > kTile ? 2 : 1;
-  const int64_t items = (int64_t)a->B * c.heads * cdiv(rows, p.tiles * kTile);
-  const int64_t each = cdiv((int64_t)c.max_blocks * c.block_size, kTile) + cdiv(a->R, kTile) + 1 + kLead;
-  int64_t tiles = items * each;
+  const bool forms = has_form(a);
+  // a group's rows are its members' R entries each, and it has no more items than they
+  p.sharing = a->shared_len && a->window == 0;
+  p.which = rows > kTile ? 2 : p.sharing && a->B * rows > kTile ? 3 : 1;
+  const int64_t blocks = cdiv(rows, p.which == 2 ? 2 * kTile : kTile);
+  const int64_t tiles = (int64_t)a->B * c.heads * blocks * (cdiv((int64_t)c.max_blocks * c.block_size, kTile) + cdiv(a->R, kTile) + 1 + kLead);
   if (tiles > INT32_MAX || (rows + 2 * kTile) * (a->Hq / c.heads) > INT32_MAX || c.num_blocks == INT32_MAX) return p;
   p.use = true;
-  // a group's rows are its members' R entries each; items of both kinds at most
-  // twice the requests' and one more a group
-  p.sharing = a->shared_len && a->window == 0 && 3 * tiles <= INT32_MAX &&
-              (a->B * rows + 2 * kTile) * (a->Hq / c.heads) <= INT32_MAX;
-  if (p.sharing) tiles *= 3;
-  if (p.sharing || has_form(a))
-    p.k = c.format == SV_KV_E4M3 ? tc_kernel_e4m3_more(c.head_dim, p.tiles) : tc_kernel_bf16_more(c.head_dim, p.tiles);
-  else
-    p.k = c.format == SV_KV_E4M3 ? tc_kernel_e4m3(c.head_dim, p.tiles) : tc_kernel_bf16(c.head_dim, p.tiles);
+  typedef TcKernel (*Of)(int, int);
+  static const Of of[2][4] = {{tc_kernel_bf16, tc_kernel_bf16_forms, tc_kernel_bf16_shared, tc_kernel_bf16_both},
+                              {tc_kernel_e4m3, tc_kernel_e4m3_forms, tc_kernel_e4m3_shared, tc_kernel_e4m3_both}};
   p.ctas = (int)(tiles < h->num_sms ? tiles : h->num_sms);
   if (p.ctas > kTickets) p.ctas = kTickets;
-  p.carry = p.bytes = kTicketBytes + up256((size_t)p.ctas * 2 * p.k.part * 4);
-  if (p.sharing) p.bytes += up256(2 * (size_t)carry_rows(*a) * (c.head_dim + 2) * 4);
+  size_t part = 0;
+  for (int l = 0; l < 2; ++l)
+    if (p.which >> l & 1) {
+      p.k[l] = of[c.format == SV_KV_E4M3][(forms ? kForms : 0) + (p.sharing ? kShare : 0)](c.head_dim, l + 1);
+      part = (size_t)p.k[l].part;
+    }
+  p.list = p.bytes = kTicketBytes + up256((size_t)p.ctas * 2 * part * 4);
+  if (forms || p.sharing) {
+    p.ranges = p.bytes += 256 + 2 * up256((size_t)a->B * sizeof(TcLot));
+    if (forms && !p.sharing && blocks > 1) p.bytes += up256((size_t)a->B * (2 * (size_t)blocks + 1) * 4);
+  }
   return p;
 }
 
@@ -395,12 +372,10 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
   P.p.ticket = static_cast<uint32_t*>(ws);
   P.p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketBytes);
   P.p.err = h->d_err;
-  P.forms = has_form(a);
-  P.sharing = plan.sharing;
-  P.carry = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.carry);
   const sv_kv_place& c = a->cache;
   P.box = 8;
-  while (P.box < kTile && c.block_size % (2 * P.box) == 0) P.box *= 2;
+  while (P.box < (plan.sharing ? kStageBox : kTile) && c.block_size % (2 * P.box) == 0) P.box *= 2;
+  P.stage_box = plan.sharing ? P.box : kStageBox;
   P.block_shift = -1;
   for (int s = 3; s < 31; ++s)
     if (c.block_size == 1 << s) P.block_shift = s;
@@ -412,34 +387,56 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
                  {c.block_size, row, row * c.block_size, c.num_blocks, per * c.layers * c.block_size}, P.box))
     return SV_ERR_CUDA;
   const sv_kv_place& g = a->stage;
-  if (g.data && !make_maps(&P.stage, &P.stage_tails, g, {g.rows, per * g.layers, row, a->B, per * g.layers * g.rows}, kStageBox))
+  if (g.data && !make_maps(&P.stage, &P.stage_tails, g, {g.rows, per * g.layers, row, a->B, per * g.layers * g.rows}, P.stage_box))
     return SV_ERR_CUDA;
-  const sv_status rr = sv_raise_dyn_smem((const void*)plan.k.fn, (size_t)plan.k.smem);
-  if (rr != SV_OK) return rr;
-  if (sv_launch_pdl(plan.k.fn, dim3((unsigned)plan.ctas), dim3((unsigned)plan.k.threads), (size_t)plan.k.smem, stream, P) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return SV_ERR_CUDA;
+  const bool forms = has_form(a), listed = forms || plan.sharing;
+  TcPlanning L = {};
+  if (listed) {
+    char* at = static_cast<char*>(ws);
+    P.entries_magic = a->R == 1 ? 0u : (uint32_t)((0x100000000ull + a->R - 1) / a->R);
+    while (P.box >> (P.box_shift + 1)) ++P.box_shift;
+    P.down = a->slopes != nullptr;
+    L.a = *a, L.which = plan.which, L.box = P.box, L.shift = P.box_shift, L.group = P.group, L.sharing = plan.sharing, L.err = h->d_err;
+    L.head = reinterpret_cast<int*>(at + plan.list);
+    for (int l = 0; l < 2; ++l) L.lots[l] = reinterpret_cast<TcLot*>(at + plan.list + 256 + l * up256((size_t)a->B * sizeof(TcLot)));
+    if (plan.bytes > plan.ranges) {
+      L.ranges = reinterpret_cast<int*>(at + plan.ranges);
+      L.words = 2 * (int)cdiv((int64_t)a->R * P.group, plan.which == 2 ? 2 * kTile : kTile) + 1;
+    }
+    const sv_status rp = plan_launch(L, stream);
+    if (rp != SV_OK) return rp;
+  }
+  P.dead = true;
+  for (int l = 0; l < 2; ++l) {
+    if (!(plan.which >> l & 1)) continue;
+    const TcKernel& k = plan.k[l];
+    P.list = {L.lots[l], listed ? L.head + 2 * l : nullptr, L.ranges, L.words};
+    const sv_status rr = sv_raise_dyn_smem((const void*)k.fn, (size_t)k.smem);
+    if (rr != SV_OK) return rr;
+    if (sv_launch_pdl(k.fn, dim3((unsigned)plan.ctas), dim3((unsigned)k.threads), (size_t)k.smem, stream, P) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return SV_ERR_CUDA;
+    }
+    P.dead = false;
   }
   return SV_OK;
 }
 
-// carry: only to join the parts of requests that share a prefix.
-static sv_status simt_launch(sv_handle* h, const sv_attention_args* a, void* ws, float* carry, cudaStream_t stream) {
+static sv_status simt_launch(sv_handle* h, const sv_attention_args* a, void* ws, cudaStream_t stream) {
   const int64_t items = simt_items(a);
   AttnParams P = {};
   P.a = *a;
   P.ticket = static_cast<uint32_t*>(ws);
   P.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketBytes);
   P.err = h->d_err;
-  P.splits = carry ? 1 : simt_splits(h, a, items);
-  P.carry = carry;
+  P.splits = simt_splits(h, a, items);
   const size_t smem = (size_t)(2 * kSimtKeys + simt_rows(a)) * (a->cache.head_dim + 4) * 4;
   typedef void (*Fn)(AttnParams);
 #define SV_SIMT(x) {{simt_attention_kernel<false, 1, x>, simt_attention_kernel<false, 2, x>, simt_attention_kernel<false, 4, x>}, \
                     {simt_attention_kernel<true, 1, x>, simt_attention_kernel<true, 2, x>, simt_attention_kernel<true, 4, x>}}
   static const Fn fns[2][2][3] = {SV_SIMT(false), SV_SIMT(true)};
 #undef SV_SIMT
-  const Fn fn = fns[has_form(a) || carry][a->dtype == SV_FP32][simt_rows(a) / 8];
+  const Fn fn = fns[has_form(a)][a->dtype == SV_FP32][simt_rows(a) / 8];
   const sv_status rr = sv_raise_dyn_smem((const void*)fn, smem);
   if (rr != SV_OK) return rr;
   if (sv_launch_pdl(fn, dim3((unsigned)items, (unsigned)P.splits), dim3(kSimtThreads), smem, stream, P) != cudaSuccess) {
@@ -500,10 +497,5 @@ extern "C" sv_status sv_tree_attention(sv_handle* h, const sv_attention_args* a,
   if (a->B == 0) return SV_OK;
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < need) return SV_ERR_INVALID;
   const TcPlan plan = tc_plan(h, a);
-  if (plan.use) {
-    const sv_status rt = tc_launch(h, a, plan, ws, (cudaStream_t)stream);
-    if (rt != SV_OK || !plan.sharing) return rt;
-  }
-  return simt_launch(h, a, ws, plan.sharing ? reinterpret_cast<float*>(static_cast<char*>(ws) + plan.carry) : nullptr,
-                     (cudaStream_t)stream);
+  return plan.use ? tc_launch(h, a, plan, ws, (cudaStream_t)stream) : simt_launch(h, a, ws, (cudaStream_t)stream);
 }
