@@ -310,39 +310,51 @@ __device__ __forceinline__ TcRow row_of(const TcParams& P, const TcSegment& s, i
   return {j, s.b + j, e - j * P.p.a.R, hq};
 }
 
-// What row (member j, entry i) sees of 32 keys of a tile that holds entries or own
-// boxes: their bits, and in u the entry number of the first of each 8 keys (negative:
-// cached positions before the request's entry 0).
+// What row (member j, entry i) sees of 32 keys of a tile, by the mask.
 template <int kMode>
-static __device__ __noinline__ uint32_t seen_of(const TcParams& P, const TcPlace& s, const TcTile& k, int j, int i, int ch, int (&u)[4]) {
+__device__ __forceinline__ uint32_t seen_of(const TcParams& P, const TcPlace& s, const TcTile& k, int j, int i, int ch) {
   const sv_attention_args& a = P.p.a;
   if (!(kMode & kShare) || !k.own) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) u[g] = k.u0 + 32 * ch + 8 * g;
     const int left = k.valid - 32 * ch;
     const uint32_t all = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u;
-    return i <= s.seg.X.n ? seen_bits(a, s.seg.b, i, s.seg.X.n, u[0]) & all : 0u;
+    return k.prefix ? all : i <= s.seg.X.n ? seen_bits(a, s.seg.b, i, s.seg.X.n, k.u0 + 32 * ch) & all : 0u;
   }
-  const int S = s.mem.S[j], n = s.mem.n[j], first = s.mem.start[j], end = s.mem.start[j + 1];
+  const int first = s.mem.start[j], end = s.mem.start[j + 1], x0 = k.x0 + (32 * ch >> P.box_shift);
+  const Extent E = {s.mem.S[j], s.mem.n[j]};
+  if (x0 >= end || x0 + (32 >> P.box_shift) <= first || i > E.n) return 0u;
+  const int cached = cached_boxes(a, P.box, P.box_shift, s.seg.X.S, E);
   uint32_t bits = 0;
-  const int x0 = k.x0 + (32 * ch >> P.box_shift);
-  if (x0 >= end || x0 + (32 >> P.box_shift) <= first || i > n) return 0u;
-  const int cached = cached_boxes(a, P.box, P.box_shift, s.seg.X.S, {S, n});
 #pragma unroll 1
-  for (int g = 0; g < 4; ++g) {
-    const int in = 8 * g & (P.box - 1), x = x0 + (8 * g >> P.box_shift);
-    u[g] = 0;
-    if (x < first || x >= end) continue;
-    const bool staged = x - first >= cached;
-    u[g] = (staged ? (x - first - cached) << P.box_shift : s.seg.X.S + ((x - first) << P.box_shift) - S) + in;
-    uint32_t w;
-    if (a.stage.data && !staged)
-      w = u[g] >= 0 ? 0u : u[g] <= -8 ? 0xFFu : (1u << -u[g]) - 1u;
-    else
-      w = seen_bits(a, s.seg.b + j, i, n, u[g]) & 0xFFu;
-    bits |= w << (8 * g);
+  for (int g = 0; g < 32; g += P.box) {
+    const int x = x0 + (g >> P.box_shift) - first;
+    if (x < 0 || x >= end - first) continue;
+    const bool staged = x >= cached;
+    const int u = staged ? (x - cached) << P.box_shift : s.seg.X.S + (x << P.box_shift) - E.S;  // the entry of the box's first row
+    const uint32_t w = a.stage.data && !staged ? u >= 0 ? 0u : u <= -32 ? 0xFFFFFFFFu : (1u << -u) - 1u : seen_bits(a, s.seg.b + j, i, E.n, u);
+    bits |= (w & ((1u << P.box) - 1u)) << g;
   }
   return bits;
+}
+
+// The place past its request's S of key `x` of a tile that is no prefix's (negative:
+// cached positions).
+template <int kMode>
+static __device__ __noinline__ int key_place(const TcParams& P, const TcPlace& s, const TcTile& k, int x) {
+  const sv_attention_args& a = P.p.a;
+  int b = s.seg.b, u = k.u0 + x, n = s.seg.X.n;
+  if ((kMode & kShare) && k.own) {
+    const int box = k.x0 + (x >> P.box_shift);
+    int lo = 0, hi = kMembers;  // start[lo] <= box < start[hi]
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (s.mem.start[mid] <= box) lo = mid; else hi = mid;
+    }
+    const Extent E = {s.mem.S[lo], s.mem.n[lo]};
+    const int in = box - s.mem.start[lo], cached = cached_boxes(a, P.box, P.box_shift, s.seg.X.S, E);
+    b += lo, n = E.n, u = (in >= cached ? (in - cached) << P.box_shift : s.seg.X.S + (in << P.box_shift) - E.S) + (x & (P.box - 1));
+  }
+  return u < 0 || u > n ? u : depth_of(a, b, u);
 }
 
 // Rows of V in a tile, [r0, r1), that some row of the item may not see though another
@@ -474,14 +486,12 @@ static __device__ __noinline__ float given_back(const TcParams& P, const TcPlace
       bool staged = k.staged;
       int u = k.u0 + r, x = k.x0 + r;  // entry number, and entry or position
       if (kMode) {
-        int first[4];
-        const uint32_t bits = seen_of<kMode>(P, at, k, row.j, row.i, r >> 5, first);
-        if (!(bits >> (r & 31) & 1)) continue;
+        if (!(seen_of<kMode>(P, at, k, row.j, row.i, r >> 5) >> (r & 31) & 1)) continue;
         if ((kMode & kShare) && k.own) {
           const Extent E = {at.mem.S[row.j], at.mem.n[row.j]};
-          u = first[r >> 3 & 3] + (r & 7);
-          staged = k.x0 + (r >> P.box_shift) - at.mem.start[row.j] >= cached_boxes(a, P.box, P.box_shift, seg.X.S, E);
-          x = staged ? u : E.S + u;
+          const int in = k.x0 + (r >> P.box_shift) - at.mem.start[row.j], cached = cached_boxes(a, P.box, P.box_shift, seg.X.S, E);
+          staged = in >= cached;
+          x = (staged ? (in - cached) << P.box_shift : seg.X.S + (in << P.box_shift)) + (r & (P.box - 1));
         }
         if (a.window > 0 && abs(depth_of(a, row.b, row.i) - (u < 0 ? u : depth_of(a, row.b, u))) >= a.window) continue;
       } else if (!(seen_bits(a, row.b, row.i, seg.X.n, u) & 1)) {
@@ -519,125 +529,94 @@ static __device__ __noinline__ void hide_unseen(const TcParams& P, int b, int i,
   tmem_wait_st();
 }
 
-// What a row's scores get from their form.
-struct TcForm {
-  int S, depth;  // the row's request's length, and its depth below that
-  float slope;   // of its head, log2 units
-};
-
-// Scores of a tile become what the softmax takes: -inf where a row does not see the
-// key; with a form times c (and K's scales ks) before, capped, and less the distance's
-// share, in log2 units.  The groups of 32 keys that any row of the warp sees are
-// returned; the others are left as they are.  In a pass of its own over tensor memory,
-// 16 columns at a time: the softmax's loop would have it twice (once more where a
-// reference moves), and 32 unrolled columns were 3100 cycles a group, mostly waits for
-// instructions (64 single tokens under a window of 1024, capped: 104 us).
-//   cap tanh(s / cap) = cap - 2 cap / (1 + 2^(2 s log2(e) / cap)); where all of a group's
-// scores are below 0.3 cap, as nearly all are, the series of tanh to the ninth power
-// (the next term is 5e-8 of it) saves two of the three special functions an element.
-template <bool F8, int kMode>
-static __device__ __noinline__ uint32_t shape_scores(const TcParams& P, const TcPlace& at, const TcTile& k, const TcForm& f, int j, int i,
-                                                     float c, const float* ks, int ch_a, int ch_e, uint32_t tS) {
-  const sv_attention_args& a = P.p.a;
-  constexpr bool kShape = kMode & kForms;
-  const float cap = kShape ? a.softcap * kLog2e : 0.0f, per = cap > 0.0f ? 1.0f / cap : 0.0f;
-  const uint64_t c2 = pair(c, c), slope2 = pair(f.slope, f.slope);
-  uint32_t some = 0;
+// Scores of 32 keys become what the softmax takes, in log2 units: times c (and K's
+// scales ks), capped, less slope times the distance (of key e, far - e, or where `apart`
+// from the keys' places past S, a lane each), -inf where `bits` are clear.
+//   cap tanh(s / cap) = cap - 2 cap / (1 + 2^(2 s log2(e) / cap)), and below 0.3 cap the
+// series of tanh to the ninth power, whose next term is 5e-8 of it.
+// The softmax's loop has this for scores below 0.3 cap and keys in a row, as nearly
+// all are.  This is for the others, and for those that a moved reference needs once more.
+// In a pass of its own for all scores, over tensor memory and by arguments in memory, it was 3000
+// cycles a group of 32 keys, mostly waits for instructions and arguments (64
+// single tokens under a window of 1024, capped: 83 us).
+template <bool F8>
+static __device__ __noinline__ void shape_chunk(uint32_t tS, float c, const float* ks, float cap, float slope, int far, bool apart, int place,
+                                                uint32_t bits) {
+  const float per = cap > 0.0f ? 1.0f / cap : 0.0f, up = 2.0f * kLog2e * per;
 #pragma unroll 1
-  for (int ch = ch_a; ch < ch_e; ++ch) {
-    // what is seen by the mask, and by the window
-    const int left = k.valid - 32 * ch, far = f.S + f.depth - (k.x0 + 32 * ch);  // of a prefix's first key
-    int u[4];
-    uint32_t bits;
-    if (k.prefix) {
-      bits = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u;
-      if (kShape && a.window > 0 && far >= a.window) bits &= far - a.window >= 31 ? 0u : 0xFFFFFFFEu << (far - a.window);
-    } else {
-      bits = seen_of<kMode>(P, at, k, j, i, ch, u);
-      if (kShape && a.window > 0) {
-#pragma unroll 1
-        for (int e = 0; e < 32; ++e) {
-          const int x = u[e >> 3] + (e & 7);
-          if (bits >> e & 1 && abs(f.depth - (x < 0 ? x : depth_of(a, at.seg.b, x))) >= a.window) bits &= ~(1u << e);
-        }
+  for (int g = 0; g < 32; g += 8) {
+    uint32_t x[8];
+    tmem_ld8(tS + g, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float z = __uint_as_float(x[e]) * c;
+      if (F8) z *= ks[g + e];
+      if (cap > 0.0f) {
+        const float w = z * per, w2 = w * w;
+        const float small = z * (1.0f + w2 * (-1.0f / 3.0f + w2 * (2.0f / 15.0f + w2 * (-17.0f / 315.0f + w2 * (62.0f / 2835.0f)))));
+        const float large = cap - 2.0f * cap * rcp(1.0f + ex2(z * up));
+        z = fabsf(w) < 0.3f ? small : large;
       }
+      const int at = apart ? abs(far - __shfl_sync(0xFFFFFFFFu, place, g + e)) : far - g - e;
+      z = slope == 0.0f ? z : z - slope * (float)at;
+      x[e] = bits >> (g + e) & 1 ? __float_as_uint(z) : 0xFF800000u;
     }
-    if (!__any_sync(0xFFFFFFFFu, bits != 0)) continue;
-    some |= 1u << ch;
-    if (!kShape && __all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) continue;
-#pragma unroll 1
-    for (int g = 0; g < 32; g += 16) {
-      uint32_t x[16];
-      uint64_t v[8];
-      tmem_ld16(tS + 32 * ch + g, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-      if (kShape) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] = mul2(v[e], c2);
-          if (F8) v[e] = mul2(v[e], *reinterpret_cast<const uint64_t*>(ks + 32 * ch + g + 2 * e));
-        }
-        if (cap > 0.0f) {
-          const uint64_t per2 = pair(per, per);
-          float most = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 y = unpair(v[e]);
-            most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
-          }
-          if (!__any_sync(0xFFFFFFFFu, most * per > 0.3f)) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint64_t w = mul2(v[e], per2), w2 = mul2(w, w);
-              uint64_t t = fma2(w2, pair(62.0f / 2835.0f, 62.0f / 2835.0f), pair(-17.0f / 315.0f, -17.0f / 315.0f));
-              t = fma2(w2, t, pair(2.0f / 15.0f, 2.0f / 15.0f));
-              t = fma2(w2, t, pair(-1.0f / 3.0f, -1.0f / 3.0f));
-              v[e] = mul2(v[e], fma2(w2, t, pair(1.0f, 1.0f)));
-            }
-          } else {
-            const float up = 2.0f * kLog2e * per;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 y = unpair(v[e]);
-              float z[2] = {y.x, y.y};
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float w = z[h] * per, w2 = w * w;
-                const float small = z[h] * (1.0f + w2 * (-1.0f / 3.0f + w2 * (2.0f / 15.0f + w2 * (-17.0f / 315.0f + w2 * (62.0f / 2835.0f)))));
-                const float large = cap - 2.0f * cap * rcp(1.0f + ex2(z[h] * up));
-                z[h] = fabsf(w) < 0.3f ? small : large;
-              }
-              v[e] = pair(z[0], z[1]);
-            }
-          }
-        }
-        if (a.slopes && k.prefix) {
-          const float b = (float)(far - g);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = fma2(slope2, pair((float)(2 * e) - b, (float)(2 * e + 1) - b), v[e]);
-        } else if (a.slopes) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int z = u[(g + e) >> 3] + (e & 7);
-            const int d = z < 0 || !(bits >> (g + e) & 1) ? z : depth_of(a, at.seg.b + j, z);
-            x[e] = __float_as_uint(-(float)abs(f.depth - d));
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = fma2(slope2, pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), v[e]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 y = unpair(v[e]);
-        x[2 * e] = bits >> (g + 2 * e) & 1 ? __float_as_uint(y.x) : 0xFF800000u;
-        x[2 * e + 1] = bits >> (g + 2 * e + 1) & 1 ? __float_as_uint(y.y) : 0xFF800000u;
-      }
-      tmem_st16(tS + 32 * ch + g, x);
-    }
+    tmem_st8(tS + g, x);
   }
   tmem_wait_st();
-  return some;
+}
+
+// What a row's scores get from their form.
+struct TcForm {
+  float c, cap, slope;  // factor of the products; log2 units
+  float per, near;      // c / cap, and the largest product that the series is for
+  int at;               // the row's position
+};
+
+// Scores of 32 keys in a row, x[e] -> log2 units, with a cap by the series and less the
+// distance's share; false: scores too large for it, x is as it was.
+template <bool F8>
+__device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, const TcForm& f, int far) {
+  uint64_t v[16];
+  const uint64_t c2 = pair(f.c, f.c);
+  if (f.cap > 0.0f) {
+    float most[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      v[e / 2] = pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+      if (F8) v[e / 2] = mul2(v[e / 2], *reinterpret_cast<const uint64_t*>(ks + e));
+      const float2 y = unpair(v[e / 2]);
+      most[e / 2 & 1] = fmaxf(most[e / 2 & 1], fmaxf(fabsf(y.x), fabsf(y.y)));
+    }
+    if (__any_sync(0xFFFFFFFFu, fmaxf(most[0], most[1]) > f.near)) return false;
+    const uint64_t per2 = pair(f.per, f.per);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint64_t w = mul2(v[e], per2), w2 = mul2(w, w);
+      uint64_t t = fma2(w2, pair(62.0f / 2835.0f, 62.0f / 2835.0f), pair(-17.0f / 315.0f, -17.0f / 315.0f));
+      t = fma2(w2, t, pair(2.0f / 15.0f, 2.0f / 15.0f));
+      t = fma2(w2, t, pair(-1.0f / 3.0f, -1.0f / 3.0f));
+      v[e] = mul2(mul2(v[e], c2), fma2(w2, t, pair(1.0f, 1.0f)));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      v[e / 2] = mul2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2);
+      if (F8) v[e / 2] = mul2(v[e / 2], *reinterpret_cast<const uint64_t*>(ks + e));
+    }
+  }
+  if (f.slope != 0.0f) {
+    const uint64_t slope2 = pair(f.slope, f.slope);
+    const float b = (float)far;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = fma2(slope2, pair((float)(2 * e) - b, (float)(2 * e + 1) - b), v[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float2 y = unpair(v[e]);
+    x[2 * e] = __float_as_uint(y.x), x[2 * e + 1] = __float_as_uint(y.y);
+  }
+  return true;
 }
 
 // The references (m, weights') of the rows that need others for 32 scores: a whole
@@ -706,28 +685,48 @@ static __device__ __noinline__ void rescale_weights(uint32_t tW, int cols, float
 }
 
 // Rows r0 .. valid - 1 of a V tile without their non-finite values (*found is
-// set where there was one), rows valid .. r1 - 1 cleared; thread of 128.
-template <bool F8>
-static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r1, int row_vecs, int thread, volatile int* found) {
-  const int sw = row_vecs < 8 ? row_vecs : 8;  // vectors of a row per half
-  for (int x = thread; x < (r1 - r0) * row_vecs; x += 128) {
-    const int r = r0 + x / row_vecs, c = x % row_vecs;
-    uint4* d = reinterpret_cast<uint4*>(v + (c / sw * kTile + r) * sw * 16 + c % sw * 16);
-    if (r >= valid) {
-      *d = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    uint4 y = *d;
-    constexpr uint32_t kMax = F8 ? 0x7F7F7F7Fu : 0x7F807F80u;
-    auto bad = [&](uint32_t z) { return F8 ? __vcmpeq4(z & kMax, kMax) : __vcmpeq2(z & kMax, kMax); };
-    const uint32_t bx = bad(y.x), by = bad(y.y), bz = bad(y.z), bw = bad(y.w);
-    if (bx | by | bz | bw) {
-      y.x &= ~bx, y.y &= ~by, y.z &= ~bz, y.w &= ~bw;
-      *d = y;
-      *found = 1;
+// set where there was one), rows valid .. r1 - 1 cleared; thread of 128.  kVecs: vectors
+// of 16 bytes of a row.
+template <bool F8, int kVecs>
+static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r1, int thread, volatile int* found) {
+  constexpr int kSw = kVecs < 8 ? kVecs : 8;  // vectors of a row per half
+  auto at = [&](int x) {
+    const int r = r0 + x / kVecs, c = x % kVecs;
+    return reinterpret_cast<uint4*>(v + (c / kSw * kTile + r) * kSw * 16 + c % kSw * 16);
+  };
+  // whether there is any: 0 times a value is NaN for bf16, an 8-bit NaN's low seven
+  // bits are ones (with the comparisons below for every vector: 4700 cycles a tile, 2300 of 8 bits)
+  uint32_t any = 0;
+#pragma unroll 4
+  for (int x = thread; x < (valid - r0) * kVecs; x += 128) {
+    const uint4 y = *at(x);
+    if (F8) {
+      any |= ((y.x & 0x7F7F7F7Fu) + 0x01010101u) | ((y.y & 0x7F7F7F7Fu) + 0x01010101u) | ((y.z & 0x7F7F7F7Fu) + 0x01010101u) |
+             ((y.w & 0x7F7F7F7Fu) + 0x01010101u);
+    } else {
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(any) : "r"(w[e]), "r"(0u));
     }
   }
-  fence_async_smem();
+  const bool dirty = F8 ? (any & 0x80808080u) != 0 : (any & 0x7FFF7FFFu) != 0;
+  for (int x = thread; x < (r1 - valid) * kVecs; x += 128) *at((valid - r0) * kVecs + x) = make_uint4(0, 0, 0, 0);
+  if (dirty)
+#pragma unroll 1
+    for (int x = thread; x < (valid - r0) * kVecs; x += 128) {
+      uint4* d = at(x);
+      uint4 y = *d;
+      constexpr uint32_t kMax = F8 ? 0x7F7F7F7Fu : 0x7F807F80u;
+      auto bad = [&](uint32_t z) { return F8 ? __vcmpeq4(z & kMax, kMax) : __vcmpeq2(z & kMax, kMax); };
+      const uint32_t bx = bad(y.x), by = bad(y.y), bz = bad(y.z), bw = bad(y.w);
+      if (bx | by | bz | bw) {
+        y.x &= ~bx, y.y &= ~by, y.z &= ~bz, y.w &= ~bw;
+        *d = y;
+        *found = 1;
+      }
+    }
+  if (dirty || r1 > valid) fence_async_smem();
 }
 
 // o = sum_x p_x V_x, p = softmax(scale q K^T), in one pass over the keys: scores
@@ -1145,10 +1144,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       const int i = me.i, hq = me.hq;
       const bool live = (kMode & kShare) && seg.m > 0 ? lrow < rows && i <= place.mem.n[me.j] : i <= seg.X.n;
       TcForm form = {};
-      if ((kMode & kForms) && live) {
-        form.S = (kMode & kShare) && seg.m > 0 ? place.mem.S[me.j] : seg.X.S;
-        form.depth = depth_of(a, me.b, i);
-        form.slope = a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
+      int deepest = 0;  // row of the warp
+      if (kMode & kForms) {
+        form.cap = a.softcap * kLog2e;
+        if (live) {
+          const int depth = depth_of(a, me.b, i);
+          form.at = ((kMode & kShare) && seg.m > 0 ? place.mem.S[me.j] : seg.X.S) + depth;
+          form.slope = a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
+          deepest = depth;
+        }
+        deepest = __reduce_max_sync(0xFFFFFFFFu, deepest);
       }
       const bool warp_live = lrow - lane < rows;
       // queries: rows of this CTA's block, read once and written to each copy,
@@ -1231,6 +1236,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       // positive (a subnormal at least), so that what is not seen stays -inf when it is scaled
       const float c_raw = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? s_qs[(QM == 2 ? st * kTile : 0) + row] : 1.0f), 0x1p-149f);
       const float c = kMode & kForms ? 1.0f : c_raw;  // shaped scores have it already
+      form.c = c_raw, form.per = c_raw / form.cap, form.near = 0.3f / form.per;
       const uint64_t c2 = pair(c, c);
       // wr: reference of 8-bit weights, log2 units; raise = 2^(kBias + m - wr)
       float m = -kInf, l = 0.0f, wr = -kInf, raise = 0.0f;
@@ -1247,11 +1253,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
         const float* sc = s_sc + (kt % kScaleRing) * 2 * kTile;
         if (warp_live) {
           const int chunks = (k.valid + 31) / 32, ch_e = min(ch_b, chunks);
-          uint32_t some = 15;  // groups of 32 keys that a row of the warp sees
-          if (kMode & kForms || ((kMode & kShare) && !full))
-            some = shape_scores<F8, kMode>(P, place, k, form, me.j, live ? i : INT32_MAX, c_raw, sc, ch_a, ch_e, tS);
-          else if (!full)
-            hide_unseen(P, seg.b, i, seg.X.n, k.prefix, k.valid, k.u0, ch_a, ch_e, tS);
+          // keys in a row that all rows of the warp see
+          const bool clear = full && (!(kMode & kForms) || a.window == 0 || seg.X.S + deepest - k.x0 < a.window);
+          if (!kMode && !full) hide_unseen(P, seg.b, i, seg.X.n, k.prefix, k.valid, k.u0, ch_a, ch_e, tS);
           // One pass over the tile's scores, 32 columns at a time, so that the
           // loop stays short.  A group of 32 that exceeds the reference by too
           // much rescales what is there, the weights before it included.
@@ -1260,7 +1264,22 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
           for (int ch = 0; ch < chunks; ++ch) {
             constexpr int kW = F8 ? 24 : 16;  // columns of 32 weights
             uint32_t w[kW];
-            if (ch < ch_a || ch >= ch_b || (kMode && !(some >> ch & 1))) {  // another copy's keys, or no one's
+            uint32_t bits = 0xFFFFFFFFu;  // keys that the row sees
+            if (kMode && !clear && ch >= ch_a && ch < ch_b) {
+              bits = live || k.prefix ? seen_of<kMode>(P, place, k, me.j, i, ch) : 0u;
+              if ((kMode & kForms) && a.window > 0) {
+                if (k.prefix) {
+                  const int far = form.at - (k.x0 + 32 * ch);  // of the first key
+                  if (far >= a.window) bits &= far - a.window >= 31 ? 0u : 0xFFFFFFFEu << (far - a.window);
+                } else {
+                  const int at = key_place<kMode>(P, place, k, 32 * ch + lane), d = form.at - seg.X.S;
+#pragma unroll 8
+                  for (int e = 0; e < 32; ++e)
+                    if (abs(d - __shfl_sync(0xFFFFFFFFu, at, e)) >= a.window) bits &= ~(1u << e);
+                }
+              }
+            }
+            if (ch < ch_a || ch >= ch_b || (kMode && !__any_sync(0xFFFFFFFFu, bits != 0))) {  // another copy's keys, or no one's
 #pragma unroll
               for (int e = 0; e < kW; ++e) w[e] = 0u;
               tmem_st(tS + kW * ch, w);
@@ -1271,9 +1290,21 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
               // one is too low, once more after they have moved.
               const float* kp = kMode & kForms ? s_ones : sc + 32 * ch;
               bool bad = m == -kInf, again = false;
+              bool shaped = kMode == 0;  // the scores in tensor memory are what the softmax takes
               uint64_t gs[2];
 #pragma unroll 1
               while (true) {
+                if (kMode && !shaped && (__any_sync(0xFFFFFFFFu, bad) || ((kMode & kForms) && a.slopes && !k.prefix) ||
+                                         (!(kMode & kForms) && __any_sync(0xFFFFFFFFu, ~bits)))) {
+                  shaped = true;
+                  if (kMode & kForms) {
+                    const bool apart = a.slopes && !k.prefix;
+                    shape_chunk<F8>(tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, apart ? form.at - ((kMode & kShare) && seg.m > 0 ? place.mem.S[me.j] : seg.X.S) : form.at - k.x0 - 32 * ch, apart,
+                                    apart ? key_place<kMode>(P, place, k, 32 * ch + lane) : 0, bits);
+                  } else if (__any_sync(0xFFFFFFFFu, ~bits)) {
+                    shape_chunk<false>(tS + 32 * ch, 1.0f, nullptr, 0.0f, 0.0f, 0, false, 0, bits);
+                  }
+                }
                 if (__any_sync(0xFFFFFFFFu, bad)) {
                   const float2 n = references(tS + 32 * ch, c, kp, sc + 32 * ch, m, wr, bad);
                   const float f = n.x > m ? ex2(m - n.x) : 1.0f, fw = n.y > wr ? ex2(wr - n.y) : 1.0f;
@@ -1287,6 +1318,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                 }
                 uint32_t x[32];
                 tmem_ld32(tS + 32 * ch, x);
+                if ((kMode & kForms) && !shaped) {
+                  if (!shape_near<F8>(x, sc + 32 * ch, form, form.at - k.x0 - 32 * ch)) {
+                    shape_chunk<F8>(tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, form.at - k.x0 - 32 * ch, false, 0, bits);
+                    shaped = true;
+                    tmem_ld32(tS + 32 * ch, x);
+                  } else if (__any_sync(0xFFFFFFFFu, ~bits)) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1 ? x[e] : 0xFF800000u;
+                  }
+                }
                 const float base = m == -kInf ? -kInf : -m;  // nothing seen: p is 0
                 const uint64_t base2 = pair(base, base), raise2 = pair(raise, raise);
                 float t4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -1323,7 +1364,21 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
             } else {
               uint32_t x[32];
               uint64_t v[16];
-              tmem_ld32(tS + 32 * ch, x);
+              if (kMode & kForms) {
+                const bool apart = a.slopes && !k.prefix;
+                if (!apart) tmem_ld32(tS + 32 * ch, x);
+                if (apart || !shape_near<F8>(x, nullptr, form, form.at - k.x0 - 32 * ch)) {
+                  shape_chunk<F8>(tS + 32 * ch, c_raw, nullptr, form.cap, form.slope, apart ? form.at - ((kMode & kShare) && seg.m > 0 ? place.mem.S[me.j] : seg.X.S) : form.at - k.x0 - 32 * ch, apart,
+                                  apart ? key_place<kMode>(P, place, k, 32 * ch + lane) : 0, bits);
+                  tmem_ld32(tS + 32 * ch, x);
+                }
+              } else {
+                tmem_ld32(tS + 32 * ch, x);
+              }
+              if (kMode && __any_sync(0xFFFFFFFFu, ~bits)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1 ? x[e] : 0xFF800000u;
+              }
               float mx4[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
@@ -1371,10 +1426,10 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
           char* v = vslots + slot * C::kTileBytes;
           wait(sync, b_vf + 8 * slot, (kt / C::kV) & 1);
           if ((kMode & kForms) && r1 < k.valid) {
-            clean_rows<F8>(v, r0, r1, r1, C::kRow / 16, row, &ints[2]);
+            clean_rows<F8, C::kRow / 16>(v, r0, r1, r1, row, &ints[2]);
             r0 = k.valid;
           }
-          clean_rows<F8>(v, r0, k.valid, end, C::kRow / 16, row, &ints[2]);
+          clean_rows<F8, C::kRow / 16>(v, r0, k.valid, end, row, &ints[2]);
         }
         if (warp_live) tmem_wait_st();
         tc_fence_before();
