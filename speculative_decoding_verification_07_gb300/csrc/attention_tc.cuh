@@ -573,37 +573,54 @@ struct TcForm {
   int at;               // the row's position
 };
 
-// Scores of 32 keys in a row, x[e] -> log2 units, with a cap by the series and less the
-// distance's share; false: scores too large for it, x is as it was.
+// Scores of 32 keys in a row, x[e] -> log2 units, capped and less the distance's
+// share; false: x is as it was.  Where scores are past the series, the formula with a
+// power of two is off by 3 x 2^-24 of the cap: 2^-14 of a weight up to the cap kCapNear (in
+// log2 units), past which scores of 0.3 caps are shape_chunk's.
+constexpr float kCapNear = 512.0f;
 template <bool F8>
 __device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, const TcForm& f, int far) {
   uint64_t v[16];
   const uint64_t c2 = pair(f.c, f.c);
-  if (f.cap > 0.0f) {
-    float most[2] = {0.0f, 0.0f};
+  uint32_t most = 0;  // of the products' sizes, within a factor of two
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      v[e / 2] = pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-      if (F8) v[e / 2] = mul2(v[e / 2], *reinterpret_cast<const uint64_t*>(ks + e));
-      const float2 y = unpair(v[e / 2]);
-      most[e / 2 & 1] = fmaxf(most[e / 2 & 1], fmaxf(fabsf(y.x), fabsf(y.y)));
+  for (int e = 0; e < 16; e += 2) {
+    v[e] = pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+    v[e + 1] = pair(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3]));
+    if (F8) {
+      const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(ks + 2 * e);
+      v[e] = mul2(v[e], s2.x), v[e + 1] = mul2(v[e + 1], s2.y);
     }
-    if (__any_sync(0xFFFFFFFFu, fmaxf(most[0], most[1]) > f.near)) return false;
-    const uint64_t per2 = pair(f.per, f.per);
+    const float2 y = unpair(v[e]), z = unpair(v[e + 1]);
+    most |= __float_as_uint(y.x) | __float_as_uint(y.y);
+    most |= __float_as_uint(z.x) | __float_as_uint(z.y);
+  }
+  if (f.cap > 0.0f) {
+    if (!__any_sync(0xFFFFFFFFu, (most & 0x7FFFFFFFu) > __float_as_uint(f.near))) {
+      const uint64_t per2 = pair(f.per, f.per);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint64_t w = mul2(v[e], per2), w2 = mul2(w, w);
-      uint64_t t = fma2(w2, pair(62.0f / 2835.0f, 62.0f / 2835.0f), pair(-17.0f / 315.0f, -17.0f / 315.0f));
-      t = fma2(w2, t, pair(2.0f / 15.0f, 2.0f / 15.0f));
-      t = fma2(w2, t, pair(-1.0f / 3.0f, -1.0f / 3.0f));
-      v[e] = mul2(mul2(v[e], c2), fma2(w2, t, pair(1.0f, 1.0f)));
+      for (int e = 0; e < 16; ++e) {
+        const uint64_t w = mul2(v[e], per2), w2 = mul2(w, w);
+        uint64_t t = fma2(w2, pair(62.0f / 2835.0f, 62.0f / 2835.0f), pair(-17.0f / 315.0f, -17.0f / 315.0f));
+        t = fma2(w2, t, pair(2.0f / 15.0f, 2.0f / 15.0f));
+        t = fma2(w2, t, pair(-1.0f / 3.0f, -1.0f / 3.0f));
+        v[e] = mul2(mul2(v[e], c2), fma2(w2, t, pair(1.0f, 1.0f)));
+      }
+    } else if (f.cap <= kCapNear) {
+      const float up = 2.0f * kLog2e * f.per;
+      const uint64_t up2 = pair(up, up), cap2 = pair(f.cap, f.cap), down2 = pair(-2.0f * f.cap, -2.0f * f.cap);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float2 y = unpair(mul2(v[e], up2));
+        const float2 z = unpair(add2(pair(ex2(y.x), ex2(y.y)), pair(1.0f, 1.0f)));
+        v[e] = fma2(pair(rcp(z.x), rcp(z.y)), down2, cap2);
+      }
+    } else {
+      return false;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      v[e / 2] = mul2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2);
-      if (F8) v[e / 2] = mul2(v[e / 2], *reinterpret_cast<const uint64_t*>(ks + e));
-    }
+    for (int e = 0; e < 16; ++e) v[e] = mul2(v[e], c2);
   }
   if (f.slope != 0.0f) {
     const uint64_t slope2 = pair(f.slope, f.slope);
@@ -1334,13 +1351,13 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                 gs[0] = gs[1] = 0;
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                  const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(kp + 2 * e);
+                  const ulonglong2 ks = kMode & kForms ? ulonglong2() : *reinterpret_cast<const ulonglong2*>(kp + 2 * e);
                   const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(sc + kTile + 32 * ch + 2 * e);
                   float2 y[2];
 #pragma unroll
                   for (int z = 0; z < 2; ++z) {
-                    const uint64_t s2 = mul2(pair(__uint_as_float(x[2 * (e + z)]), __uint_as_float(x[2 * (e + z) + 1])), c2);
-                    const float2 d = unpair(fma2(s2, z ? ks.y : ks.x, base2));  // -inf stays
+                    const uint64_t s = pair(__uint_as_float(x[2 * (e + z)]), __uint_as_float(x[2 * (e + z) + 1]));
+                    const float2 d = unpair(kMode & kForms ? add2(s, base2) : fma2(mul2(s, c2), z ? ks.y : ks.x, base2));  // -inf stays
                     const uint64_t p2 = pair(ex2(d.x), ex2(d.y));
                     gs[z] = add2(gs[z], p2);
                     y[z] = unpair(mul2(mul2(p2, z ? vs.y : vs.x), raise2));
