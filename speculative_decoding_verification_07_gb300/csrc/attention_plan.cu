@@ -20,7 +20,7 @@ __device__ __forceinline__ int block_max(int x, int* w) {
   }
   if (lane == 31) w[warp] = x;
   __syncthreads();
-  int before = lane < warp ? w[lane] : INT32_MIN;
+  int before = lane < warp ? w[lane] : INT32_MIN;  // as many words as warps
   before = __reduce_max_sync(0xFFFFFFFFu, before);
   __syncthreads();
   return max(x, before);
@@ -34,47 +34,70 @@ __device__ __forceinline__ int block_sum(int x, int* w, int* all) {
   }
   if (lane == 31) w[warp] = x;
   __syncthreads();
-  const int y = w[lane];
+  const int y = lane < blockDim.x / 32 ? w[lane] : 0;
   const int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? y : 0);
   *all = __reduce_add_sync(0xFFFFFFFFu, y);
   __syncthreads();
   return x + before;
 }
 
-// Lots of requests in their order, 1024 requests at a time.  A group is cut into equal
-// lots whose rows fill an item at most; its first request has the lot.  (A lot ends where
-// groups overlap or disagree, so that every request is in one lot at most, whatever
-// the arrays hold; such groups are reported.)
+// How many requests of a group share an item.  More of them read the prefix less often,
+// but their rows fill the tile: 32 rows are weighed by all warps together, and a tile of own
+// keys is weighed by the warps of one request alone.  In hundreds of cycles a tile and
+// CTA, from the attention's own clocks (two streams): prefixes, which come from L2,
+// 10, 12 and 18 for up to 32, 64 and 128 rows (15, 19, 27 in 8 bits), own keys 28, 28
+// and 36 (19, 25, 40), an item's start and end 80.
+__device__ __forceinline__ int lot_size(const TcPlanning& p, int size, int shared, int boxes) {
+  const int rows = p.a.R * p.group;
+  if (rows > p.rows / 2) return max(1, p.rows / rows);
+  const bool f8 = p.a.cache.format == SV_KV_E4M3;
+  const float tiles = (float)((shared + kTile - 1) / kTile), own = (float)boxes * (float)(1 << p.shift) / kTile;
+  int best = 1;
+  float least = __int_as_float(0x7F800000);
+  for (int c = 0; c < 3; ++c) {
+    const int most = min(kMembers, max(1, (32 << c) / rows)), n = (size + most - 1) / most, filled = (size + n - 1) / n * rows;
+    const float pre = filled <= 32 ? (f8 ? 15 : 10) : filled <= 64 ? (f8 ? 19 : 12) : f8 ? 27 : 18;
+    const float one = filled <= 32 ? (f8 ? 19 : 28) : filled <= 64 ? (f8 ? 25 : 28) : f8 ? 40 : 36;
+    const float cost = n * (80.0f + tiles * pre) + (own + 0.5f * n) * one;
+    if (cost < least) least = cost, best = most;
+  }
+  return best;
+}
+
+// Lots of requests in their order, blockDim.x requests at a time.  A group is cut into equal
+// lots; a lot's first request has it.  (A lot ends where groups overlap or disagree, so
+// that every request is in one lot at most, whatever the arrays hold; such groups are
+// reported.)  Then the CTAs' shares are equal numbers of units, and each gets the lot in
+// which its share starts.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ TcPlanning p) {
   pdl_wait();
   pdl_trigger();
   const sv_attention_args& a = p.a;
   __shared__ int s_boxes[kPlanThreads + kMembers], s_shared[kPlanThreads + kMembers], s_starts[kPlanThreads + kMembers],
-      s_rows[kPlanThreads + kMembers], s_w[32], s_first;
-  const int tid = threadIdx.x, rows = a.R * p.group;
-  const int widest = p.which & 2 ? 2 * kTile : kTile;
-  int units[2] = {0, 0}, lots[2] = {0, 0};
+      s_rows[kPlanThreads + kMembers], s_sum[kPlanThreads], s_w[32], s_first;
+  const int tid = threadIdx.x, threads = blockDim.x, rows = a.R * p.group;
+  int units = 0, lots = 0;
   int first0 = -1;  // the nearest request before these that starts a group
-  for (int base = 0; base < a.B; base += kPlanThreads) {
-    for (int x = tid; x < kPlanThreads + kMembers; x += kPlanThreads) {
-      const int b = base + x;
-      int boxes = 0, shared = 0, starts = 0, have = 0;
-      if (b < a.B && p.sharing) {
-        const Extent E = extent_of(a, b, x < kPlanThreads ? p.err : nullptr);
-        shared = shared_of(a, b), starts = a.shared_members[b];
-        boxes = own_boxes(a, p.box, p.shift, shared, E), have = E.n + 1;
-      }
-      s_boxes[x] = boxes, s_shared[x] = shared, s_starts[x] = starts, s_rows[x] = have;
-    }
-    __syncthreads();
+  for (int base = 0; base < a.B; base += threads) {
     const int b = base + tid;
-    TcLot lot = {};
-    int to = p.which == 2;
     bool grouped = false;
+    TcLot lot = {};
     if (p.sharing) {
+      for (int x = tid; x < threads + kMembers; x += threads) {
+        int boxes = 0, shared = 0, starts = 0, have = 0;
+        if (base + x < a.B) {
+          const Extent E = extent_of(a, base + x, x < threads ? p.err : nullptr);
+          shared = shared_of(a, base + x), starts = a.shared_members[base + x];
+          boxes = own_boxes(a, p.box, p.shift, shared, E), have = E.n + 1;
+        }
+        s_boxes[x] = boxes, s_shared[x] = shared, s_starts[x] = starts, s_rows[x] = have;
+      }
+      __syncthreads();
+      int all;
+      s_sum[tid] = block_sum(s_boxes[tid], s_w, &all);
       const int first = max(first0, block_max(s_starts[tid] > 0 ? b : -1, s_w));
-      if (tid == kPlanThreads - 1) s_first = first;
       const int before = max(first0, block_max(tid > 0 && s_starts[tid - 1] > 0 ? b - 1 : -1, s_w));
+      if (tid == threads - 1) s_first = first;
       if (b < a.B) {
         const int size = first < 0 ? 0 : min(a.shared_members[first], a.B - first), at = b - first;
         bool bad = s_starts[tid] < 0 || s_starts[tid] > a.B - b;
@@ -84,17 +107,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         if (s_starts[tid] > 0 && before >= 0) bad |= a.shared_members[before] > b - before;  // or starts one inside another
         if (bad) report(p.err, SV_ERR_STATE);
         if (grouped) {
-          const int most = min(kMembers, max(1, widest / rows)), n = (size + most - 1) / most, each = (size + n - 1) / n;
+          int most = max(1, p.rows / rows);
+          if (first >= base && first + size <= base + threads) {  // all here
+            const int own = s_sum[first + size - 1 - base] - (first > base ? s_sum[first - 1 - base] : 0);
+            most = lot_size(p, size, s_shared[first - base], own);
+          }
+          most = min(most, kMembers);
+          const int n = (size + most - 1) / most, each = (size + n - 1) / n;
           if (at % each == 0) {
             int boxes = 0, m = 0, live = 0;
             for (int j = 0; j < min(each, size - at); ++j) {
               if (s_shared[tid + j] != s_shared[tid] || (j > 0 && s_starts[tid + j] > 0)) break;
               boxes += s_boxes[tid + j], live += s_rows[tid + j], m = j + 1;
             }
-            if (p.which == 3) to = m * rows > kTile;
-            const int q = to ? 2 * kTile : kTile, tp = (s_shared[tid] + kTile - 1) / kTile;
+            const int tp = (s_shared[tid] + kTile - 1) / kTile;
             lot = {b, m, boxes, s_shared[tid], m * a.R - 1, 0, kLead + tp + ((boxes << p.shift) + kTile - 1) / kTile, tp,
-                   (m * rows + q - 1) / q, 0, 0, 0};
+                   (m * rows + p.rows - 1) / p.rows, 0, 0, 0};
             if (live > 0) lot.units = lot.T * a.cache.heads * lot.blocks;
           }
         }
@@ -102,35 +130,54 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     if (b < a.B && !grouped) {
       const Extent E = extent_of(a, b, p.err);
-      const int q = to ? 2 * kTile : kTile, begin = first_seen(a, E.S) & -p.box;  // a TMA box starts at a multiple of its rows
+      const int begin = first_seen(a, E.S) & -p.box;  // a TMA box starts at a multiple of its rows
       const int tp = (E.S - begin + (a.stage.data ? 0 : E.n + 1) + kTile - 1) / kTile;
-      lot = {b, 0, 0, E.S, E.n, begin, kLead + tp + (a.stage.data ? (E.n + kTile) / kTile : 0), tp, ((E.n + 1) * p.group + q - 1) / q, 0, 0, 0};
+      lot = {b, 0, 0, E.S, E.n, begin, kLead + tp + (a.stage.data ? (E.n + kTile) / kTile : 0), tp, ((E.n + 1) * p.group + p.rows - 1) / p.rows, 0, 0, 0};
       if (p.ranges && lot.blocks > 1) {  // units before each row block; they hold each one's own
         int* cum = p.ranges + (int64_t)b * p.words;
         int sum = 0;
         cum[0] = 0;
-        for (int r = 1; r <= lot.blocks; ++r) cum[r] = sum += cum[r];
+        for (int r0 = 1; r0 <= lot.blocks; r0 += 16) {
+          int t[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) t[r] = r0 + r <= lot.blocks ? cum[r0 + r] : 0;
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (r0 + r <= lot.blocks) cum[r0 + r] = sum += t[r];
+        }
         lot.T = sum, lot.units = sum * a.cache.heads;
       } else if (E.n >= 0) {
         lot.units = lot.T * a.cache.heads * lot.blocks;
       }
     }
-#pragma unroll
-    for (int l = 0; l < 2; ++l) {
-      if (!(p.which >> l & 1)) continue;
-      const bool mine = lot.units > 0 && to == l;
-      int n, u;
-      const int at = block_sum(mine, s_w, &n), cum = block_sum(mine ? lot.units : 0, s_w, &u);
-      if (mine) {
-        lot.cum = units[l] + cum - lot.units;
-        p.lots[l][lots[l] + at - 1] = lot;
-      }
-      lots[l] += n, units[l] += u;
+    int n, u;
+    const int at = block_sum(lot.units > 0, s_w, &n), cum = block_sum(lot.units, s_w, &u);
+    if (lot.units > 0) {
+      lot.cum = units + cum - lot.units;
+      p.lots[lots + at - 1] = lot;
     }
+    lots += n, units += u;
     __syncthreads();
     if (p.sharing) first0 = s_first;
   }
-  if (tid < 2) p.head[2 * tid] = units[tid], p.head[2 * tid + 1] = lots[tid];
+  if (tid == 0) p.head[0] = units, p.head[1] = lots;
+  // the lot that holds the first unit of each CTA's share: the last that starts at or before it
+  const int ctas = units > 0 ? sharing_ctas(a, p.group, p.ctas, units) : 0;
+  const bool here = lots <= kPlanThreads;
+  if (here)
+    for (int l = tid; l < lots; l += threads) s_boxes[l] = p.lots[l].cum;
+  __syncthreads();
+  for (int c = tid; c < p.ctas; c += threads) {
+    int lo = 0, hi = lots;
+    if (c < ctas) {
+      const int w = (int)((uint64_t)(uint32_t)units * (uint32_t)c / (uint32_t)ctas);
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if ((here ? s_boxes[mid] : p.lots[mid].cum) <= w) lo = mid; else hi = mid;
+      }
+    }
+    p.first[c] = lo;
+  }
 }
 
 // Which tiles a row block of a request sees: from the first to the last with a key that
@@ -141,7 +188,7 @@ __global__ void __launch_bounds__(kRangeThreads) ranges_kernel(const __grid_cons
   pdl_wait();
   pdl_trigger();
   const sv_attention_args& a = p.a;
-  const int rb = blockIdx.x, b = blockIdx.y, q = p.which == 2 ? 2 * kTile : kTile, G = p.group;
+  const int rb = blockIdx.x, b = blockIdx.y, q = p.rows, G = p.group;
   const Extent E = extent_of(a, b, nullptr);
   const int blocks = ((E.n + 1) * G + q - 1) / q;
   if (rb >= blocks || blocks < 2) return;
@@ -166,14 +213,16 @@ __global__ void __launch_bounds__(kRangeThreads) ranges_kernel(const __grid_cons
       for (int i = i0 + part; i <= i1; i += kRangeThreads / 32) bits |= seen_bits(a, b, i, E.n, (w0 + lane) * 32);
     if (bits) atomicOr(&s_seen[lane], bits);
     __syncthreads();
-    if (part == 0) {
-      bits = s_seen[lane];
-      if (a.window > 0)
-        for (uint32_t left = bits; left; left &= left - 1) {
-          const int d = depth_of(a, b, (w0 + lane) * 32 + __ffs(left) - 1);
-          if (d <= least - a.window || d - a.window >= most) bits &= ~(left & -left);
-        }
-      if (bits) atomicMin(&s_from, (w0 + lane) * 32 + __ffs(bits) - 1), atomicMax(&s_to, (w0 + lane) * 32 + 31 - __clz(bits));
+#pragma unroll 4
+    for (int w = part; w < 32; w += kRangeThreads / 32) {  // a lane an entry
+      const int j = (w0 + w) * 32 + lane;
+      bool on = s_seen[w] >> lane & 1;
+      if (a.window > 0 && on) {
+        const int d = depth_of(a, b, j);
+        on = d > least - a.window && d - a.window < most;
+      }
+      const uint32_t left = __ballot_sync(0xFFFFFFFFu, on);
+      if (left && lane == 0) atomicMin(&s_from, (w0 + w) * 32 + __ffs(left) - 1), atomicMax(&s_to, (w0 + w) * 32 + 31 - __clz(left));
     }
     __syncthreads();
   }
@@ -199,7 +248,8 @@ sv_status plan_launch(const TcPlanning& p, cudaStream_t stream) {
     (void)cudaGetLastError();
     return SV_ERR_CUDA;
   }
-  if (sv_launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) {
+  const int threads = p.a.B <= 128 ? 128 : p.a.B <= 512 ? 512 : kPlanThreads;
+  if (sv_launch_pdl(plan_kernel, dim3(1), dim3((unsigned)threads), 0, stream, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return SV_ERR_CUDA;
   }

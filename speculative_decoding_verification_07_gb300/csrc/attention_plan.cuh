@@ -17,6 +17,16 @@ constexpr int kForms = 1, kShare = 2;
 // 8192 positions, bf16, single tokens / trees of 15 nodes: 193 / 215 us with a
 // lead of 3, 191 / 208 with 4, 189 / 202 with 5, 192 / 200 with 6, 193 / 204 with 8.
 constexpr int kLead = 6;
+// Units of a share: more rows take longer to join.  One token (4 rows a head)
+// over 2000 positions 16.7 us with 1, 14.6 with 2, 15.7 with 4, 22.1 with 10; a
+// tree of 15 nodes (60 rows) 27.7, 22.4, 20.6 and 26.3.
+constexpr int kLeastFew = 2, kLeastMany = 4, kFewRows = 32;
+
+__device__ __forceinline__ int sharing_ctas(const sv_attention_args& a, int group, int grid, int total) {
+  const int least = a.R * group <= kFewRows ? kLeastFew : kLeastMany;
+  return min(grid, (total + least - 1) / least);
+}
+
 // Consecutive items: one a head and row block, T units each (with ranges: a head's row
 // blocks together T units), `units` in all and `cum` before them.  A request alone has
 // its rows in them, b = its number, S and n its extent, begin the first position that any
@@ -29,6 +39,7 @@ struct TcLot {
 struct TcList {
   const TcLot* lots;
   const int* head;    // units of all lots, and their number
+  const int* first;   // the lot in which each CTA's share starts
   const int* ranges;  // the tiles that row blocks see, or null: see ranges_kernel
   int words;          // of a request in it
 };
@@ -42,17 +53,15 @@ __device__ __forceinline__ int own_boxes(const sv_attention_args& a, int box, in
   return cached_boxes(a, box, shift, shared, E) + (a.stage.data ? (E.n + box) >> shift : 0);
 }
 
-// What the host decides of a call's lists.  Lists: of items of 128 rows and of 256
-// (the attention's kernels have row tiles for one or the other); which: 1, 2 or 3 (both: a
-// lot of more than 128 rows goes to the second).
+// What the host decides of a call's list.  rows: of an item, 128 or 256.
 struct TcPlanning {
   sv_attention_args a;
-  int which, box, shift, group;
+  int rows, box, shift, group, ctas;
   bool sharing;
-  int* ranges;  // of row blocks of the list's rows, or null
+  int* ranges;  // of row blocks of that many rows, or null
   int words;
-  TcLot* lots[2];
-  int* head;  // [2][2]
+  TcLot* lots;
+  int *head, *first;
   int* err;
 };
 

@@ -28,7 +28,6 @@ struct TcParams {
   uint32_t entries_magic;  // the same for R
   int box_shift;           // log2 of box
   bool down;               // items' tiles from the last to the first
-  bool dead;               // this launch writes the rows past each request's entries
   TcList list;             // what plan_kernel made
 };
 
@@ -90,7 +89,7 @@ struct TcShape {
   static constexpr int kRows = kTile * QM;
   static constexpr int kQAll = QM * kQBytes > 32768 ? QM * kQBytes : 32768;  // also holds 128 x 64 outputs, 32 of each half
   static constexpr int kMisc = 3072 + 4 * kRows + (F8 ? kScaleRing * 2 * kTile * 4 + 2 * kTile * 4 + (kMode ? 128 : 0) : 0) +
-                               (kMode ? kSegments * (int)sizeof(TcPlace) : 0);
+                               (kMode ? kSegments * (int)sizeof(TcPlace) : 0) + (kMode & kForms ? 4 * kTile * 4 : 0);
   // tiles held; a slot of K has its keys' tails and V's
   static constexpr int kTails = F8 ? 2 * kTile * kTail : 0, kKBytes = kTileBytes + kTails;
   static constexpr int kRoom = 232448 - 1024 - kMisc - kQAll, kPairs = kRoom / (kTileBytes + kKBytes);
@@ -106,11 +105,6 @@ struct TcShape {
 // positions (7 tiles, 8 heads) 13.1 us shared, 14.8 whole; six trees over 100 to
 // 1000 positions 20.7 shared, 18.6 whole; 64 over 16 to 520 51.2 and 42.8.
 constexpr int kWholeOne = 6, kWhole = 12;
-// Units of a share: more rows take longer to join.  One token (4 rows a head)
-// over 2000 positions 16.7 us with 1, 14.6 with 2, 15.7 with 4, 22.1 with 10; a
-// tree of 15 nodes (60 rows) 27.7, 22.4, 20.6 and 26.3.
-constexpr int kLeastFew = 2, kLeastMany = 4, kFewRows = 32;
-
 // One copy of the division's code for all of the walk (a small call waits for
 // instructions to arrive more than for anything else).
 static __device__ __noinline__ uint32_t quotient(uint32_t a, uint32_t b) { return a / b; }
@@ -191,18 +185,6 @@ static __device__ __noinline__ void load_lot(const TcList& l, TcWalker& k, int a
   const int4 x = __ldcg(p), y = __ldcg(p + 1), z = __ldcg(p + 2);
   k.at = at;
   k.lot = TcLot{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
-}
-
-// The lot that holds unit w0, by a whole warp: 32 probes at a time.
-static __device__ __noinline__ void find_lot(const TcList& l, TcWalker& k) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = k.count;  // lots[lo].cum <= w < lots[hi].cum
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, i < hi && __ldcg(&l.lots[i].cum) <= k.w)) - 1;
-    lo += max(0, n) * step, hi = min(hi, lo + step);
-  }
-  load_lot(l, k, lo);
 }
 
 // next_segment over the list, by a whole warp, into shared memory.
@@ -310,30 +292,50 @@ __device__ __forceinline__ TcRow row_of(const TcParams& P, const TcSegment& s, i
   return {j, s.b + j, e - j * P.p.a.R, hq};
 }
 
-// What row (member j, entry i) sees of 32 keys of a tile, by the mask.
+// A tile's keys as a row finds them, key numbers counted from the tile's first: it sees the
+// cached positions c0 .. c1 - 1, and what the mask says of the entries, entry 0 being key
+// e0; org is the key at position S, which the cached positions lead up to.
+struct TcView {
+  int c0, c1, e0, org;
+};
 template <int kMode>
-__device__ __forceinline__ uint32_t seen_of(const TcParams& P, const TcPlace& s, const TcTile& k, int j, int i, int ch) {
-  const sv_attention_args& a = P.p.a;
+__device__ __forceinline__ TcView view_of(const TcParams& P, const TcPlace& s, const TcTile& k, int j, bool live) {
+  constexpr int kFar = 1 << 29;
+  const bool staged = P.p.a.stage.data != nullptr;
+  TcView v;
   if (!(kMode & kShare) || !k.own) {
-    const int left = k.valid - 32 * ch;
-    const uint32_t all = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u;
-    return k.prefix ? all : i <= s.seg.X.n ? seen_bits(a, s.seg.b, i, s.seg.X.n, k.u0 + 32 * ch) & all : 0u;
+    v.org = (kMode & kShare) && s.seg.m > 0 ? s.mem.S[j] - k.x0 : -k.u0;
+    v.c0 = 0, v.c1 = k.prefix ? k.valid : k.staged ? 0 : v.org;
+    v.e0 = k.prefix || !live ? kFar : k.staged ? 0 : v.org;
+    return v;
   }
-  const int first = s.mem.start[j], end = s.mem.start[j + 1], x0 = k.x0 + (32 * ch >> P.box_shift);
   const Extent E = {s.mem.S[j], s.mem.n[j]};
-  if (x0 >= end || x0 + (32 >> P.box_shift) <= first || i > E.n) return 0u;
-  const int cached = cached_boxes(a, P.box, P.box_shift, s.seg.X.S, E);
-  uint32_t bits = 0;
-#pragma unroll 1
-  for (int g = 0; g < 32; g += P.box) {
-    const int x = x0 + (g >> P.box_shift) - first;
-    if (x < 0 || x >= end - first) continue;
-    const bool staged = x >= cached;
-    const int u = staged ? (x - cached) << P.box_shift : s.seg.X.S + (x << P.box_shift) - E.S;  // the entry of the box's first row
-    const uint32_t w = a.stage.data && !staged ? u >= 0 ? 0u : u <= -32 ? 0xFFFFFFFFu : (1u << -u) - 1u : seen_bits(a, s.seg.b + j, i, E.n, u);
-    bits |= (w & ((1u << P.box) - 1u)) << g;
+  v.c0 = (s.mem.start[j] - k.x0) << P.box_shift;
+  v.org = v.c0 + E.S - s.seg.X.S;
+  v.c1 = live ? v.org : v.c0;
+  v.e0 = !live ? kFar : staged ? v.c0 + (cached_boxes(P.p.a, P.box, P.box_shift, s.seg.X.S, E) << P.box_shift) : v.org;
+  return v;
+}
+
+// Words of row i of request b's mask, n entries and that: bits of the keys 32 w .. 32 w + 31
+// of the entries in `seen` (w = 0 .. 3), by five loads that wait for nothing.
+__device__ __forceinline__ void entries_seen(const sv_attention_args& a, int b, int i, int n, int e0, uint32_t (&seen)[4]) {
+  const int first = -e0 >> 5, shift = -e0 & 31;
+  uint32_t w[5];
+#pragma unroll
+  for (int x = 0; x < 5; ++x) {
+    const int at = first + x, left = n - 32 * at;
+    w[x] = 0u;
+    if (at < 0 || left < 0) continue;
+    w[x] = a.mask ? __ldg(a.mask + ((int64_t)b * a.R + i) * a.mask_ld + at) : i - 32 * at >= 31 ? 0xFFFFFFFFu : i < 32 * at ? 0u : (2u << (i - 32 * at)) - 1u;
+    if (left < 31) w[x] &= (2u << left) - 1u;
   }
-  return bits;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) seen[x] = __funnelshift_r(w[x], w[x + 1], shift);
+}
+__device__ __forceinline__ uint32_t cached_seen(const TcView& v, int ch) {
+  const int lo = max(0, v.c0 - 32 * ch), hi = min(32, v.c1 - 32 * ch);
+  return hi <= lo ? 0u : (hi >= 32 ? 0xFFFFFFFFu : (1u << hi) - 1u) & 0xFFFFFFFFu << lo;
 }
 
 // The place past its request's S of key `x` of a tile that is no prefix's (negative:
@@ -477,6 +479,7 @@ template <int kMode>
 static __device__ __noinline__ float given_back(const TcParams& P, const TcPlace& at, const TcRow& row, int col) {
   const sv_attention_args& a = P.p.a;
   const TcSegment& seg = at.seg;
+  const int n = (kMode & kShare) && seg.m > 0 ? at.mem.n[row.j] : seg.X.n;
   float sum = 0.0f;
   for (int t = seg.t0; t < seg.t1; ++t) {
     const TcTile k = tile_of<kMode>(P, seg, t);
@@ -486,15 +489,16 @@ static __device__ __noinline__ float given_back(const TcParams& P, const TcPlace
       bool staged = k.staged;
       int u = k.u0 + r, x = k.x0 + r;  // entry number, and entry or position
       if (kMode) {
-        if (!(seen_of<kMode>(P, at, k, row.j, row.i, r >> 5) >> (r & 31) & 1)) continue;
+        const TcView v = view_of<kMode>(P, at, k, row.j, true);
+        const bool entry = r >= v.e0;
+        if (entry ? r - v.e0 > n || !(seen_bits(a, row.b, row.i, n, r - v.e0) & 1) : r < v.c0 || r >= v.c1) continue;
+        u = entry ? r - v.e0 : r - v.org;
         if ((kMode & kShare) && k.own) {
-          const Extent E = {at.mem.S[row.j], at.mem.n[row.j]};
-          const int in = k.x0 + (r >> P.box_shift) - at.mem.start[row.j], cached = cached_boxes(a, P.box, P.box_shift, seg.X.S, E);
-          staged = in >= cached;
-          x = (staged ? (in - cached) << P.box_shift : seg.X.S + (in << P.box_shift)) + (r & (P.box - 1));
+          staged = entry && a.stage.data;
+          x = staged ? u : at.mem.S[row.j] + u;
         }
         if (a.window > 0 && abs(depth_of(a, row.b, row.i) - (u < 0 ? u : depth_of(a, row.b, u))) >= a.window) continue;
-      } else if (!(seen_bits(a, row.b, row.i, seg.X.n, u) & 1)) {
+      } else if (!(seen_bits(a, row.b, row.i, n, u) & 1)) {
         continue;
       }
       const sv_kv_place& pl = staged ? a.stage : a.cache;
@@ -789,6 +793,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
   float* s_wr = s_sc + kScaleRing * 2 * kTile;            // [256] references of 8-bit weights, exchanged
   float* s_ones = s_wr + 2 * kTile;                       // [32] K's scales of scores that have them already
   TcPlace* places = reinterpret_cast<TcPlace*>(misc + C::kMisc) - kSegments;  // [kSegments]
+  int* s_at = reinterpret_cast<int*>(places) - 4 * kTile;  // [2][2][128] places of a tile's keys past their S
 
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) mbar_init(b_kf + 8 * i, 1), mbar_init(b_ke + 8 * i, QM);
@@ -814,13 +819,12 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
   walk.qrows = C::kRows;
   int total = 0, ctas, w0 = 0, w1 = 0;
   auto share = [&] {
-    const int least = a.R * G <= kFewRows ? kLeastFew : kLeastMany;
-    ctas = min((int)gridDim.x, (total + least - 1) / least);
+    ctas = sharing_ctas(a, G, gridDim.x, total);
     if ((int)blockIdx.x < ctas) w0 = mul_div(total, blockIdx.x, ctas), w1 = mul_div(total, blockIdx.x + 1, ctas);
   };
   if (kMode) {  // a kernel before has counted
     total = __ldcg(P.list.head);
-    share();
+    share();  // of as many CTAs as plan_kernel has it
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1072,7 +1076,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       };
       if (kMode) {
         list.w = w0, list.w1 = w1, list.count = __ldcg(P.list.head + 1);
-        if (w0 < w1) find_lot(P.list, list);
+        load_lot(P.list, list, __ldcg(P.list.first + blockIdx.x));
         publish();
         if (!F8)
           while (more) publish();
@@ -1122,7 +1126,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
         }
       }
       // ---- rows past each request's entries --------------------------------
-      for (int r = kMode && !P.dead ? a.B * a.R : blockIdx.x; r < a.B * a.R; r += gridDim.x) {
+      for (int r = blockIdx.x; r < a.B * a.R; r += gridDim.x) {
         const int b = r / a.R, i = r - b * a.R;
         if (i <= extent_of(a, b, P.p.err).n) continue;
         const float zero[8] = {};
@@ -1252,7 +1256,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       }
       // positive (a subnormal at least), so that what is not seen stays -inf when it is scaled
       const float c_raw = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? s_qs[(QM == 2 ? st * kTile : 0) + row] : 1.0f), 0x1p-149f);
-      const float c = kMode & kForms ? 1.0f : c_raw;  // shaped scores have it already
+      const bool shape = (kMode & kForms) && (F8 || a.softcap > 0.0f || a.slopes);
+      const float c = shape ? 1.0f : c_raw;  // shaped scores have it already
       form.c = c_raw, form.per = c_raw / form.cap, form.near = 0.3f / form.per;
       const uint64_t c2 = pair(c, c);
       // wr: reference of 8-bit weights, log2 units; raise = 2^(kBias + m - wr)
@@ -1262,6 +1267,22 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
         const TcTile k = tile_of<kMode>(P, seg, seg.t0 + tt);
         const int kt = kbase + tt;
         const bool full = k.prefix && k.valid == kTile;
+        // keys in a row that all rows of the warp see; else what they see, looked up while
+        // the scores are under way, the places of keys by a thread each
+        const bool clear = full && (!(kMode & kForms) || a.window == 0 || seg.X.S + deepest - k.x0 < a.window);
+        uint32_t seen[4] = {0, 0, 0, 0};
+        TcView view = {};
+        int* places_at = s_at + (st * 2 + (kt & 1)) * kTile;  // (a warp may still read the last tile's)
+        if (kMode) {
+          if (warp_live && !clear) {
+            view = view_of<kMode>(P, place, k, me.j, live);
+            if (!k.prefix) entries_seen(a, me.b, live ? i : 0, live ? (kMode & kShare) && seg.m > 0 ? place.mem.n[me.j] : seg.X.n : -1, view.e0, seen);
+          }
+          if ((kMode & kForms) && !k.prefix && (a.window > 0 || a.slopes)) {
+            places_at[row] = key_place<kMode>(P, place, k, row);
+            named_barrier(4 + st, 128);
+          }
+        }
         wait(sync, b_s + 8 * st, ph_s);
         ph_s ^= 1;
         if (F8) wait(sync, b_sf + 8 * (kt % kScaleRing), (kt / kScaleRing) & 1);
@@ -1270,8 +1291,6 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
         const float* sc = s_sc + (kt % kScaleRing) * 2 * kTile;
         if (warp_live) {
           const int chunks = (k.valid + 31) / 32, ch_e = min(ch_b, chunks);
-          // keys in a row that all rows of the warp see
-          const bool clear = full && (!(kMode & kForms) || a.window == 0 || seg.X.S + deepest - k.x0 < a.window);
           if (!kMode && !full) hide_unseen(P, seg.b, i, seg.X.n, k.prefix, k.valid, k.u0, ch_a, ch_e, tS);
           // One pass over the tile's scores, 32 columns at a time, so that the
           // loop stays short.  A group of 32 that exceeds the reference by too
@@ -1281,18 +1300,40 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
           for (int ch = 0; ch < chunks; ++ch) {
             constexpr int kW = F8 ? 24 : 16;  // columns of 32 weights
             uint32_t w[kW];
-            uint32_t bits = 0xFFFFFFFFu;  // keys that the row sees
-            if (kMode && !clear && ch >= ch_a && ch < ch_b) {
-              bits = live || k.prefix ? seen_of<kMode>(P, place, k, me.j, i, ch) : 0u;
-              if ((kMode & kForms) && a.window > 0) {
-                if (k.prefix) {
-                  const int far = form.at - (k.x0 + 32 * ch);  // of the first key
-                  if (far >= a.window) bits &= far - a.window >= 31 ? 0u : 0xFFFFFFFEu << (far - a.window);
-                } else {
-                  const int at = key_place<kMode>(P, place, k, 32 * ch + lane), d = form.at - seg.X.S;
+            // keys that the row sees, the distance of the first, and whether the others'
+            // distances do not follow from it (then their places, a lane each)
+            uint32_t bits = 0xFFFFFFFFu;
+            int far = 0, at = 0;
+            bool apart = false;
+            if (kMode && ch >= ch_a && ch < ch_b) {
+              if (clear) {
+                far = form.at - k.x0 - 32 * ch;
+              } else {
+                const uint32_t of_mask = ch == 0 ? seen[0] : ch == 1 ? seen[1] : ch == 2 ? seen[2] : seen[3];
+                bits = of_mask | cached_seen(view, ch);
+                if (kMode & kForms) {
+                  const int d = form.at - ((kMode & kShare) && seg.m > 0 ? place.mem.S[me.j] : seg.X.S);
+                  far = d + view.org - 32 * ch;
+                  if (!k.prefix && (a.window > 0 || a.slopes) && __any_sync(0xFFFFFFFFu, of_mask != 0)) {
+                    at = places_at[32 * ch + lane];
+                    // a chain's depths follow one another: distances do for keys up to the row
+                    const int at0 = __shfl_sync(0xFFFFFFFFu, at, 0);
+                    const bool in_row = __all_sync(0xFFFFFFFFu, at == at0 + lane) && !((kMode & kShare) && k.own);
+                    if (in_row) far = d - at0;
+                    apart = !in_row || __any_sync(0xFFFFFFFFu, bits != 0 && far < 31 - __clz(bits));
+                  }
+                  if (a.window > 0) {
+                    if (!apart) {
+                      if (far >= a.window) bits &= far - a.window >= 31 ? 0u : 0xFFFFFFFEu << (far - a.window);
+                    } else {
+                      const int least = __reduce_min_sync(0xFFFFFFFFu, at), most = __reduce_max_sync(0xFFFFFFFFu, at);
+                      if (__any_sync(0xFFFFFFFFu, bits != 0 && max(abs(d - least), abs(d - most)) >= a.window))
 #pragma unroll 8
-                  for (int e = 0; e < 32; ++e)
-                    if (abs(d - __shfl_sync(0xFFFFFFFFu, at, e)) >= a.window) bits &= ~(1u << e);
+                        for (int e = 0; e < 32; ++e)
+                          if (abs(d - __shfl_sync(0xFFFFFFFFu, at, e)) >= a.window) bits &= ~(1u << e);
+                    }
+                  }
+                  if (apart) far = d;
                 }
               }
             }
@@ -1311,16 +1352,12 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
               uint64_t gs[2];
 #pragma unroll 1
               while (true) {
-                if (kMode && !shaped && (__any_sync(0xFFFFFFFFu, bad) || ((kMode & kForms) && a.slopes && !k.prefix) ||
-                                         (!(kMode & kForms) && __any_sync(0xFFFFFFFFu, ~bits)))) {
+                if (kMode && !shaped && (__any_sync(0xFFFFFFFFu, bad) || apart)) {
                   shaped = true;
-                  if (kMode & kForms) {
-                    const bool apart = a.slopes && !k.prefix;
-                    shape_chunk<F8>(tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, apart ? form.at - ((kMode & kShare) && seg.m > 0 ? place.mem.S[me.j] : seg.X.S) : form.at - k.x0 - 32 * ch, apart,
-                                    apart ? key_place<kMode>(P, place, k, 32 * ch + lane) : 0, bits);
-                  } else if (__any_sync(0xFFFFFFFFu, ~bits)) {
+                  if ((kMode & kForms) && shape)
+                    shape_chunk<F8>(tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, far, apart, at, bits);
+                  else if (__any_sync(0xFFFFFFFFu, ~bits))
                     shape_chunk<false>(tS + 32 * ch, 1.0f, nullptr, 0.0f, 0.0f, 0, false, 0, bits);
-                  }
                 }
                 if (__any_sync(0xFFFFFFFFu, bad)) {
                   const float2 n = references(tS + 32 * ch, c, kp, sc + 32 * ch, m, wr, bad);
@@ -1335,9 +1372,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                 }
                 uint32_t x[32];
                 tmem_ld32(tS + 32 * ch, x);
-                if ((kMode & kForms) && !shaped) {
-                  if (!shape_near<F8>(x, sc + 32 * ch, form, form.at - k.x0 - 32 * ch)) {
-                    shape_chunk<F8>(tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, form.at - k.x0 - 32 * ch, false, 0, bits);
+                if (kMode && !shaped) {
+                  if ((kMode & kForms) && shape && !shape_near<F8>(x, sc + 32 * ch, form, far)) {
+                    shape_chunk<F8>(tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, far, false, 0, bits);
                     shaped = true;
                     tmem_ld32(tS + 32 * ch, x);
                   } else if (__any_sync(0xFFFFFFFFu, ~bits)) {
@@ -1381,12 +1418,10 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
             } else {
               uint32_t x[32];
               uint64_t v[16];
-              if (kMode & kForms) {
-                const bool apart = a.slopes && !k.prefix;
+              if ((kMode & kForms) && shape) {
                 if (!apart) tmem_ld32(tS + 32 * ch, x);
-                if (apart || !shape_near<F8>(x, nullptr, form, form.at - k.x0 - 32 * ch)) {
-                  shape_chunk<F8>(tS + 32 * ch, c_raw, nullptr, form.cap, form.slope, apart ? form.at - ((kMode & kShare) && seg.m > 0 ? place.mem.S[me.j] : seg.X.S) : form.at - k.x0 - 32 * ch, apart,
-                                  apart ? key_place<kMode>(P, place, k, 32 * ch + lane) : 0, bits);
+                if (apart || !shape_near<F8>(x, nullptr, form, far)) {
+                  shape_chunk<F8>(tS + 32 * ch, c_raw, nullptr, form.cap, form.slope, far, apart, at, bits);
                   tmem_ld32(tS + 32 * ch, x);
                 }
               } else {
@@ -1575,6 +1610,12 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
           const float* first = P.p.part + (int64_t)(2 * ca + (mul_div(total, ca, ctas) >= seg.item0 ? 0 : 1)) * C::kPart;
           auto slot = [&](int x) { return x == ca ? first : P.p.part + (int64_t)(2 * x) * C::kPart; };
           auto part_ml = [&](int x, int r) { return __ldcg(reinterpret_cast<const float2*>(slot(x) + C::kRows * D) + r); };
+          // each part's factor of a row, where the queries were (the outputs are in registers
+          // or stored): so that the loads below wait for nothing (joining 256 rows of three
+          // parts with factors made beside them: 42000 cycles)
+          const int parts = cb - ca + 1;
+          float* factor = reinterpret_cast<float*>(sm);
+          const bool held = parts * rows * 4 <= C::kQAll;
           for (int r = tid; r < rows; r += 256) {
             float M = -kInf, L = 0.0f;
 #pragma unroll 4
@@ -1583,18 +1624,21 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
 #pragma unroll 4
             for (int x = ca; x <= cb; ++x) {
               const float2 v = part_ml(x, r);
-              L += v.y * ex2(v.x - Mb);
+              const float f = ex2(v.x - Mb);
+              L += v.y * f;
+              if (held) factor[(x - ca) * rows + r] = f;
             }
             s_ml[r] = make_float2(Mb, L);
           }
           named_barrier(1, 256);
+#pragma unroll 2
           for (int z = tid; z < rows * (D / 8); z += 256) {
             const int r = z / (D / 8), col = z % (D / 8) * 8;
             const float2 ML = s_ml[r];
             float y[8] = {};
 #pragma unroll 4
             for (int x = ca; x <= cb; ++x) {
-              const float f = ex2(part_ml(x, r).x - ML.x);
+              const float f = held ? factor[(x - ca) * rows + r] : ex2(part_ml(x, r).x - ML.x);
               const float4* v = reinterpret_cast<const float4*>(slot(x) + r * D + col);
               const float4 v0 = __ldcg(v), v1 = __ldcg(v + 1);
               y[0] += v0.x * f, y[1] += v0.y * f, y[2] += v0.z * f, y[3] += v0.w * f;

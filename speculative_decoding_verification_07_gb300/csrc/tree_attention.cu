@@ -273,9 +273,8 @@ static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct TcPlan {
   bool use;
   bool sharing;  // groups' prefixes are read once
-  int which;     // row tiles per CTA: 1, 2, or 3 for a launch of each
-  int ctas;      // grid
-  TcKernel k[2];
+  int tiles, ctas;  // row tiles per CTA, grid
+  TcKernel k;
   size_t list, ranges, bytes;  // where the list and the ranges start in the workspace, and its bytes
 };
 
@@ -294,8 +293,8 @@ static TcPlan tc_plan(const sv_handle* h, const sv_attention_args* a) {
   const bool forms = has_form(a);
   // a group's rows are its members' R entries each, and it has no more items than they
   p.sharing = a->shared_len && a->window == 0;
-  p.which = rows > kTile ? 2 : p.sharing && a->B * rows > kTile ? 3 : 1;
-  const int64_t blocks = cdiv(rows, p.which == 2 ? 2 * kTile : kTile);
+  p.tiles = rows > kTile ? 2 : 1;
+  const int64_t blocks = cdiv(rows, p.tiles * kTile);
   const int64_t tiles = (int64_t)a->B * c.heads * blocks * (cdiv((int64_t)c.max_blocks * c.block_size, kTile) + cdiv(a->R, kTile) + 1 + kLead);
   if (tiles > INT32_MAX || (rows + 2 * kTile) * (a->Hq / c.heads) > INT32_MAX || c.num_blocks == INT32_MAX) return p;
   p.use = true;
@@ -304,15 +303,10 @@ static TcPlan tc_plan(const sv_handle* h, const sv_attention_args* a) {
                               {tc_kernel_e4m3, tc_kernel_e4m3_forms, tc_kernel_e4m3_shared, tc_kernel_e4m3_both}};
   p.ctas = (int)(tiles < h->num_sms ? tiles : h->num_sms);
   if (p.ctas > kTickets) p.ctas = kTickets;
-  size_t part = 0;
-  for (int l = 0; l < 2; ++l)
-    if (p.which >> l & 1) {
-      p.k[l] = of[c.format == SV_KV_E4M3][(forms ? kForms : 0) + (p.sharing ? kShare : 0)](c.head_dim, l + 1);
-      part = (size_t)p.k[l].part;
-    }
-  p.list = p.bytes = kTicketBytes + up256((size_t)p.ctas * 2 * part * 4);
+  p.k = of[c.format == SV_KV_E4M3][(forms ? kForms : 0) + (p.sharing ? kShare : 0)](c.head_dim, p.tiles);
+  p.list = p.bytes = kTicketBytes + up256((size_t)p.ctas * 2 * p.k.part * 4);
   if (forms || p.sharing) {
-    p.ranges = p.bytes += 256 + 2 * up256((size_t)a->B * sizeof(TcLot));
+    p.ranges = p.bytes += 256 + up256((size_t)p.ctas * 4) + up256((size_t)a->B * sizeof(TcLot));
     if (forms && !p.sharing && blocks > 1) p.bytes += up256((size_t)a->B * (2 * (size_t)blocks + 1) * 4);
   }
   return p;
@@ -396,28 +390,23 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
     P.entries_magic = a->R == 1 ? 0u : (uint32_t)((0x100000000ull + a->R - 1) / a->R);
     while (P.box >> (P.box_shift + 1)) ++P.box_shift;
     P.down = a->slopes != nullptr;
-    L.a = *a, L.which = plan.which, L.box = P.box, L.shift = P.box_shift, L.group = P.group, L.sharing = plan.sharing, L.err = h->d_err;
-    L.head = reinterpret_cast<int*>(at + plan.list);
-    for (int l = 0; l < 2; ++l) L.lots[l] = reinterpret_cast<TcLot*>(at + plan.list + 256 + l * up256((size_t)a->B * sizeof(TcLot)));
+    L.a = *a, L.rows = plan.tiles * kTile, L.box = P.box, L.shift = P.box_shift, L.group = P.group, L.ctas = plan.ctas;
+    L.sharing = plan.sharing, L.err = h->d_err;
+    L.head = reinterpret_cast<int*>(at + plan.list), L.first = L.head + 64;
+    L.lots = reinterpret_cast<TcLot*>(at + plan.list + 256 + up256((size_t)plan.ctas * 4));
     if (plan.bytes > plan.ranges) {
       L.ranges = reinterpret_cast<int*>(at + plan.ranges);
-      L.words = 2 * (int)cdiv((int64_t)a->R * P.group, plan.which == 2 ? 2 * kTile : kTile) + 1;
+      L.words = 2 * (int)cdiv((int64_t)a->R * P.group, L.rows) + 1;
     }
     const sv_status rp = plan_launch(L, stream);
     if (rp != SV_OK) return rp;
   }
-  P.dead = true;
-  for (int l = 0; l < 2; ++l) {
-    if (!(plan.which >> l & 1)) continue;
-    const TcKernel& k = plan.k[l];
-    P.list = {L.lots[l], listed ? L.head + 2 * l : nullptr, L.ranges, L.words};
-    const sv_status rr = sv_raise_dyn_smem((const void*)k.fn, (size_t)k.smem);
-    if (rr != SV_OK) return rr;
-    if (sv_launch_pdl(k.fn, dim3((unsigned)plan.ctas), dim3((unsigned)k.threads), (size_t)k.smem, stream, P) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return SV_ERR_CUDA;
-    }
-    P.dead = false;
+  P.list = {L.lots, L.head, L.first, L.ranges, L.words};
+  const sv_status rr = sv_raise_dyn_smem((const void*)plan.k.fn, (size_t)plan.k.smem);
+  if (rr != SV_OK) return rr;
+  if (sv_launch_pdl(plan.k.fn, dim3((unsigned)plan.ctas), dim3((unsigned)plan.k.threads), (size_t)plan.k.smem, stream, P) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SV_ERR_CUDA;
   }
   return SV_OK;
 }
