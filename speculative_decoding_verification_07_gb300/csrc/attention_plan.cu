@@ -10,35 +10,27 @@ namespace sv {
 
 constexpr int kPlanThreads = 1024, kRangeThreads = 256;
 
-// Inclusive sums or maxima over the block's threads; w: 32 words of scratch each.
-__device__ __forceinline__ int block_max(int x, int* w) {
+// Inclusive over the block's threads: the sums of x and y and the maxima of m; w: scratch of as
+// many words as warps for each.
+struct Scan {
+  int x, y, m;
+};
+__device__ __forceinline__ Scan block_scan(Scan s, int (&w)[3][32], int* all_x, int* all_y) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x = max(x, y);
+    const int x = __shfl_up_sync(0xFFFFFFFFu, s.x, o), y = __shfl_up_sync(0xFFFFFFFFu, s.y, o), m = __shfl_up_sync(0xFFFFFFFFu, s.m, o);
+    if (lane >= o) s.x += x, s.y += y, s.m = max(s.m, m);
   }
-  if (lane == 31) w[warp] = x;
+  if (lane == 31) w[0][warp] = s.x, w[1][warp] = s.y, w[2][warp] = s.m;
   __syncthreads();
-  int before = lane < warp ? w[lane] : INT32_MIN;  // as many words as warps
-  before = __reduce_max_sync(0xFFFFFFFFu, before);
+  const bool is = lane < (int)blockDim.x / 32, before = lane < warp;
+  const int x = is ? w[0][lane] : 0, y = is ? w[1][lane] : 0, m = before ? w[2][lane] : INT32_MIN;
+  *all_x = __reduce_add_sync(0xFFFFFFFFu, x), *all_y = __reduce_add_sync(0xFFFFFFFFu, y);
+  s.x += __reduce_add_sync(0xFFFFFFFFu, before ? x : 0), s.y += __reduce_add_sync(0xFFFFFFFFu, before ? y : 0);
+  s.m = max(s.m, __reduce_max_sync(0xFFFFFFFFu, m));
   __syncthreads();
-  return max(x, before);
-}
-__device__ __forceinline__ int block_sum(int x, int* w, int* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) w[warp] = x;
-  __syncthreads();
-  const int y = lane < blockDim.x / 32 ? w[lane] : 0;
-  const int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? y : 0);
-  *all = __reduce_add_sync(0xFFFFFFFFu, y);
-  __syncthreads();
-  return x + before;
+  return s;
 }
 
 // How many requests of a group share an item.  More of them read the prefix less often,
@@ -74,7 +66,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   pdl_trigger();
   const sv_attention_args& a = p.a;
   __shared__ int s_boxes[kPlanThreads + kMembers], s_shared[kPlanThreads + kMembers], s_starts[kPlanThreads + kMembers],
-      s_rows[kPlanThreads + kMembers], s_sum[kPlanThreads], s_w[32], s_first;
+      s_rows[kPlanThreads + kMembers], s_sum[kPlanThreads], s_first[kPlanThreads], s_cum[kPlanThreads], s_w[3][32], s_items;
+  if (threadIdx.x == 0) s_items = 0;
   const int tid = threadIdx.x, threads = blockDim.x, rows = a.R * p.group;
   int units = 0, lots = 0;
   int first0 = -1;  // the nearest request before these that starts a group
@@ -93,11 +86,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         s_boxes[x] = boxes, s_shared[x] = shared, s_starts[x] = starts, s_rows[x] = have;
       }
       __syncthreads();
-      int all;
-      s_sum[tid] = block_sum(s_boxes[tid], s_w, &all);
-      const int first = max(first0, block_max(s_starts[tid] > 0 ? b : -1, s_w));
-      const int before = max(first0, block_max(tid > 0 && s_starts[tid - 1] > 0 ? b - 1 : -1, s_w));
-      if (tid == threads - 1) s_first = first;
+      int all, none;
+      const Scan so_far = block_scan({s_boxes[tid], 0, s_starts[tid] > 0 ? b : first0}, s_w, &all, &none);
+      const int first = so_far.m;
+      s_sum[tid] = so_far.x, s_first[tid] = first;
+      __syncthreads();
+      const int before = tid > 0 ? s_first[tid - 1] : first0;
       if (b < a.B) {
         const int size = first < 0 ? 0 : min(a.shared_members[first], a.B - first), at = b - first;
         bool bad = s_starts[tid] < 0 || s_starts[tid] > a.B - b;
@@ -151,29 +145,30 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       }
     }
     int n, u;
-    const int at = block_sum(lot.units > 0, s_w, &n), cum = block_sum(lot.units, s_w, &u);
+    const Scan so_far = block_scan({lot.units > 0, lot.units, 0}, s_w, &n, &u);
     if (lot.units > 0) {
-      lot.cum = units + cum - lot.units;
-      p.lots[lots + at - 1] = lot;
+      const int at = lots + so_far.x - 1;
+      lot.cum = units + so_far.y - lot.units;
+      p.lots[at] = lot;
+      if (at < kPlanThreads) s_cum[at] = lot.cum;
+      atomicAdd(&s_items, a.cache.heads * lot.blocks);
     }
     lots += n, units += u;
+    if (p.sharing) first0 = s_first[threads - 1];
     __syncthreads();
-    if (p.sharing) first0 = s_first;
   }
-  if (tid == 0) p.head[0] = units, p.head[1] = lots;
+  // short items stay whole, but where there are few of them
+  if (tid == 0) p.head[0] = units, p.head[1] = lots, p.head[2] = kLead + (s_items <= p.ctas / 4 ? kWholeOne : kWhole);
   // the lot that holds the first unit of each CTA's share: the last that starts at or before it
   const int ctas = units > 0 ? sharing_ctas(a, p.group, p.ctas, units) : 0;
   const bool here = lots <= kPlanThreads;
-  if (here)
-    for (int l = tid; l < lots; l += threads) s_boxes[l] = p.lots[l].cum;
-  __syncthreads();
   for (int c = tid; c < p.ctas; c += threads) {
     int lo = 0, hi = lots;
     if (c < ctas) {
       const int w = (int)((uint64_t)(uint32_t)units * (uint32_t)c / (uint32_t)ctas);
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if ((here ? s_boxes[mid] : p.lots[mid].cum) <= w) lo = mid; else hi = mid;
+        if ((here ? s_cum[mid] : p.lots[mid].cum) <= w) lo = mid; else hi = mid;
       }
     }
     p.first[c] = lo;

@@ -17,6 +17,12 @@ constexpr int kForms = 1, kShare = 2;
 // 8192 positions, bf16, single tokens / trees of 15 nodes: 193 / 215 us with a
 // lead of 3, 191 / 208 with 4, 189 / 202 with 5, 192 / 200 with 6, 193 / 204 with 8.
 constexpr int kLead = 6;
+// Items of up to this many key tiles are not shared between CTAs: a tile is
+// 0.9 us for a CTA alone, joining parts 3 us and more.  A single request leaves
+// most of the GPU idle, so its items are shared earlier: one token over 777
+// positions (7 tiles, 8 heads) 13.1 us shared, 14.8 whole; six trees over 100 to
+// 1000 positions 20.7 shared, 18.6 whole; 64 over 16 to 520 51.2 and 42.8.
+constexpr int kWholeOne = 6, kWhole = 12;
 // Units of a share: more rows take longer to join.  One token (4 rows a head)
 // over 2000 positions 16.7 us with 1, 14.6 with 2, 15.7 with 4, 22.1 with 10; a
 // tree of 15 nodes (60 rows) 27.7, 22.4, 20.6 and 26.3.
@@ -38,7 +44,7 @@ struct TcLot {
 
 struct TcList {
   const TcLot* lots;
-  const int* head;    // units of all lots, and their number
+  const int* head;    // units of all lots, their number, and those of an item that stays whole
   const int* first;   // the lot in which each CTA's share starts
   const int* ranges;  // the tiles that row blocks see, or null: see ranges_kernel
   int words;          // of a request in it

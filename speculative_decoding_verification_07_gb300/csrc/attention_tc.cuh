@@ -99,12 +99,6 @@ struct TcShape {
   static constexpr int kPart = kRows * (D + 2);              // floats of a partial result
 };
 
-// Items of up to this many key tiles are not shared between CTAs: a tile is
-// 0.9 us for a CTA alone, joining parts 3 us and more.  A single request leaves
-// most of the GPU idle, so its items are shared earlier: one token over 777
-// positions (7 tiles, 8 heads) 13.1 us shared, 14.8 whole; six trees over 100 to
-// 1000 positions 20.7 shared, 18.6 whole; 64 over 16 to 520 51.2 and 42.8.
-constexpr int kWholeOne = 6, kWhole = 12;
 // One copy of the division's code for all of the walk (a small call waits for
 // instructions to arrive more than for anything else).
 static __device__ __noinline__ uint32_t quotient(uint32_t a, uint32_t b) { return a / b; }
@@ -176,15 +170,14 @@ static __device__ __noinline__ int share_of(int x, int total, int ctas) {
 
 // A CTA's place in the list of lots.
 struct TcWalker {
-  int w, w1, at, count;
+  int w, w1, at, count, whole;
   TcLot lot;
 };
 
-static __device__ __noinline__ void load_lot(const TcList& l, TcWalker& k, int at) {
-  const int4* p = reinterpret_cast<const int4*>(l.lots + at);
+__device__ __forceinline__ TcLot load_lot(const TcLot* l) {
+  const int4* p = reinterpret_cast<const int4*>(l);
   const int4 x = __ldcg(p), y = __ldcg(p + 1), z = __ldcg(p + 2);
-  k.at = at;
-  k.lot = TcLot{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+  return TcLot{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
 }
 
 // next_segment over the list, by a whole warp, into shared memory.
@@ -198,7 +191,7 @@ static __device__ __noinline__ bool next_place(const TcParams& P, TcWalker& k, T
         k.w = k.w1;
         break;
       }
-      load_lot(P.list, k, k.at + 1);
+      k.lot = load_lot(P.list.lots + ++k.at);
     }
     if (k.w >= k.w1) break;
     const int at = k.w - k.lot.cum;
@@ -214,7 +207,7 @@ static __device__ __noinline__ bool next_place(const TcParams& P, TcWalker& k, T
       lo = cum[(P.list.words + 1) / 2 + rb];
     }
     int from = k.w - item0, upto = min(T, k.w1 - item0);
-    if (T <= kLead + (P.p.a.B == 1 ? kWholeOne : kWhole)) {
+    if (T <= k.whole) {
       const bool mine = 2 * from < T;  // from > 0 only at the share's start
       from = 0, upto = mine && 2 * upto >= T ? T : 0;
     }
@@ -341,7 +334,7 @@ __device__ __forceinline__ uint32_t cached_seen(const TcView& v, int ch) {
 // The place past its request's S of key `x` of a tile that is no prefix's (negative:
 // cached positions).
 template <int kMode>
-static __device__ __noinline__ int key_place(const TcParams& P, const TcPlace& s, const TcTile& k, int x) {
+__device__ __forceinline__ int key_place(const TcParams& P, const TcPlace& s, const TcTile& k, int x) {
   const sv_attention_args& a = P.p.a;
   int b = s.seg.b, u = k.u0 + x, n = s.seg.X.n;
   if ((kMode & kShare) && k.own) {
@@ -627,10 +620,10 @@ __device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, c
     for (int e = 0; e < 16; ++e) v[e] = mul2(v[e], c2);
   }
   if (f.slope != 0.0f) {
-    const uint64_t slope2 = pair(f.slope, f.slope);
-    const float b = (float)far;
+    const float b = -f.slope * (float)far;
+    const uint64_t slope2 = pair(f.slope, f.slope), b2 = pair(b, b);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = fma2(slope2, pair((float)(2 * e) - b, (float)(2 * e + 1) - b), v[e]);
+    for (int e = 0; e < 16; ++e) v[e] = add2(v[e], fma2(slope2, pair((float)(2 * e), (float)(2 * e + 1)), b2));
   }
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
@@ -1075,8 +1068,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
         ++set;
       };
       if (kMode) {
-        list.w = w0, list.w1 = w1, list.count = __ldcg(P.list.head + 1);
-        load_lot(P.list, list, __ldcg(P.list.first + blockIdx.x));
+        list.w = w0, list.w1 = w1, list.count = __ldcg(P.list.head + 1), list.whole = __ldcg(P.list.head + 2);
+        list.at = __ldcg(P.list.first + blockIdx.x), list.lot = load_lot(P.list.lots + list.at);
         publish();
         if (!F8)
           while (more) publish();
@@ -1138,7 +1131,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
     // ---- softmax ------------------------------------------------------------
     const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t tS = tmem + (quad << 21) + st * 128, tO = tmem + (quad << 21) + 256 + st * 128;
-    int kbase = 0, ph_s = 0, ph_o = 0;
+    int kbase = 0, ph_s = 0, ph_o = 0, place_next = 0;
     TcSegment seg;
     for (;; give_back_place()) {
       if (kMode) {
@@ -1278,9 +1271,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
             view = view_of<kMode>(P, place, k, me.j, live);
             if (!k.prefix) entries_seen(a, me.b, live ? i : 0, live ? (kMode & kShare) && seg.m > 0 ? place.mem.n[me.j] : seg.X.n : -1, view.e0, seen);
           }
-          if ((kMode & kForms) && !k.prefix && (a.window > 0 || a.slopes)) {
-            places_at[row] = key_place<kMode>(P, place, k, row);
-            named_barrier(4 + st, 128);
+          if ((kMode & kForms) && (a.window > 0 || a.slopes)) {
+            // (the next tile's are on their way while this one is weighed)
+            if (!k.prefix) {
+              places_at[row] = u == st ? key_place<kMode>(P, place, k, row) : place_next;
+              named_barrier(4 + st, 128);
+            }
+            if (u + 2 < units) {
+              const TcTile next = tile_of<kMode>(P, seg, seg.t0 + (QM == 2 ? (u + 2) >> 1 : u + 2));
+              if (!next.prefix) place_next = key_place<kMode>(P, place, next, row);
+            }
           }
         }
         wait(sync, b_s + 8 * st, ph_s);

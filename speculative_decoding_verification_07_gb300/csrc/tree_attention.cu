@@ -392,7 +392,7 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
     P.down = a->slopes != nullptr;
     L.a = *a, L.rows = plan.tiles * kTile, L.box = P.box, L.shift = P.box_shift, L.group = P.group, L.ctas = plan.ctas;
     L.sharing = plan.sharing, L.err = h->d_err;
-    L.head = reinterpret_cast<int*>(at + plan.list), L.first = L.head + 64;
+    L.head = reinterpret_cast<int*>(at + plan.list), L.first = reinterpret_cast<int*>(at + plan.list + 256);
     L.lots = reinterpret_cast<TcLot*>(at + plan.list + 256 + up256((size_t)plan.ctas * 4));
     if (plan.bytes > plan.ranges) {
       L.ranges = reinterpret_cast<int*>(at + plan.ranges);
