@@ -6,13 +6,16 @@ what matters is the order of the calls and what each hands to the next.
     tree_mask        the trees' ancestor bits and depths, once a pass
     kv_append        queries and keys rotated to the nodes' positions, the nodes'
                      entries written to the staging buffer in the cache's format
-    tree_attention   the nodes over the committed cache and their own ancestors
+    prefix_groups    which requests still hold the blocks of a common prompt
+    tree_attention   the nodes over the committed cache and their own ancestors; a
+                     common prompt is read once; scores capped or less with the distance
+                     where the model has them so
     adjust_logits    penalties and grammar masks on every node's row
     verify_tree      the accepted path and the next token
     kv_commit_tree   the path's entries moved into the paged cache
     commit_rollback  lengths, blocks and reference counts
 
-    python examples/tree_pass.py [--kv bf16|e4m3] [--passes N]
+    python examples/tree_pass.py [--kv bf16|e4m3] [--passes N] [--shared] [--softcap C] [--slopes] [--window W]
 """
 
 import argparse
@@ -30,9 +33,13 @@ from speculative_decoding_verification_07_gb300 import binding, rope, workloads 
 class ToyTarget:
     """tied embedding -> one attention layer (grouped heads, rotary) -> logits."""
 
-    def __init__(self, vocab=512, width=256, heads=4, kv_heads=2, head_dim=64, seed=0, device="cuda"):
+    def __init__(self, vocab=512, width=256, heads=4, kv_heads=2, head_dim=64, seed=0, device="cuda",
+                 softcap=None, slopes=False, window=None):
         g = torch.Generator(device).manual_seed(seed)
         self.heads, self.kv_heads, self.head_dim, self.vocab = heads, kv_heads, head_dim, vocab
+        # forms of the scores: s -> softcap tanh(s / softcap), then less a head's slope times the distance
+        self.softcap, self.window = softcap, window
+        self.slopes = torch.exp2(-8.0 * torch.arange(1, heads + 1, device=device) / heads) if slopes else None
 
         def weight(*shape):
             return (torch.randn(*shape, generator=g, device=device) / shape[0] ** 0.5).bfloat16()
@@ -80,6 +87,20 @@ class Session:
         self.ver.kv_append(k, v, self.seq_len, kv=self.kv, block_table=self.table, rope=self.m.table)
         self.seq_len += R
 
+    def prefill_shared(self, prompt):
+        """prompt [P]: processed once, for the first request; the others take its blocks over.  P - 1
+        fills whole blocks, so that nobody writes into a shared one."""
+        done, n = prompt[:-1].int()[None].contiguous(), len(prompt) - 1
+        assert n % self.BS == 0
+        first = slice(0, 1)
+        self.pool.reserve(self.seq_len[first], torch.full((1,), n - 1, dtype=torch.int32, device=self.device), self.table[first])
+        _, _, k, v = self.m.projections(done)
+        self.ver.kv_append(k, v, self.seq_len[first], kv=self.kv, block_table=self.table[first], rope=self.m.table)
+        others = torch.arange(1, self.B, dtype=torch.int32, device=self.device)
+        self.pool.fork_prefix(torch.zeros_like(others), others, torch.full_like(others, n // self.BS), self.table)
+        self.seq_len += n
+        self.pending = prompt[-1:].int().expand(self.B, 1).contiguous()
+
     def verify(self, parents, tokens, draft, *, temperature, rep_penalty=None, allowed=None, seed=0):
         """parents [B, N], tokens [B, N]: the drafted trees; draft [B, N + 1, V]: the draft's rows.
         Returns the verified step's outputs and the adjusted target rows."""
@@ -92,7 +113,9 @@ class Session:
         x, q, k, v = m.projections(torch.cat([self.pending, tokens], 1))
         stage = torch.empty(B, N + 1, 1, 2, m.kv_heads, self.kv.shape[-1], dtype=self.dtype, device=self.device)
         q = ver.kv_append(k, v, self.seq_len, q=q, stage=stage, rope=m.table, depth=tree["depth"])
-        attended = ver.tree_attention(q, self.kv, self.table, self.seq_len, stage=stage, mask=tree["mask"])
+        groups = ver.prefix_groups(self.table, self.seq_len, self.BS, least=self.BS)  # once a pass, for all layers
+        attended = ver.tree_attention(q, self.kv, self.table, self.seq_len, stage=stage, mask=tree["mask"],
+                                      depth=tree["depth"], groups=groups, softcap=m.softcap, slopes=m.slopes, window=m.window)
         logits = m.logits(x, attended).contiguous()
         ver.adjust_logits(logits, history=self.history, tokens=tokens, mask=tree["mask"], rep_penalty=rep_penalty,
                           allowed=allowed)
@@ -124,10 +147,17 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--kv", choices=("bf16", "e4m3"), default="e4m3")
     ap.add_argument("--passes", type=int, default=4)
+    ap.add_argument("--shared", action="store_true", help="all requests go on from one prompt")
+    ap.add_argument("--softcap", type=float)
+    ap.add_argument("--slopes", action="store_true")
+    ap.add_argument("--window", type=int)
     a = ap.parse_args()
     rng = np.random.default_rng(0)
-    s = Session(ToyTarget(), kv=a.kv)
-    s.prefill(torch.tensor(rng.integers(0, s.m.vocab, (s.B, 41)), device="cuda"))
+    s = Session(ToyTarget(softcap=a.softcap, slopes=a.slopes, window=a.window), kv=a.kv)
+    if a.shared:
+        s.prefill_shared(torch.tensor(rng.integers(0, s.m.vocab, 49), device="cuda"))
+    else:
+        s.prefill(torch.tensor(rng.integers(0, s.m.vocab, (s.B, 41)), device="cuda"))
     T = torch.full((s.B,), 0.8, device="cuda")
     for i in range(a.passes):
         out, _ = s.verify(*drafted(s, "binary:3", rng), temperature=T, rep_penalty=torch.full((s.B,), 1.2, device="cuda"),

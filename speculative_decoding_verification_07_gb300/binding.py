@@ -173,6 +173,8 @@ def load_library(path: str = LIB_PATH):
                                    POINTER(KvPayload), c_void_p]
     lib.sv_attention_workspace_size.argtypes = [c_void_p, POINTER(SvAttentionArgs),
                                                 POINTER(c_size_t)]
+    lib.sv_prefix_groups.argtypes = [c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_int32,
+                                     c_void_p, c_void_p, c_void_p]
     lib.sv_tree_attention.argtypes = [c_void_p, POINTER(SvAttentionArgs), c_void_p, c_size_t,
                                       c_void_p]
     for name in EXPORTS[1:]:

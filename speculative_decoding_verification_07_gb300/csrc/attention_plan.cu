@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kRangeThreads) ranges_kernel(const __grid_cons
   pdl_wait();
   pdl_trigger();
   const sv_attention_args& a = p.a;
-  const int rb = blockIdx.x, b = blockIdx.y, q = p.rows, G = p.group;
+  const int most_blocks = p.words / 2, b = blockIdx.x / most_blocks, rb = blockIdx.x - b * most_blocks, q = p.rows, G = p.group;
   const Extent E = extent_of(a, b, nullptr);
   const int blocks = ((E.n + 1) * G + q - 1) / q;
   if (rb >= blocks || blocks < 2) return;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kRangeThreads) ranges_kernel(const __grid_cons
 }
 
 sv_status plan_launch(const TcPlanning& p, cudaStream_t stream) {
-  if (p.ranges && sv_launch_pdl(ranges_kernel, dim3((unsigned)(p.words / 2), (unsigned)p.a.B), dim3(kRangeThreads), 0, stream, p) != cudaSuccess) {
+  if (p.ranges && sv_launch_pdl(ranges_kernel, dim3((unsigned)(p.words / 2 * p.a.B)), dim3(kRangeThreads), 0, stream, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return SV_ERR_CUDA;
   }

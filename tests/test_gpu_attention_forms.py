@@ -260,6 +260,9 @@ SHARED = [  # fmt, D, Hq, H, BS, tree, staged, prefixes' blocks, S past them, gr
     ("bf16", 64, 16, 2, 64, "binary:2", True, 5, list(range(0, 66, 3)), [22]),
     ("bf16", 128, 32, 8, 32, "random:20", True, 9, [1, 2, 3], [1, 2]),
     ("bf16", 128, 4, 4, 16, "chain:0", True, 8, [40, 50, 0, 1, 2, 3, 4], [2, 1, 4]),
+    ("bf16", 128, 16, 2, 16, "random:40", True, 20, [5, 150, 0, 9], [3, 1]),       # more than 128 rows a request
+    ("e4m3", 128, 32, 4, 8, "random:40", False, 50, [5, 260, 0, 9], [4]),          # more than 256
+    ("bf16", 64, 4, 4, 16, "chain:0", False, 9, [3 * (x % 17) for x in range(80)], [70, 1, 9]),  # one row a head, many members
     ("fp32", 64, 4, 4, 16, "chain:5", True, 9, [5, 6, 7], [3]),
     ("bf16", 80, 6, 3, 24, "chain:2", True, 6, [5, 6, 7], [3])]
 
@@ -311,6 +314,38 @@ def test_groups_that_cannot_be_are_reported(ver):
     out = x.run(ver, groups=dict(length=ints([10 ** 6, -5, 400, 0]), members=ints([0, 0, 0, 0])))  # none
     assert ver.error() == 0
     x.check(out, depth=False)
+
+
+def test_more_requests_than_a_kernels_threads(ver):
+    """Groups that cross the 1024 requests at which the list's kernel goes on, the largest lots."""
+    x = shared_batch("bf16", 64, 2, 1, 16, "chain:1", True, 8, [(7 * b) % 40 for b in range(1100)], [3, 1000, 40, 1, 56])
+    g = grouped(ver, x)
+    out = x.run(ver, groups=g)
+    assert ver.error() == 0
+    rng = np.random.default_rng(0)
+    some = {0, 2, 3, 1002, 1003, 1023, 1024, 1042, 1043, 1044, 1099, *rng.integers(0, 1100, 60).tolist()}
+    x.check(out, depth=False, rows={(b, i) for b in some for i in (0, 1)})
+
+
+@pytest.mark.parametrize("fmt,staged", [("bf16", True), ("bf16", False), ("e4m3", True), ("e4m3", False)])
+def test_special_values_of_one_request_do_not_reach_the_others(ver, fmt, staged):
+    """Own positions and entries of requests lie side by side in a tile."""
+    x = shared_batch(fmt, 128, 8, 2, 16, "chain:3", staged, 20, [40, 2, 33, 4], [4])
+    g = grouped(ver, x)
+    clean = x.run(ver, groups=g)
+    p = 20 * 16 + 7
+    x.kv[x.table[2, p // 16], 1, :, :, p % 16] = poison(fmt, (2, 2), 128)
+    out = x.run(ver, groups=g)
+    assert ver.error() == 0
+    for b in (0, 1, 3):
+        assert torch.equal(out[b], clean[b])
+    assert torch.isnan(out[2, :x.n[2] + 1]).all()
+    if staged:  # an entry of request 0, seen by the rows from it on
+        x = shared_batch(fmt, 128, 8, 2, 16, "chain:3", staged, 20, [40, 2, 33, 4], [4])
+        x.stage[0, 2, 1] = poison(fmt, (2, 2), 128)
+        out = x.run(ver, groups=g)
+        assert ver.error() == 0
+        assert torch.equal(out[1:], clean[1:]) and torch.equal(out[0, :2], clean[0, :2]) and torch.isnan(out[0, 2:]).all()
 
 
 def test_special_values_in_a_prefix_reach_its_rows_alone(ver):
