@@ -298,8 +298,8 @@ __device__ __forceinline__ TcView view_of(const TcParams& P, const TcPlace& s, c
   TcView v;
   if (!(kMode & kShare) || !k.own) {
     v.org = (kMode & kShare) && s.seg.m > 0 ? s.mem.S[j] - k.x0 : -k.u0;
-    v.c0 = 0, v.c1 = k.prefix ? k.valid : k.staged ? 0 : v.org;
-    v.e0 = k.prefix || !live ? kFar : k.staged ? 0 : v.org;
+    v.c0 = 0, v.c1 = k.prefix ? k.valid : v.org;
+    v.e0 = k.prefix || !live ? kFar : v.org;  // (staged entries' tiles have no cached positions: org <= 0)
     return v;
   }
   const Extent E = {s.mem.S[j], s.mem.n[j]};
@@ -576,7 +576,11 @@ struct TcForm {
 // log2 units), past which scores of 0.3 caps are shape_chunk's.
 constexpr float kCapNear = 512.0f;
 template <bool F8>
-__device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, const TcForm& f, int far) {
+__device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, const TcForm& f, int far, uint32_t bits) {
+  if (f.cap > 0.0f && __any_sync(0xFFFFFFFFu, ~bits)) {  // what is not seen must not choose the formula
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1 ? x[e] : 0u;
+  }
   uint64_t v[16];
   const uint64_t c2 = pair(f.c, f.c);
   uint32_t most = 0;  // of the products' sizes, within a factor of two
@@ -1265,7 +1269,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
         const bool clear = full && (!(kMode & kForms) || a.window == 0 || seg.X.S + deepest - k.x0 < a.window);
         uint32_t seen[4] = {0, 0, 0, 0};
         TcView view = {};
-        int* places_at = s_at + (st * 2 + (kt & 1)) * kTile;  // (a warp may still read the last tile's)
+        // (a warp may still read those of the stream's last tile)
+        int* places_at = s_at + (st * 2 + ((QM == 2 ? kt : kt >> 1) & 1)) * kTile;
         if (kMode) {
           if (warp_live && !clear) {
             view = view_of<kMode>(P, place, k, me.j, live);
@@ -1373,7 +1378,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                 uint32_t x[32];
                 tmem_ld32(tS + 32 * ch, x);
                 if (kMode && !shaped) {
-                  if ((kMode & kForms) && shape && !shape_near<F8>(x, sc + 32 * ch, form, far)) {
+                  if ((kMode & kForms) && shape && !shape_near<F8>(x, sc + 32 * ch, form, far, bits)) {
                     shape_chunk<F8>(tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, far, false, 0, bits);
                     shaped = true;
                     tmem_ld32(tS + 32 * ch, x);
@@ -1420,7 +1425,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
               uint64_t v[16];
               if ((kMode & kForms) && shape) {
                 if (!apart) tmem_ld32(tS + 32 * ch, x);
-                if (apart || !shape_near<F8>(x, nullptr, form, far)) {
+                if (apart || !shape_near<F8>(x, nullptr, form, far, bits)) {
                   shape_chunk<F8>(tS + 32 * ch, c_raw, nullptr, form.cap, form.slope, far, apart, at, bits);
                   tmem_ld32(tS + 32 * ch, x);
                 }
@@ -1457,9 +1462,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                   v[z] = pair(ex2(y.x), ex2(y.y));
                 }
                 const float2 y0 = unpair(v[e]), y1 = unpair(v[e + 1]);
-                ls[0] = add2(ls[0], v[e]), ls[1] = add2(ls[1], v[e + 1]);
                 w[e] = pack_bf16(y0.x, y0.y);
                 w[e + 1] = pack_bf16(y1.x, y1.y);
+                if (kMode) {  // the weights as they are multiplied: a row of few keys keeps what rounding moved between them
+                  ls[0] = add2(ls[0], pair(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)));
+                  ls[1] = add2(ls[1], pair(__uint_as_float(w[e + 1] << 16), __uint_as_float(w[e + 1] & 0xFFFF0000u)));
+                } else {
+                  ls[0] = add2(ls[0], v[e]), ls[1] = add2(ls[1], v[e + 1]);
+                }
               }
             }
             tmem_st(tS + kW * ch, w);

@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
   pdl_wait();
   pdl_trigger();
   constexpr int kRowsPerWarp = RPW, kSimtRows = RPW * kSimtWarps;
+  constexpr float kUnit = X ? kLog2e : 1.0f;  // scores with a form stay as they are, the others are in log2 units
   extern __shared__ float smem[];
   const sv_attention_args& a = P.a;
   const int D = a.cache.head_dim, DP = D + 4, H = a.cache.heads, G = a.Hq / H;
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
     float x[8] = {};
     if (i <= E.n) load8<F32>(a.q, q0 + i * a.q_stride[1] + (h * G + r % G) * a.q_stride[2] + d, x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sQ[c / (D / 8) * DP + d + e] = x[e] * (a.scale * kLog2e);
+    for (int e = 0; e < 8; ++e) sQ[c / (D / 8) * DP + d + e] = X ? x[e] : x[e] * (a.scale * kLog2e);
   }
   float m[kRowsPerWarp], l[kRowsPerWarp], o[kRowsPerWarp][kMaxHeadDim / 32];
 #pragma unroll
@@ -125,8 +126,9 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
       bool see = bits >> lane & 1;
       if (X) {
         const int hq = h * G + (row0 + warp * kRowsPerWarp + r) % G, far = i > E.n ? 0 : abs(depth_of(a, b, i) - at);
-        if (a.softcap > 0.0f) s[r] = (a.softcap * kLog2e) * tanhf(s[r] / (a.softcap * kLog2e));
-        if (a.slopes) s[r] -= a.slopes[hq] * kLog2e * (float)far;
+        s[r] *= a.scale;
+        if (a.softcap > 0.0f) s[r] = a.softcap * tanhf(s[r] / a.softcap);
+        if (a.slopes) s[r] -= a.slopes[hq] * (float)far;
         if (a.window > 0 && far >= a.window) see = false;
       }
       // a key that is not seen takes no part, whatever its score is; a NaN
@@ -136,8 +138,8 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
       for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
       const float mn = fmaxf(m[r], mx);
       const float base = mn == -__int_as_float(0x7F800000) ? 0.0f : mn;
-      p[r] = see ? exp2f(s[r] - base) : 0.0f;
-      const float alpha = exp2f(m[r] - base);
+      p[r] = see ? exp2f((s[r] - base) * kUnit) : 0.0f;
+      const float alpha = exp2f((m[r] - base) * kUnit);
       m[r] = mn;
       l[r] = l[r] * alpha + p[r];  // a lane's share of the sum
 #pragma unroll
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
       for (int e = 0; e < kMaxHeadDim / 32; ++e) o[r][e] = 0.0f;
       for (int s = 0; s < used; ++s) {
         const float* w = slot(s, r);
-        const float f = exp2f(__ldcg(w + D) - base);
+        const float f = exp2f((__ldcg(w + D) - base) * kUnit);
         l[r] += f * __ldcg(w + D + 1);
 #pragma unroll
         for (int c = 0; c < kMaxHeadDim / 128; ++c)

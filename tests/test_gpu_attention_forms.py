@@ -178,16 +178,33 @@ def test_forms(ver, fmt, D, Hq, H, BS, form):
 
 @pytest.mark.parametrize("fmt,Hq,H", [("bf16", 8, 1), ("e4m3", 28, 4), ("bf16", 4, 4), ("fp32", 4, 2)])
 @pytest.mark.parametrize("form", ["cap", "slopes", "window", "all"])
-def test_forms_of_prompts(ver, fmt, Hq, H, form):
-    """Chains of many row blocks, no depth given, most rows of other blocks than the first."""
+@pytest.mark.parametrize("staged", [False, True])
+def test_forms_of_prompts(ver, fmt, Hq, H, form, staged):
+    """Chains of many row blocks and of several tiles of entries, with no depth and with a chain's
+    given; a last block of few rows, a last tile of few keys."""
     kw = forms_of(form, Hq)
     D = 64 if fmt == "fp32" else 128
-    x = Batch(fmt, D, Hq, H, [0, 333], [299, 250], "chain:299", staged=False, seed=7)
-    out = x.run(ver, **as_call(kw))
+    x = Batch(fmt, D, Hq, H, [0, 333, 3], [299, 250, 131], "chain:299", staged=staged, seed=7)
+    rng = np.random.default_rng(0)
+    rows = {(b, int(i)) for b in range(3) for i in (0, 1, 127, 128, x.n[b], *rng.integers(0, 131, 5))}
+    for depth in (None, ints(np.tile(np.arange(300), (3, 1)))):
+        out = x.run(ver, depth=depth, **as_call(kw))
+        assert ver.error() == 0
+        x.check(out, depth=False, rows=rows, **kw)
+        assert torch.equal(out, x.run(ver, depth=depth, **as_call(kw)))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("form", ["cap", "all"])
+@pytest.mark.parametrize("staged", [False, True])
+def test_forms_of_large_trees(ver, fmt, form, staged):
+    """Trees of more entries than a tile: places do not follow one another, rows of all blocks."""
+    kw = forms_of(form, 8)
+    x = Batch(fmt, 128, 8, 2, [0, 100, 513], [179, 60, 140], "random:179", staged=staged, seed=9, trees=range(3))
+    out = x.run(ver, depth=ints(x.depth), **as_call(kw))
     assert ver.error() == 0
     rng = np.random.default_rng(0)
-    rows = {(b, int(i)) for b in (0, 1) for i in (0, 1, x.n[b], *rng.integers(0, 251, 9))}
-    x.check(out, depth=False, rows=rows, **kw)
+    x.check(out, rows={(b, int(i)) for b in range(3) for i in (0, 1, 127, 128, x.n[b], *rng.integers(0, 180, 9))}, **kw)
 
 
 @pytest.mark.parametrize("fmt,D", [("bf16", 128), ("e4m3", 64), ("fp32", 64)])
@@ -259,9 +276,13 @@ SHARED = [  # fmt, D, Hq, H, BS, tree, staged, prefixes' blocks, S past them, gr
     ("e4m3", 64, 8, 8, 8, "random:9", False, 40, [5, 0, 140, 9], [2, 2]),
     ("bf16", 64, 16, 2, 64, "binary:2", True, 5, list(range(0, 66, 3)), [22]),
     ("bf16", 128, 32, 8, 32, "random:20", True, 9, [1, 2, 3], [1, 2]),
+    ("bf16", 128, 16, 4, 16, "binary:2", True, 30, [4 + 37 * x % 300 for x in range(24)], [8, 8, 8]),  # own keys of many tiles
+    ("e4m3", 128, 16, 4, 16, "binary:2", False, 30, [4 + 37 * x % 300 for x in range(16)], [8, 8]),
     ("bf16", 128, 4, 4, 16, "chain:0", True, 8, [40, 50, 0, 1, 2, 3, 4], [2, 1, 4]),
     ("bf16", 128, 16, 2, 16, "random:40", True, 20, [5, 150, 0, 9], [3, 1]),       # more than 128 rows a request
     ("e4m3", 128, 32, 4, 8, "random:40", False, 50, [5, 260, 0, 9], [4]),          # more than 256
+    ("bf16", 128, 2, 2, 16, "random:150", True, 9, [5, 60, 0, 9], [3, 1]),         # entries of more than a tile
+    ("e4m3", 64, 2, 1, 16, "random:150", True, 9, [5, 60], [2]),
     ("bf16", 64, 4, 4, 16, "chain:0", False, 9, [3 * (x % 17) for x in range(80)], [70, 1, 9]),  # one row a head, many members
     ("fp32", 64, 4, 4, 16, "chain:5", True, 9, [5, 6, 7], [3]),
     ("bf16", 80, 6, 3, 24, "chain:2", True, 6, [5, 6, 7], [3])]
