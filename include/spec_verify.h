@@ -649,9 +649,12 @@ sv_status kv_read(sv_handle* handle, int32_t B, int32_t R, const int32_t* seq_le
  * The results are those of the call without them but for the order of sums (the
  * weights' reference is each part's own).  A shared_len that is negative or past S_b
  * counts as none.  Groups that reach past the batch, overlap, or disagree on their
- * shared_len: SV_ERR_STATE in the error word, the rows of the requests they name are
- * unspecified.  Calls with a window, over fp32 caches or with heads other than 64 and
- * 128 read every request's own blocks. */
+ * shared_len, and a shared_len of a request in no group: SV_ERR_STATE in the error word,
+ * the rows of the requests they name are unspecified.  Calls with a window, over fp32
+ * caches, with heads other than 64 and 128 or blocks that are no multiple of 8 read
+ * every request's own blocks and do not look at the groups.
+ * With a form or shared prefixes and a bf16 cache the normaliser sums the rounded
+ * probabilities. */
 #define SV_ATTENTION_CLEAR 4096
 typedef struct {
   int32_t B, R, Hq, dtype;

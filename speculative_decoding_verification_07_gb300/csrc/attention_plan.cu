@@ -3,7 +3,8 @@
 // With every CTA counting for itself, as the plain calls do, a call of 256 requests in
 // groups spent 15 us before its first tile (each group's members are looked up), and the
 // places of items 5000 to 10000 cycles each on the way; so one CTA makes a list, in
-// a few microseconds that are latency alone, and the attention's CTAs find their place in it.
+// a few microseconds that are latency alone (4 to 7 us after other work, in part under the
+// attention's own start), and the attention's CTAs find their place in it.
 #include "attention_plan.cuh"
 
 namespace sv {
@@ -178,7 +179,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 // Which tiles a row block of a request sees: from the first to the last with a key that
 // the mask and the window leave any of its rows, by a CTA each.  Without it a prompt's
 // row blocks go through all tiles: the mask hides half of them, a window nearly all.
-// Writes the block's units (kLead and its tiles) and its first tile.
+// Writes the block's units (kLead and its tiles) and its first tile.  Four prompts of up to
+// 2041 entries under a window of 1024: 14 us here, and 1971 -> 392 us for the attention with it (and
+// with scores shaped in registers).  Latency of the mask's rows bounds it.
 __global__ void __launch_bounds__(kRangeThreads) ranges_kernel(const __grid_constant__ TcPlanning p) {
   pdl_wait();
   pdl_trigger();
