@@ -292,21 +292,21 @@ struct TcView {
   int c0, c1, e0, org;
 };
 template <int kMode>
-__device__ __forceinline__ TcView view_of(const TcParams& P, const TcPlace& s, const TcTile& k, int j, bool live) {
+__device__ __forceinline__ TcView view_of(const TcParams& P, const TcSegment& s, const TcMembers* mem, const TcTile& k, int j, bool live) {
   constexpr int kFar = 1 << 29;
   const bool staged = P.p.a.stage.data != nullptr;
   TcView v;
   if (!(kMode & kShare) || !k.own) {
-    v.org = (kMode & kShare) && s.seg.m > 0 ? s.mem.S[j] - k.x0 : -k.u0;
+    v.org = (kMode & kShare) && s.m > 0 ? mem->S[j] - k.x0 : -k.u0;
     v.c0 = 0, v.c1 = k.prefix ? k.valid : v.org;
     v.e0 = k.prefix || !live ? kFar : v.org;  // (staged entries' tiles have no cached positions: org <= 0)
     return v;
   }
-  const Extent E = {s.mem.S[j], s.mem.n[j]};
-  v.c0 = (s.mem.start[j] - k.x0) << P.box_shift;
-  v.org = v.c0 + E.S - s.seg.X.S;
+  const Extent E = {mem->S[j], mem->n[j]};
+  v.c0 = (mem->start[j] - k.x0) << P.box_shift;
+  v.org = v.c0 + E.S - s.X.S;
   v.c1 = live ? v.org : v.c0;
-  v.e0 = !live ? kFar : staged ? v.c0 + (cached_boxes(P.p.a, P.box, P.box_shift, s.seg.X.S, E) << P.box_shift) : v.org;
+  v.e0 = !live ? kFar : staged ? v.c0 + (cached_boxes(P.p.a, P.box, P.box_shift, s.X.S, E) << P.box_shift) : v.org;
   return v;
 }
 
@@ -469,10 +469,9 @@ __device__ __forceinline__ float above_log2(float x) { return (float)((int)(__fl
 // What non-finite values of V, cleared from a segment's tiles, add to column
 // `col` of a row: 0, or an infinity or NaN.
 template <int kMode>
-static __device__ __noinline__ float given_back(const TcParams& P, const TcPlace& at, const TcRow& row, int col) {
+static __device__ __noinline__ float given_back(const TcParams& P, const TcSegment& seg, const TcMembers* mem, const TcRow& row, int col) {
   const sv_attention_args& a = P.p.a;
-  const TcSegment& seg = at.seg;
-  const int n = (kMode & kShare) && seg.m > 0 ? at.mem.n[row.j] : seg.X.n;
+  const int n = (kMode & kShare) && seg.m > 0 ? mem->n[row.j] : seg.X.n;
   float sum = 0.0f;
   for (int t = seg.t0; t < seg.t1; ++t) {
     const TcTile k = tile_of<kMode>(P, seg, t);
@@ -482,13 +481,13 @@ static __device__ __noinline__ float given_back(const TcParams& P, const TcPlace
       bool staged = k.staged;
       int u = k.u0 + r, x = k.x0 + r;  // entry number, and entry or position
       if (kMode) {
-        const TcView v = view_of<kMode>(P, at, k, row.j, true);
+        const TcView v = view_of<kMode>(P, seg, mem, k, row.j, true);
         const bool entry = r >= v.e0;
         if (entry ? r - v.e0 > n || !(seen_bits(a, row.b, row.i, n, r - v.e0) & 1) : r < v.c0 || r >= v.c1) continue;
         u = entry ? r - v.e0 : r - v.org;
         if ((kMode & kShare) && k.own) {
           staged = entry && a.stage.data;
-          x = staged ? u : at.mem.S[row.j] + u;
+          x = staged ? u : mem->S[row.j] + u;
         }
         if (a.window > 0 && abs(depth_of(a, row.b, row.i) - (u < 0 ? u : depth_of(a, row.b, u))) >= a.window) continue;
       } else if (!(seen_bits(a, row.b, row.i, n, u) & 1)) {
@@ -703,8 +702,31 @@ static __device__ __noinline__ void rescale_weights(uint32_t tW, int cols, float
 }
 
 // Rows r0 .. valid - 1 of a V tile without their non-finite values (*found is
-// set where there was one), rows valid .. r1 - 1 cleared; thread of 128.  kVecs: vectors
-// of 16 bytes of a row.
+// set where there was one), rows valid .. r1 - 1 cleared; thread of 128.
+template <bool F8>
+static __device__ __noinline__ void clean_rows_plain(char* v, int r0, int valid, int r1, int row_vecs, int thread, volatile int* found) {
+  const int sw = row_vecs < 8 ? row_vecs : 8;  // vectors of a row per half
+  for (int x = thread; x < (r1 - r0) * row_vecs; x += 128) {
+    const int r = r0 + x / row_vecs, c = x % row_vecs;
+    uint4* d = reinterpret_cast<uint4*>(v + (c / sw * kTile + r) * sw * 16 + c % sw * 16);
+    if (r >= valid) {
+      *d = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 y = *d;
+    constexpr uint32_t kMax = F8 ? 0x7F7F7F7Fu : 0x7F807F80u;
+    auto bad = [&](uint32_t z) { return F8 ? __vcmpeq4(z & kMax, kMax) : __vcmpeq2(z & kMax, kMax); };
+    const uint32_t bx = bad(y.x), by = bad(y.y), bz = bad(y.z), bw = bad(y.w);
+    if (bx | by | bz | bw) {
+      y.x &= ~bx, y.y &= ~by, y.z &= ~bz, y.w &= ~bw;
+      *d = y;
+      *found = 1;
+    }
+  }
+  fence_async_smem();
+}
+
+// The same where most tiles are looked at.  kVecs: vectors of 16 bytes of a row.
 template <bool F8, int kVecs>
 static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r1, int thread, volatile int* found) {
   constexpr int kSw = kVecs < 8 ? kVecs : 8;  // vectors of a row per half
@@ -899,8 +921,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
   const TcSync sync{ints + 1, P.p.err};
   // `found` is written by a call, so it lives in memory, where asm statements
   // make every use a load; the roles work on a copy in registers
-  TcPlace plain;
-  TcSegment& found = plain.seg;
+  TcSegment found;
   // With a list, one warp finds the items' places for all: a role takes the next one
   // and gives it back after its last tile.  (A role that finds that a wait has run out
   // ends; the softmax's warps, which meet at barriers, agree on that.)
@@ -1163,7 +1184,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       } else if (!next(seg)) {
         break;
       }
-      const TcPlace& place = kMode ? places[taken % kSegments] : plain;
+      const TcPlace& place = places[taken % kSegments];  // (of a list)
       const int n = seg.t1 - seg.t0, units = n * QM;
       const int i0 = seg.rb * C::kRows;
       // copies of the block's rows in the tile: this thread's copy weighs the
@@ -1287,7 +1308,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
         int* places_at = s_at + (st * 2 + ((QM == 2 ? kt : kt >> 1) & 1)) * kTile;
         if (kMode) {
           if (warp_live && !clear) {
-            view = view_of<kMode>(P, place, k, me.j, live);
+            view = view_of<kMode>(P, seg, &place.mem, k, me.j, live);
             if (!k.prefix) entries_seen(a, me.b, live ? i : 0, live ? (kMode & kShare) && seg.m > 0 ? place.mem.n[me.j] : seg.X.n : -1, view.e0, seen);
           }
           if ((kMode & kForms) && (a.window > 0 || a.slopes)) {
@@ -1505,7 +1526,10 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
             clean_rows<F8, C::kRow / 16>(v, r0, r1, r1, row, &ints[2]);
             r0 = k.valid;
           }
-          clean_rows<F8, C::kRow / 16>(v, r0, k.valid, end, row, &ints[2]);
+          if (kMode)
+            clean_rows<F8, C::kRow / 16>(v, r0, k.valid, end, row, &ints[2]);
+          else
+            clean_rows_plain<F8>(v, r0, k.valid, end, C::kRow / 16, row, &ints[2]);
         }
         if (warp_live) tmem_wait_st();
         tc_fence_before();
@@ -1578,14 +1602,14 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                                                       pack_bf16(z[4] * inv, z[5] * inv), pack_bf16(z[6] * inv, z[7] * inv));
             if (spoiled)
 #pragma unroll 1
-              for (int e = 0; e < 8; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back<kMode>(P, place, me, at + e));
+              for (int e = 0; e < 8; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back<kMode>(P, kMode ? place.seg : found, &place.mem, me, at + e));
           } else {
             float* d = part + lrow * D + at;
             *reinterpret_cast<float4*>(d) = make_float4(z[0], z[1], z[2], z[3]);
             *reinterpret_cast<float4*>(d + 4) = make_float4(z[4], z[5], z[6], z[7]);
             if (spoiled)
 #pragma unroll 1
-              for (int e = 0; e < 8; ++e) d[e] += given_back<kMode>(P, place, me, at + e);
+              for (int e = 0; e < 8; ++e) d[e] += given_back<kMode>(P, kMode ? place.seg : found, &place.mem, me, at + e);
           }
         };
         if (copies > 1) {  // each copy adds all shares of 32 / copies columns
@@ -1634,12 +1658,11 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
           const float* first = P.p.part + (int64_t)(2 * ca + (mul_div(total, ca, ctas) >= seg.item0 ? 0 : 1)) * C::kPart;
           auto slot = [&](int x) { return x == ca ? first : P.p.part + (int64_t)(2 * x) * C::kPart; };
           auto part_ml = [&](int x, int r) { return __ldcg(reinterpret_cast<const float2*>(slot(x) + C::kRows * D) + r); };
-          // each part's factor of a row, where the queries were (the outputs are in registers
-          // or stored): so that the loads below wait for nothing (joining 256 rows of three
-          // parts with factors made beside them: 42000 cycles)
-          const int parts = cb - ca + 1;
+          // With a list, each part's factor of a row, where the queries were (the outputs are
+          // stored): so that the loads below wait for nothing (joining 256 rows of three parts with
+          // factors made beside them: 42000 cycles, 28000 so)
           float* factor = reinterpret_cast<float*>(sm);
-          const bool held = parts * rows * 4 <= C::kQAll;
+          const bool held = kMode && (cb - ca + 1) * rows * 4 <= C::kQAll;
           for (int r = tid; r < rows; r += 256) {
             float M = -kInf, L = 0.0f;
 #pragma unroll 4
@@ -1655,8 +1678,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
             s_ml[r] = make_float2(Mb, L);
           }
           named_barrier(1, 256);
-#pragma unroll 2
-          for (int z = tid; z < rows * (D / 8); z += 256) {
+          auto join = [&](int z) {
             const int r = z / (D / 8), col = z % (D / 8) * 8;
             const float2 ML = s_ml[r];
             float y[8] = {};
@@ -1669,11 +1691,17 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
               y[4] += v1.x * f, y[5] += v1.y * f, y[6] += v1.z * f, y[7] += v1.w * f;
             }
             const TcRow to = row_of<kMode>(P, seg, i0 + r);
-            if ((kMode & kShare) && seg.m > 0 && to.i > place.mem.n[to.j]) continue;
+            if ((kMode & kShare) && seg.m > 0 && to.i > place.mem.n[to.j]) return;
             const float iv = 1.0f / ML.y;
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = ML.y == 0.0f ? 0.0f : y[e] * iv;
             store8<false>(a.out, to.b * a.out_stride[0] + to.i * a.out_stride[1] + to.hq * a.out_stride[2] + col, y);
+          };
+          if (kMode) {
+#pragma unroll 2
+            for (int z = tid; z < rows * (D / 8); z += 256) join(z);
+          } else {
+            for (int z = tid; z < rows * (D / 8); z += 256) join(z);
           }
         }
       }
