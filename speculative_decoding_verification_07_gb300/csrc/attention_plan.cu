@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
               boxes += s_boxes[tid + j], live += s_rows[tid + j], m = j + 1;
             }
             const int tp = (s_shared[tid] + kTile - 1) / kTile;
-            lot = {b, m, boxes, s_shared[tid], m * a.R - 1, 0, kLead + tp + ((boxes << p.shift) + kTile - 1) / kTile, tp,
+            lot = {b, m, boxes, s_shared[tid], m * a.R - 1, 0, p.lead + tp + ((boxes << p.shift) + kTile - 1) / kTile, tp,
                    (m * rows + p.rows - 1) / p.rows, 0, 0, 0};
             if (live > 0) lot.units = lot.T * a.cache.heads * lot.blocks;
           }
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const Extent E = extent_of(a, b, p.err);
       const int begin = first_seen(a, E.S) & -p.box;  // a TMA box starts at a multiple of its rows
       const int tp = (E.S - begin + (a.stage.data ? 0 : E.n + 1) + kTile - 1) / kTile;
-      lot = {b, 0, 0, E.S, E.n, begin, kLead + tp + (a.stage.data ? (E.n + kTile) / kTile : 0), tp, ((E.n + 1) * p.group + p.rows - 1) / p.rows, 0, 0, 0};
+      lot = {b, 0, 0, E.S, E.n, begin, p.lead + tp + (a.stage.data ? (E.n + kTile) / kTile : 0), tp, ((E.n + 1) * p.group + p.rows - 1) / p.rows, 0, 0, 0};
       if (p.ranges && lot.blocks > 1) {  // units before each row block; they hold each one's own
         int* cum = p.ranges + (int64_t)b * p.words;
         int sum = 0;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncthreads();
   }
   // short items stay whole, but where there are few of them
-  if (tid == 0) p.head[0] = units, p.head[1] = lots, p.head[2] = kLead + (s_items <= p.ctas / 4 ? kWholeOne : kWhole);
+  if (tid == 0) p.head[0] = units, p.head[1] = lots, p.head[2] = p.lead + (s_items <= p.ctas / 4 ? kWholeOne : kWhole);
   // the lot that holds the first unit of each CTA's share: the last that starts at or before it
   const int ctas = units > 0 ? sharing_ctas(a, p.group, p.ctas, units) : 0;
   const bool here = lots <= kPlanThreads;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kRangeThreads) ranges_kernel(const __grid_cons
       lo = (cached ? x0 : E.S - begin + jmin) / kTile, hi = (jmax >= 0 ? E.S - begin + jmax : E.S - begin - 1) / kTile + 1;
     }
     int* mine = p.ranges + (int64_t)b * p.words;
-    mine[rb + 1] = kLead + max(1, hi - lo);
+    mine[rb + 1] = p.lead + max(1, hi - lo);
     mine[(p.words + 1) / 2 + rb] = lo;
   }
 }

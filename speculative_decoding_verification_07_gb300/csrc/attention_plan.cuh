@@ -17,6 +17,9 @@ constexpr int kForms = 1, kShare = 2;
 // 8192 positions, bf16, single tokens / trees of 15 nodes: 193 / 215 us with a
 // lead of 3, 191 / 208 with 4, 189 / 202 with 5, 192 / 200 with 6, 193 / 204 with 8.
 constexpr int kLead = 6;
+// Items of 256 rows: a tile takes them 8400 cycles, their start and end 15000.  Prompts of up to 2041
+// entries under a window, listed with a lead of 6: 258 us; with 2: 245.
+constexpr int kLeadWide = 2;
 // Items of up to this many key tiles are not shared between CTAs: a tile is
 // 0.9 us for a CTA alone, joining parts 3 us and more.  A single request leaves
 // most of the GPU idle, so its items are shared earlier: one token over 777
@@ -48,6 +51,7 @@ struct TcList {
   const int* first;   // the lot in which each CTA's share starts
   const int* ranges;  // the tiles that row blocks see, or null: see ranges_kernel
   int words;          // of a request in it
+  int lead;           // units of an item besides its tiles
 };
 
 // A request's own boxes past the positions that it shares, the cached ones and all.
@@ -62,7 +66,7 @@ __device__ __forceinline__ int own_boxes(const sv_attention_args& a, int box, in
 // What the host decides of a call's list.  rows: of an item, 128 or 256.
 struct TcPlanning {
   sv_attention_args a;
-  int rows, box, shift, group, ctas;
+  int rows, lead, box, shift, group, ctas;
   bool sharing;
   int* ranges;  // of row blocks of that many rows, or null
   int words;

@@ -212,10 +212,10 @@ static __device__ __noinline__ bool next_place(const TcParams& P, TcWalker& k, T
       from = 0, upto = mine && 2 * upto >= T ? T : 0;
     }
     k.w = min(k.w1, item0 + T);
-    if (upto <= kLead) continue;  // none of the item's tiles
+    if (upto <= P.list.lead) continue;  // none of the item's tiles
     s.b = k.lot.b, s.h = k.lot.blocks == 1 ? item : (int)quotient(item, k.lot.blocks), s.rb = item - s.h * k.lot.blocks;
     s.T = T, s.tp = k.lot.tp, s.X = {k.lot.S, k.lot.n};
-    s.t0 = max(0, from - kLead), s.t1 = upto - kLead, s.item0 = item0;
+    s.t0 = max(0, from - P.list.lead), s.t1 = upto - P.list.lead, s.item0 = item0;
     s.begin = k.lot.begin, s.m = k.lot.m, s.nb = k.lot.nb, s.lo = lo, s.rev = P.down ? s.t0 + s.t1 - 1 : -1;
     break;
   }
@@ -790,7 +790,7 @@ static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r
 // the form lengthens: per 32 keys 1050 cycles of loads, factors and the form, 630 of
 // weights, 1000 of stores and what is seen); under a window of 1024 single tokens 69 us: nine tiles
 // an item are 22000 cycles, and 7500 more its start and end.  Prompts of up to 2041
-// entries and as many cached positions under that window 250 us: 256 rows a tile take
+// entries and as many cached positions under that window 245 us: 256 rows a tile take
 // 8400 cycles, half of it the softmax of eight warps.
 // Shared prefixes (kShare): a group's rows are an item's, so that the prefix is read
 // once (see lot_size), and its members' own keys are packed behind it.  A first version made
@@ -1574,7 +1574,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       }
       const int c_first = QM == 1 ? st * (D / 2) : 0;
       constexpr int kCols = QM == 1 ? D / 2 : D;
-      const bool split = seg.t0 > 0 || seg.t1 + kLead < seg.T;  // other CTAs have tiles of this item
+      const int lead = kMode ? P.list.lead : kLead;
+      const bool split = seg.t0 > 0 || seg.t1 + lead < seg.T;  // other CTAs have tiles of this item
       // a CTA has two partial results at most: of the item it starts in, and of its last
       float* part = P.p.part + (int64_t)(2 * blockIdx.x + (w0 >= seg.item0 ? 0 : 1)) * C::kPart;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -1644,7 +1645,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
         __threadfence();
         named_barrier(1, 256);
         if (tid == 0) {
-          const int ca = share_of(seg.item0 + kLead, total, ctas), cb = share_of(seg.item0 + seg.T - 1, total, ctas);
+          const int ca = share_of(seg.item0 + lead, total, ctas), cb = share_of(seg.item0 + seg.T - 1, total, ctas);
           ints[12] = ca, ints[13] = cb;
           uint32_t* ticket = P.p.ticket + ca;  // one item at most starts in a CTA and goes on in the next
           const bool last = atomicAdd(ticket, 1u) == (uint32_t)(cb - ca);

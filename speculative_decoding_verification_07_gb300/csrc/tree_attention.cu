@@ -392,7 +392,7 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
     P.entries_magic = a->R == 1 ? 0u : (uint32_t)((0x100000000ull + a->R - 1) / a->R);
     while (P.box >> (P.box_shift + 1)) ++P.box_shift;
     P.down = a->slopes != nullptr;
-    L.a = *a, L.rows = plan.tiles * kTile, L.box = P.box, L.shift = P.box_shift, L.group = P.group, L.ctas = plan.ctas;
+    L.a = *a, L.rows = plan.tiles * kTile, L.lead = plan.tiles == 2 ? kLeadWide : kLead, L.box = P.box, L.shift = P.box_shift, L.group = P.group, L.ctas = plan.ctas;
     L.sharing = plan.sharing, L.err = h->d_err;
     L.head = reinterpret_cast<int*>(at + plan.list), L.first = reinterpret_cast<int*>(at + plan.list + 256);
     L.lots = reinterpret_cast<TcLot*>(at + plan.list + 256 + up256((size_t)plan.ctas * 4));
@@ -403,7 +403,7 @@ static sv_status tc_launch(sv_handle* h, const sv_attention_args* a, const TcPla
     const sv_status rp = plan_launch(L, stream);
     if (rp != SV_OK) return rp;
   }
-  P.list = {L.lots, L.head, L.first, L.ranges, L.words};
+  P.list = {L.lots, L.head, L.first, L.ranges, L.words, L.lead};
   const sv_status rr = sv_raise_dyn_smem((const void*)plan.k.fn, (size_t)plan.k.smem);
   if (rr != SV_OK) return rr;
   if (sv_launch_pdl(plan.k.fn, dim3((unsigned)plan.ctas), dim3((unsigned)plan.k.threads), (size_t)plan.k.smem, stream, P) != cudaSuccess) {
