@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
               boxes += s_boxes[tid + j], live += s_rows[tid + j], m = j + 1;
             }
             const int tp = (s_shared[tid] + kTile - 1) / kTile;
-            lot = {b, m, boxes, s_shared[tid], m * a.R - 1, 0, p.lead + tp + ((boxes << p.shift) + kTile - 1) / kTile, tp,
+            lot = {b, m, boxes, s_shared[tid], m * a.R - 1, 0, p.lead + tp + ((boxes + (kTile >> p.shift) - 1) >> (7 - p.shift)), tp,
                    (m * rows + p.rows - 1) / p.rows, 0, 0, 0};
             if (live > 0) lot.units = lot.T * a.cache.heads * lot.blocks;
           }

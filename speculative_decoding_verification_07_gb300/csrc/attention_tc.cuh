@@ -259,7 +259,7 @@ __device__ __forceinline__ TcTile tile_of(const TcParams& P, const TcSegment& s,
   if ((kMode & kShare) && s.m > 0) {
     k.staged = false, k.prefix = !k.own;
     k.x0 = k.own ? (t - s.tp) << (7 - P.box_shift) : t * kTile;
-    k.valid = min(kTile, k.own ? (s.nb - k.x0) << P.box_shift : s.X.S - k.x0);
+    k.valid = k.own ? min(kTile >> P.box_shift, s.nb - k.x0) << P.box_shift : min(kTile, s.X.S - k.x0);
     k.u0 = 0;
     return k;
   }
@@ -310,8 +310,8 @@ __device__ __forceinline__ TcView view_of(const TcParams& P, const TcSegment& s,
   return v;
 }
 
-// Words of row i of request b's mask, n entries and that: bits of the keys 32 w .. 32 w + 31
-// of the entries in `seen` (w = 0 .. 3), by five loads that wait for nothing.
+// What row i of request b's mask (n + 1 entries) says of keys 32 w .. 32 w + 31 of a tile
+// whose key e0 is entry 0, in seen[w], by five loads that wait for nothing.
 __device__ __forceinline__ void entries_seen(const sv_attention_args& a, int b, int i, int n, int e0, uint32_t (&seen)[4]) {
   const int first = -e0 >> 5, shift = -e0 & 31;
   uint32_t w[5];
@@ -1226,7 +1226,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
           for (int it = 0; it < kAt; ++it) {
             const int idx = (it0 + it) * kGroup + qt, rr = part0 + idx / kChunks, qi = entry_of(P, rr);
             x8[it] = make_uint4(0, 0, 0, 0);
-            if ((kMode & kShare) && seg.m > 1) {
+            if ((kMode & kShare) && seg.m > 0) {  // (rows past a request's entries must not choose a formula for others)
               const TcRow to = row_of<kMode>(P, seg, rr);
               if (it0 + it < each && qi <= seg.X.n && to.i <= place.mem.n[to.j])
                 x8[it] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + to.b * a.q_stride[0] + to.i * a.q_stride[1] +

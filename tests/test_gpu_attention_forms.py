@@ -369,6 +369,24 @@ def test_special_values_of_one_request_do_not_reach_the_others(ver, fmt, staged)
         assert torch.equal(out[1:], clean[1:]) and torch.equal(out[0, :2], clean[0, :2]) and torch.isnan(out[0, 2:]).all()
 
 
+@pytest.mark.parametrize("case", [("bf16", 128, 8, 2, 16, "chain:30", True, 20, [40, 2, 33, 4], [1, 2, 1]),
+                                  ("e4m3", 128, 8, 2, 16, "chain:3", True, 20, [40, 2, 33, 4], [4])], ids=["bf16", "e4m3"])
+def test_queries_past_a_requests_entries_may_be_anything(ver, case):
+    """They are read as zeros: neither the outputs nor their last bits depend on them."""
+    x = shared_batch(*case)
+    g = grouped(ver, x)
+    one = dict(length=g["length"].clone(), members=g["members"].clone())
+    for groups in (g, one, None):
+        want = x.run(ver, groups=groups, softcap=3.0)
+        keep = x.q.clone()
+        for bad in (float("nan"), 1e30, -float("inf")):
+            for b in range(x.B):
+                x.q[b, x.n[b] + 1:] = bad
+            assert torch.equal(x.run(ver, groups=groups, softcap=3.0), want)
+        x.q.copy_(keep)
+    assert ver.error() == 0
+
+
 def test_special_values_in_a_prefix_reach_its_rows_alone(ver):
     x = shared_batch("bf16", 128, 8, 2, 16, "chain:3", True, 20, [1, 2, 3, 4], [2, 2])
     g = grouped(ver, x)
