@@ -636,7 +636,7 @@ sv_status kv_read(sv_handle* handle, int32_t B, int32_t R, const int32_t* seq_le
  * distance d = |pos(row) - pos(x)| (a cached position is its own, entry j sits at
  * S_b + depth[b][j]):
  *   softcap > 0   s = softcap * tanh(s / softcap); 2^-60 .. 2^60
- *   slopes        s = s - slopes[h] * d, [Hq] fp32, finite
+ *   slopes        s = s - slopes[h] * d, [Hq] fp32; slopes[h] * d below 2^100
  *   window > 0    the row sees x only where d < window
  * in this order.  depth [B][R] (NULL = i) is read for slopes and window alone;
  * what is not in 0 .. R - 1 counts as the nearest of them.
@@ -689,7 +689,8 @@ sv_status sv_tree_attention(sv_handle* handle, const sv_attention_args* args, vo
  * positions: shared_len [B] gets that for each of them and members [B] the group's
  * size at its first request; all else is 0.
  * A seq_len that is negative or longer than its table: SV_ERR_STATE in the error
- * word, the request is alone.  B, max_blocks >= 0, block_size >= 1. */
+ * word, the request is alone.  B, max_blocks >= 0, block_size >= 1.  The outputs overlap
+ * neither each other nor the inputs (SV_ERR_INVALID). */
 sv_status sv_prefix_groups(sv_handle* handle, int32_t B, const int32_t* seq_len,
                            const int32_t* block_table, int32_t max_blocks, int32_t block_size,
                            int32_t least, int32_t* shared_len, int32_t* shared_members,

@@ -150,6 +150,10 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kGroupThr
   }
 }
 
+static bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  return (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -160,6 +164,10 @@ extern "C" sv_status sv_prefix_groups(sv_handle* h, int32_t B, const int32_t* se
   if (!h || B < 0 || max_blocks < 0 || block_size < 1) return SV_ERR_INVALID;
   if (B == 0) return SV_OK;
   if (!seq_len || (!table && max_blocks) || !shared_len || !members) return SV_ERR_INVALID;
+  const size_t row = (size_t)B * 4;  // what one CTA writes others still read
+  for (const int32_t* out : {shared_len, members})
+    if (overlap(out, row, seq_len, row) || overlap(out, row, table, row * (size_t)max_blocks) || (out == members && overlap(out, row, shared_len, row)))
+      return SV_ERR_INVALID;
   if (B <= kClusterRequests) {
     if (sv_launch_pdl(prefix_groups_kernel, dim3(kClusterCtas), dim3(kGroupThreads), 0, (cudaStream_t)stream, B, seq_len, table, max_blocks,
                       block_size, least, shared_len, members, h->d_err) != cudaSuccess) {

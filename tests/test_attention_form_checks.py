@@ -103,6 +103,10 @@ def test_arguments_of_groups(lib):
     for args in ((-1, p, p, 4, 16), (2, None, p, 4, 16), (2, p, None, 4, 16), (2, p, p, -1, 16), (2, p, p, 4, 0)):
         assert lib.sv_prefix_groups(handle, *args, 1, p, p, None) == INVALID, args
     assert lib.sv_prefix_groups(handle, 2, p, p, 4, 16, 1, None, p, None) == INVALID
+    at = lambda n: ctypes.c_void_p((1 << 20) + n)  # noqa: E731
+    for table, length, members in ((1024, 2048, 2048), (1024, 2048, 2052), (1024, 4, 2048), (1024, 2048, 0), (1024, 1052, 2048),
+                                   (1024, 2048, 1020)):  # outputs over one another and over inputs
+        assert lib.sv_prefix_groups(handle, 2, at(0), at(table), 4, 16, 1, at(length), at(members), None) == INVALID
     assert lib.sv_prefix_groups(handle, 0, None, None, 4, 16, 1, None, None, None) == OK  # nothing to do
 
 
