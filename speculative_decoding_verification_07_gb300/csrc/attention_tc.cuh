@@ -525,36 +525,63 @@ static __device__ __noinline__ void hide_unseen(const TcParams& P, int b, int i,
   tmem_wait_st();
 }
 
-// Scores of 32 keys become what the softmax takes, in log2 units: times c (and K's
-// scales ks), capped, less slope times the distance (of key e, far - e, or where `apart`
-// from the keys' places past S, a lane each), -inf where `bits` are clear.
-//   cap tanh(s / cap) = cap - 2 cap / (1 + 2^(2 s log2(e) / cap)), and below 0.3 cap the
-// series of tanh to the ninth power, whose next term is 5e-8 of it.
-// The softmax's loop has this for scores below 0.3 cap and keys in a row, as nearly
-// all are.  This is for the others, and for those that a moved reference needs once more.
+// What a row's scores get from their form.
+struct TcForm {
+  float c, cap, slope;  // factor of the products; log2 units
+  float per;            // c / cap
+  int at;               // the row's position
+};
+
+// Scores become what the softmax takes, in log2 units: products times c (and K's scales),
+// capped, less slope times the distance.
+//   cap tanh(s / cap) = cap - 2 cap / (1 + 2^(2 s log2(e) / cap)),
+// off by 3 x 2^-24 of the cap: 2^-14 of a weight up to the cap kCapNear (in log2 units).  Past
+// it scores below 0.3 cap take the series of tanh to the ninth power, whose next term is 5e-8
+// of it.  (The series for all scores that allow it, chosen for 32 keys of 32 rows at once: 64 trees
+// capped at 50 220 us, 215 without a choice; chosen by each score 249.)  No score's form depends on
+// other scores, and the two functions below round alike, so that a row's result does not
+// depend on which of them the other rows of its warp need.
+constexpr float kCapNear = 512.0f;
+
+// Those of 32 keys where they are, key e at the distance far - e, or where `apart` as the
+// keys' places past S say, a lane each; -inf where `bits` are clear.  The softmax's loop has
+// shape_near for keys in a row, as nearly all are.  This is for the others, and for those
+// that a moved reference needs once more.
 // In a pass of its own for all scores, over tensor memory and by arguments in memory, it was 3000
 // cycles a group of 32 keys, mostly waits for instructions and arguments (64
 // single tokens under a window of 1024, capped: 83 us).
 template <bool F8>
 static __device__ __noinline__ void shape_chunk(uint32_t tS, float c, const float* ks, float cap, float slope, int far, bool apart, int place,
                                                 uint32_t bits) {
-  const float per = cap > 0.0f ? 1.0f / cap : 0.0f, up = 2.0f * kLog2e * per;
+  const float per = c / cap, near = cap <= kCapNear ? -1.0f : 0.3f / per, up = 2.0f * kLog2e * per;
 #pragma unroll 1
   for (int g = 0; g < 32; g += 8) {
     uint32_t x[8];
+    float v[8], most = 0.0f;
     tmem_ld8(tS + g, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float z = __uint_as_float(x[e]) * c;
-      if (F8) z *= ks[g + e];
+      v[e] = F8 ? __fmul_rn(__uint_as_float(x[e]), ks[g + e]) : __uint_as_float(x[e]);
+      most = fmaxf(most, fabsf(v[e]));
+      float z = __fmul_rn(v[e], c);
       if (cap > 0.0f) {
-        const float w = z * per, w2 = w * w;
-        const float small = z * (1.0f + w2 * (-1.0f / 3.0f + w2 * (2.0f / 15.0f + w2 * (-17.0f / 315.0f + w2 * (62.0f / 2835.0f)))));
-        const float large = cap - 2.0f * cap * rcp(1.0f + ex2(z * up));
-        z = fabsf(w) < 0.3f ? small : large;
+        const float w = __fmul_rn(v[e], per), w2 = __fmul_rn(w, w);
+        const float t = __fmaf_rn(w2, __fmaf_rn(w2, __fmaf_rn(w2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f);
+        z = __fmul_rn(z, __fmaf_rn(w2, t, 1.0f));
       }
-      const int at = apart ? abs(far - __shfl_sync(0xFFFFFFFFu, place, g + e)) : far - g - e;
-      z = slope == 0.0f ? z : z - slope * (float)at;
+      x[e] = __float_as_uint(z);
+    }
+    if (cap > 0.0f && __any_sync(0xFFFFFFFFu, most > near)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float large = __fmaf_rn(rcp(__fadd_rn(ex2(__fmul_rn(v[e], up)), 1.0f)), -2.0f * cap, cap);
+        x[e] = fabsf(v[e]) > near ? __float_as_uint(large) : x[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = apart ? (float)abs(far - __shfl_sync(0xFFFFFFFFu, place, g + e)) : (float)far - (float)(g + e);
+      const float z = slope == 0.0f ? __uint_as_float(x[e]) : __fmaf_rn(-slope, d, __uint_as_float(x[e]));
       x[e] = bits >> (g + e) & 1 ? __float_as_uint(z) : 0xFF800000u;
     }
     tmem_st8(tS + g, x);
@@ -562,27 +589,11 @@ static __device__ __noinline__ void shape_chunk(uint32_t tS, float c, const floa
   tmem_wait_st();
 }
 
-// What a row's scores get from their form.
-struct TcForm {
-  float c, cap, slope;  // factor of the products; log2 units
-  float per, near;      // c / cap, and the largest product that the series is for
-  int at;               // the row's position
-};
-
-// Scores of 32 keys in a row, x[e] -> log2 units, capped and less the distance's
-// share; false: nothing but unseen keys' x, now 0, has changed.  Where scores are past the series, the formula with a
-// power of two is off by 3 x 2^-24 of the cap: 2^-14 of a weight up to the cap kCapNear (in
-// log2 units), past which scores of 0.3 caps are shape_chunk's.
-constexpr float kCapNear = 512.0f;
+// Those of 32 keys in a row, in registers; false: they are shape_chunk's (a cap past kCapNear), and x is as it was.
 template <bool F8>
-__device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, const TcForm& f, int far, uint32_t bits) {
-  if (f.cap > 0.0f && __any_sync(0xFFFFFFFFu, ~bits)) {  // what is not seen must not choose the formula
-#pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1 ? x[e] : 0u;
-  }
+__device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, const TcForm& f, int far) {
   uint64_t v[16];
   const uint64_t c2 = pair(f.c, f.c);
-  uint32_t most = 0;  // of the products' sizes, within a factor of two
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {
     v[e] = pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
@@ -591,42 +602,27 @@ __device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, c
       const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(ks + 2 * e);
       v[e] = mul2(v[e], s2.x), v[e + 1] = mul2(v[e + 1], s2.y);
     }
-    const float2 y = unpair(v[e]), z = unpair(v[e + 1]);
-    most |= __float_as_uint(y.x) | __float_as_uint(y.y);
-    most |= __float_as_uint(z.x) | __float_as_uint(z.y);
   }
-  if (f.cap > 0.0f) {
-    if (!__any_sync(0xFFFFFFFFu, (most & 0x7FFFFFFFu) > __float_as_uint(f.near))) {
-      const uint64_t per2 = pair(f.per, f.per);
+  if (f.cap > kCapNear) {
+    return false;
+  } else if (f.cap > 0.0f) {
+    const float up = 2.0f * kLog2e * f.per;
+    const uint64_t up2 = pair(up, up), cap2 = pair(f.cap, f.cap), down2 = pair(-2.0f * f.cap, -2.0f * f.cap);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const uint64_t w = mul2(v[e], per2), w2 = mul2(w, w);
-        uint64_t t = fma2(w2, pair(62.0f / 2835.0f, 62.0f / 2835.0f), pair(-17.0f / 315.0f, -17.0f / 315.0f));
-        t = fma2(w2, t, pair(2.0f / 15.0f, 2.0f / 15.0f));
-        t = fma2(w2, t, pair(-1.0f / 3.0f, -1.0f / 3.0f));
-        v[e] = mul2(mul2(v[e], c2), fma2(w2, t, pair(1.0f, 1.0f)));
-      }
-    } else if (f.cap <= kCapNear) {
-      const float up = 2.0f * kLog2e * f.per;
-      const uint64_t up2 = pair(up, up), cap2 = pair(f.cap, f.cap), down2 = pair(-2.0f * f.cap, -2.0f * f.cap);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float2 y = unpair(mul2(v[e], up2));
-        const float2 z = unpair(add2(pair(ex2(y.x), ex2(y.y)), pair(1.0f, 1.0f)));
-        v[e] = fma2(pair(rcp(z.x), rcp(z.y)), down2, cap2);
-      }
-    } else {
-      return false;
+    for (int e = 0; e < 16; ++e) {
+      const float2 z = unpair(mul2(v[e], up2));
+      const float2 w = unpair(add2(pair(ex2(z.x), ex2(z.y)), pair(1.0f, 1.0f)));
+      v[e] = fma2(pair(rcp(w.x), rcp(w.y)), down2, cap2);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = mul2(v[e], c2);
   }
   if (f.slope != 0.0f) {
-    const float b = -f.slope * (float)far;
-    const uint64_t slope2 = pair(f.slope, f.slope), b2 = pair(b, b);
+    const float d = (float)far;
+    const uint64_t slope2 = pair(-f.slope, -f.slope), d2 = pair(d, d);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = add2(v[e], fma2(slope2, pair((float)(2 * e), (float)(2 * e + 1)), b2));
+    for (int e = 0; e < 16; ++e) v[e] = fma2(slope2, add2(d2, pair((float)(-2 * e), (float)(-2 * e - 1))), v[e]);
   }
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
@@ -785,10 +781,10 @@ static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r
 // warp does between products (waits, commits: a third of its time) bounds that.  Handing scores over in halves
 // of 64 keys, to have the next half's under way, doubled those steps: 249 us.
 //
-// Forms of the scores (kForms): 64 trees over 128 to 8192 positions, capped scores 209 us
-// in bf16, 201 without (bytes bound both), 8-bit with a distance's share 270 (a stream's chain, which
+// Forms of the scores (kForms): 64 trees over 128 to 8192 positions, capped scores 201 us
+// in bf16 as without (bytes bound both), 8-bit with a distance's share 267 (a stream's chain, which
 // the form lengthens: per 32 keys 1050 cycles of loads, factors and the form, 630 of
-// weights, 1000 of stores and what is seen); under a window of 1024 single tokens 70 us: nine tiles
+// weights, 1000 of stores and what is seen); under a window of 1024 single tokens 69 us: nine tiles
 // an item are 22000 cycles, and 7500 more its start and end.  Prompts of up to 2041
 // entries and as many cached positions under that window 245 us: 256 rows a tile take
 // 8400 cycles, half of it the softmax of eight warps.
@@ -1226,7 +1222,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
           for (int it = 0; it < kAt; ++it) {
             const int idx = (it0 + it) * kGroup + qt, rr = part0 + idx / kChunks, qi = entry_of(P, rr);
             x8[it] = make_uint4(0, 0, 0, 0);
-            if ((kMode & kShare) && seg.m > 0) {  // (rows past a request's entries must not choose a formula for others)
+            if ((kMode & kShare) && seg.m > 0) {
               const TcRow to = row_of<kMode>(P, seg, rr);
               if (it0 + it < each && qi <= seg.X.n && to.i <= place.mem.n[to.j])
                 x8[it] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + to.b * a.q_stride[0] + to.i * a.q_stride[1] +
@@ -1290,7 +1286,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       const float c_raw = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? s_qs[(QM == 2 ? st * kTile : 0) + row] : 1.0f), 0x1p-149f);
       const bool shape = (kMode & kForms) && (F8 || a.softcap > 0.0f || a.slopes);
       const float c = shape ? 1.0f : c_raw;  // shaped scores have it already
-      form.c = c_raw, form.per = c_raw / form.cap, form.near = 0.3f / form.per;
+      form.c = c_raw, form.per = c_raw / form.cap;
       const uint64_t c2 = pair(c, c);
       // wr: reference of 8-bit weights, log2 units; raise = 2^(kBias + m - wr)
       float m = -kInf, l = 0.0f, wr = -kInf, raise = 0.0f;
@@ -1413,7 +1409,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                 uint32_t x[32];
                 tmem_ld32(tS + 32 * ch, x);
                 if (kMode && !shaped) {
-                  if ((kMode & kForms) && shape && !shape_near<F8>(x, sc + 32 * ch, form, far, bits)) {
+                  if ((kMode & kForms) && shape && !shape_near<F8>(x, sc + 32 * ch, form, far)) {
                     shape_chunk<F8>(tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, far, false, 0, bits);
                     shaped = true;
                     tmem_ld32(tS + 32 * ch, x);
@@ -1460,7 +1456,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
               uint64_t v[16];
               if ((kMode & kForms) && shape) {
                 if (!apart) tmem_ld32(tS + 32 * ch, x);
-                if (apart || !shape_near<F8>(x, nullptr, form, far, bits)) {
+                if (apart || !shape_near<F8>(x, nullptr, form, far)) {
                   shape_chunk<F8>(tS + 32 * ch, c_raw, nullptr, form.cap, form.slope, far, apart, at, bits);
                   tmem_ld32(tS + 32 * ch, x);
                 }

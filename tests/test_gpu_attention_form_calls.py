@@ -10,7 +10,7 @@ import torch
 from oracle import entries as E
 from speculative_decoding_verification_07_gb300 import binding
 
-from tests.test_gpu_attention_forms import DEV, Batch, as_call, forms_of, grouped, ints, shared_batch, some_slopes, ver  # noqa: F401
+from tests.test_gpu_attention_forms import DEV, Batch, as_call, forms_of, grouped, ints, poison, random_entries, shared_batch, some_slopes, ver  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -193,6 +193,42 @@ def test_a_first_call_inside_a_capture_and_larger_ones_after_it():
     assert v.error() == 0 and other.error() == 0
     v.close()
     other.close()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "fp32"])
+@pytest.mark.parametrize("cap,slopes", [(3.0, False), (3.0, True), (5e3, False), (None, True)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_rows_do_not_depend_on_what_others_see(ver, fmt, cap, slopes, shared):
+    """Not even in their last bits: entries that one row sees, other requests' own positions and
+    entries, queries of any size beside a row's own."""
+    if fmt == "fp32" and shared:
+        return
+    x = shared_batch(fmt, 64, 8, 2, 16, "chain:6", True, 9, [40, 2, 33, 4], [4])
+    x.bits[:] = np.tril(np.ones((7, 7), bool))
+    kw = dict(softcap=cap, slopes=torch.tensor(some_slopes(8), device=DEV) if slopes else None, groups=grouped(ver, x) if shared else None)
+    clean = x.run(ver, **kw)
+    x.check(clean, depth=False, softcap=cap, slopes=some_slopes(8) if slopes else None)
+    large = torch.randn(2, 64, generator=torch.Generator(DEV).manual_seed(1), device=DEV) * 300
+    for what in (large, torch.full_like(large, float("nan"))):
+        if fmt == "e4m3":
+            e = poison(fmt, (2, 2), 64)
+            if not torch.isnan(what).any():
+                e[:] = random_entries((2, 2), fmt, 64, torch.Generator(DEV).manual_seed(2))
+                e[..., 64:68] = torch.full((2, 2, 1), 64.0, device=DEV).view(torch.uint8)
+        else:
+            e = torch.stack([what, what]).to(x.kv.dtype)
+        kv, stage, q = x.kv.clone(), x.stage.clone(), x.q.clone()
+        p = 9 * 16 + 11
+        x.kv[x.table[2, p // 16], 1, :, :, p % 16] = e   # of request 2's own
+        x.stage[0, 4, 1] = e                             # seen by the last rows of request 0
+        x.q[3, 1] *= 1e3
+        out = x.run(ver, **kw)
+        assert ver.error() == 0
+        assert torch.equal(out[1], clean[1]) and torch.equal(out[0, :4], clean[0, :4])
+        keep = [i for i in range(7) if i != 1]
+        assert torch.equal(out[3, keep], clean[3, keep])
+        assert not torch.equal(out[2], clean[2]) and not torch.equal(out[0, 4:], clean[0, 4:]) and not torch.equal(out[3, 1], clean[3, 1])
+        x.kv, x.stage, x.q = kv, stage, q
 
 
 def test_outputs_of_groups_that_overlap_are_refused(ver):
