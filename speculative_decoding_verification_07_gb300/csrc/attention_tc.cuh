@@ -61,6 +61,7 @@ struct TcMembers {
 };
 struct TcPlace {
   TcSegment seg;  // T = 0: the end
+  int found;      // its tiles of V had non-finite values, now cleared
   TcMembers mem;
 };
 
@@ -219,7 +220,7 @@ static __device__ __noinline__ bool next_place(const TcParams& P, TcWalker& k, T
     s.begin = k.lot.begin, s.m = k.lot.m, s.nb = k.lot.nb, s.lo = lo, s.rev = P.down ? s.t0 + s.t1 - 1 : -1;
     break;
   }
-  if (lane == 0) to->seg = s;
+  if (lane == 0) to->seg = s, to->found = 0;
   if ((kMode & kShare) && s.m > 0) {
     Extent E = {0, -1};
     if (lane < s.m) E = extent_of(P.p.a, s.b + lane, nullptr);
@@ -722,35 +723,36 @@ static __device__ __noinline__ void clean_rows_plain(char* v, int r0, int valid,
   fence_async_smem();
 }
 
-// The same where most tiles are looked at.  kVecs: vectors of 16 bytes of a row.
+// The same where most tiles are looked at, by a warp that the softmax does not wait for.  kVecs:
+// vectors of 16 bytes of a row.
 template <bool F8, int kVecs>
-static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r1, int thread, volatile int* found) {
+static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r1, int lane, volatile int* found) {
   constexpr int kSw = kVecs < 8 ? kVecs : 8;  // vectors of a row per half
   auto at = [&](int x) {
     const int r = r0 + x / kVecs, c = x % kVecs;
     return reinterpret_cast<uint4*>(v + (c / kSw * kTile + r) * kSw * 16 + c % kSw * 16);
   };
   // whether there is any: 0 times a value is NaN for bf16, an 8-bit NaN's low seven
-  // bits are ones (with the comparisons below for every vector: 4700 cycles a tile, 2300 of 8 bits)
-  uint32_t any = 0;
-#pragma unroll 4
-  for (int x = thread; x < (valid - r0) * kVecs; x += 128) {
+  // bits are ones (with the comparisons below for every vector, by 128 threads: 4700 cycles a tile, 2300 of 8 bits)
+  uint32_t any[4] = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int x = lane; x < (valid - r0) * kVecs; x += 32) {
     const uint4 y = *at(x);
     if (F8) {
-      any |= ((y.x & 0x7F7F7F7Fu) + 0x01010101u) | ((y.y & 0x7F7F7F7Fu) + 0x01010101u) | ((y.z & 0x7F7F7F7Fu) + 0x01010101u) |
-             ((y.w & 0x7F7F7F7Fu) + 0x01010101u);
+      any[0] |= ((y.x & 0x7F7F7F7Fu) + 0x01010101u) | ((y.y & 0x7F7F7F7Fu) + 0x01010101u);
+      any[1] |= ((y.z & 0x7F7F7F7Fu) + 0x01010101u) | ((y.w & 0x7F7F7F7Fu) + 0x01010101u);
     } else {
       const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(any) : "r"(w[e]), "r"(0u));
+        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(any[e]) : "r"(w[e]), "r"(0u));
     }
   }
-  const bool dirty = F8 ? (any & 0x80808080u) != 0 : (any & 0x7FFF7FFFu) != 0;
-  for (int x = thread; x < (r1 - valid) * kVecs; x += 128) *at((valid - r0) * kVecs + x) = make_uint4(0, 0, 0, 0);
+  const bool dirty = ((any[0] | any[1] | any[2] | any[3]) & (F8 ? 0x80808080u : 0x7FFF7FFFu)) != 0;
+  for (int x = lane; x < (r1 - valid) * kVecs; x += 32) *at((valid - r0) * kVecs + x) = make_uint4(0, 0, 0, 0);
   if (dirty)
 #pragma unroll 1
-    for (int x = thread; x < (valid - r0) * kVecs; x += 128) {
+    for (int x = lane; x < (valid - r0) * kVecs; x += 32) {
       uint4* d = at(x);
       uint4 y = *d;
       constexpr uint32_t kMax = F8 ? 0x7F7F7F7Fu : 0x7F807F80u;
@@ -814,7 +816,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
   // K loaded / free, V loaded / free, scores, weights, outputs, queries, scales set / read
   const uint32_t b_kf = bars, b_ke = b_kf + 8 * C::kK, b_vf = b_ke + 8 * C::kK, b_ve = b_vf + 8 * C::kV,
                  b_s = b_ve + 8 * C::kV, b_p = b_s + 16, b_o = b_s + 32, b_q = b_s + 48, b_sf = b_s + 56,
-                 b_se = b_sf + 8 * kScaleRing, b_gf = b_se + 8 * kScaleRing, b_ge = b_gf + 8 * kSegments;  // places set / read
+                 b_se = b_sf + 8 * kScaleRing, b_gf = b_se + 8 * kScaleRing, b_ge = b_gf + 8 * kSegments,  // places set / read
+                 b_vc = b_ge + 8 * kSegments;                                                          // V without non-finite values
   int* ints = reinterpret_cast<int*>(misc + 512);  // 0 tensor memory, 1 abort, 2 non-finite entries, 3 last, 4.. walk
   float2* s_ml = reinterpret_cast<float2*>(misc + 1024);  // [256] maxima and sums exchanged or joined
   float* s_qs = reinterpret_cast<float*>(misc + 3072);    // [kRows] row scales of 8-bit queries
@@ -832,6 +835,8 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
     for (int i = 0; i < kScaleRing; ++i) mbar_init(b_sf + 8 * i, 1), mbar_init(b_se + 8 * i, 4 * QM);
     if (kMode)
       for (int i = 0; i < kSegments; ++i) mbar_init(b_gf + 8 * i, 1), mbar_init(b_ge + 8 * i, 11);
+    if (kMode)
+      for (int i = 0; i < C::kV; ++i) mbar_init(b_vc + 8 * i, 1);
     ints[1] = ints[2] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&P.pages);
@@ -1044,6 +1049,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
             const uint64_t vd = v0 + vs * (C::kTileBytes >> 4);
             const bool first = x < 4;  // of this stream in this segment
             if (QM == 1 || st == 0) {  // the second row tile's keys are there
+              if (kMode) wait(sync, b_vc + 8 * vs, vlap & 1, live);
               wait(sync, b_vf + 8 * vs, vlap & 1, live);
               k_there = x < units && mbar_test_wait(b_kf + 8 * ks, klap & 1);  // while the weights are awaited
             }
@@ -1105,51 +1111,72 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       if (kMode) {
         list.w = w0, list.w1 = w1, list.count = __ldcg(P.list.head + 1), list.whole = __ldcg(P.list.head + 2);
         list.at = __ldcg(P.list.first + blockIdx.x), list.lot = load_lot(P.list.lots + list.at);
-        publish();
-        if (!F8)
-          while (more) publish();
       }
-      if (F8) {
+      if (F8 || kMode) {
         // ---- scales of 8-bit entries, from the tails that came with K into
         // what the softmax adds and multiplies by.  (Loading four bytes of an
         // entry by cp.async kept this warp 2000 cycles a tile: 64 single tokens
         // 216 us; loading the tails itself 1500: 193.)
-        int slot = 0, lap = 0, due = 0;
+        // ---- and V without non-finite values, where a list has it (see below)
+        int slot = 0, lap = 0, due = 0, vslot = 0, vlap = 0;
         TcSegment seg;
         for (;; ++taken) {
           if (kMode) {
+            // (the next one is needed, others are as soon as there is room)
+            while (more && (set <= taken || set < kSegments ||
+                            __all_sync(0xFFFFFFFFu, mbar_test_wait(b_ge + 8 * (set % kSegments), (set / kSegments - 1) & 1))))
+              publish();
             if (taken >= set) break;
             seg = places[taken % kSegments].seg;
             if (seg.T == 0) break;
-            if (more) publish();
           } else if (!next(seg)) {
             break;
           }
 #pragma unroll 1
           for (int t = seg.t0; t < seg.t1; ++t, ++due) {
-            const int box = tile_of<kMode>(P, seg, t).staged ? (kMode ? P.stage_box : kStageBox) : P.box, ring = due % kScaleRing;
-            wait(sync, b_kf + 8 * slot, lap & 1);
-            const char* tails = kslots + slot * C::kKBytes + C::kTileBytes;
-            float ks[4], vs[4];
-            // Scales are 0 .. 2^120; what is not (and what the place of a key past the
-            // valid ones held) must not reach rows that do not see the entry.  K's is
-            // 2^-126 at least (0 counts as that), so that an unseen score's -inf stays.
+            const TcTile k = tile_of<kMode>(P, seg, t);
+            if (F8) {
+              const int box = k.staged ? (kMode ? P.stage_box : kStageBox) : P.box, ring = due % kScaleRing;
+              wait(sync, b_kf + 8 * slot, lap & 1);
+              const char* tails = kslots + slot * C::kKBytes + C::kTileBytes;
+              float ks[4], vs[4];
+              // Scales are 0 .. 2^120; what is not (and what the place of a key past the
+              // valid ones held) must not reach rows that do not see the entry.  K's is
+              // 2^-126 at least (0 counts as that), so that an unseen score's -inf stays.
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = lane + 32 * e, in = r & (box - 1);
-              const char* tail = tails + ((r - in) * 2 + in) * kTail;  // a box's K, then its V
-              const float x = *reinterpret_cast<const float*>(tail), z = *reinterpret_cast<const float*>(tail + box * kTail);
-              ks[e] = fminf(fmaxf(x, kLeastScale), 0x1p120f);
-              vs[e] = fminf(fmaxf(z, 0.0f), 0x1p120f);
+              for (int e = 0; e < 4; ++e) {
+                const int r = lane + 32 * e, in = r & (box - 1);
+                const char* tail = tails + ((r - in) * 2 + in) * kTail;  // a box's K, then its V
+                const float x = *reinterpret_cast<const float*>(tail), z = *reinterpret_cast<const float*>(tail + box * kTail);
+                ks[e] = fminf(fmaxf(x, kLeastScale), 0x1p120f);
+                vs[e] = fminf(fmaxf(z, 0.0f), 0x1p120f);
+              }
+              if (due >= kScaleRing) wait(sync, b_se + 8 * ring, (due / kScaleRing - 1) & 1);
+              float* sc = s_sc + ring * 2 * kTile + lane;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[32 * e] = ks[e], sc[kTile + 32 * e] = vs[e];
+              fence_async_smem();  // the tails have been read before their place is loaded again
+              __syncwarp();
+              if (lane == 0) mbar_arrive(b_sf + 8 * ring);
+              if (++slot == C::kK) slot = 0, ++lap;
             }
-            if (due >= kScaleRing) wait(sync, b_se + 8 * ring, (due / kScaleRing - 1) & 1);
-            float* sc = s_sc + ring * 2 * kTile + lane;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[32 * e] = ks[e], sc[kTile + 32 * e] = vs[e];
-            fence_async_smem();  // the tails have been read before their place is loaded again
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_sf + 8 * ring);
-            if (++slot == C::kK) slot = 0, ++lap;
+            if (kMode) {
+              int r0, r1;
+              half_seen<kMode>(a, k, seg, &r0, &r1);
+              char* v = vslots + vslot * C::kTileBytes;
+              volatile int* spoiled = &places[taken % kSegments].found;
+              // (the products wait for each tile's arrival here, so that no load's phase is missed)
+              wait(sync, b_vf + 8 * vslot, vlap & 1);
+              if ((kMode & kForms) && r1 < k.valid) {
+                clean_rows<F8, C::kRow / 16>(v, r0, r1, r1, lane, spoiled);
+                r0 = k.valid;
+              }
+              if (r0 < k.valid || k.valid % C::kStep)
+                clean_rows<F8, C::kRow / 16>(v, r0, k.valid, (k.valid + C::kStep - 1) / C::kStep * C::kStep, lane, spoiled);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(b_vc + 8 * vslot);
+              if (++vslot == C::kV) vslot = 0, ++vlap;
+            }
           }
         }
       }
@@ -1512,20 +1539,16 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
         // past the valid ones are cleared.  Entries some rows do not see must
         // not ruin them through 0 * NaN: non-finite values of V are cleared and
         // given back to the rows that see them at the end.
-        int r0, r1;
-        half_seen<kMode>(a, k, seg, &r0, &r1);
-        if (r0 < r1 || k.valid % C::kStep) {
-          const int slot = kt % C::kV, end = (k.valid + C::kStep - 1) / C::kStep * C::kStep;
-          char* v = vslots + slot * C::kTileBytes;
-          wait(sync, b_vf + 8 * slot, (kt / C::kV) & 1);
-          if ((kMode & kForms) && r1 < k.valid) {
-            clean_rows<F8, C::kRow / 16>(v, r0, r1, r1, row, &ints[2]);
-            r0 = k.valid;
+        // With a list, most tiles are looked at in some calls (1400 of 8400 cycles of a prompt's
+        // tile), and the warp that makes the items' places does it.
+        if (!kMode) {
+          int r0, r1;
+          half_seen<kMode>(a, k, seg, &r0, &r1);
+          if (r0 < r1 || k.valid % C::kStep) {
+            const int slot = kt % C::kV, end = (k.valid + C::kStep - 1) / C::kStep * C::kStep;
+            wait(sync, b_vf + 8 * slot, (kt / C::kV) & 1);
+            clean_rows_plain<F8>(vslots + slot * C::kTileBytes, r0, k.valid, end, C::kRow / 16, row, &ints[2]);
           }
-          if (kMode)
-            clean_rows<F8, C::kRow / 16>(v, r0, k.valid, end, row, &ints[2]);
-          else
-            clean_rows_plain<F8>(v, r0, k.valid, end, C::kRow / 16, row, &ints[2]);
         }
         if (warp_live) tmem_wait_st();
         tc_fence_before();
@@ -1549,7 +1572,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       tc_fence_before();
       named_barrier(1, 256);
       tc_fence_after();
-      const bool spoiled = *reinterpret_cast<volatile int*>(&ints[2]) != 0;
+      const bool spoiled = *reinterpret_cast<const volatile int*>(kMode ? &place.found : &ints[2]) != 0;
       float f0 = 1.0f, f1 = 0.0f;  // of this copy's outputs in the two streams
       if (F8 && QM == 2) f0 = ex2(unit - (m == -kInf ? 0.0f : m));
       if (QM == 1) {
