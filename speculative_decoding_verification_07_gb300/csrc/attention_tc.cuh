@@ -636,6 +636,10 @@ __device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, c
 // The references (m, weights') of the rows that need others for 32 scores: a whole
 // number at or above the largest score, and above the largest product of p and V's
 // scale, or what kMaxRaise leaves.  Both stay -inf for a row that sees nothing.
+// With forms (small windows) a row may see one key alone, and the first reference is its score
+// to 2^-16, so that its weight is stored as a power of two and the output is its V: by a whole
+// number one output of 12000 was off by its last bit.  Later ones are whole numbers above that.
+template <bool kNear>
 static __device__ __noinline__ float2 references(uint32_t tS, float c, const float* kp, const float* sc, float m, float wr, bool need) {
   uint32_t x[32];
   tmem_ld32(tS, x);
@@ -650,7 +654,12 @@ static __device__ __noinline__ float2 references(uint32_t tS, float c, const flo
     for (int z = 0; z < 4; ++z) x[e + z] = __float_as_uint(s[z]);
     mx = fmaxf(fmaxf(mx, fmaxf(s[0], s[1])), fmaxf(s[2], s[3]));
   }
-  mx = ceilf(mx);
+  if (!kNear)
+    mx = ceilf(mx);
+  else if (m != -__builtin_huge_valf())
+    mx = m + ceilf(mx - m);
+  else
+    mx = fabsf(mx) < 128.0f ? ceilf(mx * 0x1p16f) * 0x1p-16f : ceilf(mx);
   if (mx == -__builtin_huge_valf()) return make_float2(m, wr);
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
@@ -1423,7 +1432,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                     shape_chunk<false>(tS + 32 * ch, 1.0f, nullptr, 0.0f, 0.0f, 0, false, 0, bits);
                 }
                 if (__any_sync(0xFFFFFFFFu, bad)) {
-                  const float2 n = references(tS + 32 * ch, c, kp, sc + 32 * ch, m, wr, bad);
+                  const float2 n = references<(kMode & kForms) != 0>(tS + 32 * ch, c, kp, sc + 32 * ch, m, wr, bad);
                   const float f = n.x > m ? ex2(m - n.x) : 1.0f, fw = n.y > wr ? ex2(wr - n.y) : 1.0f;
                   l *= f, ls[0] = mul2(ls[0], pair(f, f)), ls[1] = mul2(ls[1], pair(f, f));
                   m = n.x, wr = n.y;

@@ -231,6 +231,21 @@ def test_rows_do_not_depend_on_what_others_see(ver, fmt, cap, slopes, shared):
         x.kv, x.stage, x.q = kv, stage, q
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("staged", [False, True])
+@pytest.mark.parametrize("tree", ["random:25", "chain:150"])
+def test_rows_that_see_one_key_give_its_value_back(ver, fmt, staged, tree):
+    """Exactly: codes of 4 significant bits times a power of two, or bf16 values."""
+    n = int(tree.split(":")[1])
+    x = Batch(fmt, 128, 8, 2, [333, 0, 341], [n, n // 2, n], tree, staged=staged, seed=4, size=2.0)
+    out = x.run(ver, depth=ints(x.depth), window=1, softcap=67.2, slopes=torch.tensor(some_slopes(8), device=DEV))
+    assert ver.error() == 0
+    for b in range(3):
+        for h in range(8):
+            want = torch.tensor(x.V[b][x.S[b]:x.S[b] + x.n[b] + 1, h // 4], device=DEV)
+            assert torch.equal(out[b, :x.n[b] + 1, h].double(), want)
+
+
 def test_outputs_of_groups_that_overlap_are_refused(ver):
     table, S = ints([[1, 2], [1, 2]]), ints([32, 32])
     both = ints([0, 0, 0])
