@@ -17,7 +17,7 @@ constexpr int kForms = 1, kShare = 2;
 // 8192 positions, bf16, single tokens / trees of 15 nodes: 193 / 215 us with a
 // lead of 3, 191 / 208 with 4, 189 / 202 with 5, 192 / 200 with 6, 193 / 204 with 8.
 constexpr int kLead = 6;
-// Items of 256 rows: a tile takes them 8400 cycles, their start and end 15000.  Prompts of up to 2041
+// Items of 256 rows: a tile takes them 7000 cycles (8400 then), their start and end 15000.  Prompts of up to 2041
 // entries under a window, listed with a lead of 6: 258 us; with 2: 245.
 constexpr int kLeadWide = 2;
 // Items of up to this many key tiles are not shared between CTAs: a tile is
