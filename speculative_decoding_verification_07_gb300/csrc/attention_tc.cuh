@@ -548,7 +548,7 @@ constexpr float kCapNear = 512.0f;
 // argument of a cap's exponential of it) times the key's scale.  Neither of the two alone: queries of 2^-119
 // and keys of 2^117 are ordinary scores, and 2^19, such a product, times 2^111, such a key's scale,
 // is no fp32 value.  In factor_within their product is finite for every scale (2^120 at most) and
-// normal; for others the score is made first, of the larger factor last, and the cap's factor is
+// subnormal only for scores below 2^-100; for others the score is made first, of the larger factor last, and the cap's factor is
 // multiplied by after (the smallest cap's is 2^61).
 constexpr float kMostFactor = 0x1p7f;
 template <bool F8>
