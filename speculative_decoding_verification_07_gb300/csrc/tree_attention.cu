@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
     float x[8] = {};
     if (i <= E.n) load8<F32>(a.q, q0 + i * a.q_stride[1] + (h * G + r % G) * a.q_stride[2] + d, x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sQ[c / (D / 8) * DP + d + e] = X ? x[e] : x[e] * (a.scale * kLog2e);
+    for (int e = 0; e < 8; ++e) sQ[c / (D / 8) * DP + d + e] = x[e] * (X ? a.scale : a.scale * kLog2e);
   }
   float m[kRowsPerWarp], l[kRowsPerWarp], o[kRowsPerWarp][kMaxHeadDim / 32];
 #pragma unroll
@@ -126,7 +126,6 @@ __global__ void __launch_bounds__(kSimtThreads) simt_attention_kernel(const __gr
       bool see = bits >> lane & 1;
       if (X) {
         const int hq = h * G + (row0 + warp * kRowsPerWarp + r) % G, far = i > E.n ? 0 : abs(depth_of(a, b, i) - at);
-        s[r] *= a.scale;
         if (a.softcap > 0.0f) s[r] = a.softcap * tanhf(s[r] / a.softcap);
         if (a.slopes) s[r] -= a.slopes[hq] * (float)far;
         if (a.window > 0 && far >= a.window) see = false;

@@ -116,3 +116,12 @@ def test_scales_of_any_size(ver, fmt, e, cap):
     check(ver, fmt, *held, q, scale=2.0 ** (e - 3), softcap=cap)
     if cap == 30.0:
         check(ver, fmt, *held, q, scale=2.0 ** (e - 3), slopes=np.float32([0.0, 0.5, 0.01, -0.1, 0.001]))
+
+
+@pytest.mark.parametrize("fmt,D", [("fp32", 128), ("fp32", 64), ("bf16", 80), ("e4m3", 96)])
+@pytest.mark.parametrize("form", list(forms(1)))
+def test_products_past_fp32_under_a_small_scale(ver, fmt, D, form):
+    """Heads that are multiplied in fp32: the scale comes before the product, as without a form."""
+    rng = np.random.default_rng(D)
+    k, q = 2.0 ** 64 * rng.standard_normal((50, D)), 2.0 ** 64 * rng.choice([-0.25, 0.25], (6, D))
+    check(ver, fmt, *cache(ver, fmt, k, rng.standard_normal((50, D))), q, scale=2.0 ** -128, **forms(6)[form])
