@@ -1530,7 +1530,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
               }
               const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
               if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
-                const float mn = fmaxf(m, ceilf(mx)), f = mn == -kInf ? 1.0f : ex2(m - mn);
+                // (A weight's argument rounds by its reference: with a list a row's moves for the row's own
+                // scores alone.  In plain calls all lanes' move at once, and last bits may tell.)
+                const float mn = kMode && !(mx > m + kSlack) ? m : fmaxf(m, ceilf(mx)), f = mn == -kInf ? 1.0f : ex2(m - mn);
                 m = mn, l *= f;
                 const uint64_t f2 = pair(f, f);
                 ls[0] = mul2(ls[0], f2), ls[1] = mul2(ls[1], f2);
