@@ -644,15 +644,16 @@ sv_status kv_read(sv_handle* handle, int32_t B, int32_t R, const int32_t* seq_le
  * Prefixes that requests share: shared_len and shared_members [B], as of
  * sv_prefix_groups (give both or neither).  members_b consecutive requests from b
  * on hold the same K and V (the same blocks, or equal ones) at their first
- * shared_len positions, which are then read once for all of their rows; members_b
- * is 0 for requests that start no group and shared_len_b 0 for those in none.
- * The results are those of the call without them but for the order of sums (the
- * weights' reference is each part's own).  A shared_len that is negative or past S_b
- * counts as none.  Groups that reach past the batch, overlap, or disagree on their
+ * shared_len positions, which are then read once for as many of them as have their
+ * R * Hq / heads rows in one item of 128 (32 requests at most); members_b is 0 for
+ * requests that start no group and shared_len_b 0 for those in none.  The results are
+ * those of the call without them but for the order of sums (the weights' reference is
+ * each part's own).  A shared_len that is negative or past S_b counts as none.  Groups that reach past the batch, overlap, or disagree on their
  * shared_len, and a shared_len of a request in no group: SV_ERR_STATE in the error word,
  * the rows of the requests they name are unspecified.  Calls with a window, over fp32
- * caches, with heads other than 64 and 128 or blocks that are no multiple of 8 read
- * every request's own blocks and do not look at the groups.
+ * caches, with heads other than 64 and 128, blocks that are no multiple of 8 or more
+ * than 64 rows a request (R * Hq / heads) read every request's own blocks and need not
+ * look at the groups.
  * With a form or shared prefixes and a bf16 cache the normaliser sums the rounded
  * probabilities. */
 #define SV_ATTENTION_CLEAR 4096

@@ -1777,7 +1777,7 @@ struct TcKernel {
   int threads, smem, part;  // block, dynamic shared memory, floats of a partial result
 };
 
-// head_dim 64 or 128; tiles: row tiles per CTA, 1 or 2.
+// head_dim 64 or 128; tiles: row tiles per CTA, 1 or 2 (1 where requests share prefixes and scores have a form).
 TcKernel tc_kernel_bf16(int head_dim, int tiles);
 TcKernel tc_kernel_e4m3(int head_dim, int tiles);
 TcKernel tc_kernel_bf16_forms(int head_dim, int tiles);
@@ -1790,11 +1790,12 @@ TcKernel tc_kernel_e4m3_both(int head_dim, int tiles);
 template <bool F8, int kMode>
 TcKernel tc_kernel(int head_dim, int tiles) {
   auto k = [](auto shape, void (*fn)(TcParams)) { return TcKernel{fn, shape.kThreads, shape.kSmem, shape.kPart}; };
-  if (head_dim == 64)
-    return tiles == 1 ? k(TcShape<F8, 64, 1, kMode>(), tc_attention_kernel<F8, 64, 1, kMode>)
-                      : k(TcShape<F8, 64, 2, kMode>(), tc_attention_kernel<F8, 64, 2, kMode>);
-  return tiles == 1 ? k(TcShape<F8, 128, 1, kMode>(), tc_attention_kernel<F8, 128, 1, kMode>)
-                    : k(TcShape<F8, 128, 2, kMode>(), tc_attention_kernel<F8, 128, 2, kMode>);
+  if constexpr (kMode != (kForms | kShare))
+    if (tiles == 2)
+      return head_dim == 64 ? k(TcShape<F8, 64, 2, kMode>(), tc_attention_kernel<F8, 64, 2, kMode>)
+                            : k(TcShape<F8, 128, 2, kMode>(), tc_attention_kernel<F8, 128, 2, kMode>);
+  return head_dim == 64 ? k(TcShape<F8, 64, 1, kMode>(), tc_attention_kernel<F8, 64, 1, kMode>)
+                        : k(TcShape<F8, 128, 1, kMode>(), tc_attention_kernel<F8, 128, 1, kMode>);
 }
 
 }  // namespace sv

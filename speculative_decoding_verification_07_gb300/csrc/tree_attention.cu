@@ -273,13 +273,27 @@ static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct TcPlan {
   bool use;
-  bool sharing;  // groups' prefixes are read once
+  bool sharing;  // requests of a group share items
   int tiles, ctas;  // row tiles per CTA, grid
   TcKernel k;
   size_t list, ranges, bytes;  // where the list and the ranges start in the workspace, and its bytes
 };
 
 static bool has_form(const sv_attention_args* a) { return a->softcap > 0.0f || a->slopes || a->window > 0; }
+
+// Whether a call looks at its groups.  Two requests at least have to fit an item's 128 rows: where
+// each has one of its own the prefix is read for each all the same, by smaller boxes, and with a form a
+// prompt's hidden tiles are gone through.  16 groups of four trees of 15 nodes, 8 query heads a KV head,
+// over 8192 positions 337 us without groups and 350 so (8-bit 428 and 474), four capped prompts of
+// 1024 entries 257 and 295; 64 rows 322 and 196.  Prompts without a form are listed all the same
+// where their entries are a good part of their keys, since the list has a warp of its own for clearing V:
+// four of 1024 entries over 1024 positions 292 us without groups and 198 so (8-bit 339 and 286), 400
+// entries 169 and 111, but 200 of one head a KV head 54 and 58 in 8 bits, and 400 over 8192 468 and 482.
+static bool looks_at_groups(const sv_attention_args* a, int64_t rows) {
+  if (!a->shared_len || a->window > 0) return false;
+  if (2 * rows <= kTile) return true;
+  return !has_form(a) && a->R > 2 * kTile && 5 * (int64_t)a->R >= (int64_t)a->cache.max_blocks * a->cache.block_size;
+}
 
 // bf16 and 8-bit caches with heads of 64 or 128 and blocks of whole 8-row
 // groups (the swizzle's unit, so that a TMA box can start at any block) run on
@@ -293,7 +307,7 @@ static TcPlan tc_plan(const sv_handle* h, const sv_attention_args* a) {
   const int64_t rows = (int64_t)a->R * (a->Hq / c.heads);
   const bool forms = has_form(a);
   // a group's rows are its members' R entries each, and it has no more items than they
-  p.sharing = a->shared_len && a->window == 0;
+  p.sharing = looks_at_groups(a, rows);
   p.tiles = rows > kTile ? 2 : 1;
   const int64_t blocks = cdiv(rows, p.tiles * kTile);
   const int64_t tiles = (int64_t)a->B * c.heads * blocks * (cdiv((int64_t)c.max_blocks * c.block_size, kTile) + cdiv(a->R, kTile) + 1 + kLead);
