@@ -528,8 +528,7 @@ static __device__ __noinline__ void hide_unseen(const TcParams& P, int b, int i,
 
 // What a row's scores get from their form.
 struct TcForm {
-  float factor, cap, slope;  // of the products (see form_factor); log2 units
-  bool careful;              // the cap is past kCapNear, or a row of the warp is outside factor_within
+  float factor, cap, slope;  // of the products (see form_factor; 0: steps other than kDirect); log2 units
   int at;                    // the row's position
 };
 
@@ -544,17 +543,17 @@ struct TcForm {
 // depend on which of them the other rows of its warp need.
 constexpr float kCapNear = 512.0f;
 
-// What a product of codes is multiplied by first: the row's factor (c, or what makes the
-// argument of a cap's exponential of it) times the key's scale.  Neither of the two alone: queries of 2^-119
-// and keys of 2^117 are ordinary scores, and 2^19, such a product, times 2^111, such a key's scale,
-// is no fp32 value.  In factor_within their product is finite for every scale (2^120 at most) and
-// subnormal only for scores below 2^-100; for others the score is made first, of the larger factor last, and the cap's factor is
-// multiplied by after (the smallest cap's is 2^61).
-constexpr float kMostFactor = 0x1p7f;
-template <bool F8>
-__device__ __forceinline__ bool factor_within(float f) {
-  return f >= 0x1p-100f && f <= (F8 ? kMostFactor : 0x1p120f);
-}
+// A product of codes is multiplied by the row's factor (c, or what makes the argument of a cap's
+// exponential of it) before its key's scale: queries of 2^-119 and keys of 2^117 are ordinary scores,
+// and 2^19, such a product, times 2^111, such a key's scale, is no fp32 value.  In factor_within neither step
+// leaves fp32's range where the score does not (codes' products are 2^-18 to 2^25, or 0); for
+// other factors the score is made first, of what keeps it in range, and the cap's factor is multiplied by
+// after (the smallest cap's is 2^61).
+constexpr float kMostFactor = 0x1p100f;
+__device__ __forceinline__ bool factor_within(float f) { return f >= 0x1p-100f && f <= kMostFactor; }
+// How scores are made: kDirect as shape_near does; kLarge for caps past kCapNear; kCareful where a
+// row's factor is outside factor_within.
+constexpr int kDirect = 0, kLarge = 1, kCareful = 2;
 __device__ __forceinline__ float form_factor(float c, float cap) { return cap > 0.0f ? 2.0f * kLog2e * (c / cap) : c; }
 
 // Those of 32 keys where they are, key e at the distance far - e, or where `apart` as the
@@ -564,35 +563,44 @@ __device__ __forceinline__ float form_factor(float c, float cap) { return cap > 
 // In a pass of its own for all scores, over tensor memory and by arguments in memory, it was 3000
 // cycles a group of 32 keys, mostly waits for instructions and arguments (64
 // single tokens under a window of 1024, capped: 83 us).
-template <bool F8, bool kCareful>
+template <bool F8, int kSteps>
 static __device__ __noinline__ void shape_chunk(uint32_t tS, float c, const float* ks, float cap, float slope, int far, bool apart, int place,
                                                 uint32_t bits) {
-  const float f = form_factor(c, cap), inv = 1.0f / cap, twice = 2.0f * kLog2e * inv;
-  const bool near = !kCareful || cap <= kCapNear, direct = !kCareful || (near && factor_within<F8>(f));
+  const float f = form_factor(c, cap), inv = 1.0f / cap;
+  const bool near = kSteps == kDirect || (kSteps == kCareful && cap <= kCapNear), direct = kSteps == kDirect || (near && factor_within(f));
+  // a score is product * first * K's scale * last
+  const float first = kSteps == kCareful && c > kMostFactor ? 1.0f : c, last = kSteps == kCareful && c > kMostFactor ? c : 1.0f;
+  const float up = direct ? 1.0f : 2.0f * kLog2e;  // from y to an exponential's argument
 #pragma unroll 1
   for (int g = 0; g < 32; g += 8) {
     uint32_t x[8];
+    float y[8], most = 0.0f;  // the exponentials' arguments, or scores / cap
     tmem_ld8(tS + g, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float s = __uint_as_float(x[e]), k = F8 ? ks[g + e] : 1.0f;
-      float y = __fmul_rn(s, F8 ? __fmul_rn(f, k) : f), z = y;
-      if (kCareful && !direct) {
-        z = !F8 || c <= kMostFactor ? __fmul_rn(s, __fmul_rn(c, k)) : __fmul_rn(__fmul_rn(s, k), c);
-        y = __fmul_rn(z, twice);
+      float z = __fmul_rn(__fmul_rn(s, kSteps == kDirect ? f : first), k);
+      if (kSteps == kCareful) z = __fmul_rn(z, last);
+      y[e] = direct ? __fmul_rn(__fmul_rn(s, f), k) : __fmul_rn(z, inv);
+      if (!near) {
+        const float w = y[e], w2 = __fmul_rn(w, w);
+        const float t = __fmaf_rn(w2, __fmaf_rn(w2, __fmaf_rn(w2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f);
+        most = fmaxf(most, fabsf(w));
+        z = __fmul_rn(z, __fmaf_rn(w2, t, 1.0f));
       }
-      if (cap > 0.0f) {
-        const float large = __fmaf_rn(rcp(__fadd_rn(ex2(y), 1.0f)), -2.0f * cap, cap);
-        if (kCareful) {
-          const float w = __fmul_rn(z, inv), w2 = __fmul_rn(w, w);
-          const float t = __fmaf_rn(w2, __fmaf_rn(w2, __fmaf_rn(w2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f);
-          z = near || fabsf(w) > 0.3f ? large : __fmul_rn(z, __fmaf_rn(w2, t, 1.0f));
-        } else {
-          z = large;
-        }
+      x[e] = __float_as_uint(z);
+    }
+    if (cap > 0.0f && (near || __any_sync(0xFFFFFFFFu, most > 0.3f))) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float large = __fmaf_rn(rcp(__fadd_rn(ex2(kSteps == kDirect ? y[e] : __fmul_rn(y[e], up)), 1.0f)), -2.0f * cap, cap);
+        x[e] = near || fabsf(y[e]) > 0.3f ? __float_as_uint(large) : x[e];
       }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
       const float d = apart ? (float)abs(far - __shfl_sync(0xFFFFFFFFu, place, g + e)) : (float)far - (float)(g + e);
-      if (slope != 0.0f) z = __fmaf_rn(-slope, d, z);
+      const float z = slope == 0.0f ? __uint_as_float(x[e]) : __fmaf_rn(-slope, d, __uint_as_float(x[e]));
       x[e] = bits >> (g + e) & 1 ? __float_as_uint(z) : 0xFF800000u;
     }
     tmem_st8(tS + g, x);
@@ -600,33 +608,35 @@ static __device__ __noinline__ void shape_chunk(uint32_t tS, float c, const floa
   tmem_wait_st();
 }
 
-// The two as calls of their own: as one function with both, the callers keep less in registers: 64
-// 8-bit trees with slopes 277 us, 265 so.
+// Calls of their own: as one function for all steps, the callers keep less in registers (64 8-bit
+// trees with slopes 277 us, 254 so).  Caps past kCapNear have only this: the 64 trees capped at 400
+// 345 us and 392 in 8 bits, at 50 202 and 272.
 template <bool F8>
-__device__ __forceinline__ void shape_group(bool careful, uint32_t tS, float c, const float* ks, float cap, float slope, int far, bool apart, int place,
+__device__ __forceinline__ void shape_group(bool direct, uint32_t tS, float c, const float* ks, float cap, float slope, int far, bool apart, int place,
                                             uint32_t bits) {
-  if (careful)
-    shape_chunk<F8, true>(tS, c, ks, cap, slope, far, apart, place, bits);
+  if (direct)
+    shape_chunk<F8, kDirect>(tS, c, ks, cap, slope, far, apart, place, bits);
+  else if (cap > kCapNear && __all_sync(0xFFFFFFFFu, factor_within(c)))
+    shape_chunk<F8, kLarge>(tS, c, ks, cap, slope, far, apart, place, bits);
   else
-    shape_chunk<F8, false>(tS, c, ks, cap, slope, far, apart, place, bits);
+    shape_chunk<F8, kCareful>(tS, c, ks, cap, slope, far, apart, place, bits);
 }
 
 // Those of 32 keys in a row, in registers; false: they are shape_chunk's (a cap past kCapNear, factors
 // outside factor_within), and x is as it was.
 template <bool F8>
 __device__ __forceinline__ bool shape_near(uint32_t (&x)[32], const float* ks, const TcForm& f, int far) {
-  if (f.careful) return false;
+  if (f.factor == 0.0f) return false;
   uint64_t v[16];
   const uint64_t f2 = pair(f.factor, f.factor);
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {
-    ulonglong2 k2 = make_ulonglong2(f2, f2);
+    v[e] = mul2(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2);
+    v[e + 1] = mul2(pair(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3])), f2);
     if (F8) {
       const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(ks + 2 * e);
-      k2.x = mul2(f2, s2.x), k2.y = mul2(f2, s2.y);
+      v[e] = mul2(v[e], s2.x), v[e + 1] = mul2(v[e + 1], s2.y);
     }
-    v[e] = mul2(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), k2.x);
-    v[e + 1] = mul2(pair(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3])), k2.y);
   }
   if (f.cap > 0.0f) {
     const uint64_t cap2 = pair(f.cap, f.cap), down2 = pair(-2.0f * f.cap, -2.0f * f.cap);
@@ -1341,7 +1351,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
       const bool shape = (kMode & kForms) && (F8 || a.softcap > 0.0f || a.slopes);
       const float c = shape ? 1.0f : c_raw;  // shaped scores have it already
       form.factor = form_factor(c_raw, form.cap);
-      if ((kMode & kForms) && shape) form.careful = form.cap > kCapNear || __any_sync(0xFFFFFFFFu, !factor_within<F8>(form.factor));
+      if ((kMode & kForms) && shape) form.factor = form.cap <= kCapNear && __all_sync(0xFFFFFFFFu, factor_within(form.factor)) ? form.factor : 0.0f;
       const uint64_t c2 = pair(c, c);
       // wr: reference of 8-bit weights, log2 units; raise = 2^(kBias + m - wr)
       float m = -kInf, l = 0.0f, wr = -kInf, raise = 0.0f;
@@ -1446,9 +1456,9 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                 if (kMode && !shaped && (__any_sync(0xFFFFFFFFu, bad) || apart)) {
                   shaped = true;
                   if ((kMode & kForms) && shape)
-                    shape_group<F8>(form.careful, tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, far, apart, at, bits);
+                    shape_group<F8>(form.factor != 0.0f, tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, far, apart, at, bits);
                   else if (__any_sync(0xFFFFFFFFu, ~bits))
-                    shape_chunk<false, false>(tS + 32 * ch, 1.0f, nullptr, 0.0f, 0.0f, 0, false, 0, bits);
+                    shape_chunk<false, kDirect>(tS + 32 * ch, 1.0f, nullptr, 0.0f, 0.0f, 0, false, 0, bits);
                 }
                 if (__any_sync(0xFFFFFFFFu, bad)) {
                   const float2 n = references<(kMode & kForms) != 0>(tS + 32 * ch, c, kp, sc + 32 * ch, m, wr, bad);
@@ -1465,7 +1475,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
                 tmem_ld32(tS + 32 * ch, x);
                 if (kMode && !shaped) {
                   if ((kMode & kForms) && shape && !shape_near<F8>(x, sc + 32 * ch, form, far)) {
-                    shape_group<F8>(form.careful, tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, far, false, 0, bits);
+                    shape_group<F8>(form.factor != 0.0f, tS + 32 * ch, c_raw, sc + 32 * ch, form.cap, form.slope, far, false, 0, bits);
                     shaped = true;
                     tmem_ld32(tS + 32 * ch, x);
                   } else if (__any_sync(0xFFFFFFFFu, ~bits)) {
@@ -1512,7 +1522,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
               if ((kMode & kForms) && shape) {
                 if (!apart) tmem_ld32(tS + 32 * ch, x);
                 if (apart || !shape_near<F8>(x, nullptr, form, far)) {
-                  shape_group<F8>(form.careful, tS + 32 * ch, c_raw, nullptr, form.cap, form.slope, far, apart, at, bits);
+                  shape_group<F8>(form.factor != 0.0f, tS + 32 * ch, c_raw, nullptr, form.cap, form.slope, far, apart, at, bits);
                   tmem_ld32(tS + 32 * ch, x);
                 }
               } else {
