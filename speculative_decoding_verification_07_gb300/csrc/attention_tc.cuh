@@ -332,6 +332,17 @@ __device__ __forceinline__ uint32_t cached_seen(const TcView& v, int ch) {
   return hi <= lo ? 0u : (hi >= 32 ? 0xFFFFFFFFu : (1u << hi) - 1u) & 0xFFFFFFFFu << lo;
 }
 
+// Whose box a box of own keys is: start[j] <= box < start[j + 1].
+__device__ __forceinline__ int member_of(const TcMembers& mem, int box) {
+  int lo = 0, hi = kMembers;
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (mem.start[mid] <= box) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 // The place past its request's S of key `x` of a tile that is no prefix's (negative:
 // cached positions).
 template <int kMode>
@@ -339,13 +350,7 @@ __device__ __forceinline__ int key_place(const TcParams& P, const TcPlace& s, co
   const sv_attention_args& a = P.p.a;
   int b = s.seg.b, u = k.u0 + x, n = s.seg.X.n;
   if ((kMode & kShare) && k.own) {
-    const int box = k.x0 + (x >> P.box_shift);
-    int lo = 0, hi = kMembers;  // start[lo] <= box < start[hi]
-#pragma unroll 1
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (s.mem.start[mid] <= box) lo = mid; else hi = mid;
-    }
+    const int box = k.x0 + (x >> P.box_shift), lo = member_of(s.mem, box);
     const Extent E = {s.mem.S[lo], s.mem.n[lo]};
     const int in = box - s.mem.start[lo], cached = cached_boxes(a, P.box, P.box_shift, s.seg.X.S, E);
     b += lo, n = E.n, u = (in >= cached ? (in - cached) << P.box_shift : s.seg.X.S + (in << P.box_shift) - E.S) + (x & (P.box - 1));
@@ -760,21 +765,50 @@ static __device__ __noinline__ void clean_rows_plain(char* v, int r0, int valid,
   fence_async_smem();
 }
 
-// The same where most tiles are looked at, by a warp that the softmax does not wait for.  kVecs:
-// vectors of 16 bytes of a row.
-template <bool F8, int kVecs>
-static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r1, int lane, volatile int* found) {
+// The rows of a tile of own keys (x0: its first box) that hold none as zeros, by a whole warp: places past a
+// request's last position or entry in its last boxes.  What was never written is no value of V, and must not
+// look like one that has to be given back.  (Done where a tile has non-finite values at all: for every
+// tile it kept the warp, for which the products wait, and shared chains took 91 us for 76.)
+template <int kVecs>
+static __device__ __noinline__ void clear_unheld(const TcParams& P, const TcPlace& s, int x0, int valid, char* v) {
   constexpr int kSw = kVecs < 8 ? kVecs : 8;  // vectors of a row per half
-  auto at = [&](int x) {
-    const int r = r0 + x / kVecs, c = x % kVecs;
-    return reinterpret_cast<uint4*>(v + (c / kSw * kTile + r) * kSw * 16 + c % kSw * 16);
-  };
-  // whether there is any: 0 times a value is NaN for bf16, an 8-bit NaN's low seven
-  // bits are ones (with the comparisons below for every vector, by 128 threads: 4700 cycles a tile, 2300 of 8 bits)
+  const sv_attention_args& a = P.p.a;
+  const int lane = threadIdx.x & 31, at = lane << P.box_shift;
+  uint32_t held = 0;  // of a lane's box
+  if (at < valid) {
+    const int j = member_of(s.mem, x0 + lane), in = x0 + lane - s.mem.start[j];
+    const Extent E = {s.mem.S[j], s.mem.n[j]};
+    const int cached = cached_boxes(a, P.box, P.box_shift, s.seg.X.S, E);
+    const int keys = in >= cached ? E.n + 1 - ((in - cached) << P.box_shift)
+                                  : max(0, E.S - s.seg.X.S) + (a.stage.data ? 0 : E.n + 1) - (in << P.box_shift);
+    held = (1u << min(keys, P.box)) - 1u;
+  }
+  bool any = false;
+#pragma unroll 1
+  for (int w = 0; 32 * w < valid; ++w) {
+    const uint32_t all = valid - 32 * w >= 32 ? 0xFFFFFFFFu : (1u << (valid - 32 * w)) - 1u;
+    uint32_t left = all & ~__reduce_or_sync(0xFFFFFFFFu, at >> 5 == w ? held << (at & 31) : 0u);
+    any |= left != 0;
+    for (; left; left &= left - 1) {
+      const int r = 32 * w + __ffs(left) - 1;
+      if (lane < kVecs) *reinterpret_cast<uint4*>(v + (lane / kSw * kTile + r) * kSw * 16 + lane % kSw * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  if (any) fence_async_smem();
+  __syncwarp();
+}
+
+// Whether a lane's share of rows r0 .. valid - 1 of a V tile has non-finite values.
+template <bool F8, int kVecs>
+__device__ __forceinline__ bool spoiled_rows(const char* v, int r0, int valid) {
+  constexpr int kSw = kVecs < 8 ? kVecs : 8;  // vectors of a row per half
+  // 0 times a value is NaN for bf16, an 8-bit NaN's low seven bits are ones (with the comparisons
+  // below for every vector, by 128 threads: 4700 cycles a tile, 2300 of 8 bits)
   uint32_t any[4] = {0, 0, 0, 0};
 #pragma unroll 8
-  for (int x = lane; x < (valid - r0) * kVecs; x += 32) {
-    const uint4 y = *at(x);
+  for (int x = threadIdx.x & 31; x < (valid - r0) * kVecs; x += 32) {
+    const int r = r0 + x / kVecs, c = x % kVecs;
+    const uint4 y = *reinterpret_cast<const uint4*>(v + (c / kSw * kTile + r) * kSw * 16 + c % kSw * 16);
     if (F8) {
       any[0] |= ((y.x & 0x7F7F7F7Fu) + 0x01010101u) | ((y.y & 0x7F7F7F7Fu) + 0x01010101u);
       any[1] |= ((y.z & 0x7F7F7F7Fu) + 0x01010101u) | ((y.w & 0x7F7F7F7Fu) + 0x01010101u);
@@ -785,7 +819,27 @@ static __device__ __noinline__ void clean_rows(char* v, int r0, int valid, int r
         asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(any[e]) : "r"(w[e]), "r"(0u));
     }
   }
-  const bool dirty = ((any[0] | any[1] | any[2] | any[3]) & (F8 ? 0x80808080u : 0x7FFF7FFFu)) != 0;
+  return ((any[0] | any[1] | any[2] | any[3]) & (F8 ? 0x80808080u : 0x7FFF7FFFu)) != 0;
+}
+
+// As clean_rows_plain where most tiles are looked at, by a warp that the softmax does not wait for.  kVecs:
+// vectors of 16 bytes of a row.
+template <bool F8, int kMode, int kVecs>
+static __device__ __noinline__ void clean_rows(const TcParams& P, TcPlace* s, bool own, int x0, char* v, int r0, int valid, int r1) {
+  constexpr int kSw = kVecs < 8 ? kVecs : 8;
+  const int lane = threadIdx.x & 31;
+  volatile int* found = &s->found;
+  auto at = [&](int x) {
+    const int r = r0 + x / kVecs, c = x % kVecs;
+    return reinterpret_cast<uint4*>(v + (c / kSw * kTile + r) * kSw * 16 + c % kSw * 16);
+  };
+  bool dirty;
+#pragma unroll 1
+  for (bool again = false;; again = true) {
+    dirty = spoiled_rows<F8, kVecs>(v, r0, valid);
+    if (!(kMode & kShare) || !own || again || !__any_sync(0xFFFFFFFFu, dirty)) break;
+    clear_unheld<kVecs>(P, *s, x0, valid, v);
+  }
   for (int x = lane; x < (r1 - valid) * kVecs; x += 32) *at((valid - r0) * kVecs + x) = make_uint4(0, 0, 0, 0);
   if (dirty)
 #pragma unroll 1
@@ -1015,13 +1069,7 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
           int y = k.x0 + lane * box, w = seg.b;
           bool staged = k.staged;
           if ((kMode & kShare) && k.own && lane < boxes) {  // whose box it is
-            const int x = k.x0 + lane;
-            int lo = 0, hi = kMembers;  // start[lo] <= x < start[hi]
-#pragma unroll 1
-            while (hi - lo > 1) {
-              const int mid = (lo + hi) / 2;
-              if (mem.start[mid] <= x) lo = mid; else hi = mid;
-            }
+            const int x = k.x0 + lane, lo = member_of(mem, x);
             const int in = x - mem.start[lo], cached = cached_boxes(a, P.box, P.box_shift, seg.X.S, {mem.S[lo], mem.n[lo]});
             staged = in >= cached;
             w = seg.b + lo, y = staged ? (in - cached) * box : seg.X.S + in * box;
@@ -1201,15 +1249,15 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
               int r0, r1;
               half_seen<kMode>(a, k, seg, &r0, &r1);
               char* v = vslots + vslot * C::kTileBytes;
-              volatile int* spoiled = &places[taken % kSegments].found;
+              TcPlace* place = &places[taken % kSegments];
               // (the products wait for each tile's arrival here, so that no load's phase is missed)
               wait(sync, b_vf + 8 * vslot, vlap & 1);
               if ((kMode & kForms) && r1 < k.valid) {
-                clean_rows<F8, C::kRow / 16>(v, r0, r1, r1, lane, spoiled);
+                clean_rows<F8, kMode, C::kRow / 16>(P, place, k.own, k.x0, v, r0, r1, r1);
                 r0 = k.valid;
               }
               if (r0 < k.valid || k.valid % C::kStep)
-                clean_rows<F8, C::kRow / 16>(v, r0, k.valid, (k.valid + C::kStep - 1) / C::kStep * C::kStep, lane, spoiled);
+                clean_rows<F8, kMode, C::kRow / 16>(P, place, k.own, k.x0, v, r0, k.valid, (k.valid + C::kStep - 1) / C::kStep * C::kStep);
               __syncwarp();
               if (lane == 0) mbar_arrive(b_vc + 8 * vslot);
               if (++vslot == C::kV) vslot = 0, ++vlap;
