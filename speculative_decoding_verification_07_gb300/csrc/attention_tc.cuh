@@ -62,8 +62,10 @@ struct TcMembers {
 struct TcPlace {
   TcSegment seg;  // T = 0: the end
   int found;      // its tiles of V had non-finite values, now cleared
+  uint32_t spoiled[8];  // which of them: a bit for a tile, or for 2^k where they are more than 256
   TcMembers mem;
 };
+__device__ __forceinline__ int spoiled_bit(const TcSegment& s, int t) { return (t - s.t0) >> max(0, 24 - __clz(s.t1 - s.t0 - 1)); }
 
 // F8: an 8-bit cache.  D: head_dim.  QM: row tiles of 128 per CTA.
 //   QM = 1: up to 128 rows; the two streams (score, weight and output regions
@@ -221,6 +223,7 @@ static __device__ __noinline__ bool next_place(const TcParams& P, TcWalker& k, T
     break;
   }
   if (lane == 0) to->seg = s, to->found = 0;
+  if (lane < 8) to->spoiled[lane] = 0;
   if ((kMode & kShare) && s.m > 0) {
     Extent E = {0, -1};
     if (lane < s.m) E = extent_of(P.p.a, s.b + lane, nullptr);
@@ -472,43 +475,65 @@ constexpr float kMaxRaise = 126.0f;
 // The whole number above log2(x), -126 for zero and subnormal numbers.
 __device__ __forceinline__ float above_log2(float x) { return (float)((int)(__float_as_uint(x) >> 23) - 126); }
 
-// What non-finite values of V, cleared from a segment's tiles, add to column
-// `col` of a row: 0, or an infinity or NaN.
-template <int kMode>
-static __device__ __noinline__ float given_back(const TcParams& P, const TcSegment& seg, const TcMembers* mem, const TcRow& row, int col) {
+// Adds to eight columns of a row from `col` on, fp32 of a partial result or bf16 outputs, what non-finite
+// values of V that were cleared from a segment's tiles make of them: infinities or NaN.  With a list
+// the tiles that had some are noted, and a row looks through its own request's keys alone.
+template <bool F8, int kMode>
+static __device__ __noinline__ void give_back(const TcParams& P, const TcSegment& seg, const TcPlace* place, const TcRow& row, int col,
+                                              float* part, __nv_bfloat16* out) {
   const sv_attention_args& a = P.p.a;
-  const int n = (kMode & kShare) && seg.m > 0 ? mem->n[row.j] : seg.X.n;
-  float sum = 0.0f;
+  const TcMembers* mem = kMode ? &place->mem : nullptr;
+  const bool shared = (kMode & kShare) && seg.m > 0;
+  const int n = shared ? mem->n[row.j] : seg.X.n, S = shared ? mem->S[row.j] : seg.X.S;
+  float sum[8] = {};
+#pragma unroll 1
   for (int t = seg.t0; t < seg.t1; ++t) {
+    if (kMode) {
+      const int bit = spoiled_bit(seg, t);
+      if (!(const_cast<const volatile uint32_t*>(place->spoiled)[bit >> 5] >> (bit & 31) & 1)) continue;
+    }
     const TcTile k = tile_of<kMode>(P, seg, t);
     int r0, r1;
     half_seen<kMode>(a, k, seg, &r0, &r1);
-    for (int r = r0; r < r1; ++r) {
-      bool staged = k.staged;
-      int u = k.u0 + r, x = k.x0 + r;  // entry number, and entry or position
-      if (kMode) {
-        const TcView v = view_of<kMode>(P, seg, mem, k, row.j, true);
-        const bool entry = r >= v.e0;
-        if (entry ? r - v.e0 > n || !(seen_bits(a, row.b, row.i, n, r - v.e0) & 1) : r < v.c0 || r >= v.c1) continue;
-        u = entry ? r - v.e0 : r - v.org;
-        if ((kMode & kShare) && k.own) {
-          staged = entry && a.stage.data;
-          x = staged ? u : mem->S[row.j] + u;
+    const TcView v = kMode ? view_of<kMode>(P, seg, mem, k, row.j, true) : TcView{0, 0, -k.u0, -k.u0};
+#pragma unroll 1
+    for (int entries = 0; entries < 2; ++entries) {  // cached positions, then entries
+      const int end = min(r1, entries ? v.e0 + n + 1 : v.c1);
+#pragma unroll 1
+      for (int r = max(r0, entries ? v.e0 : v.c0); r < end; ++r) {
+        const int u = entries ? r - v.e0 : r - v.org;  // past S
+        if (entries && !(seen_bits(a, row.b, row.i, n, u) & 1)) continue;
+        if (kMode && a.window > 0 && abs(depth_of(a, row.b, row.i) - (entries ? depth_of(a, row.b, u) : u)) >= a.window) continue;
+        const bool staged = entries && a.stage.data;
+        const sv_kv_place& pl = staged ? a.stage : a.cache;
+        const int at = staged ? u : S + u;  // entry, or position
+        const int64_t off = entry_offset(pl, row.b, at, at);
+        if (off < 0) continue;
+        const char* vr = static_cast<const char*>(pl.data) + off + (a.cache.heads + seg.h) * row_step(pl) + col * (F8 ? 1 : 2);
+        uint32_t w[4];
+        if (F8) {
+          const uint2 y = *reinterpret_cast<const uint2*>(vr);
+          w[0] = y.x, w[1] = y.x >> 16, w[2] = y.y, w[3] = y.y >> 16;
+        } else {
+          const uint4 y = *reinterpret_cast<const uint4*>(vr);
+          w[0] = y.x, w[1] = y.y, w[2] = y.z, w[3] = y.w;
         }
-        if (a.window > 0 && abs(depth_of(a, row.b, row.i) - (u < 0 ? u : depth_of(a, row.b, u))) >= a.window) continue;
-      } else if (!(seen_bits(a, row.b, row.i, n, u) & 1)) {
-        continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 z = F8 ? e4m3x2_values(w[e] & 0xFFFFu) : make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+          if (!(fabsf(z.x) < __builtin_huge_valf())) sum[2 * e] += z.x;
+          if (!(fabsf(z.y) < __builtin_huge_valf())) sum[2 * e + 1] += z.y;
+        }
       }
-      const sv_kv_place& pl = staged ? a.stage : a.cache;
-      const int64_t off = entry_offset(pl, row.b, x, x);
-      if (off < 0) continue;
-      const char* vr = static_cast<const char*>(pl.data) + off + (a.cache.heads + seg.h) * row_step(pl);
-      const float v = pl.format == SV_KV_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(vr)[col])
-                                              : e4m3x2_values((uint32_t)(uint8_t)vr[col]).x;
-      if (!(fabsf(v) < __builtin_huge_valf())) sum += v;
     }
   }
-  return sum;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (part)
+      part[e] += sum[e];
+    else
+      out[e] = __float2bfloat16_rn(__bfloat162float(out[e]) + sum[e]);
+  }
 }
 
 // The rare steps of a tile's softmax, as calls so that they stay out of the
@@ -822,13 +847,12 @@ __device__ __forceinline__ bool spoiled_rows(const char* v, int r0, int valid) {
   return ((any[0] | any[1] | any[2] | any[3]) & (F8 ? 0x80808080u : 0x7FFF7FFFu)) != 0;
 }
 
-// As clean_rows_plain where most tiles are looked at, by a warp that the softmax does not wait for.  kVecs:
-// vectors of 16 bytes of a row.
+// As clean_rows_plain where most tiles are looked at, by a warp that the softmax does not wait for: tile t of
+// a segment.  kVecs: vectors of 16 bytes of a row.
 template <bool F8, int kMode, int kVecs>
-static __device__ __noinline__ void clean_rows(const TcParams& P, TcPlace* s, bool own, int x0, char* v, int r0, int valid, int r1) {
+static __device__ __noinline__ void clean_rows(const TcParams& P, TcPlace* s, int t, bool own, int x0, char* v, int r0, int valid, int r1) {
   constexpr int kSw = kVecs < 8 ? kVecs : 8;
   const int lane = threadIdx.x & 31;
-  volatile int* found = &s->found;
   auto at = [&](int x) {
     const int r = r0 + x / kVecs, c = x % kVecs;
     return reinterpret_cast<uint4*>(v + (c / kSw * kTile + r) * kSw * 16 + c % kSw * 16);
@@ -852,7 +876,9 @@ static __device__ __noinline__ void clean_rows(const TcParams& P, TcPlace* s, bo
       if (bx | by | bz | bw) {
         y.x &= ~bx, y.y &= ~by, y.z &= ~bz, y.w &= ~bw;
         *d = y;
-        *found = 1;
+        const int bit = spoiled_bit(s->seg, t);
+        atomicOr(&s->spoiled[bit >> 5], 1u << (bit & 31));
+        *const_cast<volatile int*>(&s->found) = 1;
       }
     }
   if (dirty || r1 > valid) fence_async_smem();
@@ -1253,11 +1279,11 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
               // (the products wait for each tile's arrival here, so that no load's phase is missed)
               wait(sync, b_vf + 8 * vslot, vlap & 1);
               if ((kMode & kForms) && r1 < k.valid) {
-                clean_rows<F8, kMode, C::kRow / 16>(P, place, k.own, k.x0, v, r0, r1, r1);
+                clean_rows<F8, kMode, C::kRow / 16>(P, place, t, k.own, k.x0, v, r0, r1, r1);
                 r0 = k.valid;
               }
               if (r0 < k.valid || k.valid % C::kStep)
-                clean_rows<F8, kMode, C::kRow / 16>(P, place, k.own, k.x0, v, r0, k.valid, (k.valid + C::kStep - 1) / C::kStep * C::kStep);
+                clean_rows<F8, kMode, C::kRow / 16>(P, place, t, k.own, k.x0, v, r0, k.valid, (k.valid + C::kStep - 1) / C::kStep * C::kStep);
               __syncwarp();
               if (lane == 0) mbar_arrive(b_vc + 8 * vslot);
               if (++vslot == C::kV) vslot = 0, ++vlap;
@@ -1708,16 +1734,12 @@ __global__ void __launch_bounds__(TcShape<F8, D, QM, kMode>::kThreads, 1) tc_att
             __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.out) + out + at;
             *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16(z[0] * inv, z[1] * inv), pack_bf16(z[2] * inv, z[3] * inv),
                                                       pack_bf16(z[4] * inv, z[5] * inv), pack_bf16(z[6] * inv, z[7] * inv));
-            if (spoiled)
-#pragma unroll 1
-              for (int e = 0; e < 8; ++e) d[e] = __float2bfloat16_rn(__bfloat162float(d[e]) + given_back<kMode>(P, kMode ? place.seg : found, &place.mem, me, at + e));
+            if (spoiled) give_back<F8, kMode>(P, kMode ? place.seg : found, &place, me, at, nullptr, d);
           } else {
             float* d = part + lrow * D + at;
             *reinterpret_cast<float4*>(d) = make_float4(z[0], z[1], z[2], z[3]);
             *reinterpret_cast<float4*>(d + 4) = make_float4(z[4], z[5], z[6], z[7]);
-            if (spoiled)
-#pragma unroll 1
-              for (int e = 0; e < 8; ++e) d[e] += given_back<kMode>(P, kMode ? place.seg : found, &place.mem, me, at + e);
+            if (spoiled) give_back<F8, kMode>(P, kMode ? place.seg : found, &place, me, at, d, nullptr);
           }
         };
         if (copies > 1) {  // each copy adds all shares of 32 / copies columns
