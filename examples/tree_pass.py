@@ -8,8 +8,8 @@ what matters is the order of the calls and what each hands to the next.
                      entries written to the staging buffer in the cache's format
     prefix_groups    which requests still hold the blocks of a common prompt
     tree_attention   the nodes over the committed cache and their own ancestors; a
-                     common prompt is read once; scores capped or less with the distance
-                     where the model has them so
+                     common prompt is read for several requests at once; scores capped or
+                     less with the distance where the model has them so
     adjust_logits    penalties and grammar masks on every node's row
     verify_tree      the accepted path and the next token
     kv_commit_tree   the path's entries moved into the paged cache

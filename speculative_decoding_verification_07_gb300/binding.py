@@ -661,7 +661,8 @@ class Verifier:
         are less by a head's slope times the distance.  window: rows see the keys
         at smaller distances alone.  depth [B, R]: the entries' positions past S
         (tree_mask's), for slopes and windows; None: a chain.  groups: what
-        prefix_groups gave for these tables, so that a group's prefix is read once."""
+        prefix_groups gave for these tables, so that a group's prefix is read once for as
+        many requests as have their rows (R * Hq / heads each, 64 at most) in one item."""
         if _allocates(stream, out, q):
             out = _empty_on(stream, q)
         s = _raw_stream(stream)

@@ -42,7 +42,7 @@ __device__ __forceinline__ Scan block_scan(Scan s, int (&w)[3][32], int* all_x, 
 // and 36 (19, 25, 40), an item's start and end 80.
 __device__ __forceinline__ int lot_size(const TcPlanning& p, int size, int shared, int boxes) {
   const int rows = p.a.R * p.group;
-  if (rows > p.rows / 2) return max(1, p.rows / rows);
+  if (rows > p.rows / 2) return 1;  // prompts
   const bool f8 = p.a.cache.format == SV_KV_E4M3;
   const float tiles = (float)((shared + kTile - 1) / kTile), own = (float)boxes * (float)(1 << p.shift) / kTile;
   int best = 1;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 // Which tiles a row block of a request sees: from the first to the last with a key that
 // the mask and the window leave any of its rows, by a CTA each.  Without it a prompt's
 // row blocks go through all tiles: the mask hides half of them, a window nearly all.
-// Writes the block's units (kLead and its tiles) and its first tile.  Four prompts of up to
+// Writes the block's units (p.lead and its tiles) and its first tile.  Four prompts of up to
 // 2041 entries under a window of 1024: 14 us here, and 1971 -> 392 us for the attention with it (and
 // with scores shaped in registers).  Latency of the mask's rows bounds it.
 __global__ void __launch_bounds__(kRangeThreads) ranges_kernel(const __grid_constant__ TcPlanning p) {

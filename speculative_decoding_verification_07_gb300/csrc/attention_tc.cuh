@@ -900,17 +900,17 @@ static __device__ __noinline__ void clean_rows(const TcParams& P, TcPlace* s, in
 // warp does between products (waits, commits: a third of its time) bounds that.  Handing scores over in halves
 // of 64 keys, to have the next half's under way, doubled those steps: 249 us.
 //
-// Forms of the scores (kForms): 64 trees over 128 to 8192 positions, capped scores 201 us
-// in bf16 as without (bytes bound both), 8-bit with a distance's share 263 (a stream's chain, which
-// the form lengthens: per 32 keys 1050 cycles of loads, factors and the form, 630 of
-// weights, 1000 of stores and what is seen); under a window of 1024 single tokens 68 us: nine tiles
+// Forms of the scores (kForms): 64 trees over 128 to 8192 positions, capped scores 202 us
+// in bf16 as without (bytes bound both), 8-bit with a distance's share 254 (a stream's chain, which
+// the form lengthens: per 32 keys some 1000 cycles of loads, factors and the form, 630 of
+// weights, 1000 of stores and what is seen); under a window of 1024 single tokens 69 us: nine tiles
 // an item are 22000 cycles, and 7500 more its start and end.  Prompts of up to 2041
-// entries and as many cached positions under that window 230 us: 256 rows a tile take
+// entries and as many cached positions under that window 233 us: 256 rows a tile take
 // 7000 cycles, more than half of it the softmax of eight warps.
-// Shared prefixes (kShare): a group's rows are an item's, so that the prefix is read
-// once (see lot_size), and its members' own keys are packed behind it.  A first version made
+// Shared prefixes (kShare): rows of as many of a group's requests as lot_size has are an item's, which
+// reads the prefix once for them, and their own keys are packed behind it.  A first version made
 // the prefix's and each request's own parts apart and joined them in another kernel: 256 chains
-// of four drafts in groups of four over 1024 shared tokens and up to 31 of their own 219 us, 76 as it is; but 64
+// of four drafts in groups of four over 1024 shared tokens and up to 31 of their own 219 us, 77 as it is; but 64
 // single tokens with 128 to 4096 own positions 157, 130 as it is, as a tile of own keys is weighed by
 // one request's warps.
 template <bool F8, int D, int QM, int kMode>
