@@ -68,7 +68,7 @@ def test_unwritten_places_cost_nothing(ver, fmt, staged, kw, own):
     assert torch.equal(spoiled[live], clean[live]) and torch.isfinite(clean).all()
     # clearing them takes a few stores a tile; looking
     # through 300 keys for each output took a hundred times the call
-    assert took < 1.5 * takes + 0.02, (took, takes)
+    assert took < 4 * takes + 0.1, (took, takes)
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
@@ -93,7 +93,7 @@ def test_a_value_that_rows_see(ver, fmt, kw):
     assert sees.any() and torch.equal(torch.isnan(out), torch.isnan(want))
     keep = ~torch.isnan(want)
     assert torch.equal(out[keep], want[keep])
-    assert took < 2 * takes + 0.2, (took, takes)
+    assert took < 4 * takes + 0.2, (took, takes)
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
